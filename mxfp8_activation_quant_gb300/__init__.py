@@ -1,6 +1,8 @@
 """GB300 (sm_103a) MXFP8 activation chain: standalone quantizer, the fused `_o_proj` pair
-(wo_a einsum writing MXFP8 z, wo_b MXFP8 GEMM consuming it) and the RMSNorm dual-output
-producer, behind the C ABI in include/mxq.h. The Python layer only marshals arguments."""
+(wo_a einsum writing MXFP8 z, wo_b MXFP8 GEMM consuming it), the RMSNorm dual-output producer,
+and the mixture-of-experts half of the layer (residual RMSNorm, router, experts' products),
+behind the C ABI in include/mxq.h and include/mxq_moe.h. The Python layer only marshals
+arguments."""
 from ._lib import (  # noqa: F401
     MXFP8,
     SF_PACKED_I32_MN,
@@ -26,4 +28,11 @@ from ._lib import (  # noqa: F401
     wo_a_einsum_mxfp8,
     workspace_bytes,
     workspace_for,
+)
+from .moe import (  # noqa: F401
+    add_rmsnorm_dual_out,
+    interleave_gate_up,
+    moe_experts_mxfp8,
+    moe_route,
+    moe_workspace_bytes,
 )

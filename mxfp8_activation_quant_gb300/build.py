@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmxq.so")
-SOURCES = ["api.cu", "quantize.cu", "gemm_mxf8.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "quantize.cu", "gemm_mxf8.cu", "noalloc.cu", "tma_maps.cu", "moe_api.cu", "add_rmsnorm.cu",
+           "moe_route.cu", "moe_experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -31,7 +32,7 @@ def nvcc() -> str:
 
 
 def _newest_input() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "mxq.h"), __file__]
+    files = [os.path.join(d, f) for d in (CSRC, INCLUDE) for f in os.listdir(d)] + [__file__]
     return max(os.path.getmtime(f) for f in files)
 
 

@@ -1,0 +1,753 @@
+// The experts' products of a mixture of experts (moe_experts_mxfp8):
+//   plan     sorts the (token, slot) pairs by expert and cuts every expert's rows into token tiles
+//   gather   copies each pair's MXFP8 activations to its expert's rows (data and scales)
+//   GEMM 1   (g, u) = W13_e x, a = MXFP8(bf16(silu(g) u)) in the epilogue
+//   GEMM 2   y = W2_e a, bf16 per pair
+//   combine  out[t] = bf16(sum_j w[t, j] y[pair(t, j)]), fp32 sum in slot order
+//
+// Both GEMMs are one kernel template on CTA pairs (tcgen05 cta_group::2, kind::mxf8f6f4 block
+// scaled), persistent, with the WEIGHTS on the MMA's M side: M = 256 weight rows (128 per CTA) and
+// N = the token tile, up to 224 tokens in steps of 16. An expert's token count is ragged and its
+// weight rows are not, so the ragged dimension sits where the MMA's size follows it exactly.
+// Two accumulators of 224 TMEM columns alternate, so a tile's epilogue runs under the next tile's
+// MMAs; the remaining 64 columns hold the scales of 5 stages.
+//
+// Up to about 224 tokens per expert the GEMMs stream the active experts' weights (33/32 B per
+// element) and are HBM bound, beyond that tensor bound.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include "mxq_device.cuh"
+#include "mxq_moe_internal.h"
+#include "mxq_tma.h"
+
+namespace mxq {
+namespace {
+
+constexpr int kTileTokens = 224;   // most tokens of a tile (MMA N)
+constexpr int kSlotRows = 256;     // scale rows reserved per tile: two F8_128x4 row tiles
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxExperts = 1024;
+constexpr int kStatusTimeout = 6;  // MXQ_ERR_TIMEOUT
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// A token tile: rows [row0, row0 + n) of the expert-sorted pairs; tiles [first, last) belong to the
+// same expert. Its scales lie in rows [256 i, 256 i + n) of the scale arrays, i the tile's index.
+struct __align__(16) Tile {
+  int32_t expert, row0, n, pad;
+  int32_t first, last, pad2, pad3;
+};
+// First item of a pair of SMs in one GEMM: linear index, tile and weight-row block.
+struct __align__(16) Start {
+  int32_t item, tile, block, pad;
+};
+
+struct Layout {  // byte offsets into the workspace
+  int64_t max_tiles, pairs_max;
+  int64_t tiles, start1, start2, pair_row, pair_slot, xp, xsf, hq, hsf, y, total;
+  Layout(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I, int sm_pairs) {
+    const int64_t P = T * k;
+    pairs_max = sm_pairs;
+    max_tiles = P / kTileTokens + (E < P ? E : P);
+    int64_t o = 0;
+    auto take = [&](int64_t bytes) {
+      const int64_t at = o;
+      o += round_up(bytes, 256);
+      return at;
+    };
+    tiles = take(max_tiles * static_cast<int64_t>(sizeof(Tile)));
+    start1 = take((pairs_max + 1) * static_cast<int64_t>(sizeof(Start)));
+    start2 = take((pairs_max + 1) * static_cast<int64_t>(sizeof(Start)));
+    pair_row = take(P * 4);
+    pair_slot = take(P * 4);
+    xp = take(P * H);
+    xsf = take(max_tiles * kSlotRows * (H / 32));
+    hq = take(P * I);
+    hsf = take(max_tiles * kSlotRows * (I / 32));
+    y = take(P * H * 2);
+    total = o;
+  }
+};
+
+// ------------------------------------------------------------------------------------------
+// plan
+// ------------------------------------------------------------------------------------------
+struct PlanArgs {
+  const int32_t* ids;
+  int32_t P, E;
+  int32_t blocks1, blocks2;  // weight-row blocks per expert of the two GEMMs
+  int32_t pairs1, pairs2;    // SM pairs of the two GEMMs
+  Tile* tiles;
+  Start* start1;
+  Start* start2;
+  int32_t* pair_row;   // expert-sorted row of pair p, or -1
+  int32_t* pair_slot;  // its row in the scale arrays
+};
+
+// Cost of a token tile in one k-block, in MMA columns: the MMAs take time proportional to n; a
+// small tile is bound by its weight rows' way through L2 and shared memory instead.
+__device__ __forceinline__ int tile_cost(int n16) { return (n16 > 96 ? n16 : 96) + 16; }
+
+struct Scan3 {
+  int rows, tiles;
+  int cost;
+};
+__device__ __forceinline__ Scan3 add3(const Scan3 a, const Scan3 b) {
+  return {a.rows + b.rows, a.tiles + b.tiles, a.cost + b.cost};
+}
+__device__ __forceinline__ Scan3 shfl_up3(const Scan3 a, int d) {
+  return {__shfl_up_sync(0xffffffffu, a.rows, d), __shfl_up_sync(0xffffffffu, a.tiles, d),
+          __shfl_up_sync(0xffffffffu, a.cost, d)};
+}
+
+// One block: counts per expert, their scans, the tiles, every pair's row, and the SM pairs' shares.
+// A row's place within its expert follows the order of shared-memory atomics; no result depends on
+// it (a column of an MMA never meets another).
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+  __shared__ int cnt[kMaxExperts], row0[kMaxExperts + 1], tile0[kMaxExperts + 1], cum[kMaxExperts + 1];
+  __shared__ int next[kMaxExperts], step[kMaxExperts];
+  __shared__ Scan3 part[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
+  cnt[tid] = 0;
+  __syncthreads();
+  for (int p = tid; p < a.P; p += kPlanThreads) {
+    const int e = a.ids[p];
+    if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
+  }
+  __syncthreads();
+  const int c = cnt[tid];
+  const int nt = (c + kTileTokens - 1) / kTileTokens;
+  const int per = nt > 0 ? ((c + nt - 1) / nt + 15) / 16 * 16 : 16;  // tokens per tile, at most 224
+  const int last_n = c - (nt - 1) * per;                            // of the last tile (at least 1)
+  const int wb = tile_cost(per);
+  const int wl = nt > 0 ? (nt - 1) * wb + tile_cost((last_n + 15) / 16 * 16) : 0;
+  Scan3 v = {c, nt, wl};
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Scan3 u = shfl_up3(v, d);
+    if (lane >= d) v = add3(v, u);
+  }
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    Scan3 s = part[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const Scan3 u = shfl_up3(s, d);
+      if (lane >= d) s = add3(s, u);
+    }
+    part[lane] = s;
+  }
+  __syncthreads();
+  if (warp > 0) v = add3(v, part[warp - 1]);  // inclusive
+  row0[tid + 1] = v.rows;
+  tile0[tid + 1] = v.tiles;
+  cum[tid + 1] = v.cost;
+  if (tid == 0) row0[0] = tile0[0] = cum[0] = 0;
+  next[tid] = 0;
+  step[tid] = per;
+  __syncthreads();
+  if (nt > 0)
+    for (int i = 0; i < nt; ++i) {
+      Tile t = {tid, row0[tid] + i * per, i == nt - 1 ? last_n : per, 0, tile0[tid], tile0[tid] + nt, 0, 0};
+      a.tiles[tile0[tid] + i] = t;
+    }
+  // first items of the SM pairs: equal shares of the cost, an item goes where its start lies
+  const int n_starts = (a.pairs1 + 1) + (a.pairs2 + 1);
+  if (tid < n_starts) {
+    const bool second = tid > a.pairs1;
+    const int p = second ? tid - a.pairs1 - 1 : tid;
+    const int np = second ? a.pairs2 : a.pairs1;
+    const int F = second ? a.blocks2 : a.blocks1;
+    const int64_t total = static_cast<int64_t>(cum[a.E]) * F;
+    const int64_t lo = total * p / np;
+    Start s = {F * tile0[a.E], tile0[a.E], 0, 0};
+    if (p < np && total > 0) {
+      int b = 0, t = a.E;  // largest e with F cum[e] <= lo
+      while (t - b > 1) {
+        const int m = (b + t) >> 1;
+        if (static_cast<int64_t>(cum[m]) * F <= lo) b = m;
+        else t = m;
+      }
+      const int w = cum[b + 1] - cum[b];  // > 0: lo < total, so the last such e has items
+      const int tiles_e = tile0[b + 1] - tile0[b];
+      const int64_t off = lo - static_cast<int64_t>(cum[b]) * F;
+      int f = static_cast<int>(off / w);
+      const int rem = static_cast<int>(off - static_cast<int64_t>(f) * w);
+      const int wbe = tile_cost(step[b]);
+      int i = (rem + wbe - 1) / wbe;
+      if (i >= tiles_e) {
+        i = 0;
+        ++f;
+      }
+      if (f >= F)
+        s = {F * tile0[b + 1], tile0[b + 1], 0, 0};
+      else
+        s = {F * tile0[b] + f * tiles_e + i, tile0[b] + i, f, 0};
+    }
+    (second ? a.start2 : a.start1)[p] = s;
+  }
+  for (int p = tid; p < a.P; p += kPlanThreads) {
+    const int e = a.ids[p];
+    int row = -1, slot = 0;
+    if (e >= 0 && e < a.E) {
+      const int r = atomicAdd(&next[e], 1);
+      const int i = r / step[e];
+      row = row0[e] + r;
+      slot = (tile0[e] + i) * kSlotRows + r - i * step[e];
+    }
+    a.pair_row[p] = row;
+    a.pair_slot[p] = slot;
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// gather: one block per token, its row read once and written to each of its k places
+// ------------------------------------------------------------------------------------------
+struct GatherArgs {
+  const uint8_t* x;
+  int64_t ldx;
+  const uint8_t* sf;
+  int32_t sf_tiled;
+  int32_t k;
+  int64_t H;
+  const int32_t* pair_row;
+  const int32_t* pair_slot;
+  uint8_t* xp;
+  uint8_t* xsf;
+};
+constexpr int kGatherThreads = 128;
+
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs a) {
+  const int64_t t = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int chunks = static_cast<int>(a.H / 16), words = static_cast<int>(a.H / 128);
+  for (int c = threadIdx.x; c < chunks; c += kGatherThreads) {
+    const uint4 v = ld_stream_u4(a.x + t * a.ldx + 16 * c);
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t r = a.pair_row[t * a.k + j];
+      if (r >= 0) *reinterpret_cast<uint4*>(a.xp + r * a.H + 16 * c) = v;
+    }
+  }
+  for (int w = threadIdx.x; w < words; w += kGatherThreads) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(
+        a.sf + (a.sf_tiled ? tiled128x4_word_offset(t, w, words) : (t * words + w) * 4));
+    for (int j = 0; j < a.k; ++j)
+      if (a.pair_row[t * a.k + j] >= 0)
+        *reinterpret_cast<uint32_t*>(a.xsf + tiled128x4_word_offset(a.pair_slot[t * a.k + j], w, words)) = v;
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// grouped GEMM
+// ------------------------------------------------------------------------------------------
+constexpr int kThreads = 352;  // producer, MMA, 8 epilogue warps, scale copies
+constexpr int BM = 128;        // weight rows per CTA
+constexpr int BK = 128;        // K bytes per stage
+constexpr int STAGES = 5;
+constexpr int kGateUp = 0, kDown = 1;
+
+template <int MODE>
+struct GemmCfg {
+  static constexpr int A_BYTES = BM * BK;
+  static constexpr int B_BYTES = kTileTokens / 2 * BK;  // a CTA holds half of the tile's tokens
+  static constexpr int SF_BYTES = 512 * 3;              // the CTA's weight rows, two token atoms
+  static constexpr int SF_COLS = 12;
+  static constexpr int OFF_B = STAGES * A_BYTES;
+  static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
+  // epilogue staging, one row per token: 64 bf16 features (gate-up) or 128 (down)
+  static constexpr int ROW_BYTES = MODE == kGateUp ? 128 : 256;
+  static constexpr int OFF_EPI = OFF_SF + STAGES * SF_BYTES;
+  static constexpr int OFF_BAR = OFF_EPI + kTileTokens * ROW_BYTES;
+  static constexpr int OFF_MISC = OFF_BAR + (3 * STAGES + 5) * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static constexpr int TMEM_SF = 2 * kTileTokens;  // first scale column
+  static_assert(B_BYTES % 1024 == 0, "swizzle atoms");
+  static_assert(TMEM_SF + STAGES * SF_COLS <= 512, "TMEM");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+struct GemmArgs {
+  const Tile* tiles;
+  const Start* start;
+  int32_t kbs;       // 128-wide k-blocks
+  int32_t blocks;    // 256-row weight blocks per expert
+  int32_t rows;      // weight rows per expert
+  // gate-up: E4M3 activations [pairs, rows / 2] and their scales by tile
+  uint8_t* hq;
+  uint8_t* hsf;
+  // down: bf16 [pairs, rows]
+  uint16_t* y;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void report(int32_t* status) {
+  if (status != nullptr) atomicCAS(status, 0, kStatusTimeout);
+}
+
+// The items of one SM pair: an expert's weight-row blocks in turn, each with all of the expert's
+// token tiles, so that the second tile finds the block's weights in L2.
+struct Items {
+  const Tile* tiles;
+  int left, tile, block, blocks;
+  Tile t;
+  __device__ __forceinline__ Items(const GemmArgs& a, int pair) {
+    const Start s = a.start[pair], e = a.start[pair + 1];
+    tiles = a.tiles;
+    left = e.item - s.item;
+    tile = s.tile;
+    block = s.block;
+    blocks = a.blocks;
+    if (left > 0) t = tiles[tile];
+  }
+  __device__ __forceinline__ void next() {
+    if (--left <= 0) return;
+    if (++tile == t.last) {
+      if (++block == blocks)
+        block = 0;
+      else
+        tile = t.first;
+    }
+    t = tiles[tile];
+  }
+  __device__ __forceinline__ int n16() const { return (t.n + 15) & ~15; }
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    experts_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ CUtensorMap tm_sfw, const __grid_constant__ CUtensorMap tm_sfx,
+                        const GemmArgs p) {
+  using C = GemmCfg<MODE>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sraw = smem_u32(smem_raw);
+  const uint32_t sbase = (sraw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - sraw);
+  const uint32_t bar_full = sbase + C::OFF_BAR;
+  const uint32_t bar_empty = bar_full + 8 * STAGES;
+  const uint32_t bar_sf = bar_empty + 8 * STAGES;
+  const uint32_t bar_accf = bar_sf + 8 * STAGES;  // two accumulators
+  const uint32_t bar_acce = bar_accf + 16;
+  const uint32_t bar_drain = bar_acce + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* issued_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
+  int* consumed_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 12);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1;
+  const int nk = p.kbs;
+
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_sfw);
+    tma_prefetch_desc(&tm_sfx);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+      mbar_init(bar_sf + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_accf + 8 * b, 1);
+      mbar_init(bar_acce + 8 * b, 16);  // the epilogue warps of both CTAs
+    }
+    mbar_init(bar_drain, 2);  // the MMA thread and the scale-copy thread
+    *abort_flag = 0;
+    *issued_cnt = 0;
+    *consumed_cnt = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before any load or commit can reach them
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait_primary();  // the plan and the activations are the preceding kernels'
+  Items item(p, pair);
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- producer (both CTAs) ----------------
+    const uint32_t full0 = mapa_shared(bar_full, 0);  // the even CTA's stage barriers
+    int it = 0;
+    for (; item.left > 0 && !*abort_flag; item.next()) {
+      const int n16 = item.n16(), half = n16 >> 1;
+      const int boxes = (half + 15) >> 4, atoms = n16 > 128 ? 2 : 1;
+      const uint32_t tx = 2u * static_cast<uint32_t>(C::A_BYTES + boxes * 2048 + 512 + 512 * atoms);
+      const int w_row = item.t.expert * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
+      const int w_atom = (w_row >> 7) * nk;
+      const int x_row = item.t.row0 + half * static_cast<int>(rank);
+      const int x_atom = item.tile * 2 * nk;
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        const int s = it % STAGES;
+        if (!mbar_wait_bounded(bar_empty + 8 * s, ((it / STAGES) & 1) ^ 1)) {
+          *abort_flag = 1;
+          report(p.status);
+          break;
+        }
+        const uint32_t fb = full0 + 8 * s;
+        if (leader) mbar_arrive_expect_tx(bar_full + 8 * s, tx);
+        const uint32_t sf = sbase + C::OFF_SF + s * C::SF_BYTES;
+        tma_load_2d_pair(sbase + s * C::A_BYTES, &tm_w, fb, kb * BK, w_row);
+        tma_load_2d_pair(sf, &tm_sfw, fb, 0, w_atom + kb);
+        for (int b = 0; b < boxes; ++b)
+          tma_load_2d_pair(sbase + C::OFF_B + s * C::B_BYTES + 2048 * b, &tm_x, fb, kb * BK, x_row + 16 * b);
+        tma_load_2d_pair(sf + 512, &tm_sfx, fb, 0, x_atom + kb);
+        if (atoms == 2) tma_load_2d_pair(sf + 1024, &tm_sfx, fb, 0, x_atom + nk + kb);
+      }
+    }
+    *issued_cnt = it;
+  } else if (warp == 1 && lane == 0) {
+    // ---------------- MMA issuer (even CTA) ----------------
+    if (leader) {
+      int it = 0, ti = 0;
+      for (; item.left > 0 && !*abort_flag; item.next(), ++ti) {
+        const int b = ti & 1;
+        if (!mbar_wait_bounded(bar_acce + 8 * b, ((ti >> 1) & 1) ^ 1)) {
+          *abort_flag = 1;
+          report(p.status);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t n16 = static_cast<uint32_t>(item.n16());
+        bool ok = true;
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait_bounded(bar_sf + 8 * s, (it / STAGES) & 1)) {
+            *abort_flag = 1;
+            report(p.status);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sfa_t = tmem + C::TMEM_SF + s * C::SF_COLS;
+          const uint64_t ad = sdesc_kmajor_sw128(sbase + s * C::A_BYTES);
+          const uint64_t bd = sdesc_kmajor_sw128(sbase + C::OFF_B + s * C::B_BYTES);
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            tc_mma_mxf8_pair(tmem + kTileTokens * b, ad + 2 * k, bd + 2 * k, idesc_mxf8(2 * BM, n16, k, k), sfa_t,
+                             sfa_t + 4, (kb | k) != 0 ? 1u : 0u);
+          tc_commit_pair(bar_empty + 8 * s, 0x3);
+        }
+        tc_commit_pair(bar_accf + 8 * b, 0x3);
+        if (!ok) break;
+      }
+      *consumed_cnt = it;
+    }
+  } else if (warp == 10) {
+    // ---------------- scale copies (even CTA) ----------------
+    if (leader && lane == 0) {
+      int it = 0;
+      for (; item.left > 0 && !*abort_flag; item.next()) {
+        const bool two = item.n16() > 128;
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait_bounded(bar_full + 8 * s, (it / STAGES) & 1)) {
+            *abort_flag = 1;
+            report(p.status);
+            break;
+          }
+          tc_fence_after();
+          const uint32_t src = sbase + C::OFF_SF + s * C::SF_BYTES;
+          const uint32_t dst = tmem + C::TMEM_SF + s * C::SF_COLS;
+          tc_cp_sf_atom_pair(dst, sdesc_sf_atom(src));
+          tc_cp_sf_atom_pair(dst + 4, sdesc_sf_atom(src + 512));
+          if (two) tc_cp_sf_atom_pair(dst + 8, sdesc_sf_atom(src + 1024));
+          tc_commit_pair(bar_sf + 8 * s, 0x1);
+        }
+      }
+    }
+  } else if (warp >= 2 && warp < 10) {
+    // ---------------- epilogue (both CTAs) ----------------
+    // TMEM lane = weight row, column = token. The warps turn the tile through shared memory (one
+    // row per token) so that a token's features leave in whole sectors. Warp q = warp % 4 owns
+    // TMEM lanes 32 q .. 32 q + 31; of the tile's 16-token chunks, warps 2..5 take the even ones
+    // and 6..9 the odd ones. Every warp runs every item's barriers, also after an abort.
+    const int q = warp & 3, odd = (warp - 2) >> 2, et = static_cast<int>(threadIdx.x) - 64;
+    const uint32_t acce0 = mapa_shared(bar_acce, 0);
+    const uint32_t stage = sbase + C::OFF_EPI;
+    int ti = 0;
+    for (; item.left > 0; item.next(), ++ti) {
+      const int b = ti & 1, n = item.t.n;
+      bool ok = !*abort_flag;
+      if (ok && !mbar_wait_bounded(bar_accf + 8 * b, (ti >> 1) & 1)) {
+        *abort_flag = 1;
+        report(p.status);
+        ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTileTokens * b;
+        for (int ch = odd; 16 * ch < n; ch += 2) {
+          uint32_t acc[16];
+          tmem_ld_x16(t_lane + 16 * ch, acc);
+          tmem_ld_wait();
+          if (MODE == kGateUp) {
+            // rows alternate gate, up: lane pairs (2 i, 2 i + 1) hold feature 16 q + i. Of two
+            // tokens the even lane finishes the first and the odd lane the second.
+            const int up = lane & 1, f = 16 * q + (lane >> 1);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float a0 = __uint_as_float(acc[2 * c]), a1 = __uint_as_float(acc[2 * c + 1]);
+              const float o = __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 1);
+              const float g = up ? o : a0, u = up ? a1 : o;
+              const float h = __fdividef(g, 1.f + __expf(-g)) * u;
+              const int tok = 16 * ch + 2 * c + up;
+              // 16-byte pieces of a 128-byte row are XOR-swizzled by the row
+              const uint32_t at = stage + tok * 128 + (((f >> 3) ^ (2 * (tok & 3))) << 4) + (f & 7) * 2;
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(bf16x2_rn(h, 0.f))) : "memory");
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint32_t w = bf16x2_rn(__uint_as_float(acc[2 * c]), __uint_as_float(acc[2 * c + 1]));
+              const uint32_t at = stage + (16 * ch + 2 * c) * 256 + (32 * q + lane) * 2;
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(w)) : "memory");
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 256), "h"(static_cast<uint16_t>(w >> 16)) : "memory");
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {  // the MMAs may overwrite this accumulator now
+          if (leader)
+            mbar_arrive(bar_acce + 8 * b);
+          else
+            mbar_arrive_remote(acce0 + 8 * b);
+        }
+      }
+      named_barrier(1, 256);
+      if (ok) {
+        if (MODE == kGateUp) {
+          // one thread = one token and one 32-feature group: the rule of mxfp8_quantize
+          const int64_t ld = p.rows / 2;
+          const int f0 = item.block * 128 + static_cast<int>(rank) * 64;
+          for (int i = et; i < 2 * n; i += 256) {
+            const int tok = i >> 1, g = i & 1;
+            uint4 v[4];
+            uint32_t amax = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = ld_smem_v4(stage + tok * 128 + (((4 * g + j) ^ (2 * (tok & 3))) << 4));
+              amax = max(amax, absmax8(v[j]));
+            }
+            const uint32_t code = ue8m0_from_bf16_amax(amax);
+            const float s = ue8m0_inverse(code);
+            const uint2 q0 = quant8(v[0], s), q1 = quant8(v[1], s), q2 = quant8(v[2], s), q3 = quant8(v[3], s);
+            const int f = f0 + 32 * g;
+            uint4* dst = reinterpret_cast<uint4*>(p.hq + (item.t.row0 + tok) * ld + f);
+            dst[0] = make_uint4(q0.x, q0.y, q1.x, q1.y);
+            dst[1] = make_uint4(q2.x, q2.y, q3.x, q3.y);
+            p.hsf[tiled128x4_word_offset(static_cast<int64_t>(item.tile) * kSlotRows + tok, f >> 7, ld >> 7) + ((f >> 5) & 3)] =
+                static_cast<uint8_t>(code);
+          }
+        } else {
+          const int f0 = item.block * (2 * BM) + static_cast<int>(rank) * BM;
+          if (f0 < p.rows)  // the last block of an odd number of 128-row tiles has one half
+            for (int i = et; i < 16 * n; i += 256) {
+              const int tok = i >> 4, j = i & 15;
+              const uint4 v = ld_smem_v4(stage + tok * 256 + 16 * j);
+              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(item.t.row0 + tok) * p.rows + f0 + 8 * j) = v;
+            }
+        }
+      }
+      named_barrier(1, 256);
+    }
+  }
+  __syncwarp();
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs have left their loops: issue counts and abort flags are final
+  if (leader && warp == 0 && lane == 0) {
+    const int peer_abort = ld_dsmem_s32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), 1));
+    if (*abort_flag || peer_abort) {
+      // wait (bounded) for every stage either CTA issued and the MMA warp did not consume
+      const int peer_issued = ld_dsmem_s32(mapa_shared(smem_u32(issued_cnt), 1));
+      const int hi = *issued_cnt > peer_issued ? *issued_cnt : peer_issued;
+      for (int i = *consumed_cnt; i < hi; ++i)
+        (void)mbar_wait_bounded(bar_full + 8 * (i % STAGES), (i / STAGES) & 1);
+      *abort_flag = 1;
+    }
+  }
+  __syncthreads();
+  if (leader && (warp == 1 || warp == 10) && lane == 0 && *abort_flag) {
+    tc_commit_pair(bar_drain, 0x1);  // arrives once every MMA / copy this thread issued has completed
+    if (warp == 1) (void)mbar_wait_bounded(bar_drain, 0);
+  }
+  __syncthreads();
+  cluster_sync_all();  // the pair's MMAs and copies are over before either CTA frees TMEM or leaves
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// combine: out[t] = bf16(sum_j w[t, j] y[row(t, j)]), 8 columns per thread
+// ------------------------------------------------------------------------------------------
+struct CombineArgs {
+  const uint16_t* y;
+  const float* weights;
+  const int32_t* pair_row;
+  int32_t k;
+  int64_t H, ldo;
+  uint16_t* out;
+};
+constexpr int kCombineThreads = 128;
+
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a) {
+  pdl_wait_primary();
+  const int64_t t = blockIdx.x;
+  const int64_t c = 8 * (static_cast<int64_t>(blockIdx.y) * kCombineThreads + threadIdx.x);
+  if (c >= a.H) return;
+  float s[8] = {};
+#pragma unroll 8
+  for (int j = 0; j < a.k; ++j) {
+    const int64_t r = a.pair_row[t * a.k + j];
+    if (r < 0) continue;
+    const float w = a.weights[t * a.k + j];
+    const uint4 v = ld_stream_u4(a.y + r * a.H + c);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[2 * i] = fmaf(w, bf16_lo(u[i]), s[2 * i]);
+      s[2 * i + 1] = fmaf(w, bf16_hi(u[i]), s[2 * i + 1]);
+    }
+  }
+  *reinterpret_cast<uint4*>(a.out + t * a.ldo + c) =
+      make_uint4(bf16x2_rn(s[0], s[1]), bf16x2_rn(s[2], s[3]), bf16x2_rn(s[4], s[5]), bf16x2_rn(s[6], s[7]));
+}
+
+// ------------------------------------------------------------------------------------------
+// host
+// ------------------------------------------------------------------------------------------
+// A launch that may begin while the preceding kernel drains (its griddepcontrol.wait orders it).
+template <typename K, typename... Args>
+cudaError_t launch_dependent(K kern, dim3 grid, int threads, int smem, int cluster, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.attrs = attrs;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int MODE>
+cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, const void* act_sf, int64_t act_rows, int64_t K,
+                             int64_t max_tiles, int pairs, const GemmArgs& ga, cudaStream_t stream) {
+  using C = GemmCfg<MODE>;
+  auto kern = experts_gemm_kernel<MODE>;
+  static const cudaError_t attr_err =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (attr_err != cudaSuccess) return attr_err;
+  CUtensorMap tm_w, tm_x, tm_sfw, tm_sfx;
+  if (!make_map(&tm_w, w.data, w.rows, K, w.ld, BM) || !make_map(&tm_x, act, act_rows, K, K, 16) ||
+      !make_sf_map(&tm_sfw, w.sf, w.rows / 128 * (K / 128)) || !make_sf_map(&tm_sfx, act_sf, max_tiles * 2 * (K / 128)))
+    return cudaErrorInvalidValue;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads, C::SMEM_BYTES, 2, stream, tm_w,
+                          tm_x, tm_sfw, tm_sfx, ga);
+}
+
+}  // namespace
+
+int64_t experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I) {
+  return Layout(T, k, E, H, I, num_sms() / 2).total;
+}
+
+cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
+  const int sm_pairs = num_sms() / 2;
+  const Layout lay(l.T, l.k, l.E, l.H, l.I, sm_pairs);
+  uint8_t* ws = static_cast<uint8_t*>(l.workspace);
+  const int64_t P = l.T * l.k;
+  const int64_t blocks1 = ceil_div(2 * l.I, 2 * BM), blocks2 = ceil_div(l.H, 2 * BM);
+  auto pairs_for = [&](int64_t blocks) {
+    const int64_t items = lay.max_tiles * blocks;
+    return static_cast<int>(items < sm_pairs ? items : sm_pairs);
+  };
+  PlanArgs pa = {};
+  pa.ids = l.ids;
+  pa.P = static_cast<int32_t>(P);
+  pa.E = l.E;
+  pa.blocks1 = static_cast<int32_t>(blocks1);
+  pa.blocks2 = static_cast<int32_t>(blocks2);
+  pa.pairs1 = pairs_for(blocks1);
+  pa.pairs2 = pairs_for(blocks2);
+  pa.tiles = reinterpret_cast<Tile*>(ws + lay.tiles);
+  pa.start1 = reinterpret_cast<Start*>(ws + lay.start1);
+  pa.start2 = reinterpret_cast<Start*>(ws + lay.start2);
+  pa.pair_row = reinterpret_cast<int32_t*>(ws + lay.pair_row);
+  pa.pair_slot = reinterpret_cast<int32_t*>(ws + lay.pair_slot);
+  plan_kernel<<<1, kPlanThreads, 0, stream>>>(pa);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  GatherArgs ga = {};
+  ga.x = static_cast<const uint8_t*>(l.x->data);
+  ga.ldx = l.x->ld;
+  ga.sf = static_cast<const uint8_t*>(l.x->sf);
+  ga.sf_tiled = l.x->sf_layout == MXQ_SF_TILED_128X4;
+  ga.k = l.k;
+  ga.H = l.H;
+  ga.pair_row = pa.pair_row;
+  ga.pair_slot = pa.pair_slot;
+  ga.xp = ws + lay.xp;
+  ga.xsf = ws + lay.xsf;
+  e = launch_dependent(gather_kernel, dim3(static_cast<unsigned>(l.T), 1, 1), kGatherThreads, 0, 1, stream, ga);
+  if (e != cudaSuccess) return e;
+
+  GemmArgs g1 = {};
+  g1.tiles = pa.tiles;
+  g1.start = pa.start1;
+  g1.kbs = static_cast<int32_t>(l.H / BK);
+  g1.blocks = pa.blocks1;
+  g1.rows = static_cast<int32_t>(2 * l.I);
+  g1.hq = ws + lay.hq;
+  g1.hsf = ws + lay.hsf;
+  g1.status = l.status;
+  e = launch_gemm_mode<kGateUp>(*l.w13, ga.xp, ga.xsf, P, l.H, lay.max_tiles, pa.pairs1, g1, stream);
+  if (e != cudaSuccess) return e;
+
+  GemmArgs g2 = {};
+  g2.tiles = pa.tiles;
+  g2.start = pa.start2;
+  g2.kbs = static_cast<int32_t>(l.I / BK);
+  g2.blocks = pa.blocks2;
+  g2.rows = static_cast<int32_t>(l.H);
+  g2.y = reinterpret_cast<uint16_t*>(ws + lay.y);
+  g2.status = l.status;
+  e = launch_gemm_mode<kDown>(*l.w2, g1.hq, g1.hsf, P, l.I, lay.max_tiles, pa.pairs2, g2, stream);
+  if (e != cudaSuccess) return e;
+
+  CombineArgs ca = {g2.y, l.weights, pa.pair_row, l.k, l.H, l.ldo, static_cast<uint16_t*>(l.out)};
+  return launch_dependent(combine_kernel,
+                          dim3(static_cast<unsigned>(l.T), static_cast<unsigned>(ceil_div(l.H, 8 * kCombineThreads)), 1),
+                          kCombineThreads, 0, 1, stream, ca);
+}
+
+}  // namespace mxq

@@ -13,6 +13,7 @@
 
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
+#include "mxq_scales.cuh"
 
 namespace mxq {
 namespace {
@@ -23,35 +24,6 @@ constexpr int kWarpsPerBlock = 4;  // 128-thread blocks: about 1 % faster than 2
 // [32768, 8192] 2 units lose 10 %)
 constexpr int64_t kSmallQuantElems = int64_t(8) << 20;
 constexpr int64_t kEarlyGammaRows = 256;  // RMSNorm row counts that load gamma early (measured)
-
-struct QuantArgs {
-  const uint16_t* x;
-  int64_t M, K, ldx;
-  uint8_t* q;
-  int64_t ldq;
-  uint8_t* sf_rm;   // [M, Kg]
-  uint32_t* sf_pk;  // [Kw, Mp4]
-  uint8_t* sf_tl;   // F8_128x4
-  int64_t Kg, Kw, Mp4, Mp128;
-  int64_t rows_total;  // rows covered (padding rows write zero scale words only)
-  int32_t chunks;      // warp segments per row
-};
-
-// Scales of one 256-column unit: row-major bytes, packed word, tiled word.
-__device__ __forceinline__ void store_unit_scales(const QuantArgs& a, int64_t row, int64_t c, uint32_t code,
-                                                  int lane) {
-  if (a.sf_rm != nullptr && row < a.M && (lane & 3) == 0 && c < a.K) a.sf_rm[row * a.Kg + (c >> 5)] = code;
-  uint32_t w = code;
-  w |= __shfl_down_sync(0xffffffffu, code, 4) << 8;
-  w |= __shfl_down_sync(0xffffffffu, code, 8) << 16;
-  w |= __shfl_down_sync(0xffffffffu, code, 12) << 24;
-  if ((lane & 15) == 0 && c < a.K) {
-    const int64_t wi = c >> 7;
-    if (a.sf_pk != nullptr && row < a.Mp4) a.sf_pk[wi * a.Mp4 + row] = w;
-    if (a.sf_tl != nullptr && row < a.Mp128)
-      *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(row, wi, a.Kw)) = w;
-  }
-}
 
 // at least 12 blocks per SM (40 registers): 75 % occupancy instead of 62.5 %, 1-2 % faster at
 // large sizes (16 blocks forces spills and is slower)
