@@ -34,23 +34,21 @@ constexpr int kStatusTimeout = 6;  // MXQ_ERR_TIMEOUT
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-// A token tile: rows [row0, row0 + n) of the expert-sorted pairs; tiles [first, last) belong to the
-// same expert. Its scales lie in rows [256 i, 256 i + n) of the scale arrays, i the tile's index.
-struct __align__(16) Tile {
-  int32_t expert, row0, n, pad;
-  int32_t first, last, pad2, pad3;
-};
-// First item of a pair of SMs in one GEMM: linear index, tile and weight-row block.
-struct __align__(16) Start {
-  int32_t item, tile, block, pad;
+// One unit of work of a GEMM: a block of 256 weight rows of an expert against a token tile, rows
+// [row0, row0 + n) of the expert-sorted pairs. The tile's scales lie in slot `tile` of the scale
+// arrays: [tile][k-block][2 atoms of 128 rows][512 bytes].
+struct __align__(16) Item {
+  int32_t expert, row0, n, tile;
+  int32_t block, pad[3];
 };
 
 struct Layout {  // byte offsets into the workspace
-  int64_t max_tiles, pairs_max;
-  int64_t tiles, start1, start2, pair_row, pair_slot, xp, xsf, hq, hsf, y, total;
-  Layout(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I, int sm_pairs) {
+  int64_t max_tiles, blocks1, blocks2;
+  int64_t n_items, items1, items2, pair_row, pair_slot, xp, xsf, hq, hsf, y, total;
+  Layout(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I) {
     const int64_t P = T * k;
-    pairs_max = sm_pairs;
+    blocks1 = ceil_div(2 * I, 256);
+    blocks2 = ceil_div(H, 256);
     max_tiles = P / kTileTokens + (E < P ? E : P);
     int64_t o = 0;
     auto take = [&](int64_t bytes) {
@@ -58,9 +56,9 @@ struct Layout {  // byte offsets into the workspace
       o += round_up(bytes, 256);
       return at;
     };
-    tiles = take(max_tiles * static_cast<int64_t>(sizeof(Tile)));
-    start1 = take((pairs_max + 1) * static_cast<int64_t>(sizeof(Start)));
-    start2 = take((pairs_max + 1) * static_cast<int64_t>(sizeof(Start)));
+    n_items = take(8);
+    items1 = take(max_tiles * blocks1 * static_cast<int64_t>(sizeof(Item)));
+    items2 = take(max_tiles * blocks2 * static_cast<int64_t>(sizeof(Item)));
     pair_row = take(P * 4);
     pair_slot = take(P * 4);
     xp = take(P * H);
@@ -79,130 +77,116 @@ struct PlanArgs {
   const int32_t* ids;
   int32_t P, E;
   int32_t blocks1, blocks2;  // weight-row blocks per expert of the two GEMMs
-  int32_t pairs1, pairs2;    // SM pairs of the two GEMMs
-  Tile* tiles;
-  Start* start1;
-  Start* start2;
+  int32_t* n_items;          // of the two GEMMs
+  Item* items1;
+  Item* items2;
   int32_t* pair_row;   // expert-sorted row of pair p, or -1
-  int32_t* pair_slot;  // its row in the scale arrays
+  int32_t* pair_slot;  // its row in the scale slots (256 per tile)
 };
 
-// Cost of a token tile in one k-block, in MMA columns: the MMAs take time proportional to n; a
-// small tile is bound by its weight rows' way through L2 and shared memory instead.
-__device__ __forceinline__ int tile_cost(int n16) { return (n16 > 96 ? n16 : 96) + 16; }
-
-struct Scan3 {
-  int rows, tiles;
-  int cost;
-};
-__device__ __forceinline__ Scan3 add3(const Scan3 a, const Scan3 b) {
-  return {a.rows + b.rows, a.tiles + b.tiles, a.cost + b.cost};
-}
-__device__ __forceinline__ Scan3 shfl_up3(const Scan3 a, int d) {
-  return {__shfl_up_sync(0xffffffffu, a.rows, d), __shfl_up_sync(0xffffffffu, a.tiles, d),
-          __shfl_up_sync(0xffffffffu, a.cost, d)};
+__device__ __forceinline__ int2 add2(const int2 a, const int2 b) { return make_int2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ int2 shfl_up2(const int2 a, int d) {
+  return make_int2(__shfl_up_sync(0xffffffffu, a.x, d), __shfl_up_sync(0xffffffffu, a.y, d));
 }
 
-// One block: counts per expert, their scans, the tiles, every pair's row, and the SM pairs' shares.
+// One block: counts per expert, the experts in falling order of their counts, scans of rows and
+// tiles in that order, every pair's row, and the items of both GEMMs.
+//
+// SM pair p of NP takes items p, p + NP, ...: the pairs work on neighbouring items at any time, a
+// few experts whose weights and tokens then stay in L2, and the falling order gives every round
+// items of nearly the same cost and ends on the cheapest. (Contiguous shares of equal cost per
+// pair balanced as well, but the 76 pairs' operands did not fit in L2 together: GEMM 1 at 4096
+// tokens, 64 experts, 5120 -> 2 x 1024, took 588 us.)
+//
 // A row's place within its expert follows the order of shared-memory atomics; no result depends on
 // it (a column of an MMA never meets another).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
-  __shared__ int cnt[kMaxExperts], row0[kMaxExperts + 1], tile0[kMaxExperts + 1], cum[kMaxExperts + 1];
-  __shared__ int next[kMaxExperts], step[kMaxExperts];
-  __shared__ Scan3 part[32];
+  __shared__ int cnt[kMaxExperts], order[kMaxExperts];
+  __shared__ int row0[kMaxExperts], tile0[kMaxExperts + 1];  // by rank
+  __shared__ int rank_of[kMaxExperts], next[kMaxExperts], step[kMaxExperts];  // by expert
+  __shared__ int2 part[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   cnt[tid] = 0;
+  next[tid] = 0;
   __syncthreads();
   for (int p = tid; p < a.P; p += kPlanThreads) {
     const int e = a.ids[p];
     if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
-  const int c = cnt[tid];
+  if (tid < a.E) {
+    const int mine = cnt[tid];
+    int r = 0;
+    for (int e = 0; e < a.E; ++e) r += (cnt[e] > mine || (cnt[e] == mine && e < tid)) ? 1 : 0;
+    rank_of[tid] = r;
+    order[r] = tid;
+  }
+  __syncthreads();
+  const int expert = tid < a.E ? order[tid] : 0;  // thread r: the expert of rank r
+  const int c = tid < a.E ? cnt[expert] : 0;
   const int nt = (c + kTileTokens - 1) / kTileTokens;
   const int per = nt > 0 ? ((c + nt - 1) / nt + 15) / 16 * 16 : 16;  // tokens per tile, at most 224
-  const int last_n = c - (nt - 1) * per;                            // of the last tile (at least 1)
-  const int wb = tile_cost(per);
-  const int wl = nt > 0 ? (nt - 1) * wb + tile_cost((last_n + 15) / 16 * 16) : 0;
-  Scan3 v = {c, nt, wl};
+  int2 v = make_int2(c, nt);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const Scan3 u = shfl_up3(v, d);
-    if (lane >= d) v = add3(v, u);
+    const int2 u = shfl_up2(v, d);
+    if (lane >= d) v = add2(v, u);
   }
   if (lane == 31) part[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    Scan3 s = part[lane];
+    int2 s = part[lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const Scan3 u = shfl_up3(s, d);
-      if (lane >= d) s = add3(s, u);
+      const int2 u = shfl_up2(s, d);
+      if (lane >= d) s = add2(s, u);
     }
     part[lane] = s;
   }
   __syncthreads();
-  if (warp > 0) v = add3(v, part[warp - 1]);  // inclusive
-  row0[tid + 1] = v.rows;
-  tile0[tid + 1] = v.tiles;
-  cum[tid + 1] = v.cost;
-  if (tid == 0) row0[0] = tile0[0] = cum[0] = 0;
-  next[tid] = 0;
-  step[tid] = per;
+  if (warp > 0) v = add2(v, part[warp - 1]);  // inclusive
+  row0[tid] = v.x - c;
+  tile0[tid + 1] = v.y;
+  if (tid == 0) tile0[0] = 0;
+  if (tid < a.E) step[expert] = per;
   __syncthreads();
-  if (nt > 0)
-    for (int i = 0; i < nt; ++i) {
-      Tile t = {tid, row0[tid] + i * per, i == nt - 1 ? last_n : per, 0, tile0[tid], tile0[tid] + nt, 0, 0};
-      a.tiles[tile0[tid] + i] = t;
-    }
-  // first items of the SM pairs: equal shares of the cost, an item goes where its start lies
-  const int n_starts = (a.pairs1 + 1) + (a.pairs2 + 1);
-  if (tid < n_starts) {
-    const bool second = tid > a.pairs1;
-    const int p = second ? tid - a.pairs1 - 1 : tid;
-    const int np = second ? a.pairs2 : a.pairs1;
-    const int F = second ? a.blocks2 : a.blocks1;
-    const int64_t total = static_cast<int64_t>(cum[a.E]) * F;
-    const int64_t lo = total * p / np;
-    Start s = {F * tile0[a.E], tile0[a.E], 0, 0};
-    if (p < np && total > 0) {
-      int b = 0, t = a.E;  // largest e with F cum[e] <= lo
+  const int tiles = tile0[a.E];
+  if (tid < 2) a.n_items[tid] = tiles * (tid == 0 ? a.blocks1 : a.blocks2);
+  // items: an expert's weight-row blocks in turn, each with all of the expert's tiles
+  for (int g = 0; g < 2; ++g) {
+    const int F = g == 0 ? a.blocks1 : a.blocks2;
+    Item* items = g == 0 ? a.items1 : a.items2;
+    for (int i = tid; i < tiles * F; i += kPlanThreads) {
+      int b = 0, t = a.E;  // the largest rank with F tile0 <= i (it has tiles)
       while (t - b > 1) {
         const int m = (b + t) >> 1;
-        if (static_cast<int64_t>(cum[m]) * F <= lo) b = m;
+        if (tile0[m] * F <= i) b = m;
         else t = m;
       }
-      const int w = cum[b + 1] - cum[b];  // > 0: lo < total, so the last such e has items
-      const int tiles_e = tile0[b + 1] - tile0[b];
-      const int64_t off = lo - static_cast<int64_t>(cum[b]) * F;
-      int f = static_cast<int>(off / w);
-      const int rem = static_cast<int>(off - static_cast<int64_t>(f) * w);
-      const int wbe = tile_cost(step[b]);
-      int i = (rem + wbe - 1) / wbe;
-      if (i >= tiles_e) {
-        i = 0;
-        ++f;
-      }
-      if (f >= F)
-        s = {F * tile0[b + 1], tile0[b + 1], 0, 0};
-      else
-        s = {F * tile0[b] + f * tiles_e + i, tile0[b] + i, f, 0};
+      const int e = order[b], n_e = tile0[b + 1] - tile0[b], local = i - tile0[b] * F;
+      const int block = local / n_e, j = local - block * n_e;
+      const int left = cnt[e] - j * step[e];
+      items[i] = {e, row0[b] + j * step[e], left < step[e] ? left : step[e], tile0[b] + j, block, {0, 0, 0}};
     }
-    (second ? a.start2 : a.start1)[p] = s;
   }
   for (int p = tid; p < a.P; p += kPlanThreads) {
     const int e = a.ids[p];
     int row = -1, slot = 0;
     if (e >= 0 && e < a.E) {
-      const int r = atomicAdd(&next[e], 1);
-      const int i = r / step[e];
-      row = row0[e] + r;
-      slot = (tile0[e] + i) * kSlotRows + r - i * step[e];
+      const int k = rank_of[e], r = atomicAdd(&next[e], 1), i = r / step[e];
+      row = row0[k] + r;
+      slot = (tile0[k] + i) * kSlotRows + r - i * step[e];
     }
     a.pair_row[p] = row;
     a.pair_slot[p] = slot;
   }
+}
+
+// Byte offset of (row `slot` of the scale slots, k-block w) in a scale array of `kbs` k-blocks.
+__device__ __forceinline__ int64_t slot_word_offset(int64_t slot, int w, int kbs) {
+  const int64_t atom = ((slot >> 8) * kbs + w) * 2 + ((slot >> 7) & 1);
+  return atom * 512 + (slot & 31) * 16 + ((slot >> 5) & 3) * 4;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -239,7 +223,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
         a.sf + (a.sf_tiled ? tiled128x4_word_offset(t, w, words) : (t * words + w) * 4));
     for (int j = 0; j < a.k; ++j)
       if (a.pair_row[t * a.k + j] >= 0)
-        *reinterpret_cast<uint32_t*>(a.xsf + tiled128x4_word_offset(a.pair_slot[t * a.k + j], w, words)) = v;
+        *reinterpret_cast<uint32_t*>(a.xsf + slot_word_offset(a.pair_slot[t * a.k + j], w, words)) = v;
   }
 }
 
@@ -272,11 +256,17 @@ struct GemmCfg {
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
+constexpr int kBoxes = 4;  // token-row boxes of the operand loads: 16, 48, 80 or 112 rows, one load
+struct GemmMaps {
+  CUtensorMap w, sfw;      // weights (128 rows) and their scale atoms
+  CUtensorMap x[kBoxes];   // activations
+  CUtensorMap sfx[2];      // one or both scale atoms of a tile
+};
+
 struct GemmArgs {
-  const Tile* tiles;
-  const Start* start;
+  const Item* items;
+  const int32_t* n_items;
   int32_t kbs;       // 128-wide k-blocks
-  int32_t blocks;    // 256-row weight blocks per expert
   int32_t rows;      // weight rows per expert
   // gate-up: E4M3 activations [pairs, rows / 2] and their scales by tile
   uint8_t* hq;
@@ -290,39 +280,40 @@ __device__ __forceinline__ void report(int32_t* status) {
   if (status != nullptr) atomicCAS(status, 0, kStatusTimeout);
 }
 
-// The items of one SM pair: an expert's weight-row blocks in turn, each with all of the expert's
-// token tiles, so that the second tile finds the block's weights in L2.
+// The items of one SM pair: index pair, pair + pairs, ...
 struct Items {
-  const Tile* tiles;
-  int left, tile, block, blocks;
-  Tile t;
-  __device__ __forceinline__ Items(const GemmArgs& a, int pair) {
-    const Start s = a.start[pair], e = a.start[pair + 1];
-    tiles = a.tiles;
-    left = e.item - s.item;
-    tile = s.tile;
-    block = s.block;
-    blocks = a.blocks;
-    if (left > 0) t = tiles[tile];
+  const Item* items;
+  int at, stride, end;
+  int4 t;  // expert, row0, n, tile
+  int block;
+  __device__ __forceinline__ Items(const GemmArgs& a, int pair, int pairs) {
+    items = a.items;
+    at = pair;
+    stride = pairs;
+    end = *a.n_items;
+    load();
   }
-  __device__ __forceinline__ void next() {
-    if (--left <= 0) return;
-    if (++tile == t.last) {
-      if (++block == blocks)
-        block = 0;
-      else
-        tile = t.first;
+  __device__ __forceinline__ void load() {
+    if (at < end) {
+      t = *reinterpret_cast<const int4*>(items + at);
+      block = items[at].block;
     }
-    t = tiles[tile];
   }
-  __device__ __forceinline__ int n16() const { return (t.n + 15) & ~15; }
+  __device__ __forceinline__ bool more() const { return at < end; }
+  __device__ __forceinline__ void next() {
+    at += stride;
+    load();
+  }
+  __device__ __forceinline__ int expert() const { return t.x; }
+  __device__ __forceinline__ int row0() const { return t.y; }
+  __device__ __forceinline__ int n() const { return t.z; }
+  __device__ __forceinline__ int tile() const { return t.w; }
+  __device__ __forceinline__ int n16() const { return (t.z + 15) & ~15; }
 };
 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
-    experts_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                        const __grid_constant__ CUtensorMap tm_sfw, const __grid_constant__ CUtensorMap tm_sfx,
-                        const GemmArgs p) {
+    experts_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
   using C = GemmCfg<MODE>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sraw = smem_u32(smem_raw);
@@ -346,10 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nk = p.kbs;
 
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tm_w);
-    tma_prefetch_desc(&tm_x);
-    tma_prefetch_desc(&tm_sfw);
-    tma_prefetch_desc(&tm_sfx);
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.sfw);
+    for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.x[i]);
+    for (int i = 0; i < 2; ++i) tma_prefetch_desc(&maps.sfx[i]);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
@@ -376,20 +367,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
   pdl_wait_primary();  // the plan and the activations are the preceding kernels'
-  Items item(p, pair);
+  Items item(p, pair, gridDim.x >> 1);
 
   if (warp == 0 && lane == 0) {
     // ---------------- producer (both CTAs) ----------------
     const uint32_t full0 = mapa_shared(bar_full, 0);  // the even CTA's stage barriers
     int it = 0;
-    for (; item.left > 0 && !*abort_flag; item.next()) {
+    for (; item.more() && !*abort_flag; item.next()) {
       const int n16 = item.n16(), half = n16 >> 1;
-      const int boxes = (half + 15) >> 4, atoms = n16 > 128 ? 2 : 1;
-      const uint32_t tx = 2u * static_cast<uint32_t>(C::A_BYTES + boxes * 2048 + 512 + 512 * atoms);
-      const int w_row = item.t.expert * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
+      const int box = (half + 15) >> 5, atoms = n16 > 128 ? 2 : 1;  // 32 box + 16 >= half rows
+      const uint32_t tx = 2u * static_cast<uint32_t>(C::A_BYTES + (32 * box + 16) * BK + 512 + 512 * atoms);
+      const CUtensorMap* tm_x = &maps.x[box];
+      const CUtensorMap* tm_sfx = &maps.sfx[atoms - 1];
+      const int w_row = item.expert() * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
       const int w_atom = (w_row >> 7) * nk;
-      const int x_row = item.t.row0 + half * static_cast<int>(rank);
-      const int x_atom = item.tile * 2 * nk;
+      const int x_row = item.row0() + half * static_cast<int>(rank);
+      const int x_atom = item.tile() * nk;
       for (int kb = 0; kb < nk; ++kb, ++it) {
         const int s = it % STAGES;
         if (!mbar_wait_bounded(bar_empty + 8 * s, ((it / STAGES) & 1) ^ 1)) {
@@ -400,12 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t fb = full0 + 8 * s;
         if (leader) mbar_arrive_expect_tx(bar_full + 8 * s, tx);
         const uint32_t sf = sbase + C::OFF_SF + s * C::SF_BYTES;
-        tma_load_2d_pair(sbase + s * C::A_BYTES, &tm_w, fb, kb * BK, w_row);
-        tma_load_2d_pair(sf, &tm_sfw, fb, 0, w_atom + kb);
-        for (int b = 0; b < boxes; ++b)
-          tma_load_2d_pair(sbase + C::OFF_B + s * C::B_BYTES + 2048 * b, &tm_x, fb, kb * BK, x_row + 16 * b);
-        tma_load_2d_pair(sf + 512, &tm_sfx, fb, 0, x_atom + kb);
-        if (atoms == 2) tma_load_2d_pair(sf + 1024, &tm_sfx, fb, 0, x_atom + nk + kb);
+        tma_load_2d_pair(sbase + s * C::A_BYTES, &maps.w, fb, kb * BK, w_row);
+        tma_load_2d_pair(sbase + C::OFF_B + s * C::B_BYTES, tm_x, fb, kb * BK, x_row);
+        tma_load_2d_pair(sf, &maps.sfw, fb, 0, w_atom + kb);
+        tma_load_2d_pair(sf + 512, tm_sfx, fb, 0, 2 * (x_atom + kb));
       }
     }
     *issued_cnt = it;
@@ -413,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- MMA issuer (even CTA) ----------------
     if (leader) {
       int it = 0, ti = 0;
-      for (; item.left > 0 && !*abort_flag; item.next(), ++ti) {
+      for (; item.more() && !*abort_flag; item.next(), ++ti) {
         const int b = ti & 1;
         if (!mbar_wait_bounded(bar_acce + 8 * b, ((ti >> 1) & 1) ^ 1)) {
           *abort_flag = 1;
@@ -450,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- scale copies (even CTA) ----------------
     if (leader && lane == 0) {
       int it = 0;
-      for (; item.left > 0 && !*abort_flag; item.next()) {
+      for (; item.more() && !*abort_flag; item.next()) {
         const bool two = item.n16() > 128;
         for (int kb = 0; kb < nk; ++kb, ++it) {
           const int s = it % STAGES;
@@ -479,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t acce0 = mapa_shared(bar_acce, 0);
     const uint32_t stage = sbase + C::OFF_EPI;
     int ti = 0;
-    for (; item.left > 0; item.next(), ++ti) {
-      const int b = ti & 1, n = item.t.n;
+    for (; item.more(); item.next(), ++ti) {
+      const int b = ti & 1, n = item.n();
       bool ok = !*abort_flag;
       if (ok && !mbar_wait_bounded(bar_accf + 8 * b, (ti >> 1) & 1)) {
         *abort_flag = 1;
@@ -548,10 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float s = ue8m0_inverse(code);
             const uint2 q0 = quant8(v[0], s), q1 = quant8(v[1], s), q2 = quant8(v[2], s), q3 = quant8(v[3], s);
             const int f = f0 + 32 * g;
-            uint4* dst = reinterpret_cast<uint4*>(p.hq + (item.t.row0 + tok) * ld + f);
+            uint4* dst = reinterpret_cast<uint4*>(p.hq + (item.row0() + tok) * ld + f);
             dst[0] = make_uint4(q0.x, q0.y, q1.x, q1.y);
             dst[1] = make_uint4(q2.x, q2.y, q3.x, q3.y);
-            p.hsf[tiled128x4_word_offset(static_cast<int64_t>(item.tile) * kSlotRows + tok, f >> 7, ld >> 7) + ((f >> 5) & 3)] =
+            p.hsf[slot_word_offset(static_cast<int64_t>(item.tile()) * kSlotRows + tok, f >> 7, static_cast<int>(ld >> 7)) + ((f >> 5) & 3)] =
                 static_cast<uint8_t>(code);
           }
         } else {
@@ -560,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = et; i < 16 * n; i += 256) {
               const int tok = i >> 4, j = i & 15;
               const uint4 v = ld_smem_v4(stage + tok * 256 + 16 * j);
-              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(item.t.row0 + tok) * p.rows + f0 + 8 * j) = v;
+              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(item.row0() + tok) * p.rows + f0 + 8 * j) = v;
             }
         }
       }
@@ -666,26 +657,27 @@ cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, const void
   static const cudaError_t attr_err =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (attr_err != cudaSuccess) return attr_err;
-  CUtensorMap tm_w, tm_x, tm_sfw, tm_sfx;
-  if (!make_map(&tm_w, w.data, w.rows, K, w.ld, BM) || !make_map(&tm_x, act, act_rows, K, K, 16) ||
-      !make_sf_map(&tm_sfw, w.sf, w.rows / 128 * (K / 128)) || !make_sf_map(&tm_sfx, act_sf, max_tiles * 2 * (K / 128)))
+  GemmMaps maps;
+  if (!make_map(&maps.w, w.data, w.rows, K, w.ld, BM) || !make_sf_map(&maps.sfw, w.sf, w.rows / 128 * (K / 128)))
     return cudaErrorInvalidValue;
-  return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads, C::SMEM_BYTES, 2, stream, tm_w,
-                          tm_x, tm_sfw, tm_sfx, ga);
+  for (int i = 0; i < kBoxes; ++i)
+    if (!make_map(&maps.x[i], act, act_rows, K, K, 32 * i + 16)) return cudaErrorInvalidValue;
+  for (int i = 0; i < 2; ++i)
+    if (!make_sf_map(&maps.sfx[i], act_sf, max_tiles * 2 * (K / 128), i + 1)) return cudaErrorInvalidValue;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads, C::SMEM_BYTES, 2, stream, maps, ga);
 }
 
 }  // namespace
 
 int64_t experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I) {
-  return Layout(T, k, E, H, I, num_sms() / 2).total;
+  return Layout(T, k, E, H, I).total;
 }
 
 cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   const int sm_pairs = num_sms() / 2;
-  const Layout lay(l.T, l.k, l.E, l.H, l.I, sm_pairs);
+  const Layout lay(l.T, l.k, l.E, l.H, l.I);
   uint8_t* ws = static_cast<uint8_t*>(l.workspace);
   const int64_t P = l.T * l.k;
-  const int64_t blocks1 = ceil_div(2 * l.I, 2 * BM), blocks2 = ceil_div(l.H, 2 * BM);
   auto pairs_for = [&](int64_t blocks) {
     const int64_t items = lay.max_tiles * blocks;
     return static_cast<int>(items < sm_pairs ? items : sm_pairs);
@@ -694,13 +686,11 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   pa.ids = l.ids;
   pa.P = static_cast<int32_t>(P);
   pa.E = l.E;
-  pa.blocks1 = static_cast<int32_t>(blocks1);
-  pa.blocks2 = static_cast<int32_t>(blocks2);
-  pa.pairs1 = pairs_for(blocks1);
-  pa.pairs2 = pairs_for(blocks2);
-  pa.tiles = reinterpret_cast<Tile*>(ws + lay.tiles);
-  pa.start1 = reinterpret_cast<Start*>(ws + lay.start1);
-  pa.start2 = reinterpret_cast<Start*>(ws + lay.start2);
+  pa.blocks1 = static_cast<int32_t>(lay.blocks1);
+  pa.blocks2 = static_cast<int32_t>(lay.blocks2);
+  pa.n_items = reinterpret_cast<int32_t*>(ws + lay.n_items);
+  pa.items1 = reinterpret_cast<Item*>(ws + lay.items1);
+  pa.items2 = reinterpret_cast<Item*>(ws + lay.items2);
   pa.pair_row = reinterpret_cast<int32_t*>(ws + lay.pair_row);
   pa.pair_slot = reinterpret_cast<int32_t*>(ws + lay.pair_slot);
   plan_kernel<<<1, kPlanThreads, 0, stream>>>(pa);
@@ -722,26 +712,24 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
 
   GemmArgs g1 = {};
-  g1.tiles = pa.tiles;
-  g1.start = pa.start1;
+  g1.items = pa.items1;
+  g1.n_items = pa.n_items;
   g1.kbs = static_cast<int32_t>(l.H / BK);
-  g1.blocks = pa.blocks1;
   g1.rows = static_cast<int32_t>(2 * l.I);
   g1.hq = ws + lay.hq;
   g1.hsf = ws + lay.hsf;
   g1.status = l.status;
-  e = launch_gemm_mode<kGateUp>(*l.w13, ga.xp, ga.xsf, P, l.H, lay.max_tiles, pa.pairs1, g1, stream);
+  e = launch_gemm_mode<kGateUp>(*l.w13, ga.xp, ga.xsf, P, l.H, lay.max_tiles, pairs_for(lay.blocks1), g1, stream);
   if (e != cudaSuccess) return e;
 
   GemmArgs g2 = {};
-  g2.tiles = pa.tiles;
-  g2.start = pa.start2;
+  g2.items = pa.items2;
+  g2.n_items = pa.n_items + 1;
   g2.kbs = static_cast<int32_t>(l.I / BK);
-  g2.blocks = pa.blocks2;
   g2.rows = static_cast<int32_t>(l.H);
   g2.y = reinterpret_cast<uint16_t*>(ws + lay.y);
   g2.status = l.status;
-  e = launch_gemm_mode<kDown>(*l.w2, g1.hq, g1.hsf, P, l.I, lay.max_tiles, pa.pairs2, g2, stream);
+  e = launch_gemm_mode<kDown>(*l.w2, g1.hq, g1.hsf, P, l.I, lay.max_tiles, pairs_for(lay.blocks2), g2, stream);
   if (e != cudaSuccess) return e;
 
   CombineArgs ca = {g2.y, l.weights, pa.pair_row, l.k, l.H, l.ldo, static_cast<uint16_t*>(l.out)};

@@ -11,8 +11,8 @@ namespace mxq {
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 // 2-D E4M3 tensor [rows, cols], row stride ld bytes; box = 128 bytes x box_rows, 128B swizzle.
 bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);
-// Scale atoms of an F8_128x4 array as a 2-D tensor [atoms, 128 x u32]: one 512-byte atom per box.
-bool make_sf_map(CUtensorMap* m, const void* base, int64_t atoms);
+// Scale atoms of an F8_128x4 array as a 2-D tensor [atoms, 128 x u32]: box_atoms 512-byte atoms per box.
+bool make_sf_map(CUtensorMap* m, const void* base, int64_t atoms, int box_atoms = 1);
 // SMs of the current device.
 int num_sms();
 

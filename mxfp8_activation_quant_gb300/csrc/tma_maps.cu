@@ -34,13 +34,13 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Scale atoms of an F8_128x4 array as a 2-D tensor [atoms, 128 x u32]: one 512-byte atom per box.
-bool make_sf_map(CUtensorMap* m, const void* base, int64_t atoms) {
+// Scale atoms of an F8_128x4 array as a 2-D tensor [atoms, 128 x u32]: box_atoms 512-byte atoms per box.
+bool make_sf_map(CUtensorMap* m, const void* base, int64_t atoms, int box_atoms) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {128u, static_cast<cuuint64_t>(atoms)};
   cuuint64_t strides[1] = {512u};
-  cuuint32_t box[2] = {128u, 1u};
+  cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(box_atoms)};
   cuuint32_t estr[2] = {1u, 1u};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
