@@ -7,12 +7,12 @@
 //
 // Both GEMMs are one kernel template on CTA pairs (tcgen05 cta_group::2, kind::mxf8f6f4 block
 // scaled), persistent, with the WEIGHTS on the MMA's M side: M = 256 weight rows (128 per CTA) and
-// N = the token tile, up to 224 tokens in steps of 16. An expert's token count is ragged and its
+// N = the token tile, up to 208 tokens in steps of 16. An expert's token count is ragged and its
 // weight rows are not, so the ragged dimension sits where the MMA's size follows it exactly.
-// Two accumulators of 224 TMEM columns alternate, so a tile's epilogue runs under the next tile's
-// MMAs; the remaining 64 columns hold the scales of 5 stages.
+// Two accumulators of 208 TMEM columns alternate, so a tile's epilogue runs under the next tile's
+// MMAs; the remaining 96 columns hold the scales of 6 stages.
 //
-// Up to about 224 tokens per expert the GEMMs stream the active experts' weights (33/32 B per
+// Up to about 208 tokens per expert the GEMMs stream the active experts' weights (33/32 B per
 // element) and are HBM bound, beyond that tensor bound.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -25,7 +25,7 @@
 namespace mxq {
 namespace {
 
-constexpr int kTileTokens = 224;   // most tokens of a tile (MMA N)
+constexpr int kTileTokens = 208;   // most tokens of a tile (MMA N)
 constexpr int kSlotRows = 256;     // scale rows reserved per tile: two F8_128x4 row tiles
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxExperts = 1024;
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   const int expert = tid < a.E ? order[tid] : 0;  // thread r: the expert of rank r
   const int c = tid < a.E ? cnt[expert] : 0;
   const int nt = (c + kTileTokens - 1) / kTileTokens;
-  const int per = nt > 0 ? ((c + nt - 1) / nt + 15) / 16 * 16 : 16;  // tokens per tile, at most 224
+  const int per = nt > 0 ? ((c + nt - 1) / nt + 15) / 16 * 16 : 16;  // tokens per tile, at most 208
   int2 v = make_int2(c, nt);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -230,25 +230,29 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
 // ------------------------------------------------------------------------------------------
 // grouped GEMM
 // ------------------------------------------------------------------------------------------
-constexpr int kThreads = 352;  // producer, MMA, 8 epilogue warps, scale copies
+constexpr int kThreads = 384;  // operand loads, MMA, 8 epilogue warps, scale copies, scale loads
 constexpr int BM = 128;        // weight rows per CTA
 constexpr int BK = 128;        // K bytes per stage
-constexpr int STAGES = 5;
+constexpr int STAGES = 6;
+constexpr int kSfKb = 4;      // k-blocks per scale chunk
+constexpr int kSfChunks = 3;  // scale chunks in flight
 constexpr int kGateUp = 0, kDown = 1;
 
 template <int MODE>
 struct GemmCfg {
   static constexpr int A_BYTES = BM * BK;
   static constexpr int B_BYTES = kTileTokens / 2 * BK;  // a CTA holds half of the tile's tokens
-  static constexpr int SF_BYTES = 512 * 3;              // the CTA's weight rows, two token atoms
-  static constexpr int SF_COLS = 12;
+  static constexpr int SF_COLS = 12;                    // the CTA's weight rows, two token atoms
+  static constexpr int SFA_BYTES = 512 * kSfKb, SFB_BYTES = 1024 * kSfKb;
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
-  // epilogue staging, one row per token: 64 bf16 features (gate-up) or 128 (down)
+  // epilogue staging, one row per token: 64 bf16 features of every token of the tile (gate-up), or
+  // 128 of up to 112 tokens, two passes (down)
   static constexpr int ROW_BYTES = MODE == kGateUp ? 128 : 256;
-  static constexpr int OFF_EPI = OFF_SF + STAGES * SF_BYTES;
-  static constexpr int OFF_BAR = OFF_EPI + kTileTokens * ROW_BYTES;
-  static constexpr int OFF_MISC = OFF_BAR + (3 * STAGES + 5) * 8;
+  static constexpr int PASS_TOKENS = MODE == kGateUp ? kTileTokens : 112;
+  static constexpr int OFF_EPI = OFF_SF + kSfChunks * (SFA_BYTES + SFB_BYTES);
+  static constexpr int OFF_BAR = OFF_EPI + PASS_TOKENS * ROW_BYTES;
+  static constexpr int OFF_MISC = OFF_BAR + (3 * STAGES + 2 * kSfChunks + 5) * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static constexpr int TMEM_SF = 2 * kTileTokens;  // first scale column
   static_assert(B_BYTES % 1024 == 0, "swizzle atoms");
@@ -256,11 +260,11 @@ struct GemmCfg {
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
-constexpr int kBoxes = 4;  // token-row boxes of the operand loads: 16, 48, 80 or 112 rows, one load
+constexpr int kBoxes = 4;  // token-row boxes of the operand loads: 8, 40, 72 or 104 rows, one load
 struct GemmMaps {
   CUtensorMap w, sfw;      // weights (128 rows) and their scale atoms
   CUtensorMap x[kBoxes];   // activations
-  CUtensorMap sfx[2];      // one or both scale atoms of a tile
+  CUtensorMap sfx;         // a chunk of the tile's scale atoms
 };
 
 struct GemmArgs {
@@ -280,28 +284,46 @@ __device__ __forceinline__ void report(int32_t* status) {
   if (status != nullptr) atomicCAS(status, 0, kStatusTimeout);
 }
 
-// The items of one SM pair: index pair, pair + pairs, ...
+// A ring position: slot and phase parity.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// The items of one SM pair: index pair, pair + pairs, ... The next one is loaded an item ahead.
 struct Items {
   const Item* items;
   int at, stride, end;
-  int4 t;  // expert, row0, n, tile
-  int block;
+  int4 t, t_next;  // expert, row0, n, tile
+  int block, block_next;
   __device__ __forceinline__ Items(const GemmArgs& a, int pair, int pairs) {
     items = a.items;
-    at = pair;
+    at = pair - pairs;
     stride = pairs;
     end = *a.n_items;
+    t_next = make_int4(0, 0, 0, 0);
+    block_next = 0;
     load();
+    next();
   }
   __device__ __forceinline__ void load() {
-    if (at < end) {
-      t = *reinterpret_cast<const int4*>(items + at);
-      block = items[at].block;
+    if (at + stride < end) {
+      t_next = *reinterpret_cast<const int4*>(items + at + stride);
+      block_next = items[at + stride].block;
     }
   }
   __device__ __forceinline__ bool more() const { return at < end; }
   __device__ __forceinline__ void next() {
     at += stride;
+    t = t_next;
+    block = block_next;
     load();
   }
   __device__ __forceinline__ int expert() const { return t.x; }
@@ -322,15 +344,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_full = sbase + C::OFF_BAR;
   const uint32_t bar_empty = bar_full + 8 * STAGES;
   const uint32_t bar_sf = bar_empty + 8 * STAGES;
-  const uint32_t bar_accf = bar_sf + 8 * STAGES;  // two accumulators
+  const uint32_t bar_sff = bar_sf + 8 * STAGES;        // scale chunk landed
+  const uint32_t bar_sfe = bar_sff + 8 * kSfChunks;    // scale chunk copied to TMEM
+  const uint32_t bar_accf = bar_sfe + 8 * kSfChunks;  // two accumulators
   const uint32_t bar_acce = bar_accf + 16;
   const uint32_t bar_drain = bar_acce + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* issued_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
   int* consumed_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 12);
+  int* sf_issued_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);
+  int* sf_consumed_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 20);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const bool elected = elect_one();
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1;
@@ -340,11 +367,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.w);
     tma_prefetch_desc(&maps.sfw);
     for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.x[i]);
-    for (int i = 0; i < 2; ++i) tma_prefetch_desc(&maps.sfx[i]);
+    tma_prefetch_desc(&maps.sfx);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
       mbar_init(bar_sf + 8 * s, 1);
+    }
+    for (int c = 0; c < kSfChunks; ++c) {
+      mbar_init(bar_sff + 8 * c, 1);
+      mbar_init(bar_sfe + 8 * c, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_accf + 8 * b, 1);
@@ -354,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     *issued_cnt = 0;
     *consumed_cnt = 0;
+    *sf_issued_cnt = 0;
+    *sf_consumed_cnt = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -369,41 +402,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_primary();  // the plan and the activations are the preceding kernels'
   Items item(p, pair, gridDim.x >> 1);
 
-  if (warp == 0 && lane == 0) {
-    // ---------------- producer (both CTAs) ----------------
+  if (warp == 0 && elected) {
+    // ---------------- operand loads (both CTAs) ----------------
     const uint32_t full0 = mapa_shared(bar_full, 0);  // the even CTA's stage barriers
     int it = 0;
+    Ring<STAGES> ring;
     for (; item.more() && !*abort_flag; item.next()) {
-      const int n16 = item.n16(), half = n16 >> 1;
-      const int box = (half + 15) >> 5, atoms = n16 > 128 ? 2 : 1;  // 32 box + 16 >= half rows
-      const uint32_t tx = 2u * static_cast<uint32_t>(C::A_BYTES + (32 * box + 16) * BK + 512 + 512 * atoms);
+      const int half = item.n16() >> 1;
+      const int box = (half + 23) >> 5;  // 32 box + 8 >= half rows
+      const uint32_t tx = 2u * static_cast<uint32_t>(C::A_BYTES + (32 * box + 8) * BK);
       const CUtensorMap* tm_x = &maps.x[box];
-      const CUtensorMap* tm_sfx = &maps.sfx[atoms - 1];
       const int w_row = item.expert() * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
-      const int w_atom = (w_row >> 7) * nk;
       const int x_row = item.row0() + half * static_cast<int>(rank);
-      const int x_atom = item.tile() * nk;
-      for (int kb = 0; kb < nk; ++kb, ++it) {
-        const int s = it % STAGES;
-        if (!mbar_wait_bounded(bar_empty + 8 * s, ((it / STAGES) & 1) ^ 1)) {
+      for (int kb = 0; kb < nk; ++kb, ++it, ring.next()) {
+        const int s = ring.slot;
+        if (!mbar_wait_bounded(bar_empty + 8 * s, ring.phase ^ 1)) {
           *abort_flag = 1;
           report(p.status);
           break;
         }
         const uint32_t fb = full0 + 8 * s;
         if (leader) mbar_arrive_expect_tx(bar_full + 8 * s, tx);
-        const uint32_t sf = sbase + C::OFF_SF + s * C::SF_BYTES;
         tma_load_2d_pair(sbase + s * C::A_BYTES, &maps.w, fb, kb * BK, w_row);
         tma_load_2d_pair(sbase + C::OFF_B + s * C::B_BYTES, tm_x, fb, kb * BK, x_row);
-        tma_load_2d_pair(sf, &maps.sfw, fb, 0, w_atom + kb);
-        tma_load_2d_pair(sf + 512, tm_sfx, fb, 0, 2 * (x_atom + kb));
       }
     }
     *issued_cnt = it;
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 11 && elected) {
+    // ---------------- scale loads (both CTAs) ----------------
+    // The scales of kSfKb k-blocks at a time, in a ring of their own that runs ahead of the operands
+    const uint32_t full0 = mapa_shared(bar_sff, 0);
+    int ic = 0;
+    Ring<kSfChunks> ring;
+    for (; item.more() && !*abort_flag; item.next()) {
+      const int w_row = item.expert() * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
+      const int w_atom = (w_row >> 7) * nk;
+      const int x_atom = item.tile() * nk * 2;
+      for (int kb = 0; kb < nk; kb += kSfKb, ++ic, ring.next()) {
+        const int c = ring.slot;
+        if (!mbar_wait_bounded(bar_sfe + 8 * c, ring.phase ^ 1)) {
+          *abort_flag = 1;
+          report(p.status);
+          break;
+        }
+        if (leader) mbar_arrive_expect_tx(bar_sff + 8 * c, 2u * (C::SFA_BYTES + C::SFB_BYTES));
+        const uint32_t dst = sbase + C::OFF_SF + c * (C::SFA_BYTES + C::SFB_BYTES);
+        // (k-blocks past the last read the following atoms, or zeros past the arrays' ends)
+        tma_load_2d_pair(dst, &maps.sfw, full0 + 8 * c, 0, w_atom + kb);
+        tma_load_2d_pair(dst + C::SFA_BYTES, &maps.sfx, full0 + 8 * c, 0, x_atom + 2 * kb);
+      }
+    }
+    *sf_issued_cnt = ic;
+  } else if (warp == 1 && elected) {
     // ---------------- MMA issuer (even CTA) ----------------
     if (leader) {
       int it = 0, ti = 0;
+      Ring<STAGES> ring;
       for (; item.more() && !*abort_flag; item.next(), ++ti) {
         const int b = ti & 1;
         if (!mbar_wait_bounded(bar_acce + 8 * b, ((ti >> 1) & 1) ^ 1)) {
@@ -414,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t n16 = static_cast<uint32_t>(item.n16());
         bool ok = true;
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait_bounded(bar_sf + 8 * s, (it / STAGES) & 1)) {
+        for (int kb = 0; kb < nk; ++kb, ++it, ring.next()) {
+          const int s = ring.slot;
+          if (!mbar_wait_bounded(bar_sf + 8 * s, ring.phase) || !mbar_wait_bounded(bar_full + 8 * s, ring.phase)) {
             *abort_flag = 1;
             report(p.status);
             ok = false;
@@ -439,26 +493,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 10) {
     // ---------------- scale copies (even CTA) ----------------
-    if (leader && lane == 0) {
-      int it = 0;
-      for (; item.more() && !*abort_flag; item.next()) {
+    // A stage's scale columns are free with the stage; its scales have landed long before its
+    // operands, so the copies run under the operands' loads and no MMA waits for them.
+    if (leader && elected) {
+      int ic = 0;
+      Ring<STAGES> ring;
+      Ring<kSfChunks> chunk;
+      bool ok = true;
+      for (; item.more() && ok && !*abort_flag; item.next()) {
         const bool two = item.n16() > 128;
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait_bounded(bar_full + 8 * s, (it / STAGES) & 1)) {
+        for (int kb = 0; kb < nk && ok; ++kb, ring.next()) {
+          const int s = ring.slot, c = chunk.slot, j = kb % kSfKb;
+          if ((j == 0 && !mbar_wait_bounded(bar_sff + 8 * c, chunk.phase)) ||
+              !mbar_wait_bounded(bar_empty + 8 * s, ring.phase ^ 1)) {
             *abort_flag = 1;
             report(p.status);
+            ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t src = sbase + C::OFF_SF + s * C::SF_BYTES;
+          const uint32_t src = sbase + C::OFF_SF + c * (C::SFA_BYTES + C::SFB_BYTES);
           const uint32_t dst = tmem + C::TMEM_SF + s * C::SF_COLS;
-          tc_cp_sf_atom_pair(dst, sdesc_sf_atom(src));
-          tc_cp_sf_atom_pair(dst + 4, sdesc_sf_atom(src + 512));
-          if (two) tc_cp_sf_atom_pair(dst + 8, sdesc_sf_atom(src + 1024));
+          tc_cp_sf_atom_pair(dst, sdesc_sf_atom(src + 512 * j));
+          tc_cp_sf_atom_pair(dst + 4, sdesc_sf_atom(src + C::SFA_BYTES + 1024 * j));
+          if (two) tc_cp_sf_atom_pair(dst + 8, sdesc_sf_atom(src + C::SFA_BYTES + 1024 * j + 512));
           tc_commit_pair(bar_sf + 8 * s, 0x1);
+          if (j == kSfKb - 1 || kb == nk - 1) {
+            tc_commit_pair(bar_sfe + 8 * c, 0x3);
+            ++ic;
+            chunk.next();
+          }
         }
       }
+      *sf_consumed_cnt = ic;
     }
   } else if (warp >= 2 && warp < 10) {
     // ---------------- epilogue (both CTAs) ----------------
@@ -479,83 +546,89 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
       }
       ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        tc_fence_after();
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTileTokens * b;
-        for (int ch = odd; 16 * ch < n; ch += 2) {
-          uint32_t acc[16];
-          tmem_ld_x16(t_lane + 16 * ch, acc);
-          tmem_ld_wait();
-          if (MODE == kGateUp) {
-            // rows alternate gate, up: lane pairs (2 i, 2 i + 1) hold feature 16 q + i. Of two
-            // tokens the even lane finishes the first and the odd lane the second.
-            const int up = lane & 1, f = 16 * q + (lane >> 1);
+      for (int t0 = 0; t0 < n; t0 += C::PASS_TOKENS) {  // (one pass, or two for a large down tile)
+        const int tn = n - t0 < C::PASS_TOKENS ? n - t0 : C::PASS_TOKENS;
+        if (ok) {
+          tc_fence_after();
+          const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTileTokens * b + t0;
+          for (int ch = odd; 16 * ch < tn; ch += 2) {
+            uint32_t acc[16];
+            tmem_ld_x16(t_lane + 16 * ch, acc);
+            tmem_ld_wait();
+            if (MODE == kGateUp) {
+              // rows alternate gate, up: lane pairs (2 i, 2 i + 1) hold feature 16 q + i. Of two
+              // tokens the even lane finishes the first and the odd lane the second.
+              const int up = lane & 1, f = 16 * q + (lane >> 1);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float a0 = __uint_as_float(acc[2 * c]), a1 = __uint_as_float(acc[2 * c + 1]);
-              const float o = __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 1);
-              const float g = up ? o : a0, u = up ? a1 : o;
-              const float h = __fdividef(g, 1.f + __expf(-g)) * u;
-              const int tok = 16 * ch + 2 * c + up;
-              // 16-byte pieces of a 128-byte row are XOR-swizzled by the row
-              const uint32_t at = stage + tok * 128 + (((f >> 3) ^ (2 * (tok & 3))) << 4) + (f & 7) * 2;
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(bf16x2_rn(h, 0.f))) : "memory");
+              for (int c = 0; c < 8; ++c) {
+                const float a0 = __uint_as_float(acc[2 * c]), a1 = __uint_as_float(acc[2 * c + 1]);
+                const float o = __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 1);
+                const float g = up ? o : a0, u = up ? a1 : o;
+                const float h = __fdividef(g, 1.f + __expf(-g)) * u;
+                const int tok = 16 * ch + 2 * c + up;
+                // 16-byte pieces of a 128-byte row are XOR-swizzled by the row
+                const uint32_t at = stage + tok * 128 + (((f >> 3) ^ (2 * (tok & 3))) << 4) + (f & 7) * 2;
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(bf16x2_rn(h, 0.f))) : "memory");
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const uint32_t w = bf16x2_rn(__uint_as_float(acc[2 * c]), __uint_as_float(acc[2 * c + 1]));
+                const uint32_t at = stage + (16 * ch + 2 * c) * 256 + (32 * q + lane) * 2;
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(w)) : "memory");
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 256), "h"(static_cast<uint16_t>(w >> 16)) : "memory");
+              }
+            }
+          }
+          if (t0 + C::PASS_TOKENS >= n) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {  // the MMAs may overwrite this accumulator now
+              if (leader)
+                mbar_arrive(bar_acce + 8 * b);
+              else
+                mbar_arrive_remote(acce0 + 8 * b);
+            }
+          }
+        }
+        named_barrier(1, 256);
+        if (ok) {
+          const int64_t row0 = item.row0() + t0;
+          if (MODE == kGateUp) {
+            // one thread = one token and one 32-feature group: the rule of mxfp8_quantize
+            const int64_t ld = p.rows / 2;
+            const int f0 = item.block * 128 + static_cast<int>(rank) * 64;
+            for (int i = et; i < 2 * tn; i += 256) {
+              const int tok = i >> 1, g = i & 1;
+              uint4 v[4];
+              uint32_t amax = 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                v[j] = ld_smem_v4(stage + tok * 128 + (((4 * g + j) ^ (2 * (tok & 3))) << 4));
+                amax = max(amax, absmax8(v[j]));
+              }
+              const uint32_t code = ue8m0_from_bf16_amax(amax);
+              const float s = ue8m0_inverse(code);
+              const uint2 q0 = quant8(v[0], s), q1 = quant8(v[1], s), q2 = quant8(v[2], s), q3 = quant8(v[3], s);
+              const int f = f0 + 32 * g;
+              uint4* dst = reinterpret_cast<uint4*>(p.hq + (row0 + tok) * ld + f);
+              dst[0] = make_uint4(q0.x, q0.y, q1.x, q1.y);
+              dst[1] = make_uint4(q2.x, q2.y, q3.x, q3.y);
+              p.hsf[slot_word_offset(static_cast<int64_t>(item.tile()) * kSlotRows + tok, f >> 7, static_cast<int>(ld >> 7)) +
+                    ((f >> 5) & 3)] = static_cast<uint8_t>(code);
             }
           } else {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint32_t w = bf16x2_rn(__uint_as_float(acc[2 * c]), __uint_as_float(acc[2 * c + 1]));
-              const uint32_t at = stage + (16 * ch + 2 * c) * 256 + (32 * q + lane) * 2;
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(w)) : "memory");
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 256), "h"(static_cast<uint16_t>(w >> 16)) : "memory");
-            }
+            const int f0 = item.block * (2 * BM) + static_cast<int>(rank) * BM;
+            if (f0 < p.rows)  // the last block of an odd number of 128-row tiles has one half
+              for (int i = et; i < 16 * tn; i += 256) {
+                const int tok = i >> 4, j = i & 15;
+                const uint4 v = ld_smem_v4(stage + tok * 256 + 16 * j);
+                *reinterpret_cast<uint4*>(p.y + (row0 + tok) * p.rows + f0 + 8 * j) = v;
+              }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {  // the MMAs may overwrite this accumulator now
-          if (leader)
-            mbar_arrive(bar_acce + 8 * b);
-          else
-            mbar_arrive_remote(acce0 + 8 * b);
-        }
+        named_barrier(1, 256);
       }
-      named_barrier(1, 256);
-      if (ok) {
-        if (MODE == kGateUp) {
-          // one thread = one token and one 32-feature group: the rule of mxfp8_quantize
-          const int64_t ld = p.rows / 2;
-          const int f0 = item.block * 128 + static_cast<int>(rank) * 64;
-          for (int i = et; i < 2 * n; i += 256) {
-            const int tok = i >> 1, g = i & 1;
-            uint4 v[4];
-            uint32_t amax = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[j] = ld_smem_v4(stage + tok * 128 + (((4 * g + j) ^ (2 * (tok & 3))) << 4));
-              amax = max(amax, absmax8(v[j]));
-            }
-            const uint32_t code = ue8m0_from_bf16_amax(amax);
-            const float s = ue8m0_inverse(code);
-            const uint2 q0 = quant8(v[0], s), q1 = quant8(v[1], s), q2 = quant8(v[2], s), q3 = quant8(v[3], s);
-            const int f = f0 + 32 * g;
-            uint4* dst = reinterpret_cast<uint4*>(p.hq + (item.row0() + tok) * ld + f);
-            dst[0] = make_uint4(q0.x, q0.y, q1.x, q1.y);
-            dst[1] = make_uint4(q2.x, q2.y, q3.x, q3.y);
-            p.hsf[slot_word_offset(static_cast<int64_t>(item.tile()) * kSlotRows + tok, f >> 7, static_cast<int>(ld >> 7)) + ((f >> 5) & 3)] =
-                static_cast<uint8_t>(code);
-          }
-        } else {
-          const int f0 = item.block * (2 * BM) + static_cast<int>(rank) * BM;
-          if (f0 < p.rows)  // the last block of an odd number of 128-row tiles has one half
-            for (int i = et; i < 16 * n; i += 256) {
-              const int tok = i >> 4, j = i & 15;
-              const uint4 v = ld_smem_v4(stage + tok * 256 + 16 * j);
-              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(item.row0() + tok) * p.rows + f0 + 8 * j) = v;
-            }
-        }
-      }
-      named_barrier(1, 256);
     }
   }
   __syncwarp();
@@ -571,11 +644,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hi = *issued_cnt > peer_issued ? *issued_cnt : peer_issued;
       for (int i = *consumed_cnt; i < hi; ++i)
         (void)mbar_wait_bounded(bar_full + 8 * (i % STAGES), (i / STAGES) & 1);
+      const int peer_sf = ld_dsmem_s32(mapa_shared(smem_u32(sf_issued_cnt), 1));
+      const int hi_sf = *sf_issued_cnt > peer_sf ? *sf_issued_cnt : peer_sf;
+      for (int i = *sf_consumed_cnt; i < hi_sf; ++i)
+        (void)mbar_wait_bounded(bar_sff + 8 * (i % kSfChunks), (i / kSfChunks) & 1);
       *abort_flag = 1;
     }
   }
   __syncthreads();
-  if (leader && (warp == 1 || warp == 10) && lane == 0 && *abort_flag) {
+  if (leader && (warp == 1 || warp == 10) && elected && *abort_flag) {
     tc_commit_pair(bar_drain, 0x1);  // arrives once every MMA / copy this thread issued has completed
     if (warp == 1) (void)mbar_wait_bounded(bar_drain, 0);
   }
@@ -658,12 +735,11 @@ cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, const void
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (attr_err != cudaSuccess) return attr_err;
   GemmMaps maps;
-  if (!make_map(&maps.w, w.data, w.rows, K, w.ld, BM) || !make_sf_map(&maps.sfw, w.sf, w.rows / 128 * (K / 128)))
+  if (!make_map(&maps.w, w.data, w.rows, K, w.ld, BM) || !make_sf_map(&maps.sfw, w.sf, w.rows / 128 * (K / 128), kSfKb) ||
+      !make_sf_map(&maps.sfx, act_sf, max_tiles * 2 * (K / 128), 2 * kSfKb))
     return cudaErrorInvalidValue;
   for (int i = 0; i < kBoxes; ++i)
-    if (!make_map(&maps.x[i], act, act_rows, K, K, 32 * i + 16)) return cudaErrorInvalidValue;
-  for (int i = 0; i < 2; ++i)
-    if (!make_sf_map(&maps.sfx[i], act_sf, max_tiles * 2 * (K / 128), i + 1)) return cudaErrorInvalidValue;
+    if (!make_map(&maps.x[i], act, act_rows, K, K, 32 * i + 8)) return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads, C::SMEM_BYTES, 2, stream, maps, ga);
 }
 

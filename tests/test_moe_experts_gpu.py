@@ -101,7 +101,7 @@ def test_against_the_definition(small, T, k, layout):
     small.check(x, xv, *small.route(T, k))
 
 
-@pytest.mark.parametrize("n", [1, 15, 16, 17, 31, 32, 33, 111, 112, 113, 127, 128, 129, 208, 223, 224, 225, 239, 448, 449])
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 31, 32, 33, 111, 112, 113, 127, 128, 129, 207, 208, 209, 223, 224, 225, 239, 416, 417, 448, 449])
 def test_one_expert_with_n_tokens(small, n):
     """Token tiles at every border of the MMA's N, of the loads and of the scale atoms; the other
     experts are empty but for a last one with a single token."""
