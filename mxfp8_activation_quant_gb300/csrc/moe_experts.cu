@@ -234,6 +234,7 @@ constexpr int kThreads = 384;  // operand loads, MMA, 8 epilogue warps, scale co
 constexpr int BM = 128;        // weight rows per CTA
 constexpr int BK = 128;        // K bytes per stage
 constexpr int STAGES = 6;
+constexpr int kAccBlocks = 4;  // 32-token blocks of a tile that one epilogue warp may hold
 constexpr int kSfKb = 4;      // k-blocks per scale chunk
 constexpr int kSfChunks = 3;  // scale chunks in flight
 constexpr int kGateUp = 0, kDown = 1;
@@ -247,11 +248,12 @@ struct GemmCfg {
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
   // epilogue staging, one row per token: 64 bf16 features of every token of the tile (gate-up), or
-  // 128 of up to 112 tokens, two passes (down)
+  // 128 features of 64 tokens, two buffers in turn (down)
   static constexpr int ROW_BYTES = MODE == kGateUp ? 128 : 256;
-  static constexpr int PASS_TOKENS = MODE == kGateUp ? kTileTokens : 112;
+  static constexpr int PASS_TOKENS = MODE == kGateUp ? kTileTokens : 64;
+  static constexpr int EPI_BYTES = PASS_TOKENS * ROW_BYTES * (MODE == kGateUp ? 1 : 2);
   static constexpr int OFF_EPI = OFF_SF + kSfChunks * (SFA_BYTES + SFB_BYTES);
-  static constexpr int OFF_BAR = OFF_EPI + PASS_TOKENS * ROW_BYTES;
+  static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + (3 * STAGES + 2 * kSfChunks + 5) * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static constexpr int TMEM_SF = 2 * kTileTokens;  // first scale column
@@ -265,6 +267,7 @@ struct GemmMaps {
   CUtensorMap w, sfw;      // weights (128 rows) and their scale atoms
   CUtensorMap x[kBoxes];   // activations
   CUtensorMap sfx;         // a chunk of the tile's scale atoms
+  CUtensorMap y32, y8;     // down: bf16 output boxes of 128 features x 32 or 8 rows
 };
 
 struct GemmArgs {
@@ -368,6 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.sfw);
     for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.x[i]);
     tma_prefetch_desc(&maps.sfx);
+    if (MODE == kDown) {
+      tma_prefetch_desc(&maps.y32);
+      tma_prefetch_desc(&maps.y8);
+    }
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
@@ -536,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, odd = (warp - 2) >> 2, et = static_cast<int>(threadIdx.x) - 64;
     const uint32_t acce0 = mapa_shared(bar_acce, 0);
     const uint32_t stage = sbase + C::OFF_EPI;
-    int ti = 0;
+    int ti = 0, pass = 0;
     for (; item.more(); item.next(), ++ti) {
       const int b = ti & 1, n = item.n();
       bool ok = !*abort_flag;
@@ -546,90 +553,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
       }
       ok = __all_sync(0xffffffffu, ok);
-      for (int t0 = 0; t0 < n; t0 += C::PASS_TOKENS) {  // (one pass, or two for a large down tile)
-        const int tn = n - t0 < C::PASS_TOKENS ? n - t0 : C::PASS_TOKENS;
-        if (ok) {
-          tc_fence_after();
-          const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTileTokens * b + t0;
-          for (int ch = odd; 16 * ch < tn; ch += 2) {
-            uint32_t acc[16];
-            tmem_ld_x16(t_lane + 16 * ch, acc);
-            tmem_ld_wait();
-            if (MODE == kGateUp) {
-              // rows alternate gate, up: lane pairs (2 i, 2 i + 1) hold feature 16 q + i. Of two
-              // tokens the even lane finishes the first and the odd lane the second.
-              const int up = lane & 1, f = 16 * q + (lane >> 1);
+      // All of the warp's columns at once (32-token blocks odd, odd + 2, ...), one wait, and the
+      // accumulator goes back: a tcgen05.ld behind running MMAs takes long, mostly in the odd CTA.
+      uint32_t acc[kAccBlocks][32];
+      if (ok) {
+        tc_fence_after();
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTileTokens * b + 32 * odd;
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const float a0 = __uint_as_float(acc[2 * c]), a1 = __uint_as_float(acc[2 * c + 1]);
+        for (int i = 0; i < kAccBlocks; ++i)
+          if (64 * i + 32 * odd < n) tmem_ld_x32(t_lane + 64 * i, acc[i]);  // (columns past n are not used)
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {  // the MMAs may overwrite this accumulator now
+          if (leader)
+            mbar_arrive(bar_acce + 8 * b);
+          else
+            mbar_arrive_remote_relaxed(acce0 + 8 * b);
+        }
+      }
+      if constexpr (MODE == kGateUp) {
+        if (ok) {
+          // rows alternate gate, up: lane pairs (2 i, 2 i + 1) hold feature 16 q + i. Of two tokens
+          // the even lane finishes the first and the odd lane the second.
+          const int up = lane & 1, f = 16 * q + (lane >> 1);
+#pragma unroll
+          for (int i = 0; i < kAccBlocks; ++i) {
+            const int tok0 = 64 * i + 32 * odd + up;
+            if (64 * i + 32 * odd < n) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float a0 = __uint_as_float(acc[i][2 * c]), a1 = __uint_as_float(acc[i][2 * c + 1]);
                 const float o = __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 1);
                 const float g = up ? o : a0, u = up ? a1 : o;
                 const float h = __fdividef(g, 1.f + __expf(-g)) * u;
-                const int tok = 16 * ch + 2 * c + up;
+                const int tok = tok0 + 2 * c;
                 // 16-byte pieces of a 128-byte row are XOR-swizzled by the row
                 const uint32_t at = stage + tok * 128 + (((f >> 3) ^ (2 * (tok & 3))) << 4) + (f & 7) * 2;
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(bf16x2_rn(h, 0.f))) : "memory");
+                if (tok < kTileTokens)
+                  asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(bf16x2_rn(h, 0.f)))
+                               : "memory");
               }
-            } else {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint32_t w = bf16x2_rn(__uint_as_float(acc[2 * c]), __uint_as_float(acc[2 * c + 1]));
-                const uint32_t at = stage + (16 * ch + 2 * c) * 256 + (32 * q + lane) * 2;
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(w)) : "memory");
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 256), "h"(static_cast<uint16_t>(w >> 16)) : "memory");
-              }
-            }
-          }
-          if (t0 + C::PASS_TOKENS >= n) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {  // the MMAs may overwrite this accumulator now
-              if (leader)
-                mbar_arrive(bar_acce + 8 * b);
-              else
-                mbar_arrive_remote(acce0 + 8 * b);
             }
           }
         }
         named_barrier(1, 256);
         if (ok) {
-          const int64_t row0 = item.row0() + t0;
-          if (MODE == kGateUp) {
-            // one thread = one token and one 32-feature group: the rule of mxfp8_quantize
-            const int64_t ld = p.rows / 2;
-            const int f0 = item.block * 128 + static_cast<int>(rank) * 64;
-            for (int i = et; i < 2 * tn; i += 256) {
-              const int tok = i >> 1, g = i & 1;
-              uint4 v[4];
-              uint32_t amax = 0;
+          // one thread = one token and one 32-feature group: the rule of mxfp8_quantize
+          const int64_t ld = p.rows / 2;
+          const int f0 = item.block * 128 + static_cast<int>(rank) * 64;
+          for (int i = et; i < 2 * n; i += 256) {
+            const int tok = i >> 1, g = i & 1;
+            uint4 v[4];
+            uint32_t amax = 0;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                v[j] = ld_smem_v4(stage + tok * 128 + (((4 * g + j) ^ (2 * (tok & 3))) << 4));
-                amax = max(amax, absmax8(v[j]));
-              }
-              const uint32_t code = ue8m0_from_bf16_amax(amax);
-              const float s = ue8m0_inverse(code);
-              const uint2 q0 = quant8(v[0], s), q1 = quant8(v[1], s), q2 = quant8(v[2], s), q3 = quant8(v[3], s);
-              const int f = f0 + 32 * g;
-              uint4* dst = reinterpret_cast<uint4*>(p.hq + (row0 + tok) * ld + f);
-              dst[0] = make_uint4(q0.x, q0.y, q1.x, q1.y);
-              dst[1] = make_uint4(q2.x, q2.y, q3.x, q3.y);
-              p.hsf[slot_word_offset(static_cast<int64_t>(item.tile()) * kSlotRows + tok, f >> 7, static_cast<int>(ld >> 7)) +
-                    ((f >> 5) & 3)] = static_cast<uint8_t>(code);
+            for (int j = 0; j < 4; ++j) {
+              v[j] = ld_smem_v4(stage + tok * 128 + (((4 * g + j) ^ (2 * (tok & 3))) << 4));
+              amax = max(amax, absmax8(v[j]));
             }
-          } else {
-            const int f0 = item.block * (2 * BM) + static_cast<int>(rank) * BM;
-            if (f0 < p.rows)  // the last block of an odd number of 128-row tiles has one half
-              for (int i = et; i < 16 * tn; i += 256) {
-                const int tok = i >> 4, j = i & 15;
-                const uint4 v = ld_smem_v4(stage + tok * 256 + 16 * j);
-                *reinterpret_cast<uint4*>(p.y + (row0 + tok) * p.rows + f0 + 8 * j) = v;
-              }
+            const uint32_t code = ue8m0_from_bf16_amax(amax);
+            const float s = ue8m0_inverse(code);
+            const uint2 q0 = quant8(v[0], s), q1 = quant8(v[1], s), q2 = quant8(v[2], s), q3 = quant8(v[3], s);
+            const int f = f0 + 32 * g;
+            uint4* dst = reinterpret_cast<uint4*>(p.hq + (item.row0() + tok) * ld + f);
+            dst[0] = make_uint4(q0.x, q0.y, q1.x, q1.y);
+            dst[1] = make_uint4(q2.x, q2.y, q3.x, q3.y);
+            p.hsf[slot_word_offset(static_cast<int64_t>(item.tile()) * kSlotRows + tok, f >> 7, static_cast<int>(ld >> 7)) +
+                  ((f >> 5) & 3)] = static_cast<uint8_t>(code);
           }
         }
         named_barrier(1, 256);
+      } else {
+        // 64 tokens a pass: a warp turns 32 lanes (features) x 32 columns (tokens) into the staging
+        // rows, which leave by TMA: boxes of 32 and 8 rows, and the last rows one by one. (256-byte
+        // copies of every row took 1000 cycles a pass, stores from registers through the load/store
+        // unit as long.) A buffer is written again two passes later; its copies have been read out
+        // before the barrier between.
+        const int f0 = item.block * (2 * BM) + static_cast<int>(rank) * BM;
+        const bool live = f0 < p.rows;  // the last block of an odd number of 128-row tiles has one half
+#pragma unroll
+        for (int i = 0; i < kAccBlocks; ++i) {
+          const int t0 = C::PASS_TOKENS * i;
+          if (t0 >= n) break;
+          const int tn = n - t0 < C::PASS_TOKENS ? n - t0 : C::PASS_TOKENS;
+          const uint32_t buf = stage + static_cast<uint32_t>(pass) * (C::PASS_TOKENS * C::ROW_BYTES);
+          if (ok && 32 * odd < tn) {
+            const uint32_t at = buf + 32 * odd * 256 + (32 * q + lane) * 2;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const uint32_t w = bf16x2_rn(__uint_as_float(acc[i][2 * c]), __uint_as_float(acc[i][2 * c + 1]));
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 512 * c), "h"(static_cast<uint16_t>(w)) : "memory");
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 512 * c + 256), "h"(static_cast<uint16_t>(w >> 16))
+                           : "memory");
+            }
+            fence_proxy_async_smem();
+          }
+          if (et < 32) bulk_wait_read();  // this thread's copies out of the other buffer
+          named_barrier(1, 256);
+          if (ok && live && et < 32) {
+            const int row = item.row0() + t0, n32 = tn >> 5, n8 = (tn & 31) >> 3, n1 = tn & 7;
+            if (et < n32)
+              tma_store_2d(&maps.y32, buf + et * 32 * 256, f0, row + 32 * et);
+            else if (et < n32 + n8)
+              tma_store_2d(&maps.y8, buf + (32 * n32 + 8 * (et - n32)) * 256, f0, row + 32 * n32 + 8 * (et - n32));
+            else if (et < n32 + n8 + n1) {
+              const int r = tn - n1 + et - n32 - n8;
+              bulk_store(p.y + (static_cast<int64_t>(item.row0()) + t0 + r) * p.rows + f0, buf + r * 256, 256);
+            }
+            bulk_commit();
+          }
+          pass ^= 1;
+        }
       }
     }
+    if (MODE == kDown) bulk_wait_all();  // the copies have left shared memory and are written
   }
   __syncwarp();
 
@@ -740,6 +777,10 @@ cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, const void
     return cudaErrorInvalidValue;
   for (int i = 0; i < kBoxes; ++i)
     if (!make_map(&maps.x[i], act, act_rows, K, K, 32 * i + 8)) return cudaErrorInvalidValue;
+  maps.y32 = maps.y8 = maps.sfx;  // (unused by gate-up)
+  if (MODE == kDown && (!make_bf16_map(&maps.y32, ga.y, act_rows, ga.rows, ga.rows, 32) ||
+                        !make_bf16_map(&maps.y8, ga.y, act_rows, ga.rows, ga.rows, 8)))
+    return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads, C::SMEM_BYTES, 2, stream, maps, ga);
 }
 
