@@ -98,7 +98,8 @@ MXQ_API mxq_status moe_route(const void* logits, int32_t logits_type, int64_t ld
  *        contents need no clearing; calls that overlap in time need separate workspaces.
  *   status: optional device status word (mxq_status_bytes()).
  * Requires T >= 1, 1 <= k <= 64, 1 <= E <= 1024, H % 128 == 0, I % 128 == 0, T * k <= 2^24.
- * Five launches (plan, gather, two grouped GEMMs, combine); the results do not depend on timing.
+ * Four launches (plan, two grouped GEMMs, combine), five with many pairs (the scales' copies apart);
+ * the results do not depend on timing.
  */
 MXQ_API int64_t mxq_moe_workspace_bytes(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I);
 

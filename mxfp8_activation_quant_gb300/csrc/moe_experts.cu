@@ -1,7 +1,9 @@
 // The experts' products of a mixture of experts (moe_experts_mxfp8):
 //   plan     sorts the (token, slot) pairs by expert and cuts every expert's rows into token tiles
-//   gather   copies each pair's MXFP8 activations to its expert's rows (data and scales)
-//   GEMM 1   (g, u) = W13_e x, a = MXFP8(bf16(silu(g) u)) in the epilogue
+//   rows     gives each pair its row and copies its activation scales to its tile's slot, and with
+//            many tokens per expert its activations too (all within plan for few pairs)
+//   GEMM 1   (g, u) = W13_e x, a = MXFP8(bf16(silu(g) u)) in the epilogue; a tile's token rows come
+//            from the copies, or with few tokens per expert straight from x, four rows per load
 //   GEMM 2   y = W2_e a, bf16 per pair
 //   combine  out[t] = bf16(sum_j w[t, j] y[pair(t, j)]), fp32 sum in slot order
 //
@@ -42,9 +44,21 @@ struct __align__(16) Item {
   int32_t block, pad[3];
 };
 
+// Where an expert's pairs go, and how many have been placed. (A cache line each: the counters of 64
+// experts in 8 lines made 32768 atomics take 9 us longer.)
+struct __align__(128) ExpertRows {
+  int32_t row0, tile0, step, next;
+};
+
+// Whether the token rows are copied in expert order before GEMM 1. Its loads of four rows at a time
+// keep up with the MMAs of small tiles only: at 97 tokens per expert (777 tokens, 64 experts, top 8,
+// 5120 -> 2 x 1024) reading x in place takes the call from 225 to 216 us, at 512 per expert GEMM 1
+// takes 288 us in place and 231 us from copies that cost 26 us.
+inline bool copies_rows(int64_t P, int32_t E) { return P > static_cast<int64_t>(160) * E; }
+
 struct Layout {  // byte offsets into the workspace
   int64_t max_tiles, blocks1, blocks2;
-  int64_t n_items, items1, items2, pair_row, pair_slot, xp, xsf, hq, hsf, y, total;
+  int64_t n_items, experts, items1, items2, pair_row, row_token, xp, xsf, hq, hsf, y, total;
   Layout(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I) {
     const int64_t P = T * k;
     blocks1 = ceil_div(2 * I, 256);
@@ -57,11 +71,12 @@ struct Layout {  // byte offsets into the workspace
       return at;
     };
     n_items = take(8);
+    experts = take(E * static_cast<int64_t>(sizeof(ExpertRows)));
     items1 = take(max_tiles * blocks1 * static_cast<int64_t>(sizeof(Item)));
     items2 = take(max_tiles * blocks2 * static_cast<int64_t>(sizeof(Item)));
     pair_row = take(P * 4);
-    pair_slot = take(P * 4);
-    xp = take(P * H);
+    row_token = take(P * 4);
+    xp = copies_rows(P, E) ? take(P * H) : o;
     xsf = take(max_tiles * kSlotRows * (H / 32));
     hq = take(P * I);
     hsf = take(max_tiles * kSlotRows * (I / 32));
@@ -80,9 +95,24 @@ struct PlanArgs {
   int32_t* n_items;          // of the two GEMMs
   Item* items1;
   Item* items2;
-  int32_t* pair_row;   // expert-sorted row of pair p, or -1
-  int32_t* pair_slot;  // its row in the scale slots (256 per tile)
+  ExpertRows* experts;  // null: few pairs, placed here (and their scales copied)
+  int32_t* pair_row;    // expert-sorted row of pair p, or -1
+  int32_t* row_token;   // token of an expert-sorted row
+  int32_t k;
+  // activation scales, row-major or F8_128x4, of `words` k-blocks; their slots (256 rows per tile)
+  const uint8_t* sf;
+  int32_t sf_tiled, words;
+  uint8_t* xsf;
 };
+
+// Byte offset of (row `slot` of the scale slots, k-block w) in a scale array of `kbs` k-blocks.
+__device__ __forceinline__ int64_t slot_word_offset(int64_t slot, int w, int kbs) {
+  const int64_t atom = ((slot >> 8) * kbs + w) * 2 + ((slot >> 7) & 1);
+  return atom * 512 + (slot & 31) * 16 + ((slot >> 5) & 3) * 4;
+}
+__device__ __forceinline__ uint32_t sf_word(const uint8_t* sf, bool tiled, int64_t t, int w, int words) {
+  return *reinterpret_cast<const uint32_t*>(sf + (tiled ? tiled128x4_word_offset(t, w, words) : (t * words + w) * 4));
+}
 
 __device__ __forceinline__ int2 add2(const int2 a, const int2 b) { return make_int2(a.x + b.x, a.y + b.y); }
 __device__ __forceinline__ int2 shfl_up2(const int2 a, int d) {
@@ -110,7 +140,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   cnt[tid] = 0;
   next[tid] = 0;
   __syncthreads();
-  for (int p = tid; p < a.P; p += kPlanThreads) {
+  const bool quads = (reinterpret_cast<uintptr_t>(a.ids) & 15u) == 0;  // ids four at a time
+  const int P4 = quads ? a.P / 4 : 0;
+#pragma unroll 4
+  for (int i = tid; i < P4; i += kPlanThreads) {
+    const int4 e = reinterpret_cast<const int4*>(a.ids)[i];
+    if (e.x >= 0 && e.x < a.E) atomicAdd(&cnt[e.x], 1);
+    if (e.y >= 0 && e.y < a.E) atomicAdd(&cnt[e.y], 1);
+    if (e.z >= 0 && e.z < a.E) atomicAdd(&cnt[e.z], 1);
+    if (e.w >= 0 && e.w < a.E) atomicAdd(&cnt[e.w], 1);
+  }
+  for (int p = 4 * P4 + tid; p < a.P; p += kPlanThreads) {
     const int e = a.ids[p];
     if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
   }
@@ -170,74 +210,131 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       items[i] = {e, row0[b] + j * step[e], left < step[e] ? left : step[e], tile0[b] + j, block, {0, 0, 0}};
     }
   }
-  for (int p = tid; p < a.P; p += kPlanThreads) {
-    const int e = a.ids[p];
-    int row = -1, slot = 0;
+  if (a.experts != nullptr) {
+    if (tid < a.E) a.experts[expert] = {row0[tid], tile0[tid], per, 0};
+    return;
+  }
+  // few pairs (at most one per thread): their scales too
+  __syncthreads();  // cnt has been read: it takes the pairs' slots
+  if (tid < a.P) {
+    const int e = a.ids[tid];
+    int row = -1, slot = -1;
     if (e >= 0 && e < a.E) {
       const int k = rank_of[e], r = atomicAdd(&next[e], 1), i = r / step[e];
       row = row0[k] + r;
       slot = (tile0[k] + i) * kSlotRows + r - i * step[e];
+      a.row_token[row] = tid / a.k;
     }
-    a.pair_row[p] = row;
-    a.pair_slot[p] = slot;
+    a.pair_row[tid] = row;
+    cnt[tid] = slot;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.P * a.words; i += kPlanThreads) {
+    const int p = i / a.words, w = i - p * a.words, slot = cnt[p];
+    if (slot >= 0)
+      *reinterpret_cast<uint32_t*>(a.xsf + slot_word_offset(slot, w, a.words)) = sf_word(a.sf, a.sf_tiled, p / a.k, w, a.words);
   }
 }
 
-// Byte offset of (row `slot` of the scale slots, k-block w) in a scale array of `kbs` k-blocks.
-__device__ __forceinline__ int64_t slot_word_offset(int64_t slot, int w, int kbs) {
-  const int64_t atom = ((slot >> 8) * kbs + w) * 2 + ((slot >> 7) & 1);
-  return atom * 512 + (slot & 31) * 16 + ((slot >> 5) & 3) * 4;
-}
-
 // ------------------------------------------------------------------------------------------
-// gather: one block per token, its row read once and written to each of its k places
+// rows: a warp per token, or a block where its activations are copied. Lane j places the token's pair j (one atomic on its expert's counter);
+// the token's scale words, and its activations if they are copied, are read once and written to
+// each of its places.
 // ------------------------------------------------------------------------------------------
-struct GatherArgs {
-  const uint8_t* x;
-  int64_t ldx;
+struct RowsArgs {
+  const int32_t* ids;
+  int32_t E, k;
+  int64_t T;
+  ExpertRows* experts;
+  int32_t* pair_row;
+  int32_t* row_token;
   const uint8_t* sf;
-  int32_t sf_tiled;
-  int32_t k;
-  int64_t H;
-  const int32_t* pair_row;
-  const int32_t* pair_slot;
-  uint8_t* xp;
+  int32_t sf_tiled, words;
   uint8_t* xsf;
+  const uint8_t* x;
+  int64_t ldx, H;
+  uint8_t* xp;
 };
-constexpr int kGatherThreads = 128;
+constexpr int kRowsThreads = 128;
+constexpr int64_t kScalesInPlan = 8192;  // most scale words that plan copies itself
 
-__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs a) {
-  const int64_t t = blockIdx.x;
+template <bool COPY>
+__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
+  constexpr int kTokens = COPY ? 1 : kRowsThreads / 32, kPer = kRowsThreads / kTokens;  // threads per token
+  __shared__ int2 places[kTokens][32];  // row and scale slot
+  const int lane = threadIdx.x & 31, sub = threadIdx.x / kPer, tid = threadIdx.x % kPer;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + sub;
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int chunks = static_cast<int>(a.H / 16), words = static_cast<int>(a.H / 128);
-  for (int c = threadIdx.x; c < chunks; c += kGatherThreads) {
-    const uint4 v = ld_stream_u4(a.x + t * a.ldx + 16 * c);
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t r = a.pair_row[t * a.k + j];
-      if (r >= 0) *reinterpret_cast<uint4*>(a.xp + r * a.H + 16 * c) = v;
+  const bool live = t < a.T;
+  const int chunks = static_cast<int>(a.H / 16);
+  for (int j0 = 0; j0 < a.k; j0 += 32) {
+    const int kj = a.k - j0 < 32 ? a.k - j0 : 32;
+    uint4 v[3];  // the first chunks, on their way while the places are found
+    if (COPY) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (kPer * i + tid < chunks) v[i] = ld_stream_u4(a.x + t * a.ldx + 16 * (kPer * i + tid));
     }
-  }
-  for (int w = threadIdx.x; w < words; w += kGatherThreads) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(
-        a.sf + (a.sf_tiled ? tiled128x4_word_offset(t, w, words) : (t * words + w) * 4));
-    for (int j = 0; j < a.k; ++j)
-      if (a.pair_row[t * a.k + j] >= 0)
-        *reinterpret_cast<uint32_t*>(a.xsf + slot_word_offset(a.pair_slot[t * a.k + j], w, words)) = v;
+    if (tid < kj && live) {
+      const int64_t p = t * a.k + j0 + lane;
+      const int e = a.ids[p];
+      int2 at = make_int2(-1, -1);
+      if (e >= 0 && e < a.E) {
+        const int4 x = *reinterpret_cast<const int4*>(a.experts + e);  // row0, tile0, step
+        const int r = atomicAdd(&a.experts[e].next, 1), i = r / x.z;
+        at = make_int2(x.x + r, (x.y + i) * kSlotRows + r - i * x.z);
+        a.row_token[at.x] = static_cast<int>(t);
+      }
+      a.pair_row[p] = at.x;
+      places[sub][lane] = at;
+    }
+    __syncthreads();
+    if (live) {
+      for (int w = tid; w < a.words; w += kPer) {
+        const uint32_t u = sf_word(a.sf, a.sf_tiled, t, w, a.words);
+        for (int j = 0; j < kj; ++j)
+          if (places[sub][j].y >= 0)
+            *reinterpret_cast<uint32_t*>(a.xsf + slot_word_offset(places[sub][j].y, w, a.words)) = u;
+      }
+      if (COPY)
+        for (int c0 = 0; c0 < chunks; c0 += 3 * kPer) {
+          if (c0 > 0) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              if (c0 + kPer * i + tid < chunks) v[i] = ld_stream_u4(a.x + t * a.ldx + 16 * (c0 + kPer * i + tid));
+          }
+          for (int j = 0; j < kj; ++j) {
+            const int64_t r = places[sub][j].x;
+            if (r < 0) continue;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              if (c0 + kPer * i + tid < chunks)
+                *reinterpret_cast<uint4*>(a.xp + r * a.H + 16 * (c0 + kPer * i + tid)) = v[i];
+          }
+        }
+    }
+    __syncthreads();
   }
 }
 
 // ------------------------------------------------------------------------------------------
 // grouped GEMM
 // ------------------------------------------------------------------------------------------
-constexpr int kThreads = 384;  // operand loads, MMA, 8 epilogue warps, scale copies, scale loads
+constexpr int kGateUp = 0;        // GEMM 1, token rows from the copies
+constexpr int kDown = 1;          // GEMM 2
+constexpr int kGateUpInPlace = 2; // GEMM 1, token rows from x
+// operand loads, MMA, 8 epilogue warps, scale copies, scale loads; in place: 3 more warps that load
+// token rows
+template <int MODE>
+constexpr int kThreads = MODE == kGateUpInPlace ? 480 : 384;
 constexpr int BM = 128;        // weight rows per CTA
 constexpr int BK = 128;        // K bytes per stage
 constexpr int STAGES = 6;
-constexpr int kAccBlocks = 4;  // 32-token blocks of a tile that one epilogue warp may hold
+constexpr int kAccBlocks = 4;  // most 32-token blocks of a tile that one epilogue warp takes
+constexpr int kRowLoaders = 4;  // threads that load token rows (in place)
 constexpr int kSfKb = 4;      // k-blocks per scale chunk
 constexpr int kSfChunks = 3;  // scale chunks in flight
-constexpr int kGateUp = 0, kDown = 1;
 
 template <int MODE>
 struct GemmCfg {
@@ -249,9 +346,9 @@ struct GemmCfg {
   static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
   // epilogue staging, one row per token: 64 bf16 features of every token of the tile (gate-up), or
   // 128 features of 64 tokens, two buffers in turn (down)
-  static constexpr int ROW_BYTES = MODE == kGateUp ? 128 : 256;
-  static constexpr int PASS_TOKENS = MODE == kGateUp ? kTileTokens : 64;
-  static constexpr int EPI_BYTES = PASS_TOKENS * ROW_BYTES * (MODE == kGateUp ? 1 : 2);
+  static constexpr int ROW_BYTES = MODE == kDown ? 256 : 128;
+  static constexpr int PASS_TOKENS = MODE == kDown ? 64 : kTileTokens;
+  static constexpr int EPI_BYTES = PASS_TOKENS * ROW_BYTES * (MODE == kDown ? 2 : 1);
   static constexpr int OFF_EPI = OFF_SF + kSfChunks * (SFA_BYTES + SFB_BYTES);
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + (3 * STAGES + 2 * kSfChunks + 5) * 8;
@@ -265,9 +362,9 @@ struct GemmCfg {
 constexpr int kBoxes = 4;  // token-row boxes of the operand loads: 8, 40, 72 or 104 rows, one load
 struct GemmMaps {
   CUtensorMap w, sfw;      // weights (128 rows) and their scale atoms
-  CUtensorMap x[kBoxes];   // activations
+  CUtensorMap x[kBoxes];   // activations (in place: x[0], single rows)
   CUtensorMap sfx;         // a chunk of the tile's scale atoms
-  CUtensorMap y32, y8;     // down: bf16 output boxes of 128 features x 32 or 8 rows
+  CUtensorMap y32;         // down: bf16 output boxes of 128 features x 32 rows
 };
 
 struct GemmArgs {
@@ -275,6 +372,7 @@ struct GemmArgs {
   const int32_t* n_items;
   int32_t kbs;       // 128-wide k-blocks
   int32_t rows;      // weight rows per expert
+  const int32_t* row_token;  // gate-up in place
   // gate-up: E4M3 activations [pairs, rows / 2] and their scales by tile
   uint8_t* hq;
   uint8_t* hsf;
@@ -336,8 +434,31 @@ struct Items {
   __device__ __forceinline__ int n16() const { return (t.z + 15) & ~15; }
 };
 
+// The token rows of a tile's half, four at a time: thread `part` of kRowLoaders takes quads part,
+// part + kRowLoaders, ... Rows past the tile's last token repeat it (their columns are not used).
+constexpr int kRowQuads = (kTileTokens / 2 / 4 + kRowLoaders - 1) / kRowLoaders;
+__device__ __forceinline__ void load_quads(const GemmArgs& p, const Items& item, uint32_t rank, int part,
+                                           int (&tok)[kRowQuads][4]) {
+  const int half = item.n16() >> 1, first = half * static_cast<int>(rank), last = item.n() - 1;
+#pragma unroll
+  for (int i = 0; i < kRowQuads; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = first + 4 * (part + kRowLoaders * i) + j;
+      tok[i][j] = p.row_token[item.row0() + (r < last ? r : last)];
+    }
+}
+__device__ __forceinline__ void issue_quads(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int x, int half, int part,
+                                            const int (&tok)[kRowQuads][4]) {
+#pragma unroll
+  for (int i = 0; i < kRowQuads; ++i) {
+    const int quad = part + kRowLoaders * i;
+    if (4 * quad < half) tma_gather4_pair(dst + 512 * quad, tm, bar, x, tok[i][0], tok[i][1], tok[i][2], tok[i][3]);
+  }
+}
+
 template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<MODE>, 1)
     experts_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
   using C = GemmCfg<MODE>;
   extern __shared__ uint8_t smem_raw[];
@@ -369,12 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&maps.w);
     tma_prefetch_desc(&maps.sfw);
-    for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.x[i]);
+    for (int i = 0; i < (MODE == kGateUpInPlace ? 1 : kBoxes); ++i) tma_prefetch_desc(&maps.x[i]);
     tma_prefetch_desc(&maps.sfx);
-    if (MODE == kDown) {
-      tma_prefetch_desc(&maps.y32);
-      tma_prefetch_desc(&maps.y8);
-    }
+    if (MODE == kDown) tma_prefetch_desc(&maps.y32);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
@@ -417,10 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; item.more() && !*abort_flag; item.next()) {
       const int half = item.n16() >> 1;
       const int box = (half + 23) >> 5;  // 32 box + 8 >= half rows
-      const uint32_t tx = 2u * static_cast<uint32_t>(C::A_BYTES + (32 * box + 8) * BK);
-      const CUtensorMap* tm_x = &maps.x[box];
+      const uint32_t tx = 2u * static_cast<uint32_t>(C::A_BYTES + (MODE == kGateUpInPlace ? half : 32 * box + 8) * BK);
+      const CUtensorMap* tm_x = &maps.x[MODE == kGateUpInPlace ? 0 : box];
       const int w_row = item.expert() * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
       const int x_row = item.row0() + half * static_cast<int>(rank);
+      int tok[kRowQuads][4];
+      if (MODE == kGateUpInPlace) load_quads(p, item, rank, 0, tok);
       for (int kb = 0; kb < nk; ++kb, ++it, ring.next()) {
         const int s = ring.slot;
         if (!mbar_wait_bounded(bar_empty + 8 * s, ring.phase ^ 1)) {
@@ -431,10 +551,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t fb = full0 + 8 * s;
         if (leader) mbar_arrive_expect_tx(bar_full + 8 * s, tx);
         tma_load_2d_pair(sbase + s * C::A_BYTES, &maps.w, fb, kb * BK, w_row);
-        tma_load_2d_pair(sbase + C::OFF_B + s * C::B_BYTES, tm_x, fb, kb * BK, x_row);
+        if (MODE == kGateUpInPlace)
+          issue_quads(sbase + C::OFF_B + s * C::B_BYTES, tm_x, fb, kb * BK, half, 0, tok);
+        else
+          tma_load_2d_pair(sbase + C::OFF_B + s * C::B_BYTES, tm_x, fb, kb * BK, x_row);
       }
     }
     *issued_cnt = it;
+  } else if (MODE == kGateUpInPlace && warp >= 12 && elected) {
+    // ---------------- token rows (both CTAs; with warp 0, every fourth quad of rows each) ----------------
+    const uint32_t full0 = mapa_shared(bar_full, 0);
+    Ring<STAGES> ring;
+    for (; item.more() && !*abort_flag; item.next()) {
+      const int half = item.n16() >> 1;
+      int tok[kRowQuads][4];
+      load_quads(p, item, rank, warp - 11, tok);
+      for (int kb = 0; kb < nk; ++kb, ring.next()) {
+        const int s = ring.slot;
+        if (!mbar_wait_bounded(bar_empty + 8 * s, ring.phase ^ 1)) {
+          *abort_flag = 1;
+          report(p.status);
+          break;
+        }
+        issue_quads(sbase + C::OFF_B + s * C::B_BYTES, &maps.x[0], full0 + 8 * s, kb * BK, half, warp - 11, tok);
+      }
+    }
   } else if (warp == 11 && elected) {
     // ---------------- scale loads (both CTAs) ----------------
     // The scales of kSfKb k-blocks at a time, in a ring of their own that runs ahead of the operands
@@ -553,41 +694,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
       }
       ok = __all_sync(0xffffffffu, ok);
-      // All of the warp's columns at once (32-token blocks odd, odd + 2, ...), one wait, and the
-      // accumulator goes back: a tcgen05.ld behind running MMAs takes long, mostly in the odd CTA.
-      uint32_t acc[kAccBlocks][32];
-      if (ok) {
-        tc_fence_after();
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTileTokens * b + 32 * odd;
-#pragma unroll
-        for (int i = 0; i < kAccBlocks; ++i)
-          if (64 * i + 32 * odd < n) tmem_ld_x32(t_lane + 64 * i, acc[i]);  // (columns past n are not used)
-        tmem_ld_wait();
+      // Several loads of columns in flight before one wait: a tcgen05.ld behind running MMAs takes
+      // long. (32-token blocks odd, odd + 2, ... of the tile; columns past n are not used.)
+      const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTileTokens * b + 32 * odd;
+      auto release = [&] {  // the MMAs may overwrite this accumulator now
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {  // the MMAs may overwrite this accumulator now
+        if (lane == 0) {
           if (leader)
             mbar_arrive(bar_acce + 8 * b);
           else
             mbar_arrive_remote_relaxed(acce0 + 8 * b);
         }
-      }
-      if constexpr (MODE == kGateUp) {
+      };
+      if constexpr (MODE != kDown) {
         if (ok) {
+          tc_fence_after();
           // rows alternate gate, up: lane pairs (2 i, 2 i + 1) hold feature 16 q + i. Of two tokens
           // the even lane finishes the first and the odd lane the second.
           const int up = lane & 1, f = 16 * q + (lane >> 1);
 #pragma unroll
-          for (int i = 0; i < kAccBlocks; ++i) {
-            const int tok0 = 64 * i + 32 * odd + up;
-            if (64 * i + 32 * odd < n) {
+          for (int h2 = 0; h2 < kAccBlocks / 2; ++h2) {
+            uint32_t acc[2][32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (64 * (2 * h2 + i) + 32 * odd < n) tmem_ld_x32(t_lane + 64 * (2 * h2 + i), acc[i]);
+            tmem_ld_wait();
+            if (h2 == kAccBlocks / 2 - 1) release();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int t0 = 64 * (2 * h2 + i) + 32 * odd;
+              if (t0 >= n) break;
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 const float a0 = __uint_as_float(acc[i][2 * c]), a1 = __uint_as_float(acc[i][2 * c + 1]);
                 const float o = __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 1);
                 const float g = up ? o : a0, u = up ? a1 : o;
                 const float h = __fdividef(g, 1.f + __expf(-g)) * u;
-                const int tok = tok0 + 2 * c;
+                const int tok = t0 + 2 * c + up;
                 // 16-byte pieces of a 128-byte row are XOR-swizzled by the row
                 const uint32_t at = stage + tok * 128 + (((f >> 3) ^ (2 * (tok & 3))) << 4) + (f & 7) * 2;
                 if (tok < kTileTokens)
@@ -625,10 +769,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_barrier(1, 256);
       } else {
         // 64 tokens a pass: a warp turns 32 lanes (features) x 32 columns (tokens) into the staging
-        // rows, which leave by TMA: boxes of 32 and 8 rows, and the last rows one by one. (256-byte
-        // copies of every row took 1000 cycles a pass, stores from registers through the load/store
-        // unit as long.) A buffer is written again two passes later; its copies have been read out
-        // before the barrier between.
+        // rows, which leave by TMA in boxes of 32 rows, the last rows through the load/store unit.
+        // (256-byte copies of every row took 1000 cycles a pass, the load/store unit alone as long.)
+        // A buffer is written again two passes later; its rows have been read out before the
+        // barrier between.
+        uint32_t acc[kAccBlocks][32];
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < kAccBlocks; ++i)
+            if (64 * i + 32 * odd < n) tmem_ld_x32(t_lane + 64 * i, acc[i]);
+          tmem_ld_wait();
+          release();
+        }
         const int f0 = item.block * (2 * BM) + static_cast<int>(rank) * BM;
         const bool live = f0 < p.rows;  // the last block of an odd number of 128-row tiles has one half
 #pragma unroll
@@ -650,17 +803,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (et < 32) bulk_wait_read();  // this thread's copies out of the other buffer
           named_barrier(1, 256);
-          if (ok && live && et < 32) {
-            const int row = item.row0() + t0, n32 = tn >> 5, n8 = (tn & 31) >> 3, n1 = tn & 7;
-            if (et < n32)
-              tma_store_2d(&maps.y32, buf + et * 32 * 256, f0, row + 32 * et);
-            else if (et < n32 + n8)
-              tma_store_2d(&maps.y8, buf + (32 * n32 + 8 * (et - n32)) * 256, f0, row + 32 * n32 + 8 * (et - n32));
-            else if (et < n32 + n8 + n1) {
-              const int r = tn - n1 + et - n32 - n8;
-              bulk_store(p.y + (static_cast<int64_t>(item.row0()) + t0 + r) * p.rows + f0, buf + r * 256, 256);
-            }
-            bulk_commit();
+          if (ok && live) {
+            const int n32 = tn >> 5;
+            if (et < n32) tma_store_2d(&maps.y32, buf + et * 32 * 256, f0, item.row0() + t0 + 32 * et);
+            if (et < 32) bulk_commit();
+            for (int j = 512 * n32 + et; j < 16 * tn; j += 256)
+              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(item.row0() + t0 + (j >> 4)) * p.rows + f0 + 8 * (j & 15)) =
+                  ld_smem_v4(buf + 16 * j);
           }
           pass ^= 1;
         }
@@ -764,24 +913,23 @@ cudaError_t launch_dependent(K kern, dim3 grid, int threads, int smem, int clust
 }
 
 template <int MODE>
-cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, const void* act_sf, int64_t act_rows, int64_t K,
+cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t act_ld, const void* act_sf, int64_t act_rows, int64_t K,
                              int64_t max_tiles, int pairs, const GemmArgs& ga, cudaStream_t stream) {
   using C = GemmCfg<MODE>;
   auto kern = experts_gemm_kernel<MODE>;
   static const cudaError_t attr_err =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (attr_err != cudaSuccess) return attr_err;
-  GemmMaps maps;
+  GemmMaps maps = {};
   if (!make_map(&maps.w, w.data, w.rows, K, w.ld, BM) || !make_sf_map(&maps.sfw, w.sf, w.rows / 128 * (K / 128), kSfKb) ||
       !make_sf_map(&maps.sfx, act_sf, max_tiles * 2 * (K / 128), 2 * kSfKb))
     return cudaErrorInvalidValue;
   for (int i = 0; i < kBoxes; ++i)
-    if (!make_map(&maps.x[i], act, act_rows, K, K, 32 * i + 8)) return cudaErrorInvalidValue;
-  maps.y32 = maps.y8 = maps.sfx;  // (unused by gate-up)
-  if (MODE == kDown && (!make_bf16_map(&maps.y32, ga.y, act_rows, ga.rows, ga.rows, 32) ||
-                        !make_bf16_map(&maps.y8, ga.y, act_rows, ga.rows, ga.rows, 8)))
-    return cudaErrorInvalidValue;
-  return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads, C::SMEM_BYTES, 2, stream, maps, ga);
+    if (MODE == kGateUpInPlace ? i == 0 && !make_map(&maps.x[i], act, act_rows, K, act_ld, 1)
+                               : !make_map(&maps.x[i], act, act_rows, K, act_ld, 32 * i + 8))
+      return cudaErrorInvalidValue;
+  if (MODE == kDown && !make_bf16_map(&maps.y32, ga.y, act_rows, ga.rows, ga.rows, 32)) return cudaErrorInvalidValue;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads<MODE>, C::SMEM_BYTES, 2, stream, maps, ga);
 }
 
 }  // namespace
@@ -809,34 +957,41 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   pa.items1 = reinterpret_cast<Item*>(ws + lay.items1);
   pa.items2 = reinterpret_cast<Item*>(ws + lay.items2);
   pa.pair_row = reinterpret_cast<int32_t*>(ws + lay.pair_row);
-  pa.pair_slot = reinterpret_cast<int32_t*>(ws + lay.pair_slot);
+  pa.row_token = reinterpret_cast<int32_t*>(ws + lay.row_token);
+  pa.k = l.k;
+  pa.sf = static_cast<const uint8_t*>(l.x->sf);
+  pa.sf_tiled = l.x->sf_layout == MXQ_SF_TILED_128X4;
+  pa.words = static_cast<int32_t>(l.H / 128);
+  pa.xsf = ws + lay.xsf;
+  const bool copy = copies_rows(P, l.E);
+  const bool in_plan = !copy && P <= kPlanThreads && P * pa.words <= kScalesInPlan;
+  pa.experts = in_plan ? nullptr : reinterpret_cast<ExpertRows*>(ws + lay.experts);
   plan_kernel<<<1, kPlanThreads, 0, stream>>>(pa);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-
-  GatherArgs ga = {};
-  ga.x = static_cast<const uint8_t*>(l.x->data);
-  ga.ldx = l.x->ld;
-  ga.sf = static_cast<const uint8_t*>(l.x->sf);
-  ga.sf_tiled = l.x->sf_layout == MXQ_SF_TILED_128X4;
-  ga.k = l.k;
-  ga.H = l.H;
-  ga.pair_row = pa.pair_row;
-  ga.pair_slot = pa.pair_slot;
-  ga.xp = ws + lay.xp;
-  ga.xsf = ws + lay.xsf;
-  e = launch_dependent(gather_kernel, dim3(static_cast<unsigned>(l.T), 1, 1), kGatherThreads, 0, 1, stream, ga);
-  if (e != cudaSuccess) return e;
+  uint8_t* xp = ws + lay.xp;
+  if (!in_plan) {
+    const RowsArgs ra = {l.ids, l.E, l.k, l.T, pa.experts, pa.pair_row, pa.row_token, pa.sf, pa.sf_tiled, pa.words, pa.xsf,
+                         static_cast<const uint8_t*>(l.x->data), l.x->ld, l.H, xp};
+    e = launch_dependent(copy ? rows_kernel<true> : rows_kernel<false>,
+                         dim3(static_cast<unsigned>(copy ? l.T : ceil_div(l.T, kRowsThreads / 32)), 1, 1), kRowsThreads, 0, 1,
+                         stream, ra);
+    if (e != cudaSuccess) return e;
+  }
 
   GemmArgs g1 = {};
   g1.items = pa.items1;
   g1.n_items = pa.n_items;
   g1.kbs = static_cast<int32_t>(l.H / BK);
   g1.rows = static_cast<int32_t>(2 * l.I);
+  g1.row_token = pa.row_token;
   g1.hq = ws + lay.hq;
   g1.hsf = ws + lay.hsf;
   g1.status = l.status;
-  e = launch_gemm_mode<kGateUp>(*l.w13, ga.xp, ga.xsf, P, l.H, lay.max_tiles, pairs_for(lay.blocks1), g1, stream);
+  const int pairs1 = pairs_for(lay.blocks1);
+  e = copy ? launch_gemm_mode<kGateUp>(*l.w13, xp, l.H, pa.xsf, P, l.H, lay.max_tiles, pairs1, g1, stream)
+           : launch_gemm_mode<kGateUpInPlace>(*l.w13, l.x->data, l.x->ld, pa.xsf, l.T, l.H, lay.max_tiles, pairs1, g1,
+                                              stream);
   if (e != cudaSuccess) return e;
 
   GemmArgs g2 = {};
@@ -846,7 +1001,7 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   g2.rows = static_cast<int32_t>(l.H);
   g2.y = reinterpret_cast<uint16_t*>(ws + lay.y);
   g2.status = l.status;
-  e = launch_gemm_mode<kDown>(*l.w2, g1.hq, g1.hsf, P, l.I, lay.max_tiles, pairs_for(lay.blocks2), g2, stream);
+  e = launch_gemm_mode<kDown>(*l.w2, g1.hq, l.I, g1.hsf, P, l.I, lay.max_tiles, pairs_for(lay.blocks2), g2, stream);
   if (e != cudaSuccess) return e;
 
   CombineArgs ca = {g2.y, l.weights, pa.pair_row, l.k, l.H, l.ldo, static_cast<uint16_t*>(l.out)};

@@ -298,6 +298,15 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* desc,
       "l"(desc), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
+// Four rows r0..r3 of a tensor map whose box is one row, to consecutive rows of the tile.
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const void* desc, uint32_t bar, int32_t x, int32_t r0,
+                                                 int32_t r1, int32_t r2, int32_t r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(desc), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+      : "memory");
+}
 // Arrive on an mbarrier of another CTA of the cluster (release at cluster scope).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
