@@ -34,8 +34,9 @@ typedef enum mxq_moe_scoring {
  *   h[t, j]  = RNE_st( x[t, j] + residual[t, j] )                 st: the stream's type
  *   y[t, j]  = RNE_bf16( (h[t, j] * r_t) * gamma[j] ),  r_t = 1 / sqrt(mean_j h[t, j]^2 + eps)
  *   (y_q, scales) = mxfp8_quantize(y)                             of that bf16 y, bit-identical
- * The sum is taken in fp32 and rounded once to the stream's type; the norm reads the rounded h,
- * in fp32.
+ * The sum is taken in fp32 and rounded once to the stream's type; the norm reads the rounded h. The
+ * value of y is the formula's, rounded once to fp32 (the sum of squares, r and the products carry
+ * their error terms), before it is rounded to bf16.
  *
  *   x_bf16       [T, H] bf16, row stride ldx elements.
  *   residual     [T, H] of residual_type (MXQ_TYPE_BF16 or MXQ_TYPE_FP32), row stride ldr elements.

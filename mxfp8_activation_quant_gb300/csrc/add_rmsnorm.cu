@@ -9,6 +9,14 @@
 // in registers between the sum of squares and the outputs; thread t owns the 8-element chunks t,
 // t + NT, ... of the row, in 16-byte loads. NT is a multiple of 16, so a scale word's 16 chunks stay
 // in 16 lanes of one warp.
+//
+// y is rounded from the exact value of the formula in fp32, rounded once: its group's scale and codes
+// hang on the bf16 rounding, and a chain of fp32 roundings would fall one value in ten thousand on the
+// other side. The sum of squares
+// and r are held as unevaluated sums of two floats (error-free sums and products, Dekker 1971, Knuth
+// 4.2.2); (h r) gamma is taken in fp32, within 4 ulp, and only where that lies within 4 ulp of a bf16
+// midpoint (one value in 7000) it is taken again with its error terms. 8192 x 5120: 57 us without and
+// 60.5 us with it.
 #include <cuda_runtime.h>
 
 #include "mxq_device.cuh"
@@ -45,16 +53,104 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return bf16x2_rn(bf16_lo(a) + bf16_lo(b), bf16_hi(a) + bf16_hi(b));
 }
 
+// Two floats in one register pair: one instruction does both.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 pack2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// (s, lo) += v, both halves; the error of every addition goes to lo. (a - b as fma(b, -1, a): exact.)
+__device__ __forceinline__ void dd_add2(F2& s, F2& lo, F2 v, F2 minus1) {
+  const F2 t = add2(s, v), d = fma2(s, minus1, t);
+  const F2 e = add2(fma2(fma2(d, minus1, t), minus1, s), fma2(d, minus1, v));
+  s = t;
+  lo = add2(lo, e);
+}
+
+// a + b as a rounded sum and its error (any order of magnitudes)
+__device__ __forceinline__ float two_sum(float a, float b, float& err) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  err = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+  return s;
+}
+// (s, lo) += (v, v_lo)
+__device__ __forceinline__ void dd_add(float& s, float& lo, float v, float v_lo) {
+  float e;
+  s = two_sum(s, v, e);
+  lo = __fadd_rn(lo, __fadd_rn(e, v_lo));
+}
+
+// 1 / sqrt(sum / n + eps) in two parts, relative error below 2^-43: one Newton step whose residual
+// 1 - m r^2 is formed from exact products.
+__device__ __forceinline__ float2 dd_rsqrt_mean(float s, float lo, float n, float eps) {
+  float e;
+  const float q = __fdiv_rn(s, n);
+  const float q_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, n, s), lo), n);
+  const float m = two_sum(q, eps, e);
+  const float m_lo = __fadd_rn(e, q_lo);
+  const float r = rsqrtf(m);
+  const float p = __fmul_rn(r, r), pe = __fmaf_rn(r, r, -p);
+  float t = __fmaf_rn(-m, p, 1.f);
+  t = __fmaf_rn(-m, pe, t);
+  t = __fmaf_rn(-m_lo, p, t);
+  const float c = 0.5f * r * t;
+  const float hi = __fadd_rn(r, c);
+  return make_float2(hi, __fadd_rn(__fsub_rn(r, hi), c));
+}
+
+// Within 4 ulp of the midpoint of two bf16 values; of two values at once, the smaller distance (plus 4)
+// of each half and `least`.
+__device__ __forceinline__ bool near_midpoint(float y) { return ((__float_as_uint(y) - 0x7FFCu) & 0xFFFFu) <= 8u; }
+__device__ __forceinline__ uint32_t midpoint_min2(float y0, float y1, uint32_t least) {
+  const uint32_t low = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x5410);
+  return __viaddmin_u16x2(low, 0x80048004u, least);  // - 0x7FFC in each half
+}
+
+// (h r) g rounded once to fp32.
+__device__ __forceinline__ float rounded_once(float h, float2 r, float g) {
+  const float p = __fmul_rn(h, r.x), pe = __fmaf_rn(h, r.y, __fmaf_rn(h, r.x, -p));
+  const float q = __fmul_rn(p, g), qe = __fmaf_rn(pe, g, __fmaf_rn(p, g, -q));
+  return __fadd_rn(q, qe);
+}
+
+// Blocks per SM that the registers have to leave room for, by the floats that a thread holds.
 template <int CPT, bool F32, int NT>
-__global__ void __launch_bounds__(NT) add_rmsnorm_kernel(const AddRmsArgs a) {
+constexpr int kMinBlocks = (CPT * (F32 ? 2 : 1) <= 4 ? 1280 : CPT * (F32 ? 2 : 1) <= 8 ? 800 : 320) / NT;
+
+template <int CPT, bool F32, int NT>
+__global__ void __launch_bounds__(NT, (kMinBlocks<CPT, F32, NT>)) add_rmsnorm_kernel(const AddRmsArgs a) {
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool vrow = row < a.T;  // (rows past T only zero the padding of the scale layouts)
-  __shared__ float red[NT / 32];
+  __shared__ float2 red[NT / 32];
 
   uint4 hb[F32 ? 1 : CPT];       // the stored h: packed bf16, or fp32
   float hf[F32 ? CPT * 8 : 1];
-  float ss = 0.f;
+  const F2 minus1 = pack2(-1.f, -1.f);
+  F2 ss2 = pack2(0.f, 0.f), lo2 = ss2;  // sum of squares and its error, even and odd elements
   if constexpr (!F32) {
     uint4 xv[CPT], rv[CPT];
 #pragma unroll
@@ -73,9 +169,8 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_kernel(const AddRmsArgs a) {
       const uint32_t w[4] = {hb[j].x, hb[j].y, hb[j].z, hb[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float lo = bf16_lo(w[i]), hi = bf16_hi(w[i]);
-        ss = fmaf(lo, lo, ss);
-        ss = fmaf(hi, hi, ss);
+        const F2 h = pack2(bf16_lo(w[i]), bf16_hi(w[i]));
+        dd_add2(ss2, lo2, mul2(h, h), minus1);  // (squares of bf16 are exact)
       }
     }
   } else {
@@ -105,17 +200,27 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_kernel(const AddRmsArgs a) {
         dst[1] = make_float4(h[4], h[5], h[6], h[7]);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(h[i], h[i], ss);
+      for (int i = 0; i < 4; ++i) {
+        const F2 v = pack2(h[2 * i], h[2 * i + 1]), sq = mul2(v, v);
+        lo2 = add2(lo2, fma2(v, v, fma2(sq, minus1, pack2(0.f, 0.f))));
+        dd_add2(ss2, lo2, sq, minus1);
+      }
     }
   }
+  float ss = unpack2(ss2).x, ss_lo = unpack2(lo2).x;
+  dd_add(ss, ss_lo, unpack2(ss2).y, unpack2(lo2).y);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (lane == 0) red[warp] = ss;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float v = __shfl_xor_sync(0xffffffffu, ss, o), v_lo = __shfl_xor_sync(0xffffffffu, ss_lo, o);
+    dd_add(ss, ss_lo, v, v_lo);
+  }
+  if (lane == 0) red[warp] = make_float2(ss, ss_lo);
   __syncthreads();
-  float total = 0.f;
+  ss = ss_lo = 0.f;
 #pragma unroll
-  for (int i = 0; i < NT / 32; ++i) total += red[i];
-  const float r = rsqrtf(total / a.h + a.eps);
+  for (int i = 0; i < NT / 32; ++i) dd_add(ss, ss_lo, red[i].x, red[i].y);
+  const float2 r = dd_rsqrt_mean(ss, ss_lo, a.h, a.eps);
+  const F2 rr = pack2(r.x, r.x);
 
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
@@ -125,20 +230,32 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_kernel(const AddRmsArgs a) {
     if (vrow && c < a.H) {
       const uint4 g = *reinterpret_cast<const uint4*>(a.gamma + c);
       const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
-      uint32_t yw[4];
+      float hv[8], yv[8];
+      uint32_t least = 0xFFFFFFFFu;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float lo, hi;
         if constexpr (F32) {
-          lo = hf[8 * j + 2 * i];
-          hi = hf[8 * j + 2 * i + 1];
+          hv[2 * i] = hf[8 * j + 2 * i];
+          hv[2 * i + 1] = hf[8 * j + 2 * i + 1];
         } else {
           const uint32_t w = i == 0 ? hb[j].x : i == 1 ? hb[j].y : i == 2 ? hb[j].z : hb[j].w;
-          lo = bf16_lo(w);
-          hi = bf16_hi(w);
+          hv[2 * i] = bf16_lo(w);
+          hv[2 * i + 1] = bf16_hi(w);
         }
-        yw[i] = bf16x2_rn((lo * r) * bf16_lo(gw[i]), (hi * r) * bf16_hi(gw[i]));
+        const float2 v = unpack2(mul2(mul2(pack2(hv[2 * i], hv[2 * i + 1]), rr), pack2(bf16_lo(gw[i]), bf16_hi(gw[i]))));
+        yv[2 * i] = v.x;
+        yv[2 * i + 1] = v.y;
+        least = midpoint_min2(v.x, v.y, least);
       }
+      const bool near = min(least & 0xFFFFu, least >> 16) <= 8u;
+      if (near) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (near_midpoint(yv[i])) yv[i] = rounded_once(hv[i], r, i & 1 ? bf16_hi(gw[i / 2]) : bf16_lo(gw[i / 2]));
+      }
+      uint32_t yw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) yw[i] = bf16x2_rn(yv[2 * i], yv[2 * i + 1]);
       y = make_uint4(yw[0], yw[1], yw[2], yw[3]);
       if (a.y != nullptr) *reinterpret_cast<uint4*>(a.y + row * a.H + c) = y;
     }
@@ -165,6 +282,18 @@ cudaError_t launch_nt(const AddRmsArgs& a, cudaStream_t stream) {
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
+}
+
+// Threads per row. Few rows: a row is one block's latency, so 320 threads (1 x 5120 5.2 us, against 5.6
+// with 256 and 6.5 with 160; 333 x 7168 in fp32 9.5 against 9.9 and 10.3). Many rows: more, smaller
+// blocks hide one another's reductions (8192 x 5120 60.5 us with 160 threads in 8 blocks per SM,
+// against 64.5 with 256 and 66.1 with 320), as few as hold the row.
+constexpr int64_t kFewRows = 512;
+
+template <bool F32>
+cudaError_t launch_type(const AddRmsArgs& a, cudaStream_t stream) {
+  if (a.rows_total <= kFewRows || a.H > 8 * 8 * 160) return launch_nt<F32, 320>(a, stream);
+  return a.H <= 2 * 8 * 64 ? launch_nt<F32, 64>(a, stream) : launch_nt<F32, 160>(a, stream);
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -197,7 +326,7 @@ cudaError_t launch_add_rmsnorm(const AddRmsnormLaunch& l, cudaStream_t stream) {
   a.q.Mp128 = ceil_div(l.T, 128) * 128;
   a.rows_total = l.sf_tiled ? a.q.Mp128 : (l.sf_packed ? a.q.Mp4 : l.T);
   if (a.rows_total > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  return l.fp32_stream ? launch_nt<true, 256>(a, stream) : launch_nt<false, 256>(a, stream);
+  return l.fp32_stream ? launch_type<true>(a, stream) : launch_type<false>(a, stream);
 }
 
 }  // namespace mxq

@@ -2,15 +2,19 @@
 // renormalised weights, one warp per token.
 //
 // 4 E bytes read and 8 k written per token against E exponentials: at any T this is a matter of
-// latency and instruction issue, so a token's E logits stay in one warp's registers (expert
-// 32 i + lane in register i, no alignment asked of rows), the groups' values meet in shared
-// memory, and each of the k picks is two warp reductions (largest key, then lowest index of it).
+// latency and instruction issue, so a token's E logits stay in one warp's registers. Lane l holds
+// experts VPL l .. VPL l + VPL - 1: a group is then a run of lanes wherever VPL divides its size
+// (two shuffles at 8 groups of 32; otherwise its values meet in shared memory), the lowest lane
+// holds the lowest index of a tie, and each of the k picks is one warp maximum and one ballot.
 //
 // Which experts are chosen does not depend on fp32 rounding. Without a bias the order of the
 // choices is that of the logits, which is exact. Otherwise choices and group values are computed
-// in fp32 with a known error bound; where two values whose order matters are nearer than the
-// bound, the warp decides the row again in fp64 (about one row in a thousand at 256 experts with
-// standard-normal logits).
+// in fp32 with a known error bound, and values nearer than the bound are compared in fp64: for
+// sigmoid scores only the picks in question (a lane each), otherwise, or where groups are in
+// question, the whole row. About 3 rows in a thousand at 256 experts with logits of deviation 1.6.
+//
+// 16384 tokens, 256 experts, 8 of 4 of 8 groups: 57 us with one expert per 32 in a lane and groups
+// through shared memory, 40 us so.
 #include <cfloat>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -30,6 +34,8 @@ struct RouteArgs {
   int64_t T;
   int32_t E, k, groups, topk_groups, group_top, gsize;
   uint32_t gmul;  // expert e lies in group (e * gmul) >> 22
+  int32_t group_lanes;  // lanes that hold a group, a power of two; 0: groups do not end between lanes
+  int32_t vec;          // rows are 16-byte aligned
   int32_t softmax, renorm;
   float scale;
   int32_t* ids;
@@ -62,18 +68,13 @@ __device__ __forceinline__ float score32(float l, bool softmax, float m, float i
   return softmax ? expf(l - m) * inv : 1.f / (1.f + expf(-l));
 }
 
-// Relative error bounds of score32. expf is within 2 ulp (2^-22). Sigmoid: exp, sum and division
-// stay below 2^-21.4. Softmax adds the rounding of l - m (|l - m| 2^-24 relative to a score that
-// is itself e^-|l - m| of the largest), the sum of E terms in at most 37 additions, a reciprocal
-// and a product: below 2^-18.4 for every score above 2^-24 of the largest.
-constexpr float kSigmoidErr = 4.8e-7f;  // 2^-21
-constexpr float kSoftmaxErr = 3.9e-6f;  // 2^-18
-
-// Whether two fp32 values may be out of order: score_err bounds their scores' errors together,
-// and each value carries up to three roundings of numbers no larger than `size`.
-__device__ __forceinline__ bool too_near(float hi, float lo, float score_err, float size) {
-  return hi - lo <= score_err + 4.8e-7f * size;
-}
+// Error bounds of the fp32 scores that choices are made of. Sigmoid, 1 / (1 + __expf(-l)): __expf is
+// within 2 + 1.173 |l| ulp, which the sigmoid's slope reduces to (2 s + 0.33) 2^-23, the sum and the
+// quotient add 2.5 s 2^-23: below 6e-7 in all. Softmax, expf(l - m) / sum: the rounding of l - m
+// (|l - m| 2^-24 relative to a score that is itself e^-|l - m| of the largest), expf within 2 ulp,
+// the sum in at most 37 additions: below 3.9e-6 of the row's largest score.
+constexpr float kSigmoidErr = 6.0e-7f;
+constexpr float kSoftmaxErr = 3.9e-6f;
 
 // One row decided in fp64. `d` holds E doubles per warp. Returns this lane's pick (lane r: slot r).
 template <int VPL, bool BF16>
@@ -154,22 +155,49 @@ __device__ __noinline__ int route_row_f64(const RouteArgs& a, int64_t row, doubl
   return mine;
 }
 
+// VPL consecutive logits of a row from expert e0, in vectors where `vec` says that they are aligned.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int e0, float (&c)[VPL]) {
+  constexpr int kVec = BF16 ? 8 : 4;  // elements of 16 bytes
+  if (VPL % kVec == 0 && a.vec && e0 + VPL <= a.E) {
+    const char* src = static_cast<const char*>(a.logits) + (row * a.ldl + e0) * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int i = 0; i < VPL / kVec; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (BF16) {
+          c[kVec * i + 2 * j] = bf16_lo(w[j]);
+          c[kVec * i + 2 * j + 1] = bf16_hi(w[j]);
+        } else {
+          c[kVec * i + j] = __uint_as_float(w[j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = c[i] > FLT_MAX ? FLT_MAX : c[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = e0 + i < a.E ? load_logit<BF16>(a, row, e0 + i) : -CUDART_INF_F;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (!(c[i] > -CUDART_INF_F)) c[i] = -CUDART_INF_F;  // NaN too
+}
+
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   __shared__ double scratch[kWarps][VPL * 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if (row >= a.T) return;  // whole warps; the block never synchronizes
+  const int e0 = VPL * lane;
 
   float c[VPL];  // logits, then choices
   uint32_t key[VPL];
+  load_logits<VPL, BF16>(a, row, e0, c);
   float m = -CUDART_INF_F, inv = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = 32 * i + lane;
-    c[i] = e < a.E ? load_logit<BF16>(a, row, e) : -CUDART_INF_F;
-    if (!(c[i] > -CUDART_INF_F)) c[i] = -CUDART_INF_F;  // NaN too
-  }
   if (a.softmax) {
     uint32_t mk = 0;
 #pragma unroll
@@ -183,121 +211,168 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     inv = sum > 0.f ? 1.f / sum : 0.f;
   }
-  const float rel = a.softmax ? kSoftmaxErr : kSigmoidErr;
   const bool sums = a.groups > 1 && a.group_top == 2;
   const bool values = a.bias != nullptr || sums;  // choices are computed, not only ordered
-  float smax = 0.f, cmax = 0.f;
+  float cmax = 0.f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = 32 * i + lane;
     const bool there = c[i] > -CUDART_INF_F;
     key[i] = order_key(c[i]);
     if (values) {
-      const float s = there ? score32(c[i], a.softmax, m, inv) : 0.f;
-      smax = fmaxf(smax, s);
-      c[i] = there ? s + (a.bias != nullptr ? a.bias[e] : 0.f) : -CUDART_INF_F;
+      const float s = a.softmax ? expf(c[i] - m) * inv : __fdividef(1.f, 1.f + __expf(-c[i]));
+      c[i] = there ? s + (a.bias != nullptr ? a.bias[e0 + i < a.E ? e0 + i : 0] : 0.f) : -CUDART_INF_F;
       if (a.bias != nullptr) key[i] = order_key(c[i]);
       if (there) cmax = fmaxf(cmax, fabsf(c[i]));
     }
   }
+  // Two choices of the row further apart than `tol` are in their exact order: both scores' errors,
+  // and up to three roundings of numbers no larger than the choices.
+  float err = kSigmoidErr, tol = 0.f;
+  if (values) {
+    if (a.softmax) err = kSoftmaxErr * inv;  // the largest score is expf(0) * inv
+    cmax = key_value(__reduce_max_sync(0xffffffffu, order_key(cmax)));
+    tol = 2.f * err + 4.8e-7f * cmax;
+  }
 
-  bool near = false;
+  bool whole = false;  // decide the whole row in fp64
   if (a.groups > 1) {
-    float* sc = reinterpret_cast<float*>(scratch[warp]);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (32 * i + lane < a.E) sc[32 * i + lane] = key[i] ? c[i] : -CUDART_INF_F;
-    __syncwarp();
-    float v = -CUDART_INF_F;
-    if (lane < a.groups) {
+    float v = -CUDART_INF_F;  // value of group `mine_g`
+    int g, kept_lanes = a.group_lanes;
+    if (kept_lanes > 0) {  // a group is a run of lanes
       float b0 = -CUDART_INF_F, b1 = -CUDART_INF_F;
-      int i = lane % a.gsize;  // lanes start at different members: fewer bank conflicts
-      for (int n = 0; n < a.gsize; ++n) {
-        const float u = sc[lane * a.gsize + i];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const float u = key[i] ? c[i] : -CUDART_INF_F;
         b1 = fmaxf(b1, fminf(b0, u));
         b0 = fmaxf(b0, u);
-        i = i + 1 == a.gsize ? 0 : i + 1;
+      }
+      for (int o = 1; o < kept_lanes; o <<= 1) {
+        const float o0 = __shfl_xor_sync(0xffffffffu, b0, o), o1 = __shfl_xor_sync(0xffffffffu, b1, o);
+        b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
+        b0 = fmaxf(b0, o0);
       }
       v = b0;
       if (a.group_top == 2 && b1 > -CUDART_INF_F) v += b1;
+      g = lane / kept_lanes;
+    } else {  // through shared memory, lane g sums up group g
+      float* sc = reinterpret_cast<float*>(scratch[warp]);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (e0 + i < a.E) sc[e0 + i] = key[i] ? c[i] : -CUDART_INF_F;
+      __syncwarp();
+      if (lane < a.groups) {
+        float b0 = -CUDART_INF_F, b1 = -CUDART_INF_F;
+        int i = lane % a.gsize;  // lanes start at different members: fewer bank conflicts
+        for (int n = 0; n < a.gsize; ++n) {
+          const float u = sc[lane * a.gsize + i];
+          b1 = fmaxf(b1, fminf(b0, u));
+          b0 = fmaxf(b0, u);
+          i = i + 1 == a.gsize ? 0 : i + 1;
+        }
+        v = b0;
+        if (a.group_top == 2 && b1 > -CUDART_INF_F) v += b1;
+      }
+      g = lane;
+      kept_lanes = 1;
     }
     int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const float u = __shfl_sync(0xffffffffu, v, g);
-      rank += (u > v || (u == v && g < lane)) ? 1 : 0;
+    for (int h = 0; h < a.groups; ++h) {
+      const float u = __shfl_sync(0xffffffffu, v, h * kept_lanes);
+      rank += (u > v || (u == v && h < g)) ? 1 : 0;
     }
-    const bool have = lane < a.groups && v > -CUDART_INF_F;
-    const uint32_t kept = __ballot_sync(0xffffffffu, have && rank < a.topk_groups);
+    const bool have = g < a.groups && v > -CUDART_INF_F;
+    const bool keep = have && rank < a.topk_groups;
     if (values) {
       // the least kept value against the largest one left out
-      smax = key_value(__reduce_max_sync(0xffffffffu, order_key(smax)));
-      cmax = key_value(__reduce_max_sync(0xffffffffu, order_key(cmax)));
-      const uint32_t in = __reduce_min_sync(0xffffffffu, have && rank < a.topk_groups ? order_key(v) : 0xFFFFFFFFu);
-      const uint32_t out = __reduce_max_sync(0xffffffffu, have && rank >= a.topk_groups ? order_key(v) : 0u);
-      if (out != 0u) near = too_near(key_value(in), key_value(out), 2.f * a.group_top * rel * smax, 2.f * cmax);
+      const uint32_t in = __reduce_min_sync(0xffffffffu, keep ? order_key(v) : 0xFFFFFFFFu);
+      const uint32_t out = __reduce_max_sync(0xffffffffu, have && !keep ? order_key(v) : 0u);
+      whole = out != 0u && key_value(in) - key_value(out) <= 2.f * tol;
     }
+    if (a.group_lanes > 0) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const uint32_t g = (static_cast<uint32_t>(32 * i + lane) * a.gmul) >> 22;
-      if (!((kept >> (g & 31u)) & 1u)) key[i] = 0u;
+      for (int i = 0; i < VPL; ++i)
+        if (!keep) key[i] = 0u;
+    } else {
+      const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (!((kept >> (((static_cast<uint32_t>(e0 + i) * a.gmul) >> 22) & 31u)) & 1u)) key[i] = 0u;
     }
   }
 
-  // k picks, and the runner-up when the choices carry errors
-  const int rounds = a.k + (a.bias != nullptr ? 1 : 0);
-  int mine = -1;
-  float my_c = -CUDART_INF_F, next_c = -CUDART_INF_F;
-  int next = -1;
+  // k picks; with a bias one more, and on while the last two may be out of order
+  int mine = -1, picks = 0;
+  float my_c = -CUDART_INF_F, last = 0.f;
+  bool near = false;  // some neighbours of the list may be out of order
   uint32_t best = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
-  for (int r = 0; r < rounds; ++r) {
+  for (;; ++picks) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
     if (top == 0u) break;
-    int at = 0x7FFFFFFF;
-    if (best == top) {
-#pragma unroll
-      for (int i = VPL - 1; i >= 0; --i)
-        if (key[i] == top) at = 32 * i + lane;
-    }
-    at = __reduce_min_sync(0xffffffffu, at);
-    if (r == a.k) {
-      next = at;
-      next_c = key_value(top);
+    if (a.bias != nullptr) {
+      const float now = key_value(top);
+      const bool close = picks > 0 && last - now <= tol;
+      if (picks >= a.k && !close) break;
+      near |= close;
+      last = now;
+      if (picks == 32) {  // the list may go on
+        whole = true;
+        break;
+      }
+    } else if (picks >= a.k) {
       break;
     }
-    if (lane == r) {
-      mine = at;
-      my_c = key_value(top);
-    }
-    if ((at & 31) == lane) {
+    const int src = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+    int at = 0;
+    if (lane == src) {
+#pragma unroll
+      for (int i = VPL - 1; i >= 0; --i)
+        if (key[i] == top) at = i;
       best = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (32 * i + lane == at) key[i] = 0u;
+        if (i == at) key[i] = 0u;
         best = max(best, key[i]);
       }
     }
-  }
-  float s = mine >= 0 ? score32(load_logit<BF16>(a, row, mine), a.softmax, m, inv) : 0.f;
-  if (a.bias != nullptr) {
-    // neighbours in the order (lane r against slot r + 1, the last one against the runner-up)
-    float s2 = __shfl_down_sync(0xffffffffu, s, 1), c2 = __shfl_down_sync(0xffffffffu, my_c, 1);
-    if (lane == a.k - 1) {
-      c2 = next_c;
-      s2 = next >= 0 ? score32(load_logit<BF16>(a, row, next), a.softmax, m, inv) : 0.f;
+    at = __shfl_sync(0xffffffffu, e0 + at, src);
+    if (lane == picks) {
+      mine = at;
+      my_c = key_value(top);
     }
-    const bool pair = mine >= 0 && lane < a.k && c2 > -CUDART_INF_F;
-    near = __any_sync(0xffffffffu, near || (pair && too_near(my_c, c2, rel * (s + s2), fmaxf(fabsf(my_c), fabsf(c2)))));
   }
-  if (near) {
+  if (near && !whole) {
+    if (a.softmax) {
+      whole = true;  // the sum too is wanted in fp64
+    } else {
+      // Everything outside the list is certainly below all of it: its order in fp64, a lane each.
+      double d = -CUDART_INF;
+      if (mine >= 0)
+        d = 1.0 / (1.0 + exp(-static_cast<double>(load_logit<BF16>(a, row, mine)))) + static_cast<double>(a.bias[mine]);
+      int rank = 0;
+      for (int r = 0; r < picks; ++r) {
+        const double u = __shfl_sync(0xffffffffu, d, r);
+        const int e = __shfl_sync(0xffffffffu, mine, r);
+        rank += (u > d || (u == d && e < mine)) ? 1 : 0;
+      }
+      int ordered = -1;
+      for (int r = 0; r < picks; ++r) {
+        const int e = __shfl_sync(0xffffffffu, mine, r), at = __shfl_sync(0xffffffffu, rank, r);
+        if (at == lane) ordered = e;
+      }
+      mine = ordered;
+    }
+  }
+  if (whole) {
     __syncwarp();  // the float scratch is read no more
     mine = route_row_f64<VPL, BF16>(a, row, scratch[warp], lane);
-    s = mine >= 0 ? score32(load_logit<BF16>(a, row, mine), a.softmax, m, inv) : 0.f;
   }
+  if (lane >= a.k) mine = -1;
+  const float s = mine >= 0 ? score32(load_logit<BF16>(a, row, mine), a.softmax, m, inv) : 0.f;
   float w = s;
   if (a.renorm) {
-    float sum = lane < a.k ? s : 0.f;
+    float sum = s;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     w = s / (sum + 1e-20f);
@@ -309,7 +384,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
 }
 
 template <int VPL>
-cudaError_t launch_vpl(const RouteArgs& a, bool bf16, cudaStream_t stream) {
+cudaError_t launch_vpl(RouteArgs a, bool bf16, cudaStream_t stream) {
+  const int lanes = a.gsize % VPL == 0 ? a.gsize / VPL : 0;
+  a.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
   const unsigned grid = static_cast<unsigned>((a.T + kWarps - 1) / kWarps);
   if (bf16)
     route_kernel<VPL, true><<<grid, kWarps * 32, 0, stream>>>(a);
@@ -333,11 +410,14 @@ cudaError_t launch_route(const RouteLaunch& l, cudaStream_t stream) {
   a.group_top = l.group_top;
   a.gsize = l.E / l.groups;
   a.gmul = (1u << 22) / static_cast<uint32_t>(a.gsize) + 1u;
+  const int64_t es = l.bf16_logits ? 2 : 4;
+  a.vec = reinterpret_cast<uintptr_t>(l.logits) % 16 == 0 && l.ldl * es % 16 == 0;
   a.softmax = l.softmax;
   a.renorm = l.renormalize;
   a.scale = l.scale;
   a.ids = l.ids;
   a.weights = l.weights;
+  if (l.E <= 32) return launch_vpl<1>(a, l.bf16_logits, stream);
   if (l.E <= 64) return launch_vpl<2>(a, l.bf16_logits, stream);
   if (l.E <= 128) return launch_vpl<4>(a, l.bf16_logits, stream);
   if (l.E <= 256) return launch_vpl<8>(a, l.bf16_logits, stream);

@@ -37,8 +37,9 @@ _bound = None
 def _fns():
     """The loaded library with this module's signatures set."""
     global _bound
-    lib = _lib.load()
-    if _bound is not lib:
+    lib = _lib._lib
+    if lib is None or _bound is not lib:
+        lib = _lib.load()
         for name, (args, res) in SIGNATURES.items():
             fn = getattr(lib, name)
             fn.argtypes = args
