@@ -157,7 +157,7 @@ def status_bytes() -> int:
 
 
 def empty_sf(layout: int, M: int, K: int, device="cuda") -> torch.Tensor:
-    n = sf_bytes(layout, M, K)
+    n = int((_lib or load()).mxq_sf_bytes(layout, M, K))
     if n == 0:
         raise ValueError(f"no scale layout {layout} for [{M}, {K}]")
     return torch.empty(n, dtype=torch.uint8, device=device)

@@ -54,16 +54,19 @@ def add_rmsnorm_dual_out(x: torch.Tensor, residual: torch.Tensor, gamma: torch.T
                          stream=None) -> None:
     """residual_out = x + residual (bf16 or fp32 stream; may be `residual` itself), and its RMSNorm
     as bf16 y and/or MXFP8 yq with any subset of the three scale layouts."""
-    assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
-    assert residual.dtype in _TYPES and residual.shape == x.shape and residual.stride(1) == 1
-    assert residual_out.dtype == residual.dtype and residual_out.shape == x.shape and residual_out.stride(1) == 1
     T, H = x.shape
-    assert gamma.dtype == torch.bfloat16 and gamma.shape == (H,) and gamma.is_contiguous()
-    assert y is None or (y.dtype == torch.bfloat16 and y.shape == (T, H) and y.is_contiguous())
-    assert yq is None or (yq.dtype == torch.uint8 and yq.shape == (T, H) and yq.is_contiguous())
-    _check(_fns().add_rmsnorm_dual_out(_ptr(x), x.stride(0), _ptr(residual), _TYPES[residual.dtype],
-                                       residual.stride(0), _ptr(gamma), float(eps), T, H, _ptr(residual_out),
-                                       residual_out.stride(0), _ptr(y), _ptr(yq), _ptr(sf_packed), _ptr(sf_rowmajor),
+    ldx, one = x.stride()
+    ldr, one_r = residual.stride()
+    ldo, one_o = residual_out.stride()
+    st = residual.dtype
+    assert x.dtype is torch.bfloat16 and st in _TYPES and residual_out.dtype is st and one == one_r == one_o == 1
+    assert residual.shape == x.shape == residual_out.shape
+    assert gamma.dtype is torch.bfloat16 and gamma.numel() == H and gamma.is_contiguous()
+    n = T * H
+    assert y is None or (y.dtype is torch.bfloat16 and y.numel() == n and y.is_contiguous())
+    assert yq is None or (yq.dtype is torch.uint8 and yq.numel() == n and yq.is_contiguous())
+    _check(_fns().add_rmsnorm_dual_out(_ptr(x), ldx, _ptr(residual), _TYPES[st], ldr, _ptr(gamma), eps, T, H,
+                                       _ptr(residual_out), ldo, _ptr(y), _ptr(yq), _ptr(sf_packed), _ptr(sf_rowmajor),
                                        _ptr(sf_128x4), _stream(stream)), "add_rmsnorm_dual_out")
 
 
@@ -71,16 +74,18 @@ def moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, bi
               scoring: str = "sigmoid", groups: int = 1, topk_groups: int = 1, group_top: int = 2,
               renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
     """logits [T, E] (fp32 or bf16) -> ids int32 [T, k], weights fp32 [T, k]."""
-    assert logits.dtype in _TYPES and logits.dim() == 2 and logits.stride(1) == 1
     T, E = logits.shape
-    assert ids.dtype == torch.int32 and ids.dim() == 2 and ids.shape[0] == T and ids.is_contiguous()
-    assert weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
-    assert bias is None or (bias.dtype == torch.float32 and bias.shape == (E,) and bias.is_contiguous())
+    ldl, one = logits.stride()
+    rows, k = ids.shape
+    assert logits.dtype in _TYPES and one == 1
+    assert ids.dtype is torch.int32 and rows == T and ids.is_contiguous()
+    assert weights.dtype is torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
+    assert bias is None or (bias.dtype is torch.float32 and bias.numel() == E and bias.is_contiguous())
     if scoring not in _SCORING:
         raise ValueError(f"scoring {scoring!r}: 'sigmoid' or 'softmax'")
-    _check(_fns().moe_route(_ptr(logits), _TYPES[logits.dtype], logits.stride(0), _ptr(bias), T, E, ids.shape[1],
-                            _SCORING[scoring], groups, topk_groups, group_top, int(renormalize), float(scale),
-                            _ptr(ids), _ptr(weights), _stream(stream)), "moe_route")
+    _check(_fns().moe_route(_ptr(logits), _TYPES[logits.dtype], ldl, _ptr(bias), T, E, k, _SCORING[scoring], groups,
+                            topk_groups, group_top, 1 if renormalize else 0, scale, _ptr(ids), _ptr(weights),
+                            _stream(stream)), "moe_route")
 
 
 def moe_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:
