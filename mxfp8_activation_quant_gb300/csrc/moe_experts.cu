@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   __shared__ int2 places[kTokens][32];  // row and scale slot
   const int lane = threadIdx.x & 31, sub = threadIdx.x / kPer, tid = threadIdx.x % kPer;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + sub;
-  pdl_launch_dependents();
   pdl_wait_primary();
+  pdl_launch_dependents();
   const bool live = t < a.T;
   const int chunks = static_cast<int>(a.H / 16);
   for (int j0 = 0; j0 < a.k; j0 += 32) {
@@ -523,8 +523,13 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   cluster_sync_all();  // both CTAs' barriers exist before any load or commit can reach them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_launch_dependents();
-  pdl_wait_primary();  // the plan and the activations are the preceding kernels'
+  // GEMM 1 waits for the plan and the activations. Its dependents are launched after that, so GEMM 2
+  // and combine may read the plan at once: GEMM 2 fetches its first weights and only its loads of
+  // GEMM 1's activations wait (one token: the call 43.9 -> 41.2 us).
+  if (MODE != kDown) {
+    pdl_wait_primary();
+    pdl_launch_dependents();
+  }
   Items item(p, pair, gridDim.x >> 1);
 
   if (warp == 0 && elected) {
@@ -532,6 +537,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     const uint32_t full0 = mapa_shared(bar_full, 0);  // the even CTA's stage barriers
     int it = 0;
     Ring<STAGES> ring;
+    bool first = MODE == kDown;
     for (; item.more() && !*abort_flag; item.next()) {
       const int half = item.n16() >> 1;
       const int box = (half + 23) >> 5;  // 32 box + 8 >= half rows
@@ -541,7 +547,20 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       const int x_row = item.row0() + half * static_cast<int>(rank);
       int tok[kRowQuads][4];
       if (MODE == kGateUpInPlace) load_quads(p, item, rank, 0, tok);
-      for (int kb = 0; kb < nk; ++kb, ++it, ring.next()) {
+      int kb = 0;
+      if (first) {  // the ring is empty: stage i takes k-block i
+        const int pre = nk < STAGES ? nk : STAGES;
+        for (int i = 0; i < pre; ++i) {
+          if (leader) mbar_arrive_expect_tx(bar_full + 8 * i, tx);
+          tma_load_2d_pair(sbase + i * C::A_BYTES, &maps.w, full0 + 8 * i, i * BK, w_row);
+        }
+        pdl_wait_primary();
+        pdl_launch_dependents();
+        for (; kb < pre; ++kb, ++it, ring.next())
+          tma_load_2d_pair(sbase + C::OFF_B + kb * C::B_BYTES, tm_x, full0 + 8 * kb, kb * BK, x_row);
+        first = false;
+      }
+      for (; kb < nk; ++kb, ++it, ring.next()) {
         const int s = ring.slot;
         if (!mbar_wait_bounded(bar_empty + 8 * s, ring.phase ^ 1)) {
           *abort_flag = 1;
@@ -558,6 +577,10 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       }
     }
     *issued_cnt = it;
+    if (first) {  // no item: the grid still ends after GEMM 1
+      pdl_wait_primary();
+      pdl_launch_dependents();
+    }
   } else if (MODE == kGateUpInPlace && warp >= 12 && elected) {
     // ---------------- token rows (both CTAs; with warp 0, every fourth quad of rows each) ----------------
     const uint32_t full0 = mapa_shared(bar_full, 0);
@@ -582,11 +605,26 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     const uint32_t full0 = mapa_shared(bar_sff, 0);
     int ic = 0;
     Ring<kSfChunks> ring;
+    bool first = MODE == kDown;
     for (; item.more() && !*abort_flag; item.next()) {
       const int w_row = item.expert() * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
       const int w_atom = (w_row >> 7) * nk;
       const int x_atom = item.tile() * nk * 2;
-      for (int kb = 0; kb < nk; kb += kSfKb, ++ic, ring.next()) {
+      int kb = 0;
+      if (first) {
+        const int chunks = (nk + kSfKb - 1) / kSfKb, pre = chunks < kSfChunks ? chunks : kSfChunks;
+        const uint32_t dst = sbase + C::OFF_SF;
+        for (int i = 0; i < pre; ++i) {
+          if (leader) mbar_arrive_expect_tx(bar_sff + 8 * i, 2u * (C::SFA_BYTES + C::SFB_BYTES));
+          tma_load_2d_pair(dst + i * (C::SFA_BYTES + C::SFB_BYTES), &maps.sfw, full0 + 8 * i, 0, w_atom + i * kSfKb);
+        }
+        pdl_wait_primary();
+        for (; ic < pre; kb += kSfKb, ++ic, ring.next())
+          tma_load_2d_pair(dst + ic * (C::SFA_BYTES + C::SFB_BYTES) + C::SFA_BYTES, &maps.sfx, full0 + 8 * ic, 0,
+                           x_atom + 2 * kb);
+        first = false;
+      }
+      for (; kb < nk; kb += kSfKb, ++ic, ring.next()) {
         const int c = ring.slot;
         if (!mbar_wait_bounded(bar_sfe + 8 * c, ring.phase ^ 1)) {
           *abort_flag = 1;
@@ -864,16 +902,24 @@ struct CombineArgs {
 constexpr int kCombineThreads = 128;
 
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a) {
-  pdl_wait_primary();
+  // (the rows and weights are known before GEMM 2 ends: see there)
+  __shared__ int rows[64];
+  __shared__ float ws[64];
   const int64_t t = blockIdx.x;
+  for (int j = threadIdx.x; j < a.k; j += kCombineThreads) {
+    rows[j] = a.pair_row[t * a.k + j];
+    ws[j] = a.weights[t * a.k + j];
+  }
+  __syncthreads();
+  pdl_wait_primary();
   const int64_t c = 8 * (static_cast<int64_t>(blockIdx.y) * kCombineThreads + threadIdx.x);
   if (c >= a.H) return;
   float s[8] = {};
 #pragma unroll 8
   for (int j = 0; j < a.k; ++j) {
-    const int64_t r = a.pair_row[t * a.k + j];
+    const int64_t r = rows[j];
     if (r < 0) continue;
-    const float w = a.weights[t * a.k + j];
+    const float w = ws[j];
     const uint4 v = ld_stream_u4(a.y + r * a.H + c);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
