@@ -256,7 +256,9 @@ struct RowsArgs {
   uint8_t* xp;
 };
 constexpr int kRowsThreads = 128;
-constexpr int64_t kScalesInPlan = 8192;  // most scale words that plan copies itself
+// Most scale words that plan copies itself (one token of 5120 in 8 places has 320; at 15360, 48 tokens,
+// the call takes 177 us so and 172 us with the kernel for rows).
+constexpr int64_t kScalesInPlan = 8192;
 
 template <bool COPY>
 __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
@@ -373,6 +375,7 @@ struct GemmArgs {
   int32_t kbs;       // 128-wide k-blocks
   int32_t rows;      // weight rows per expert
   const int32_t* row_token;  // gate-up in place
+  int32_t early;             // the plan is older than the kernel ahead
   // gate-up: E4M3 activations [pairs, rows / 2] and their scales by tile
   uint8_t* hq;
   uint8_t* hsf;
@@ -523,10 +526,12 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   cluster_sync_all();  // both CTAs' barriers exist before any load or commit can reach them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // GEMM 1 waits for the plan and the activations. Its dependents are launched after that, so GEMM 2
-  // and combine may read the plan at once: GEMM 2 fetches its first weights and only its loads of
-  // GEMM 1's activations wait (one token: the call 43.9 -> 41.2 us).
-  if (MODE != kDown) {
+  // A kernel of the call launches its dependents only once its own wait is over, so that they may read
+  // what the kernels before it wrote at once. Where the plan is such (GEMM 2; GEMM 1 behind the kernel
+  // for rows), the first weights and scales are fetched while the kernel ahead still runs, and only
+  // the loads of what that one writes wait (one token: the call 43.9 -> 41.2 us).
+  const bool early = MODE == kDown || p.early;
+  if (!early) {
     pdl_wait_primary();
     pdl_launch_dependents();
   }
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     const uint32_t full0 = mapa_shared(bar_full, 0);  // the even CTA's stage barriers
     int it = 0;
     Ring<STAGES> ring;
-    bool first = MODE == kDown;
+    bool first = early;
     for (; item.more() && !*abort_flag; item.next()) {
       const int half = item.n16() >> 1;
       const int box = (half + 23) >> 5;  // 32 box + 8 >= half rows
@@ -546,7 +551,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       const int w_row = item.expert() * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
       const int x_row = item.row0() + half * static_cast<int>(rank);
       int tok[kRowQuads][4];
-      if (MODE == kGateUpInPlace) load_quads(p, item, rank, 0, tok);
+      if (MODE == kGateUpInPlace && !first) load_quads(p, item, rank, 0, tok);
       int kb = 0;
       if (first) {  // the ring is empty: stage i takes k-block i
         const int pre = nk < STAGES ? nk : STAGES;
@@ -556,8 +561,13 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
         }
         pdl_wait_primary();
         pdl_launch_dependents();
-        for (; kb < pre; ++kb, ++it, ring.next())
-          tma_load_2d_pair(sbase + C::OFF_B + kb * C::B_BYTES, tm_x, full0 + 8 * kb, kb * BK, x_row);
+        if (MODE == kGateUpInPlace) load_quads(p, item, rank, 0, tok);
+        for (; kb < pre; ++kb, ++it, ring.next()) {
+          if (MODE == kGateUpInPlace)
+            issue_quads(sbase + C::OFF_B + kb * C::B_BYTES, tm_x, full0 + 8 * kb, kb * BK, half, 0, tok);
+          else
+            tma_load_2d_pair(sbase + C::OFF_B + kb * C::B_BYTES, tm_x, full0 + 8 * kb, kb * BK, x_row);
+        }
         first = false;
       }
       for (; kb < nk; ++kb, ++it, ring.next()) {
@@ -584,6 +594,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   } else if (MODE == kGateUpInPlace && warp >= 12 && elected) {
     // ---------------- token rows (both CTAs; with warp 0, every fourth quad of rows each) ----------------
     const uint32_t full0 = mapa_shared(bar_full, 0);
+    if (early) pdl_wait_primary();
     Ring<STAGES> ring;
     for (; item.more() && !*abort_flag; item.next()) {
       const int half = item.n16() >> 1;
@@ -605,7 +616,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     const uint32_t full0 = mapa_shared(bar_sff, 0);
     int ic = 0;
     Ring<kSfChunks> ring;
-    bool first = MODE == kDown;
+    bool first = early;
     for (; item.more() && !*abort_flag; item.next()) {
       const int w_row = item.expert() * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
       const int w_atom = (w_row >> 7) * nk;
@@ -1031,6 +1042,7 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   g1.kbs = static_cast<int32_t>(l.H / BK);
   g1.rows = static_cast<int32_t>(2 * l.I);
   g1.row_token = pa.row_token;
+  g1.early = in_plan ? 0 : 1;
   g1.hq = ws + lay.hq;
   g1.hsf = ws + lay.hsf;
   g1.status = l.status;
