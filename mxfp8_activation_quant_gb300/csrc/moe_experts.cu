@@ -493,9 +493,8 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&maps.w);
     tma_prefetch_desc(&maps.sfw);
-    for (int i = 0; i < (MODE == kGateUpInPlace ? 1 : kBoxes); ++i) tma_prefetch_desc(&maps.x[i]);
+    tma_prefetch_desc(&maps.x[0]);
     tma_prefetch_desc(&maps.sfx);
-    if (MODE == kDown) tma_prefetch_desc(&maps.y32);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
@@ -971,7 +970,7 @@ cudaError_t launch_dependent(K kern, dim3 grid, int threads, int smem, int clust
 
 template <int MODE>
 cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t act_ld, const void* act_sf, int64_t act_rows, int64_t K,
-                             int64_t max_tiles, int pairs, const GemmArgs& ga, cudaStream_t stream) {
+                             int64_t max_tiles, int64_t most, int pairs, const GemmArgs& ga, cudaStream_t stream) {
   using C = GemmCfg<MODE>;
   auto kern = experts_gemm_kernel<MODE>;
   static const cudaError_t attr_err =
@@ -981,11 +980,14 @@ cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t ac
   if (!make_map(&maps.w, w.data, w.rows, K, w.ld, BM) || !make_sf_map(&maps.sfw, w.sf, w.rows / 128 * (K / 128), kSfKb) ||
       !make_sf_map(&maps.sfx, act_sf, max_tiles * 2 * (K / 128), 2 * kSfKb))
     return cudaErrorInvalidValue;
+  // (encoding a map costs the host about a microsecond: only those that tiles of `most` tokens use)
+  const int64_t half = round_up(most < kTileTokens ? most : kTileTokens, 16) / 2;
   for (int i = 0; i < kBoxes; ++i)
     if (MODE == kGateUpInPlace ? i == 0 && !make_map(&maps.x[i], act, act_rows, K, act_ld, 1)
-                               : !make_map(&maps.x[i], act, act_rows, K, act_ld, 32 * i + 8))
+                               : half > 32 * i - 24 && !make_map(&maps.x[i], act, act_rows, K, act_ld, 32 * i + 8))
       return cudaErrorInvalidValue;
-  if (MODE == kDown && !make_bf16_map(&maps.y32, ga.y, act_rows, ga.rows, ga.rows, 32)) return cudaErrorInvalidValue;
+  if (MODE == kDown && most >= 32 && !make_bf16_map(&maps.y32, ga.y, act_rows, ga.rows, ga.rows, 32))
+    return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads<MODE>, C::SMEM_BYTES, 2, stream, maps, ga);
 }
 
@@ -1047,8 +1049,8 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   g1.hsf = ws + lay.hsf;
   g1.status = l.status;
   const int pairs1 = pairs_for(lay.blocks1);
-  e = copy ? launch_gemm_mode<kGateUp>(*l.w13, xp, l.H, pa.xsf, P, l.H, lay.max_tiles, pairs1, g1, stream)
-           : launch_gemm_mode<kGateUpInPlace>(*l.w13, l.x->data, l.x->ld, pa.xsf, l.T, l.H, lay.max_tiles, pairs1, g1,
+  e = copy ? launch_gemm_mode<kGateUp>(*l.w13, xp, l.H, pa.xsf, P, l.H, lay.max_tiles, P, pairs1, g1, stream)
+           : launch_gemm_mode<kGateUpInPlace>(*l.w13, l.x->data, l.x->ld, pa.xsf, l.T, l.H, lay.max_tiles, P, pairs1, g1,
                                               stream);
   if (e != cudaSuccess) return e;
 
@@ -1059,7 +1061,7 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   g2.rows = static_cast<int32_t>(l.H);
   g2.y = reinterpret_cast<uint16_t*>(ws + lay.y);
   g2.status = l.status;
-  e = launch_gemm_mode<kDown>(*l.w2, g1.hq, l.I, g1.hsf, P, l.I, lay.max_tiles, pairs_for(lay.blocks2), g2, stream);
+  e = launch_gemm_mode<kDown>(*l.w2, g1.hq, l.I, g1.hsf, P, l.I, lay.max_tiles, P, pairs_for(lay.blocks2), g2, stream);
   if (e != cudaSuccess) return e;
 
   CombineArgs ca = {g2.y, l.weights, pa.pair_row, l.k, l.H, l.ldo, static_cast<uint16_t*>(l.out)};
