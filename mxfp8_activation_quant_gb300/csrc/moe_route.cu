@@ -10,11 +10,13 @@
 // Which experts are chosen does not depend on fp32 rounding. Without a bias the order of the
 // choices is that of the logits, which is exact. Otherwise choices and group values are computed
 // in fp32 with a known error bound, and values nearer than the bound are compared in fp64: for
-// sigmoid scores only the picks in question (a lane each), otherwise, or where groups are in
-// question, the whole row. About 3 rows in a thousand at 256 experts with logits of deviation 1.6.
+// sigmoid scores only the groups or picks in question, one value per lane (an fp64 exponential
+// takes a warp about 0.7 us; the whole row's, which one row in 10^4 took at first, added 10 us to a
+// launch), for softmax scores the whole row. Three rows in a thousand have such picks at 256 experts
+// with logits of deviation 1.6.
 //
 // 16384 tokens, 256 experts, 8 of 4 of 8 groups: 57 us with one expert per 32 in a lane and groups
-// through shared memory, 40 us so.
+// through shared memory, 29 us so.
 #include <cfloat>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -35,7 +37,7 @@ struct RouteArgs {
   int32_t E, k, groups, topk_groups, group_top, gsize;
   uint32_t gmul;  // expert e lies in group (e * gmul) >> 22
   int32_t group_lanes;  // lanes that hold a group, a power of two; 0: groups do not end between lanes
-  int32_t vec;          // rows are 16-byte aligned
+  int32_t vec, bias_vec;  // rows, and the bias, are 16-byte aligned
   int32_t softmax, renorm;
   float scale;
   int32_t* ids;
@@ -186,6 +188,24 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int
     if (!(c[i] > -CUDART_INF_F)) c[i] = -CUDART_INF_F;  // NaN too
 }
 
+// VPL consecutive biases from expert e0 (0 past the last).
+template <int VPL>
+__device__ __forceinline__ void load_bias(const RouteArgs& a, int e0, float (&v)[VPL]) {
+  if (VPL % 4 == 0 && a.bias_vec && e0 + VPL <= a.E) {
+#pragma unroll
+    for (int i = 0; i < VPL / 4; ++i) {
+      const float4 u = *reinterpret_cast<const float4*>(a.bias + e0 + 4 * i);
+      v[4 * i] = u.x;
+      v[4 * i + 1] = u.y;
+      v[4 * i + 2] = u.z;
+      v[4 * i + 3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = e0 + i < a.E ? a.bias[e0 + i] : 0.f;
+  }
+}
+
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   __shared__ double scratch[kWarps][VPL * 32];
@@ -214,16 +234,21 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   const bool sums = a.groups > 1 && a.group_top == 2;
   const bool values = a.bias != nullptr || sums;  // choices are computed, not only ordered
   float cmax = 0.f;
+  if (values) {
+    float bias[VPL] = {};
+    if (a.bias != nullptr) load_bias<VPL>(a, e0, bias);
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const bool there = c[i] > -CUDART_INF_F;
-    key[i] = order_key(c[i]);
-    if (values) {
+    for (int i = 0; i < VPL; ++i) {
+      const bool there = c[i] > -CUDART_INF_F;
       const float s = a.softmax ? expf(c[i] - m) * inv : __fdividef(1.f, 1.f + __expf(-c[i]));
-      c[i] = there ? s + (a.bias != nullptr ? a.bias[e0 + i < a.E ? e0 + i : 0] : 0.f) : -CUDART_INF_F;
+      key[i] = a.bias != nullptr ? 0u : order_key(c[i]);
+      c[i] = there ? s + bias[i] : -CUDART_INF_F;
       if (a.bias != nullptr) key[i] = order_key(c[i]);
       if (there) cmax = fmaxf(cmax, fabsf(c[i]));
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = order_key(c[i]);
   }
   // Two choices of the row further apart than `tol` are in their exact order: both scores' errors,
   // and up to three roundings of numbers no larger than the choices.
@@ -236,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
 
   bool whole = false;  // decide the whole row in fp64
   if (a.groups > 1) {
-    float v = -CUDART_INF_F;  // value of group `mine_g`
+    float v = -CUDART_INF_F, least = -CUDART_INF_F;  // value of this lane's group, and its last term
     int g, kept_lanes = a.group_lanes;
     if (kept_lanes > 0) {  // a group is a run of lanes
       float b0 = -CUDART_INF_F, b1 = -CUDART_INF_F;
@@ -251,8 +276,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
         b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
         b0 = fmaxf(b0, o0);
       }
-      v = b0;
-      if (a.group_top == 2 && b1 > -CUDART_INF_F) v += b1;
+      v = least = b0;
+      if (a.group_top == 2 && b1 > -CUDART_INF_F) {
+        v += b1;
+        least = b1;
+      }
       g = lane / kept_lanes;
     } else {  // through shared memory, lane g sums up group g
       float* sc = reinterpret_cast<float*>(scratch[warp]);
@@ -269,8 +297,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
           b0 = fmaxf(b0, u);
           i = i + 1 == a.gsize ? 0 : i + 1;
         }
-        v = b0;
-        if (a.group_top == 2 && b1 > -CUDART_INF_F) v += b1;
+        v = least = b0;
+        if (a.group_top == 2 && b1 > -CUDART_INF_F) {
+          v += b1;
+          least = b1;
+        }
       }
       g = lane;
       kept_lanes = 1;
@@ -281,12 +312,66 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
       rank += (u > v || (u == v && h < g)) ? 1 : 0;
     }
     const bool have = g < a.groups && v > -CUDART_INF_F;
-    const bool keep = have && rank < a.topk_groups;
+    bool keep = have && rank < a.topk_groups;
     if (values) {
       // the least kept value against the largest one left out
-      const uint32_t in = __reduce_min_sync(0xffffffffu, keep ? order_key(v) : 0xFFFFFFFFu);
-      const uint32_t out = __reduce_max_sync(0xffffffffu, have && !keep ? order_key(v) : 0u);
-      whole = out != 0u && key_value(in) - key_value(out) <= 2.f * tol;
+      const uint32_t ki = __reduce_min_sync(0xffffffffu, keep ? order_key(v) : 0xFFFFFFFFu);
+      const uint32_t ko = __reduce_max_sync(0xffffffffu, have && !keep ? order_key(v) : 0u);
+      const float in = key_value(ki), out = key_value(ko);
+      if (ko != 0u && in - out <= 2.f * tol) {
+        // Some groups lie too near to the border: they are ranked by their values in fp64, a lane for
+        // each expert that may be among a group's largest.
+        const bool border = have && (keep ? v - out <= 2.f * tol : in - v <= 2.f * tol);
+        int* list = reinterpret_cast<int*>(reinterpret_cast<float*>(scratch[warp]) + VPL * 32);
+        int n = 0;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const int holder = a.group_lanes > 0 ? lane : min((e0 + i) / a.gsize, 31);
+          const float thr = __shfl_sync(0xffffffffu, least, holder);
+          const bool mine = __shfl_sync(0xffffffffu, border, holder) && key[i] != 0u && c[i] >= thr - tol;
+          const uint32_t who = __ballot_sync(0xffffffffu, mine);
+          const int at = n + __popc(who & ((1u << lane) - 1u));
+          if (mine && at < 32) list[at] = e0 + i;
+          n += __popc(who);
+        }
+        __syncwarp();
+        if (a.softmax || n > 32) {
+          whole = true;  // the sum too is wanted in fp64, or too many experts are in question
+        } else {
+          const int e = lane < n ? list[lane] : -1, eg = e >= 0 ? e / a.gsize : -1;
+          double d = -CUDART_INF;
+          if (e >= 0) {
+            d = 1.0 / (1.0 + exp(-static_cast<double>(load_logit<BF16>(a, row, e))));
+            if (a.bias != nullptr) d += static_cast<double>(a.bias[e]);
+          }
+          double b0 = -CUDART_INF, b1 = -CUDART_INF;
+          bool first = e >= 0;  // the lane that speaks for its group
+          for (int r = 0; r < n; ++r) {
+            const double u = __shfl_sync(0xffffffffu, d, r);
+            if (__shfl_sync(0xffffffffu, eg, r) != eg) continue;
+            if (r < lane) first = false;
+            if (u > b0) {
+              b1 = b0;
+              b0 = u;
+            } else if (u > b1) {
+              b1 = u;
+            }
+          }
+          const double value = a.group_top == 2 && b1 > -CUDART_INF ? b0 + b1 : b0;
+          int above = 0;
+          for (int r = 0; r < n; ++r) {
+            const double u = __shfl_sync(0xffffffffu, value, r);
+            const int h = __shfl_sync(0xffffffffu, eg, r);
+            if (__shfl_sync(0xffffffffu, first, r)) above += (u > value || (u == value && h < eg)) ? 1 : 0;
+          }
+          // groups kept for certain, a bit each
+          uint32_t kept = __reduce_or_sync(0xffffffffu, keep && !border ? 1u << g : 0u);
+          const int room = a.topk_groups - __popc(kept);
+          kept |= __reduce_or_sync(0xffffffffu, first && above < room ? 1u << eg : 0u);
+          keep = have && ((kept >> g) & 1u);
+        }
+      }
     }
     if (a.group_lanes > 0) {
 #pragma unroll
@@ -412,6 +497,7 @@ cudaError_t launch_route(const RouteLaunch& l, cudaStream_t stream) {
   a.gmul = (1u << 22) / static_cast<uint32_t>(a.gsize) + 1u;
   const int64_t es = l.bf16_logits ? 2 : 4;
   a.vec = reinterpret_cast<uintptr_t>(l.logits) % 16 == 0 && l.ldl * es % 16 == 0;
+  a.bias_vec = reinterpret_cast<uintptr_t>(l.bias) % 16 == 0;
   a.softmax = l.softmax;
   a.renorm = l.renormalize;
   a.scale = l.scale;

@@ -142,6 +142,29 @@ def test_values_next_to_the_border(mxq, scoring):
     check(mxq, logits, 8, bias=bias, scoring=scoring, groups=8, topk_groups=3)
 
 
+@pytest.mark.parametrize("E,groups,kept,top", [(64, 8, 3, 2), (64, 8, 5, 1), (96, 8, 4, 2), (256, 8, 4, 2), (40, 5, 2, 2)])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_groups_next_to_the_border(mxq, scoring, E, groups, kept, top):
+    """Group values nearer than fp32 can tell: two experts of each group get biases that bring the sum
+    of their choices to within a few 2^-26 of the other groups'; the rest stay far below."""
+    T = 128
+    logits, _ = gate(T, E, seed=E + kept)
+    logits[:] = logits[:1]
+    l = logits[0].double().cpu()
+    s = torch.sigmoid(l) if scoring == "sigmoid" else torch.softmax(l, 0)
+    g = torch.Generator().manual_seed(E)
+    bias = torch.full((E,), -3.0, dtype=torch.float64)
+    n = E // groups
+    for i in range(groups):
+        a, b = i * n + 1, i * n + n - 1
+        d = 0.05 * torch.rand(1, generator=g).item() if top == 2 else 0.0
+        bias[a], bias[b] = 1.0 + d - s[a], 1.0 - d - s[b]
+    # logits of other rows differ in their last bits: the order of the exact sums changes with them
+    logits += (torch.randint(-3, 4, (T, E), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+               * torch.finfo(torch.float32).eps)
+    check(mxq, logits, 2 * kept, bias=bias.float().cuda(), scoring=scoring, groups=groups, topk_groups=kept, group_top=top)
+
+
 def test_strided_rows_large_logits_and_stream(mxq):
     logits, bias = gate(50, 320, seed=7)
     view = (logits * 8.0)[:, 3:259]  # odd offset, row stride 320
