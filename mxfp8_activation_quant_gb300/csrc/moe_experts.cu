@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     const uint32_t full0 = mapa_shared(bar_full, 0);  // the even CTA's stage barriers
     int it = 0;
     Ring<STAGES> ring;
-    bool first = early;
+    bool first = true;
     for (; item.more() && !*abort_flag; item.next()) {
       const int half = item.n16() >> 1;
       const int box = (half + 23) >> 5;  // 32 box + 8 >= half rows
@@ -558,8 +558,10 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
           if (leader) mbar_arrive_expect_tx(bar_full + 8 * i, tx);
           tma_load_2d_pair(sbase + i * C::A_BYTES, &maps.w, full0 + 8 * i, i * BK, w_row);
         }
-        pdl_wait_primary();
-        pdl_launch_dependents();
+        if (early) {
+          pdl_wait_primary();
+          pdl_launch_dependents();
+        }
         if (MODE == kGateUpInPlace) load_quads(p, item, rank, 0, tok);
         for (; kb < pre; ++kb, ++it, ring.next()) {
           if (MODE == kGateUpInPlace)
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       }
     }
     *issued_cnt = it;
-    if (first) {  // no item: the grid still ends after GEMM 1
+    if (first && early) {  // no item: the grid still ends after GEMM 1
       pdl_wait_primary();
       pdl_launch_dependents();
     }
@@ -925,17 +927,23 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
   const int64_t c = 8 * (static_cast<int64_t>(blockIdx.y) * kCombineThreads + threadIdx.x);
   if (c >= a.H) return;
   float s[8] = {};
-#pragma unroll 8
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t r = rows[j];
-    if (r < 0) continue;
-    const float w = ws[j];
-    const uint4 v = ld_stream_u4(a.y + r * a.H + c);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  for (int j0 = 0; j0 < a.k; j0 += 4) {  // four rows in flight
+    uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[2 * i] = fmaf(w, bf16_lo(u[i]), s[2 * i]);
-      s[2 * i + 1] = fmaf(w, bf16_hi(u[i]), s[2 * i + 1]);
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = j0 + j < a.k ? rows[j0 + j] : -1;
+      v[j] = r >= 0 ? ld_stream_u4(a.y + r * a.H + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j0 + j >= a.k || rows[j0 + j] < 0) continue;  // (the weight of an empty slot may be anything)
+      const float w = ws[j0 + j];
+      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[2 * i] = fmaf(w, bf16_lo(u[i]), s[2 * i]);
+        s[2 * i + 1] = fmaf(w, bf16_hi(u[i]), s[2 * i + 1]);
+      }
     }
   }
   *reinterpret_cast<uint4*>(a.out + t * a.ldo + c) =
