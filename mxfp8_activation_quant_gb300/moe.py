@@ -32,6 +32,7 @@ SIGNATURES = {
 }
 
 _bound = None
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _fns():
@@ -48,26 +49,44 @@ def _fns():
     return lib
 
 
+def _host(*tensors):
+    """For a call that was given a host tensor."""
+    for t in tensors:
+        _ptr(t)
+
+
+# The first two calls take a few microseconds on the GPU for few tokens, less than their tensors take to
+# be looked over here: so each property is asked for once, and pointers are taken in place.
 def add_rmsnorm_dual_out(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor, eps: float,
                          residual_out: torch.Tensor, y: Optional[torch.Tensor] = None,
                          yq: Optional[torch.Tensor] = None, sf_packed=None, sf_rowmajor=None, sf_128x4=None,
                          stream=None) -> None:
     """residual_out = x + residual (bf16 or fp32 stream; may be `residual` itself), and its RMSNorm
     as bf16 y and/or MXFP8 yq with any subset of the three scale layouts."""
-    T, H = x.shape
+    shape = x.shape
+    T, H = shape
     ldx, one = x.stride()
     ldr, one_r = residual.stride()
     ldo, one_o = residual_out.stride()
     st = residual.dtype
     assert x.dtype is torch.bfloat16 and st in _TYPES and residual_out.dtype is st and one == one_r == one_o == 1
-    assert residual.shape == x.shape == residual_out.shape
+    assert residual.shape == shape and residual_out.shape == shape
     assert gamma.dtype is torch.bfloat16 and gamma.numel() == H and gamma.is_contiguous()
     n = T * H
     assert y is None or (y.dtype is torch.bfloat16 and y.numel() == n and y.is_contiguous())
     assert yq is None or (yq.dtype is torch.uint8 and yq.numel() == n and yq.is_contiguous())
-    _check(_fns().add_rmsnorm_dual_out(_ptr(x), ldx, _ptr(residual), _TYPES[st], ldr, _ptr(gamma), eps, T, H,
-                                       _ptr(residual_out), ldo, _ptr(y), _ptr(yq), _ptr(sf_packed), _ptr(sf_rowmajor),
-                                       _ptr(sf_128x4), _stream(stream)), "add_rmsnorm_dual_out")
+    assert sf_rowmajor is None or sf_rowmajor.nbytes * 32 >= n
+    assert sf_packed is None or sf_packed.nbytes * 32 >= -(-T // 4) * 4 * H
+    assert sf_128x4 is None or sf_128x4.nbytes >= -(-T // 128) * 128 * -(-H // 128) * 4
+    if not (x.is_cuda and residual.is_cuda and gamma.is_cuda and residual_out.is_cuda):
+        _host(x, residual, gamma, residual_out)
+    status = _fns().add_rmsnorm_dual_out(
+        x.data_ptr(), ldx, residual.data_ptr(), _TYPES[st], ldr, gamma.data_ptr(), eps, T, H, residual_out.data_ptr(), ldo,
+        None if y is None else _ptr(y), None if yq is None else _ptr(yq), None if sf_packed is None else _ptr(sf_packed),
+        None if sf_rowmajor is None else _ptr(sf_rowmajor), None if sf_128x4 is None else _ptr(sf_128x4),
+        _raw_stream(_device()) if stream is None else _stream(stream))
+    if status:
+        _check(status, "add_rmsnorm_dual_out")
 
 
 def moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -83,9 +102,14 @@ def moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, bi
     assert bias is None or (bias.dtype is torch.float32 and bias.numel() == E and bias.is_contiguous())
     if scoring not in _SCORING:
         raise ValueError(f"scoring {scoring!r}: 'sigmoid' or 'softmax'")
-    _check(_fns().moe_route(_ptr(logits), _TYPES[logits.dtype], ldl, _ptr(bias), T, E, k, _SCORING[scoring], groups,
-                            topk_groups, group_top, 1 if renormalize else 0, scale, _ptr(ids), _ptr(weights),
-                            _stream(stream)), "moe_route")
+    if not (logits.is_cuda and ids.is_cuda and weights.is_cuda):
+        _host(logits, ids, weights)
+    status = _fns().moe_route(
+        logits.data_ptr(), _TYPES[logits.dtype], ldl, None if bias is None else _ptr(bias), T, E, k, _SCORING[scoring],
+        groups, topk_groups, group_top, 1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(),
+        _raw_stream(_device()) if stream is None else _stream(stream))
+    if status:
+        _check(status, "moe_route")
 
 
 def moe_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:
@@ -114,6 +138,11 @@ def moe_experts_mxfp8(x: MXFP8, ids: torch.Tensor, weights: torch.Tensor, w13: M
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
             with torch.cuda.stream(s):
                 workspace = torch.empty(n, dtype=torch.uint8, device=out.device)
+    for m in (x, w13, w2):  # (weights' rows are multiples of 128)
+        R, C = m.data.shape
+        rows = R if m.layout == _lib.SF_ROWMAJOR_U8 else -(-R // 128) * 128
+        assert m.sf.nbytes * 32 >= rows * C, "scales are missing"
+        _host(m.data, m.sf)
     xc, ac, bc = x.c(), w13.c(), w2.c()
     _check(lib.moe_experts_mxfp8(ctypes.byref(xc), _ptr(ids), _ptr(weights), T, k, ctypes.byref(ac), ctypes.byref(bc),
                                  E, H, I, _ptr(out), out.stride(0), _ptr(workspace),

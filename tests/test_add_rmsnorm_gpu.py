@@ -120,6 +120,27 @@ def test_zero_and_constant_rows(mxq):
     assert torch.all(yq[0] == 0) and torch.all(rm.view(T, -1)[0] == 0) and torch.all(rm.view(T, -1)[2] == 0)
 
 
+def test_offsets_past_32_bits(mxq):
+    """2^31 elements and a few rows more, in place: sampled rows against the same rows alone."""
+    H = 16384
+    T = 2 ** 31 // H + 5
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    r = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    gamma = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    t = torch.tensor([0, 1, 70000, T - 6, T - 2, T - 1], device="cuda")
+    x1, r1 = x[t].contiguous(), r[t].contiguous()
+    yq, tl = torch.empty((T, H), dtype=torch.uint8, device="cuda"), mxq.empty_sf(2, T, H)
+    mxq.add_rmsnorm_dual_out(x, r, gamma, 1e-6, r, yq=yq, sf_128x4=tl)
+    yq1, rm1 = torch.empty((6, H), dtype=torch.uint8, device="cuda"), mxq.empty_sf(0, 6, H)
+    mxq.add_rmsnorm_dual_out(x1, r1, gamma, 1e-6, r1, yq=yq1, sf_rowmajor=rm1)
+    assert torch.equal(r[t], r1) and torch.equal(yq[t], yq1)
+    # the tiled scales of those rows
+    c = torch.arange(H // 32, device="cuda")
+    at = ((t[:, None] // 128) * (H // 128) + c // 4) * 512 + (t[:, None] % 32) * 16 + (t[:, None] % 128) // 32 * 4 + c % 4
+    assert torch.equal(tl[at.reshape(-1)], rm1)
+
+
 def test_other_stream_and_graph(mxq):
     T, H = 33, 1024
     x, r, gamma = inputs(T, H, torch.bfloat16, 3)

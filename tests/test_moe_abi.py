@@ -121,8 +121,31 @@ def test_host_tensors_are_refused(lib):
         moe.add_rmsnorm_dual_out(x, x.clone(), torch.ones(64, dtype=torch.bfloat16), 1e-6, x.clone(), x.clone())
     with pytest.raises(ValueError, match="device tensors"):
         moe.moe_route(torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))
+    q = moe.MXFP8(torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(16, dtype=torch.uint8), 0)
+    w13 = moe.MXFP8(torch.zeros(256, 128, dtype=torch.uint8), torch.zeros(1024, dtype=torch.uint8))
+    w2 = moe.MXFP8(torch.zeros(128, 128, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8))
+    args = (torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, 1), w13, w2, torch.zeros(4, 128, dtype=torch.bfloat16))
+    ws = torch.zeros(moe.moe_workspace_bytes(4, 1, 1, 128, 128), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="device tensors"):
+        moe.moe_experts_mxfp8(q, *args, workspace=ws)
+    with pytest.raises(AssertionError, match="scales"):
+        moe.moe_experts_mxfp8(moe.MXFP8(q.data, q.sf[:8], 0), *args, workspace=ws)
     with pytest.raises(ValueError, match="sigmoid"):
         moe.moe_route(torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), scoring="tanh")
+
+
+def test_small_scale_buffers_are_refused(lib):
+    import torch
+
+    from mxfp8_activation_quant_gb300 import moe
+
+    x = torch.zeros(5, 256, dtype=torch.bfloat16)
+    q, g = torch.zeros(5, 256, dtype=torch.uint8), torch.ones(256, dtype=torch.bfloat16)
+    for name, n in (("sf_rowmajor", 40), ("sf_packed", 64), ("sf_128x4", 1024)):
+        with pytest.raises(AssertionError):
+            moe.add_rmsnorm_dual_out(x, x.clone(), g, 1e-6, x.clone(), None, q, **{name: torch.zeros(n - 4, dtype=torch.uint8)})
+        with pytest.raises(ValueError, match="device tensors"):
+            moe.add_rmsnorm_dual_out(x, x.clone(), g, 1e-6, x.clone(), None, q, **{name: torch.zeros(n, dtype=torch.uint8)})
 
 
 def test_interleave_gate_up():

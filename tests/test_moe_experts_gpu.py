@@ -214,6 +214,27 @@ def test_other_stream_and_graph(small):
         assert torch.equal(o2, want)
 
 
+def test_offsets_past_32_bits(mxq):
+    """70000 tokens in 8 places: 2.3e9 elements of copied rows and of GEMM 2's output. A token's result
+    does not depend on its batch, so a few tokens alone say what the large call has to give."""
+    T, k, H = 70000, 8, 4096
+    m = Model(mxq, 4, H, 128, seed=21)
+    x, _ = m.mx(torch.randn((512, H), generator=m.gen, device="cuda").to(torch.bfloat16), 0)
+    pick = torch.randint(0, 512, (T,), generator=m.gen, device="cuda")
+    big = mxq.MXFP8(x.data[pick].contiguous(), x.sf.view(512, -1)[pick].contiguous(), 0)
+    ids = torch.randint(0, 4, (T, k), generator=m.gen, device="cuda", dtype=torch.int32)
+    w = torch.rand((T, k), generator=m.gen, device="cuda")
+    out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    status = mxq.new_status()
+    mxq.moe_experts_mxfp8(big, ids, w, m.w13, m.w2, out, status=status)
+    mxq.check_status(status)
+    t = torch.cat([torch.arange(8), torch.randint(8, T - 8, (40,)), torch.arange(T - 8, T)]).cuda()
+    few = torch.empty((t.numel(), H), dtype=torch.bfloat16, device="cuda")
+    mxq.moe_experts_mxfp8(mxq.MXFP8(big.data[t].contiguous(), big.sf[t].contiguous(), 0), ids[t].contiguous(),
+                          w[t].contiguous(), m.w13, m.w2, few)
+    assert torch.equal(out[t], few)
+
+
 def test_exact_integers(mxq):
     """Small whole numbers: every product and sum is exact, so silu's argument is chosen large (silu(g)
     = g to fp32 for g >= 32) and the result is the exact one, rounded to bf16."""
