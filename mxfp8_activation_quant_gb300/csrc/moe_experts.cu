@@ -334,6 +334,7 @@ constexpr int BM = 128;        // weight rows per CTA
 constexpr int BK = 128;        // K bytes per stage
 constexpr int STAGES = 6;
 constexpr int kAccBlocks = 4;  // most 32-token blocks of a tile that one epilogue warp takes
+constexpr int kNextItems = 2;   // items of GEMM 2 whose weights a pair of GEMM 1 fetches into L2
 constexpr int kRowLoaders = 4;  // threads that load token rows (in place)
 constexpr int kSfKb = 4;      // k-blocks per scale chunk
 constexpr int kSfChunks = 3;  // scale chunks in flight
@@ -367,6 +368,7 @@ struct GemmMaps {
   CUtensorMap x[kBoxes];   // activations (in place: x[0], single rows)
   CUtensorMap sfx;         // a chunk of the tile's scale atoms
   CUtensorMap y32;         // down: bf16 output boxes of 128 features x 32 rows
+  CUtensorMap w_next;      // gate-up: the weights of GEMM 2
 };
 
 struct GemmArgs {
@@ -375,6 +377,10 @@ struct GemmArgs {
   int32_t kbs;       // 128-wide k-blocks
   int32_t rows;      // weight rows per expert
   const int32_t* row_token;  // gate-up in place
+  // gate-up: GEMM 2's items, k-blocks, weight rows per expert and SM pairs
+  const Item* next_items;
+  const int32_t* next_n;
+  int32_t next_kbs, next_rows, next_pairs;
   int32_t early;             // the plan is older than the kernel ahead
   // gate-up: E4M3 activations [pairs, rows / 2] and their scales by tile
   uint8_t* hq;
@@ -601,6 +607,18 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       }
     }
     *issued_cnt = it;
+    if (MODE != kDown && item.end <= item.stride && !*abort_flag && pair < p.next_pairs) {
+      // One round of items: with the last loads on their way HBM idles until GEMM 2 begins, so the weights
+      // of this pair's first items there are fetched into L2 (one token 38.8 -> 37.5 us; with more
+      // rounds other pairs are still loading, and nothing was gained).
+      const int n = *p.next_n;
+      for (int j = 0; j < kNextItems; ++j) {
+        const int at = pair + j * p.next_pairs;
+        if (at >= n) break;
+        const int row = p.next_items[at].expert * p.next_rows + p.next_items[at].block * (2 * BM) + BM * static_cast<int>(rank);
+        for (int kb = 0; kb < p.next_kbs; ++kb) tma_prefetch_2d(&maps.w_next, kb * BK, row);
+      }
+    }
     if (first && early) {  // no item: the grid still ends after GEMM 1
       pdl_wait_primary();
       pdl_launch_dependents();
@@ -991,7 +1009,8 @@ cudaError_t launch_dependent(K kern, dim3 grid, int threads, int smem, int clust
 
 template <int MODE>
 cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t act_ld, const void* act_sf, int64_t act_rows, int64_t K,
-                             int64_t max_tiles, int64_t most, int pairs, const GemmArgs& ga, cudaStream_t stream) {
+                             int64_t max_tiles, int64_t most, int pairs, const GemmArgs& ga, const mxq_mx_tensor* next,
+                             cudaStream_t stream) {
   using C = GemmCfg<MODE>;
   auto kern = experts_gemm_kernel<MODE>;
   static const cudaError_t attr_err =
@@ -1009,6 +1028,7 @@ cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t ac
       return cudaErrorInvalidValue;
   if (MODE == kDown && most >= 32 && !make_bf16_map(&maps.y32, ga.y, act_rows, ga.rows, ga.rows, 32))
     return cudaErrorInvalidValue;
+  if (next != nullptr && !make_map(&maps.w_next, next->data, next->rows, next->cols, next->ld, BM)) return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads<MODE>, C::SMEM_BYTES, 2, stream, maps, ga);
 }
 
@@ -1070,9 +1090,14 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   g1.hsf = ws + lay.hsf;
   g1.status = l.status;
   const int pairs1 = pairs_for(lay.blocks1);
-  e = copy ? launch_gemm_mode<kGateUp>(*l.w13, xp, l.H, pa.xsf, P, l.H, lay.max_tiles, P, pairs1, g1, stream)
+  g1.next_items = pa.items2;
+  g1.next_n = pa.n_items + 1;
+  g1.next_kbs = static_cast<int32_t>(l.I / BK);
+  g1.next_rows = static_cast<int32_t>(l.H);
+  g1.next_pairs = pairs_for(lay.blocks2);
+  e = copy ? launch_gemm_mode<kGateUp>(*l.w13, xp, l.H, pa.xsf, P, l.H, lay.max_tiles, P, pairs1, g1, l.w2, stream)
            : launch_gemm_mode<kGateUpInPlace>(*l.w13, l.x->data, l.x->ld, pa.xsf, l.T, l.H, lay.max_tiles, P, pairs1, g1,
-                                              stream);
+                                              l.w2, stream);
   if (e != cudaSuccess) return e;
 
   GemmArgs g2 = {};
@@ -1082,7 +1107,7 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   g2.rows = static_cast<int32_t>(l.H);
   g2.y = reinterpret_cast<uint16_t*>(ws + lay.y);
   g2.status = l.status;
-  e = launch_gemm_mode<kDown>(*l.w2, g1.hq, l.I, g1.hsf, P, l.I, lay.max_tiles, P, pairs_for(lay.blocks2), g2, stream);
+  e = launch_gemm_mode<kDown>(*l.w2, g1.hq, l.I, g1.hsf, P, l.I, lay.max_tiles, P, pairs_for(lay.blocks2), g2, nullptr, stream);
   if (e != cudaSuccess) return e;
 
   CombineArgs ca = {g2.y, l.weights, pa.pair_row, l.k, l.H, l.ldo, static_cast<uint16_t*>(l.out)};

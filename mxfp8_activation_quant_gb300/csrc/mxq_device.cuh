@@ -185,6 +185,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// A tensor map's box into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void* desc, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(desc), "r"(x), "r"(y) : "memory");
+}
+
 // ------------------------------------------------------------------------------------------
 // tcgen05 (5th-generation tensor cores, tensor memory)
 // ------------------------------------------------------------------------------------------
