@@ -299,14 +299,19 @@ cudaError_t launch_nt(const AddRmsArgs& a, cudaStream_t stream) {
 // Threads per row. Few rows: a row is one block's latency, so 320 threads (1 x 5120 5.2 us, against 5.6
 // with 256 and 6.5 with 160; 333 x 7168 in fp32 9.5 against 9.9 and 10.3). Many rows: more, smaller
 // blocks hide one another's reductions (8192 x 5120 60.5 us with 160 threads in 8 blocks per SM,
-// against 64.5 with 256 and 66.1 with 320), as few as hold the row.
+// against 64.5 with 256 and 66.1 with 320), the fewest with at most four chunks a thread (4000 x 8096
+// 52 us with 256 and 66 us with 160, whose eight chunks cost it its residency).
 constexpr int64_t kFewRows = 512;
 constexpr int64_t kFarBytes = int64_t(96) << 20;  // three quarters of L2
 
 template <bool F32>
 cudaError_t launch_type(const AddRmsArgs& a, cudaStream_t stream) {
-  if (a.rows_total <= kFewRows || a.H > 8 * 8 * 160) return launch_nt<F32, 320>(a, stream);
-  return a.H <= 2 * 8 * 64 ? launch_nt<F32, 64>(a, stream) : launch_nt<F32, 160>(a, stream);
+  const int64_t chunks = a.H / 8;
+  if (a.rows_total <= kFewRows || chunks > 4 * 512) return launch_nt<F32, 320>(a, stream);
+  if (chunks <= 2 * 64) return launch_nt<F32, 64>(a, stream);
+  if (chunks <= 4 * 160) return launch_nt<F32, 160>(a, stream);
+  if (chunks <= 4 * 256) return launch_nt<F32, 256>(a, stream);
+  return chunks <= 4 * 320 ? launch_nt<F32, 320>(a, stream) : launch_nt<F32, 512>(a, stream);
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -12,7 +12,7 @@
 // in fp32 with a known error bound, and values nearer than the bound are compared in fp64: for
 // sigmoid scores only the groups or picks in question, one value per lane (an fp64 exponential
 // takes a warp about 0.7 us; the whole row's, which one row in 10^4 took at first, added 10 us to a
-// launch), for softmax scores the whole row. Three rows in a thousand have such picks at 256 experts
+// launch), for softmax scores the sum as well. Three rows in a thousand have such picks at 256 experts
 // with logits of deviation 1.6.
 //
 // 16384 tokens, 256 experts, 8 of 4 of 8 groups: 57 us with one expert per 32 in a lane and groups
@@ -78,26 +78,37 @@ __device__ __forceinline__ float score32(float l, bool softmax, float m, float i
 constexpr float kSigmoidErr = 6.0e-7f;
 constexpr float kSoftmaxErr = 3.9e-6f;
 
+// The largest logit and the sum of the softmax in fp64, of one row by its warp.
+template <bool BF16>
+__device__ __noinline__ double2 softmax_f64(const RouteArgs& a, int64_t row, int lane) {
+  double m = -CUDART_INF, sum = 0.0;
+  for (int e = lane; e < a.E; e += 32) {
+    const float l = load_logit<BF16>(a, row, e);
+    if (l > -CUDART_INF_F) m = fmax(m, static_cast<double>(l));
+  }
+  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int e = lane; e < a.E; e += 32) {
+    const float l = load_logit<BF16>(a, row, e);
+    if (l > -CUDART_INF_F) sum += exp(static_cast<double>(l) - m);
+  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return make_double2(m, sum);
+}
+// An expert's choice in fp64; `soft` from softmax_f64 where that is the score.
+template <bool BF16>
+__device__ __forceinline__ double choice_f64(const RouteArgs& a, int64_t row, int e, double2 soft) {
+  const double l = load_logit<BF16>(a, row, e);
+  const double s = a.softmax ? exp(l - soft.x) / soft.y : 1.0 / (1.0 + exp(-l));
+  return a.bias != nullptr ? s + static_cast<double>(a.bias[e]) : s;
+}
+
 // One row decided in fp64. `d` holds E doubles per warp. Returns this lane's pick (lane r: slot r).
 template <int VPL, bool BF16>
 __device__ __noinline__ int route_row_f64(const RouteArgs& a, int64_t row, double* d, int lane) {
-  double m = -CUDART_INF, sum = 0.0;
-  if (a.softmax) {
-    for (int e = lane; e < a.E; e += 32) {
-      const float l = load_logit<BF16>(a, row, e);
-      if (l > -CUDART_INF_F) m = fmax(m, static_cast<double>(l));
-    }
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int e = lane; e < a.E; e += 32) {
-      const float l = load_logit<BF16>(a, row, e);
-      if (l > -CUDART_INF_F) sum += exp(static_cast<double>(l) - m);
-    }
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
+  const double2 soft = a.softmax ? softmax_f64<BF16>(a, row, lane) : make_double2(0.0, 0.0);
   for (int e = lane; e < a.E; e += 32) {
     const double l = load_logit<BF16>(a, row, e);
-    double c = a.softmax ? exp(l - m) / sum : 1.0 / (1.0 + exp(-l));
-    if (a.bias != nullptr) c += static_cast<double>(a.bias[e]);
+    double c = choice_f64<BF16>(a, row, e, soft);
     if (!(l > -CUDART_INF) || !(c > -CUDART_INF)) c = -CUDART_INF;
     d[e] = c;
   }
@@ -260,6 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   }
 
   bool whole = false;  // decide the whole row in fp64
+  double2 soft = make_double2(0.0, 0.0);  // softmax_f64, once it has been wanted
   if (a.groups > 1) {
     float v = -CUDART_INF_F, least = -CUDART_INF_F;  // value of this lane's group, and its last term
     int g, kept_lanes = a.group_lanes;
@@ -336,15 +348,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
           n += __popc(who);
         }
         __syncwarp();
-        if (a.softmax || n > 32) {
-          whole = true;  // the sum too is wanted in fp64, or too many experts are in question
+        if (n > 32) {
+          whole = true;  // too many experts are in question
         } else {
+          if (a.softmax) soft = softmax_f64<BF16>(a, row, lane);
           const int e = lane < n ? list[lane] : -1, eg = e >= 0 ? e / a.gsize : -1;
           double d = -CUDART_INF;
-          if (e >= 0) {
-            d = 1.0 / (1.0 + exp(-static_cast<double>(load_logit<BF16>(a, row, e))));
-            if (a.bias != nullptr) d += static_cast<double>(a.bias[e]);
-          }
+          if (e >= 0) d = choice_f64<BF16>(a, row, e, soft);
           double b0 = -CUDART_INF, b1 = -CUDART_INF;
           bool first = e >= 0;  // the lane that speaks for its group
           for (int r = 0; r < n; ++r) {
@@ -428,26 +438,21 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     }
   }
   if (near && !whole) {
-    if (a.softmax) {
-      whole = true;  // the sum too is wanted in fp64
-    } else {
-      // Everything outside the list is certainly below all of it: its order in fp64, a lane each.
-      double d = -CUDART_INF;
-      if (mine >= 0)
-        d = 1.0 / (1.0 + exp(-static_cast<double>(load_logit<BF16>(a, row, mine)))) + static_cast<double>(a.bias[mine]);
-      int rank = 0;
-      for (int r = 0; r < picks; ++r) {
-        const double u = __shfl_sync(0xffffffffu, d, r);
-        const int e = __shfl_sync(0xffffffffu, mine, r);
-        rank += (u > d || (u == d && e < mine)) ? 1 : 0;
-      }
-      int ordered = -1;
-      for (int r = 0; r < picks; ++r) {
-        const int e = __shfl_sync(0xffffffffu, mine, r), at = __shfl_sync(0xffffffffu, rank, r);
-        if (at == lane) ordered = e;
-      }
-      mine = ordered;
+    // Everything outside the list is certainly below all of it: its order in fp64, a lane each.
+    if (a.softmax && soft.y == 0.0) soft = softmax_f64<BF16>(a, row, lane);
+    const double d = mine >= 0 ? choice_f64<BF16>(a, row, mine, soft) : -CUDART_INF;
+    int rank = 0;
+    for (int r = 0; r < picks; ++r) {
+      const double u = __shfl_sync(0xffffffffu, d, r);
+      const int e = __shfl_sync(0xffffffffu, mine, r);
+      rank += (u > d || (u == d && e < mine)) ? 1 : 0;
     }
+    int ordered = -1;
+    for (int r = 0; r < picks; ++r) {
+      const int e = __shfl_sync(0xffffffffu, mine, r), at = __shfl_sync(0xffffffffu, rank, r);
+      if (at == lane) ordered = e;
+    }
+    mine = ordered;
   }
   if (whole) {
     __syncwarp();  // the float scratch is read no more
