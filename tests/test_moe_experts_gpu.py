@@ -214,6 +214,34 @@ def test_other_stream_and_graph(small):
         assert torch.equal(o2, want)
 
 
+def test_completes_while_other_work_holds_sms(small):
+    """With most SMs held by another stream the call's blocks run in turns: no block waits for one that
+    has not started, so it completes, with the same bytes."""
+    import time
+
+    T, k = 300, 4
+    x, xv = small.x(T)
+    ids, w = small.route(T, k)
+    want = small.check(x, xv, ids, w)
+    out, status = torch.zeros_like(want), small.mxq.new_status()
+    ws = torch.empty(small.mxq.moe_workspace_bytes(T, k, small.E, small.H, small.I), dtype=torch.uint8, device="cuda")
+    s_hold, s_call = torch.cuda.Stream(), torch.cuda.Stream()
+    e_hold, e_call = torch.cuda.Event(), torch.cuda.Event()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    torch.cuda.synchronize()
+    small.mxq.selftest_hold_sms(sms // 2 - 12, 600_000, stream=s_hold)
+    e_hold.record(s_hold)
+    time.sleep(0.05)  # the holding kernel takes its SMs first
+    small.mxq.moe_experts_mxfp8(x, ids, w, small.w13, small.w2, out, status=status, stream=s_call, workspace=ws)
+    e_call.record(s_call)
+    e_call.synchronize()
+    held_still = not e_hold.query()
+    torch.cuda.synchronize()
+    small.mxq.check_status(status)
+    assert held_still, "the call did not run beside the holding kernel"
+    assert torch.equal(out, want)
+
+
 def test_offsets_past_32_bits(mxq):
     """70000 tokens in 8 places: 2.3e9 elements of copied rows and of GEMM 2's output. A token's result
     does not depend on its batch, so a few tokens alone say what the large call has to give."""
