@@ -214,6 +214,25 @@ def test_other_stream_and_graph(small):
         assert torch.equal(o2, want)
 
 
+def test_two_streams_at_once(small):
+    """Calls that overlap on two streams, each with a workspace of its own."""
+    calls = []
+    for T, k in ((700, 4), (33, 2)):
+        x, xv = small.x(T)
+        ids, w = small.route(T, k)
+        want = small.check(x, xv, ids, w)
+        ws = torch.empty(small.mxq.moe_workspace_bytes(T, k, small.E, small.H, small.I), dtype=torch.uint8, device="cuda")
+        calls.append((x, ids, w, want, torch.zeros_like(want), ws, small.mxq.new_status(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, ids, w, _, out, ws, status, stream in calls:
+            small.mxq.moe_experts_mxfp8(x, ids, w, small.w13, small.w2, out, status=status, stream=stream, workspace=ws)
+    torch.cuda.synchronize()
+    for *_, want, out, ws, status, stream in calls:
+        small.mxq.check_status(status)
+        assert torch.equal(out, want)
+
+
 def test_completes_while_other_work_holds_sms(small):
     """With most SMs held by another stream the call's blocks run in turns: no block waits for one that
     has not started, so it completes, with the same bytes."""
