@@ -52,8 +52,8 @@ struct __align__(128) ExpertRows {
 
 // Whether the token rows are copied in expert order before GEMM 1. Its loads of four rows at a time
 // keep up with the MMAs of small tiles only: at 97 tokens per expert (777 tokens, 64 experts, top 8,
-// 5120 -> 2 x 1024) reading x in place takes the call from 225 to 216 us, at 512 per expert GEMM 1
-// takes 288 us in place and 231 us from copies that cost 26 us.
+// 5120 -> 2 x 1024) reading x in place takes the call from 225 to 216 us, at 160 there is no difference,
+// and at 512 GEMM 1 takes 288 us in place and 231 us from copies that cost 26 us.
 inline bool copies_rows(int64_t P, int32_t E) { return P > static_cast<int64_t>(160) * E; }
 
 struct Layout {  // byte offsets into the workspace
@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 }
 
 // ------------------------------------------------------------------------------------------
-// rows: a warp per token, or a block where its activations are copied. Lane j places the token's pair j (one atomic on its expert's counter);
+// rows: a warp per token, or a block where its activations are copied. Lane j places the token's
+// pair j (one atomic on its expert's counter);
 // the token's scale words, and its activations if they are copied, are read once and written to
 // each of its places.
 // ------------------------------------------------------------------------------------------
@@ -1016,7 +1017,8 @@ cudaError_t launch_dependent(K kern, dim3 grid, int threads, int smem, int clust
 }
 
 template <int MODE>
-cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t act_ld, const void* act_sf, int64_t act_rows, int64_t K,
+cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t act_ld, const void* act_sf,
+                             int64_t act_rows, int64_t K,
                              int64_t max_tiles, int64_t most, int pairs, const GemmArgs& ga, const mxq_mx_tensor* next,
                              cudaStream_t stream) {
   using C = GemmCfg<MODE>;
@@ -1036,7 +1038,8 @@ cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t ac
       return cudaErrorInvalidValue;
   if (MODE == kDown && most >= 32 && !make_bf16_map(&maps.y32, ga.y, act_rows, ga.rows, ga.rows, 32))
     return cudaErrorInvalidValue;
-  if (next != nullptr && !make_map(&maps.w_next, next->data, next->rows, next->cols, next->ld, BM)) return cudaErrorInvalidValue;
+  if (next != nullptr && !make_map(&maps.w_next, next->data, next->rows, next->cols, next->ld, BM))
+    return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads<MODE>, C::SMEM_BYTES, 2, stream, maps, ga);
 }
 
