@@ -84,7 +84,7 @@ MXQ_API mxq_status moe_route(const void* logits, int32_t logits_type, int64_t ld
  * moe_experts_mxfp8 -- the experts' products:
  *   (g, u)    = W13_e x_t                       fp32 accumulation, e = ids[t, j]
  *   a         = MXFP8( RNE_bf16( silu(g) * u ) )  the rule of mxfp8_quantize
- *   out[t]    = RNE_bf16( sum_j weights[t, j] * RNE_bf16( W2_e a ) )   fp32 sum, j ascending
+ *   out[t]    = RNE_bf16( sum_j weights[t, j] * (W2_e a) )        fp32 throughout, j ascending
  * An id outside [0, E) takes no part; a token without any gives zeros. The same id may appear
  * more than once in a row.
  *

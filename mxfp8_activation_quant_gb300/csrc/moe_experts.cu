@@ -4,7 +4,7 @@
 //            many tokens per expert its activations too (all within plan for few pairs)
 //   GEMM 1   (g, u) = W13_e x, a = MXFP8(bf16(silu(g) u)) in the epilogue; a tile's token rows come
 //            from the copies, or with few tokens per expert straight from x, four rows per load
-//   GEMM 2   y = W2_e a, bf16 per pair
+//   GEMM 2   y = W2_e a, fp32 per pair: y is a part of the sum over a token's experts
 //   combine  out[t] = bf16(sum_j w[t, j] y[pair(t, j)]), fp32 sum in slot order
 //
 // Both GEMMs are one kernel template on CTA pairs (tcgen05 cta_group::2, kind::mxf8f6f4 block
@@ -80,7 +80,7 @@ struct Layout {  // byte offsets into the workspace
     xsf = take(max_tiles * kSlotRows * (H / 32));
     hq = take(P * I);
     hsf = take(max_tiles * kSlotRows * (I / 32));
-    y = take(P * H * 2);
+    y = take(P * H * 4);
     total = o;
   }
 };
@@ -348,11 +348,8 @@ struct GemmCfg {
   static constexpr int SFA_BYTES = 512 * kSfKb, SFB_BYTES = 1024 * kSfKb;
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
-  // epilogue staging, one row per token: 64 bf16 features of every token of the tile (gate-up), or
-  // 128 features of 64 tokens, two buffers in turn (down)
-  static constexpr int ROW_BYTES = MODE == kDown ? 256 : 128;
-  static constexpr int PASS_TOKENS = MODE == kDown ? 64 : kTileTokens;
-  static constexpr int EPI_BYTES = PASS_TOKENS * ROW_BYTES * (MODE == kDown ? 2 : 1);
+  // epilogue staging (gate-up): one row per token, 64 bf16 features of every token of the tile
+  static constexpr int EPI_BYTES = MODE == kDown ? 0 : kTileTokens * 128;
   static constexpr int OFF_EPI = OFF_SF + kSfChunks * (SFA_BYTES + SFB_BYTES);
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2 * kSfChunks + 5) * 8;
@@ -368,7 +365,6 @@ struct GemmMaps {
   CUtensorMap w, sfw;      // weights (128 rows) and their scale atoms
   CUtensorMap x[kBoxes];   // activations (in place: x[0], single rows)
   CUtensorMap sfx;         // a chunk of the tile's scale atoms
-  CUtensorMap y32;         // down: bf16 output boxes of 128 features x 32 rows
   CUtensorMap w_next;      // gate-up: the weights of GEMM 2
 };
 
@@ -386,8 +382,8 @@ struct GemmArgs {
   // gate-up: E4M3 activations [pairs, rows / 2] and their scales by tile
   uint8_t* hq;
   uint8_t* hsf;
-  // down: bf16 [pairs, rows]
-  uint16_t* y;
+  // down: fp32 [pairs, rows]
+  float* y;
   int32_t* status;
 };
 
@@ -767,14 +763,15 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     }
   } else if (warp >= 2 && warp < 10) {
     // ---------------- epilogue (both CTAs) ----------------
-    // TMEM lane = weight row, column = token. The warps turn the tile through shared memory (one
-    // row per token) so that a token's features leave in whole sectors. Warp q = warp % 4 owns
-    // TMEM lanes 32 q .. 32 q + 31; of the tile's 16-token chunks, warps 2..5 take the even ones
-    // and 6..9 the odd ones. Every warp runs every item's barriers, also after an abort.
+    // TMEM lane = weight row, column = token. Warp q = warp % 4 owns TMEM lanes 32 q .. 32 q + 31; of
+    // the tile's 32-token blocks, warps 2..5 take the even ones and 6..9 the odd ones. Gate-up: the
+    // warps turn the tile through shared memory (one row per token) for the groups' scales, and so that a
+    // token's features leave in whole sectors; every warp runs every item's barriers, also after an abort.
+    // Down: a warp's 32 features of a token are 128 bytes of fp32, one store.
     const int q = warp & 3, odd = (warp - 2) >> 2, et = static_cast<int>(threadIdx.x) - 64;
     const uint32_t acce0 = mapa_shared(bar_acce, 0);
     const uint32_t stage = sbase + C::OFF_EPI;
-    int ti = 0, pass = 0;
+    int ti = 0;
     for (; item.more(); item.next(), ++ti) {
       const int b = ti & 1, n = item.n();
       bool ok = !*abort_flag;
@@ -858,11 +855,6 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
         }
         named_barrier(1, 256);
       } else {
-        // 64 tokens a pass: a warp turns 32 lanes (features) x 32 columns (tokens) into the staging
-        // rows, which leave by TMA in boxes of 32 rows, the last rows through the load/store unit.
-        // (256-byte copies of every row took 1000 cycles a pass, the load/store unit alone as long.)
-        // A buffer is written again two passes later; its rows have been read out before the
-        // barrier between.
         uint32_t acc[kAccBlocks][32];
         if (ok) {
           tc_fence_after();
@@ -873,39 +865,20 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
           release();
         }
         const int f0 = item.block * (2 * BM) + static_cast<int>(rank) * BM;
-        const bool live = f0 < p.rows;  // the last block of an odd number of 128-row tiles has one half
+        // (the last block of an odd number of 128-row tiles has one half)
+        if (ok && f0 < p.rows) {
+          float* dst = p.y + static_cast<int64_t>(item.row0()) * p.rows + f0 + 32 * q + lane;
 #pragma unroll
-        for (int i = 0; i < kAccBlocks; ++i) {
-          const int t0 = C::PASS_TOKENS * i;
-          if (t0 >= n) break;
-          const int tn = n - t0 < C::PASS_TOKENS ? n - t0 : C::PASS_TOKENS;
-          const uint32_t buf = stage + static_cast<uint32_t>(pass) * (C::PASS_TOKENS * C::ROW_BYTES);
-          if (ok && 32 * odd < tn) {
-            const uint32_t at = buf + 32 * odd * 256 + (32 * q + lane) * 2;
+          for (int i = 0; i < kAccBlocks; ++i) {
+            const int t0 = 64 * i + 32 * odd;
+            if (t0 >= n) break;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const uint32_t w = bf16x2_rn(__uint_as_float(acc[i][2 * c]), __uint_as_float(acc[i][2 * c + 1]));
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 512 * c), "h"(static_cast<uint16_t>(w)) : "memory");
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 512 * c + 256), "h"(static_cast<uint16_t>(w >> 16))
-                           : "memory");
-            }
-            fence_proxy_async_smem();
+            for (int c = 0; c < 32; ++c)
+              if (t0 + c < n) dst[static_cast<int64_t>(t0 + c) * p.rows] = __uint_as_float(acc[i][c]);
           }
-          if (et < 32) bulk_wait_read();  // this thread's copies out of the other buffer
-          named_barrier(1, 256);
-          if (ok && live) {
-            const int n32 = tn >> 5;
-            if (et < n32) tma_store_2d(&maps.y32, buf + et * 32 * 256, f0, item.row0() + t0 + 32 * et);
-            if (et < 32) bulk_commit();
-            for (int j = 512 * n32 + et; j < 16 * tn; j += 256)
-              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(item.row0() + t0 + (j >> 4)) * p.rows + f0 + 8 * (j & 15)) =
-                  ld_smem_v4(buf + 16 * j);
-          }
-          pass ^= 1;
         }
       }
     }
-    if (MODE == kDown) bulk_wait_all();  // the copies have left shared memory and are written
   }
   __syncwarp();
 
@@ -941,17 +914,17 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
 }
 
 // ------------------------------------------------------------------------------------------
-// combine: out[t] = bf16(sum_j w[t, j] y[row(t, j)]), 8 columns per thread
+// combine: out[t] = bf16(sum_j w[t, j] y[row(t, j)]), 4 columns per thread
 // ------------------------------------------------------------------------------------------
 struct CombineArgs {
-  const uint16_t* y;
+  const float* y;
   const float* weights;
   const int32_t* pair_row;
   int32_t k;
   int64_t H, ldo;
   uint16_t* out;
 };
-constexpr int kCombineThreads = 128;
+constexpr int kCombineThreads = 256;
 
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a) {
   // (the rows and weights are known before GEMM 2 ends: see there)
@@ -964,9 +937,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
   }
   __syncthreads();
   pdl_wait_primary();
-  const int64_t c = 8 * (static_cast<int64_t>(blockIdx.y) * kCombineThreads + threadIdx.x);
+  const int64_t c = 4 * (static_cast<int64_t>(blockIdx.y) * kCombineThreads + threadIdx.x);
   if (c >= a.H) return;
-  float s[8] = {};
+  float s[4] = {};
   for (int j0 = 0; j0 < a.k; j0 += 4) {  // four rows in flight
     uint4 v[4];
 #pragma unroll
@@ -978,16 +951,13 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
     for (int j = 0; j < 4; ++j) {
       if (j0 + j >= a.k || rows[j0 + j] < 0) continue;  // (the weight of an empty slot may be anything)
       const float w = ws[j0 + j];
-      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[2 * i] = fmaf(w, bf16_lo(u[i]), s[2 * i]);
-        s[2 * i + 1] = fmaf(w, bf16_hi(u[i]), s[2 * i + 1]);
-      }
+      s[0] = fmaf(w, __uint_as_float(v[j].x), s[0]);
+      s[1] = fmaf(w, __uint_as_float(v[j].y), s[1]);
+      s[2] = fmaf(w, __uint_as_float(v[j].z), s[2]);
+      s[3] = fmaf(w, __uint_as_float(v[j].w), s[3]);
     }
   }
-  *reinterpret_cast<uint4*>(a.out + t * a.ldo + c) =
-      make_uint4(bf16x2_rn(s[0], s[1]), bf16x2_rn(s[2], s[3]), bf16x2_rn(s[4], s[5]), bf16x2_rn(s[6], s[7]));
+  *reinterpret_cast<uint2*>(a.out + t * a.ldo + c) = make_uint2(bf16x2_rn(s[0], s[1]), bf16x2_rn(s[2], s[3]));
 }
 
 // ------------------------------------------------------------------------------------------
@@ -1036,8 +1006,6 @@ cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t ac
     if (MODE == kGateUpInPlace ? i == 0 && !make_map(&maps.x[i], act, act_rows, K, act_ld, 1)
                                : half > 32 * i - 24 && !make_map(&maps.x[i], act, act_rows, K, act_ld, 32 * i + 8))
       return cudaErrorInvalidValue;
-  if (MODE == kDown && most >= 32 && !make_bf16_map(&maps.y32, ga.y, act_rows, ga.rows, ga.rows, 32))
-    return cudaErrorInvalidValue;
   if (next != nullptr && !make_map(&maps.w_next, next->data, next->rows, next->cols, next->ld, BM))
     return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads<MODE>, C::SMEM_BYTES, 2, stream, maps, ga);
@@ -1116,14 +1084,14 @@ cudaError_t launch_experts(const ExpertsLaunch& l, cudaStream_t stream) {
   g2.n_items = pa.n_items + 1;
   g2.kbs = static_cast<int32_t>(l.I / BK);
   g2.rows = static_cast<int32_t>(l.H);
-  g2.y = reinterpret_cast<uint16_t*>(ws + lay.y);
+  g2.y = reinterpret_cast<float*>(ws + lay.y);
   g2.status = l.status;
   e = launch_gemm_mode<kDown>(*l.w2, g1.hq, l.I, g1.hsf, P, l.I, lay.max_tiles, P, pairs_for(lay.blocks2), g2, nullptr, stream);
   if (e != cudaSuccess) return e;
 
   CombineArgs ca = {g2.y, l.weights, pa.pair_row, l.k, l.H, l.ldo, static_cast<uint16_t*>(l.out)};
   return launch_dependent(combine_kernel,
-                          dim3(static_cast<unsigned>(l.T), static_cast<unsigned>(ceil_div(l.H, 8 * kCombineThreads)), 1),
+                          dim3(static_cast<unsigned>(l.T), static_cast<unsigned>(ceil_div(l.H, 4 * kCombineThreads)), 1),
                           kCombineThreads, 0, 1, stream, ca);
 }
 
