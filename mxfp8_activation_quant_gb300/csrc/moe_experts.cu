@@ -335,6 +335,7 @@ constexpr int BM = 128;        // weight rows per CTA
 constexpr int BK = 128;        // K bytes per stage
 constexpr int STAGES = 6;
 constexpr int kAccBlocks = 4;  // most 32-token blocks of a tile that one epilogue warp takes
+constexpr int kPassTokens = 16;  // token rows of a staging buffer of GEMM 2
 constexpr int kNextItems = 2;   // items of GEMM 2 whose weights a pair of GEMM 1 fetches into L2
 constexpr int kRowLoaders = 4;  // threads that load token rows (in place)
 constexpr int kSfKb = 4;      // k-blocks per scale chunk
@@ -348,8 +349,9 @@ struct GemmCfg {
   static constexpr int SFA_BYTES = 512 * kSfKb, SFB_BYTES = 1024 * kSfKb;
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
-  // epilogue staging (gate-up): one row per token, 64 bf16 features of every token of the tile
-  static constexpr int EPI_BYTES = MODE == kDown ? 0 : kTileTokens * 128;
+  // epilogue staging, one row per token: 64 bf16 features of every token of the tile (gate-up), or 128
+  // fp32 features of kPassTokens tokens, two buffers in turn for each half of the warps (down)
+  static constexpr int EPI_BYTES = MODE == kDown ? 4 * kPassTokens * 512 : kTileTokens * 128;
   static constexpr int OFF_EPI = OFF_SF + kSfChunks * (SFA_BYTES + SFB_BYTES);
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2 * kSfChunks + 5) * 8;
@@ -365,6 +367,7 @@ struct GemmMaps {
   CUtensorMap w, sfw;      // weights (128 rows) and their scale atoms
   CUtensorMap x[kBoxes];   // activations (in place: x[0], single rows)
   CUtensorMap sfx;         // a chunk of the tile's scale atoms
+  CUtensorMap y16;         // down: fp32 output boxes of 128 features x kPassTokens rows
   CUtensorMap w_next;      // gate-up: the weights of GEMM 2
 };
 
@@ -763,15 +766,14 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     }
   } else if (warp >= 2 && warp < 10) {
     // ---------------- epilogue (both CTAs) ----------------
-    // TMEM lane = weight row, column = token. Warp q = warp % 4 owns TMEM lanes 32 q .. 32 q + 31; of
-    // the tile's 32-token blocks, warps 2..5 take the even ones and 6..9 the odd ones. Gate-up: the
-    // warps turn the tile through shared memory (one row per token) for the groups' scales, and so that a
-    // token's features leave in whole sectors; every warp runs every item's barriers, also after an abort.
-    // Down: a warp's 32 features of a token are 128 bytes of fp32, one store.
+    // TMEM lane = weight row, column = token. The warps turn the tile through shared memory (one
+    // row per token). Warp q = warp % 4 owns TMEM lanes 32 q .. 32 q + 31; of the tile's 32-token
+    // blocks, warps 2..5 take the even ones and 6..9 the odd ones. Every warp runs every item's
+    // barriers, also after an abort.
     const int q = warp & 3, odd = (warp - 2) >> 2, et = static_cast<int>(threadIdx.x) - 64;
     const uint32_t acce0 = mapa_shared(bar_acce, 0);
     const uint32_t stage = sbase + C::OFF_EPI;
-    int ti = 0;
+    int ti = 0, pass = 0;
     for (; item.more(); item.next(), ++ti) {
       const int b = ti & 1, n = item.n();
       bool ok = !*abort_flag;
@@ -865,20 +867,42 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
           release();
         }
         const int f0 = item.block * (2 * BM) + static_cast<int>(rank) * BM;
-        // (the last block of an odd number of 128-row tiles has one half)
-        if (ok && f0 < p.rows) {
-          float* dst = p.y + static_cast<int64_t>(item.row0()) * p.rows + f0 + 32 * q + lane;
+        const bool live = ok && f0 < p.rows;  // the last block of an odd number of 128-row tiles has one half
+        const bool issuer = (et & 127) == 0;
+        const uint32_t group = stage + static_cast<uint32_t>(odd) * (2 * kPassTokens * 512);
+        // A half of the warps passes kPassTokens tokens at a time through its two buffers, which leave by
+        // TMA; the last tokens of a tile go from the registers, 128 bytes of a token a store. A buffer is
+        // written again two passes later; its rows have been read out before the barrier between. (4096
+        // tokens: GEMM 2 179 us, and 204 us with all rows from the registers.)
 #pragma unroll
-          for (int i = 0; i < kAccBlocks; ++i) {
-            const int t0 = 64 * i + 32 * odd;
-            if (t0 >= n) break;
+        for (int i = 0; i < 2 * kAccBlocks; ++i) {
+          const int t0 = 64 * (i >> 1) + 32 * odd + kPassTokens * (i & 1), tn = n - t0;
+          const uint32_t* v = acc[i >> 1] + kPassTokens * (i & 1);
+          if (tn >= kPassTokens) {
+            const uint32_t buf = group + static_cast<uint32_t>(pass) * (kPassTokens * 512);
+            if (live) {
+              const uint32_t at = buf + (32 * q + lane) * 4;
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (t0 + c < n) dst[static_cast<int64_t>(t0 + c) * p.rows] = __uint_as_float(acc[i][c]);
+              for (int c = 0; c < kPassTokens; ++c) st_smem_u32(at + 512 * c, v[c]);
+              fence_proxy_async_smem();
+            }
+            if (issuer) bulk_wait_read();  // this thread's copy out of the other buffer
+            named_barrier(1 + odd, 128);
+            if (issuer && live) {
+              tma_store_2d(&maps.y16, buf, f0, item.row0() + t0);
+              bulk_commit();
+            }
+            pass ^= 1;
+          } else if (tn > 0 && live) {
+            float* dst = p.y + static_cast<int64_t>(item.row0() + t0) * p.rows + f0 + 32 * q + lane;
+#pragma unroll
+            for (int c = 0; c < kPassTokens; ++c)
+              if (c < tn) dst[static_cast<int64_t>(c) * p.rows] = __uint_as_float(v[c]);
           }
         }
       }
     }
+    if (MODE == kDown) bulk_wait_all();  // the copies have left shared memory and are written
   }
   __syncwarp();
 
@@ -1006,6 +1030,8 @@ cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t ac
     if (MODE == kGateUpInPlace ? i == 0 && !make_map(&maps.x[i], act, act_rows, K, act_ld, 1)
                                : half > 32 * i - 24 && !make_map(&maps.x[i], act, act_rows, K, act_ld, 32 * i + 8))
       return cudaErrorInvalidValue;
+  if (MODE == kDown && most >= kPassTokens && !make_f32_map(&maps.y16, ga.y, act_rows, ga.rows, ga.rows, kPassTokens))
+    return cudaErrorInvalidValue;
   if (next != nullptr && !make_map(&maps.w_next, next->data, next->rows, next->cols, next->ld, BM))
     return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1), kThreads<MODE>, C::SMEM_BYTES, 2, stream, maps, ga);

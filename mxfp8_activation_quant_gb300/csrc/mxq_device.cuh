@@ -401,6 +401,16 @@ __device__ __forceinline__ void bulk_s2s(uint32_t remote_dst, uint32_t src, uint
                "r"(src), "r"(bytes), "r"(remote_bar)
                : "memory");
 }
+// A box of a tensor map from shared to global memory in this thread's bulk group; wait_read: the group's
+// sources may be overwritten, wait_all: the copies are complete.
+__device__ __forceinline__ void tma_store_2d(const void* desc, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(desc), "r"(src),
+               "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Orders this thread's generic-proxy shared-memory writes before later async-proxy reads
 // (bulk copies) of them.
 __device__ __forceinline__ void fence_proxy_async_smem() {
