@@ -22,6 +22,7 @@
 
 #include "mxq_device.cuh"
 #include "mxq_moe_internal.h"
+#include "mxq_settle.h"
 #include "mxq_tma.h"
 
 namespace mxq {
@@ -355,7 +356,8 @@ struct GemmCfg {
   static constexpr int OFF_EPI = OFF_SF + kSfChunks * (SFA_BYTES + SFB_BYTES);
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2 * kSfChunks + 5) * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
+  static constexpr int LOADERS = MODE == kGateUpInPlace ? kRowLoaders : 1;  // threads that load operands
   static constexpr int TMEM_SF = 2 * kTileTokens;  // first scale column
   static_assert(B_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(TMEM_SF + STAGES * SF_COLS <= 512, "TMEM");
@@ -363,6 +365,8 @@ struct GemmCfg {
 };
 
 constexpr int kBoxes = 4;  // token-row boxes of the operand loads: 8, 40, 72 or 104 rows, one load
+__device__ __forceinline__ int token_box(int half) { return (half + 23) >> 5; }  // the least of at least `half` rows
+__device__ __forceinline__ int token_box_rows(int half) { return 32 * token_box(half) + 8; }
 struct GemmMaps {
   CUtensorMap w, sfw;      // weights (128 rows) and their scale atoms
   CUtensorMap x[kBoxes];   // activations (in place: x[0], single rows)
@@ -486,10 +490,12 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   const uint32_t bar_drain = bar_acce + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  int* issued_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
-  int* consumed_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 12);
-  int* sf_issued_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);
-  int* sf_consumed_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 20);
+  // stages (chunks) that each thread has dealt with when it stops
+  int* issued_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // [kRowLoaders]
+  int* consumed_cnt = issued_cnt + kRowLoaders;
+  int* staged_cnt = consumed_cnt + 1;
+  int* sf_issued_cnt = consumed_cnt + 2;
+  int* sf_consumed_cnt = consumed_cnt + 3;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const bool elected = elect_one();
@@ -517,10 +523,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     }
     mbar_init(bar_drain, 2);  // the MMA thread and the scale-copy thread
     *abort_flag = 0;
-    *issued_cnt = 0;
-    *consumed_cnt = 0;
-    *sf_issued_cnt = 0;
-    *sf_consumed_cnt = 0;
+    for (int i = 0; i < kRowLoaders + 4; ++i) issued_cnt[i] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -561,9 +564,8 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     };
     for (; item.more() && !*abort_flag; item.next()) {
       const int half = item.n16() >> 1;
-      const int box = (half + 23) >> 5;  // 32 box + 8 >= half rows
-      const uint32_t tx = 2u * static_cast<uint32_t>(C::A_BYTES + (MODE == kGateUpInPlace ? half : 32 * box + 8) * BK);
-      const CUtensorMap* tm_x = &maps.x[MODE == kGateUpInPlace ? 0 : box];
+      const uint32_t tx = 2u * static_cast<uint32_t>(C::A_BYTES + (MODE == kGateUpInPlace ? half : token_box_rows(half)) * BK);
+      const CUtensorMap* tm_x = &maps.x[MODE == kGateUpInPlace ? 0 : token_box(half)];
       const int w_row = item.expert() * p.rows + item.block * (2 * BM) + BM * static_cast<int>(rank);
       const int x_row = item.row0() + half * static_cast<int>(rank);
       int tok[kRowQuads][4];
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
           tma_load_2d_pair(sbase + C::OFF_B + s * C::B_BYTES, tm_x, fb, kb * BK, x_row);
       }
     }
-    *issued_cnt = it;
+    issued_cnt[0] = it;
     if (MODE != kDown && item.end <= item.stride && !*abort_flag && pair < p.next_pairs) {
       // One round of items: with the last loads on their way HBM idles until GEMM 2 begins, so the weights
       // of this pair's first items there are fetched into L2 (one token 38.8 -> 37.5 us; with more
@@ -625,12 +627,13 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     // ---------------- token rows (both CTAs; with warp 0, every fourth quad of rows each) ----------------
     const uint32_t full0 = mapa_shared(bar_full, 0);
     if (early) pdl_wait_primary();
+    int it = 0;
     Ring<STAGES> ring;
     for (; item.more() && !*abort_flag; item.next()) {
       const int half = item.n16() >> 1;
       int tok[kRowQuads][4];
       load_quads(p, item, rank, warp - 11, tok);
-      for (int kb = 0; kb < nk; ++kb, ring.next()) {
+      for (int kb = 0; kb < nk; ++kb, ++it, ring.next()) {
         const int s = ring.slot;
         if (!mbar_wait_bounded(bar_empty + 8 * s, ring.phase ^ 1)) {
           *abort_flag = 1;
@@ -640,6 +643,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
         issue_quads(sbase + C::OFF_B + s * C::B_BYTES, &maps.x[0], full0 + 8 * s, kb * BK, half, warp - 11, tok);
       }
     }
+    issued_cnt[warp - 11] = it;
   } else if (warp == 11 && elected) {
     // ---------------- scale loads (both CTAs) ----------------
     // The scales of kSfKb k-blocks at a time, in a ring of their own that runs ahead of the operands
@@ -724,7 +728,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     // operands, so the copies run under the operands' loads. They count on the stage's own barrier,
     // which spares the MMA thread a second wait of 65 cycles for each of its 352 (176 tokens).
     if (leader && elected) {
-      int ic = 0;
+      int ic = 0, staged = 0;
       Ring<STAGES> ring;
       Ring<kSfChunks> chunk;
       bool ok = true;
@@ -753,6 +757,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
               tc_cp_sf_atom_pair(dst + 4, sdesc_sf_atom(src + C::SFA_BYTES + 1024 * j));
               if (two) tc_cp_sf_atom_pair(dst + 8, sdesc_sf_atom(src + C::SFA_BYTES + 1024 * j + 512));
               tc_commit_pair(bar_full + 8 * ring.slot, 0x1);
+              ++staged;
               ring.next();
             }
           if (kb % kSfKb + 2 == kSfKb || kb + 2 >= nk) {
@@ -762,6 +767,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
           }
         }
       }
+      *staged_cnt = staged;
       *sf_consumed_cnt = ic;
     }
   } else if (warp >= 2 && warp < 10) {
@@ -912,15 +918,29 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   if (leader && warp == 0 && lane == 0) {
     const int peer_abort = ld_dsmem_s32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), 1));
     if (*abort_flag || peer_abort) {
-      // wait (bounded) for every stage either CTA issued and the MMA warp did not consume
-      const int peer_issued = ld_dsmem_s32(mapa_shared(smem_u32(issued_cnt), 1));
-      const int hi = *issued_cnt > peer_issued ? *issued_cnt : peer_issued;
-      for (int i = *consumed_cnt; i < hi; ++i)
-        (void)mbar_wait_bounded(bar_full + 8 * (i % STAGES), (i / STAGES) & 1);
-      const int peer_sf = ld_dsmem_s32(mapa_shared(smem_u32(sf_issued_cnt), 1));
-      const int hi_sf = *sf_issued_cnt > peer_sf ? *sf_issued_cnt : peer_sf;
-      for (int i = *sf_consumed_cnt; i < hi_sf; ++i)
-        (void)mbar_wait_bounded(bar_sff + 8 * (i % kSfChunks), (i / kSfChunks) & 1);
+      // Some loads of either CTA may be in flight for stages that the MMA thread (chunks that the
+      // scale copies) did not take. The loaders stop at different stages: the barriers are brought
+      // to wait for what was issued, and then waited for (bounded).
+      auto settle = [](uint32_t bar, uint32_t phase, Owed o) {
+        if (o.bytes > 0) mbar_expect_tx(bar, static_cast<uint32_t>(o.bytes));
+        if (o.bytes < 0) mbar_complete_tx(bar, static_cast<uint32_t>(-o.bytes));
+        for (int i = 0; i < o.arrivals; ++i) mbar_arrive(bar);
+        (void)mbar_wait_bounded(bar, phase);
+      };
+      int count[2][C::LOADERS], hi = 0;
+      for (int l = 0; l < C::LOADERS; ++l) {
+        count[0][l] = issued_cnt[l];
+        count[1][l] = ld_dsmem_s32(mapa_shared(smem_u32(issued_cnt + l), 1));
+        hi = max(hi, max(count[0][l], count[1][l]));
+      }
+      for (int i = *consumed_cnt; i < hi; ++i) {  // (at most STAGES: the ring lets none further ahead)
+        const int half = ((p.items[pair + i / nk * static_cast<int>(gridDim.x >> 1)].n + 15) & ~15) >> 1;
+        const int rows = MODE == kGateUpInPlace ? half : token_box_rows(half);
+        settle(bar_full + 8 * (i % STAGES), (i / STAGES) & 1, owed_operands(i, count, *staged_cnt, C::A_BYTES, rows * BK));
+      }
+      const int sf0 = *sf_issued_cnt, sf1 = ld_dsmem_s32(mapa_shared(smem_u32(sf_issued_cnt), 1));
+      for (int i = *sf_consumed_cnt; i < max(sf0, sf1); ++i)
+        settle(bar_sff + 8 * (i % kSfChunks), (i / kSfChunks) & 1, owed_scales(i, sf0, sf1, C::SFA_BYTES + C::SFB_BYTES));
       *abort_flag = 1;
     }
   }
