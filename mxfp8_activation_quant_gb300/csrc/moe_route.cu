@@ -9,7 +9,7 @@
 //
 // Which experts are chosen does not depend on fp32 rounding. Without a bias the order of the
 // choices is that of the logits, which is exact. Otherwise choices and group values are computed
-// in fp32 with a known error bound, and values nearer than the bound are compared in fp64: for
+// in fp32 with an error bound each, and values nearer than their bounds are compared in fp64: for
 // sigmoid scores only the groups or picks in question, one value per lane (an fp64 exponential
 // takes a warp about 0.7 us; the whole row's, which one row in 10^4 took at first, added 10 us to a
 // launch), for softmax scores the sum as well. Three rows in a thousand have such picks at 256 experts
@@ -77,6 +77,34 @@ __device__ __forceinline__ float score32(float l, bool softmax, float m, float i
 // the sum in at most 37 additions: below 3.9e-6 of the row's largest score.
 constexpr float kSigmoidErr = 6.0e-7f;
 constexpr float kSoftmaxErr = 3.9e-6f;
+
+// A choice's exact value is within radius(c, err) of c: the score's error `err`, and kRel |c| for the rounding
+// of the sum (2^-24) and of what is reckoned with the two. (A bias may lie far from the scores; the
+// bound goes by the choice itself, so that one such expert does not widen the others'.) An infinite choice
+// is that of an infinite bias: exact.
+constexpr float kRel = 2.4e-7f;
+__device__ __forceinline__ float radius(float c, float err) {
+  return fabsf(c) <= FLT_MAX ? fmaf(kRel, fabsf(c), err) : 0.f;
+}
+
+// A group's value, the least of its terms, and the value's error bound: its terms' (which may cancel) and a
+// rounding no larger than theirs. A sum of finite terms that leaves fp32 stands at the type's end.
+struct GroupValue {
+  float value, least, radius;
+};
+__device__ __forceinline__ GroupValue group_value(float b0, float b1, int top, float err) {
+  GroupValue v = {b0, b0, radius(b0, err)};
+  if (top == 2 && b1 > -CUDART_INF_F) {
+    v.value = b0 <= FLT_MAX ? fminf(fmaxf(b0 + b1, -FLT_MAX), FLT_MAX) : b0;
+    v.least = b1;
+    v.radius = b0 <= FLT_MAX ? v.radius + radius(b1, err) : 0.f;
+  }
+  return v;
+}
+// order_key of the end of a range of finite values: past the type's end it stands there.
+__device__ __forceinline__ uint32_t range_key(float v, float value) {
+  return fabsf(value) <= FLT_MAX ? order_key(fminf(fmaxf(v, -FLT_MAX), FLT_MAX)) : order_key(value);
+}
 
 // The largest logit and the sum of the softmax in fp64, of one row by its warp.
 template <bool BF16>
@@ -244,7 +272,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   }
   const bool sums = a.groups > 1 && a.group_top == 2;
   const bool values = a.bias != nullptr || sums;  // choices are computed, not only ordered
-  float cmax = 0.f;
   if (values) {
     float bias[VPL] = {};
     if (a.bias != nullptr) load_bias<VPL>(a, e0, bias);
@@ -255,25 +282,18 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
       key[i] = a.bias != nullptr ? 0u : order_key(c[i]);
       c[i] = there ? s + bias[i] : -CUDART_INF_F;
       if (a.bias != nullptr) key[i] = order_key(c[i]);
-      if (there) cmax = fmaxf(cmax, fabsf(c[i]));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] = order_key(c[i]);
   }
-  // Two choices of the row further apart than `tol` are in their exact order: both scores' errors,
-  // and up to three roundings of numbers no larger than the choices.
-  float err = kSigmoidErr, tol = 0.f;
-  if (values) {
-    if (a.softmax) err = kSoftmaxErr * inv;  // the largest score is expf(0) * inv
-    cmax = key_value(__reduce_max_sync(0xffffffffu, order_key(cmax)));
-    tol = 2.f * err + 4.8e-7f * cmax;
-  }
+  float err = kSigmoidErr;
+  if (a.softmax) err = kSoftmaxErr * inv;  // the largest score is expf(0) * inv
 
   bool whole = false;  // decide the whole row in fp64
   double2 soft = make_double2(0.0, 0.0);  // softmax_f64, once it has been wanted
   if (a.groups > 1) {
-    float v = -CUDART_INF_F, least = -CUDART_INF_F;  // value of this lane's group, and its last term
+    GroupValue v = {-CUDART_INF_F, -CUDART_INF_F, 0.f};  // of this lane's group
     int g, kept_lanes = a.group_lanes;
     if (kept_lanes > 0) {  // a group is a run of lanes
       float b0 = -CUDART_INF_F, b1 = -CUDART_INF_F;
@@ -288,11 +308,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
         b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
         b0 = fmaxf(b0, o0);
       }
-      v = least = b0;
-      if (a.group_top == 2 && b1 > -CUDART_INF_F) {
-        v += b1;
-        least = b1;
-      }
+      v = group_value(b0, b1, a.group_top, err);
       g = lane / kept_lanes;
     } else {  // through shared memory, lane g sums up group g
       float* sc = reinterpret_cast<float*>(scratch[warp]);
@@ -309,39 +325,35 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
           b0 = fmaxf(b0, u);
           i = i + 1 == a.gsize ? 0 : i + 1;
         }
-        v = least = b0;
-        if (a.group_top == 2 && b1 > -CUDART_INF_F) {
-          v += b1;
-          least = b1;
-        }
+        v = group_value(b0, b1, a.group_top, err);
       }
       g = lane;
       kept_lanes = 1;
     }
     int rank = 0;
     for (int h = 0; h < a.groups; ++h) {
-      const float u = __shfl_sync(0xffffffffu, v, h * kept_lanes);
-      rank += (u > v || (u == v && h < g)) ? 1 : 0;
+      const float u = __shfl_sync(0xffffffffu, v.value, h * kept_lanes);
+      rank += (u > v.value || (u == v.value && h < g)) ? 1 : 0;
     }
-    const bool have = g < a.groups && v > -CUDART_INF_F;
+    const bool have = g < a.groups && v.value > -CUDART_INF_F;
     bool keep = have && rank < a.topk_groups;
     if (values) {
-      // the least kept value against the largest one left out
-      const uint32_t ki = __reduce_min_sync(0xffffffffu, keep ? order_key(v) : 0xFFFFFFFFu);
-      const uint32_t ko = __reduce_max_sync(0xffffffffu, have && !keep ? order_key(v) : 0u);
-      const float in = key_value(ki), out = key_value(ko);
-      if (ko != 0u && in - out <= 2.f * tol) {
+      // the least that a kept value may be against the most that one left out may be
+      const float lo = v.value - v.radius, hi = v.value + v.radius;
+      const uint32_t ki = __reduce_min_sync(0xffffffffu, keep ? range_key(lo, v.value) : 0xFFFFFFFFu);
+      const uint32_t ko = __reduce_max_sync(0xffffffffu, have && !keep ? range_key(hi, v.value) : 0u);
+      if (ko != 0u && ki <= ko) {
         // Some groups lie too near to the border: they are ranked by their values in fp64, a lane for
         // each expert that may be among a group's largest.
-        const bool border = have && (keep ? v - out <= 2.f * tol : in - v <= 2.f * tol);
+        const bool border = have && (keep ? range_key(lo, v.value) <= ko : range_key(hi, v.value) >= ki);
         int* list = reinterpret_cast<int*>(reinterpret_cast<float*>(scratch[warp]) + VPL * 32);
         int n = 0;
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
           const int holder = a.group_lanes > 0 ? lane : min((e0 + i) / a.gsize, 31);
-          const float thr = __shfl_sync(0xffffffffu, least, holder);
-          const bool mine = __shfl_sync(0xffffffffu, border, holder) && key[i] != 0u && c[i] >= thr - tol;
+          const float thr = __shfl_sync(0xffffffffu, v.least - radius(v.least, err), holder);
+          const bool mine = __shfl_sync(0xffffffffu, border, holder) && key[i] != 0u && c[i] + radius(c[i], err) >= thr;
           const uint32_t who = __ballot_sync(0xffffffffu, mine);
           const int at = n + __popc(who & ((1u << lane) - 1u));
           if (mine && at < 32) list[at] = e0 + i;
@@ -397,7 +409,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
 
   // k picks; with a bias one more, and on while the last two may be out of order
   int mine = -1, picks = 0;
-  float my_c = -CUDART_INF_F, last = 0.f;
+  float last_lo = 0.f;
   bool near = false;  // some neighbours of the list may be out of order
   uint32_t best = 0;
 #pragma unroll
@@ -407,10 +419,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     if (top == 0u) break;
     if (a.bias != nullptr) {
       const float now = key_value(top);
-      const bool close = picks > 0 && last - now <= tol;
+      // (after an infinite choice last_lo is NaN, and its order is exact)
+      const bool close = picks > 0 && last_lo <= fmaf(kRel, fabsf(now), now + err);
       if (picks >= a.k && !close) break;
       near |= close;
-      last = now;
+      last_lo = fmaf(-kRel, fabsf(now), now - err);
       if (picks == 32) {  // the list may go on
         whole = true;
         break;
@@ -432,10 +445,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
       }
     }
     at = __shfl_sync(0xffffffffu, e0 + at, src);
-    if (lane == picks) {
-      mine = at;
-      my_c = key_value(top);
-    }
+    if (lane == picks) mine = at;
   }
   if (near && !whole) {
     // Everything outside the list is certainly below all of it: its order in fp64, a lane each.
