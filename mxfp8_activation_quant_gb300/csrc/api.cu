@@ -343,8 +343,8 @@ mxq_status mxq_selftest_hold_sms(int64_t sm_pairs, int64_t hold_us, void* stream
   if (st == MXQ_OK) st = from_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   if (st != MXQ_OK) return st;
   if (sm_pairs < 1 || sm_pairs > sms / 2 || hold_us < 1 || hold_us > 2000000) return MXQ_ERR_INVALID_ARG;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(selftest_hold_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHoldSmemBytes);
+  static mxq::PerDevice smem_set;
+  const cudaError_t attr = mxq::allow_smem(smem_set, selftest_hold_kernel, kHoldSmemBytes);
   if (attr != cudaSuccess) return from_cuda(attr);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * sm_pairs), 1, 1);

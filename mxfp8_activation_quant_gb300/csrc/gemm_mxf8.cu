@@ -1710,14 +1710,6 @@ __global__ void __launch_bounds__(kThreadsPair, 1)
 // ------------------------------------------------------------------------------------------
 // host side
 // ------------------------------------------------------------------------------------------
-// Dynamic shared memory limit. The L1/shared split stays the driver's choice: forcing the
-// largest carveout lets a programmatic dependent's CTAs (wo_b) sit beside wo_a's, where their
-// early weight loads slow wo_a more than they save (measured on the T <= 16 pair).
-template <typename K>
-cudaError_t set_smem_attrs(K kern, int bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <int BN, int STAGES, int ACT = kActMx>
@@ -1732,7 +1724,8 @@ template <int BN, int STAGES, bool SWAP, int ACT = kActMx, int US = 0>
 cudaError_t launch_cfg(const GemmLaunch& l, const KArgs& ka, dim3 grid, int cluster_z, cudaStream_t stream) {
   using C = Cfg<BN, STAGES, ACT>;
   auto kern = gemm_mxf8_kernel<BN, STAGES, SWAP, ACT, US>;
-  static const cudaError_t attr_err = set_smem_attrs(kern, C::SMEM_LAUNCH);
+  static PerDevice smem_set;
+  const cudaError_t attr_err = allow_smem(smem_set, kern, C::SMEM_LAUNCH);
   if (attr_err != cudaSuccess) return attr_err;
   CUtensorMap tma_act, tma_wt;
   if (ACT == kActBf16) {
@@ -1782,7 +1775,8 @@ int uneven_clusters_resident() {
   static const int n = [] {
     using C = Cfg<BN, STAGES, ACT>;
     auto kern = gemm_mxf8_kernel<BN, STAGES, true, ACT, US>;
-    if (set_smem_attrs(kern, C::SMEM_LAUNCH) != cudaSuccess) return 0;
+    PerDevice smem_set;
+    if (allow_smem(smem_set, kern, C::SMEM_LAUNCH) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, static_cast<unsigned>(8 * US));
     cfg.blockDim = dim3(kThreads, 1, 1);
@@ -1904,7 +1898,8 @@ template <int STAGES, bool PK = false, bool CV = false>
 cudaError_t launch_pair(const GemmLaunch& l, KArgs ka, cudaStream_t stream) {
   using C = PairCfg<STAGES, PK, CV>;
   auto kern = gemm_mxf8_pair<STAGES, false, PK, CV>;
-  static const cudaError_t attr_err = set_smem_attrs(kern, C::SMEM_BYTES);
+  static PerDevice smem_set;
+  const cudaError_t attr_err = allow_smem(smem_set, kern, C::SMEM_BYTES);
   if (attr_err != cudaSuccess) return attr_err;
   ka.splits = 1;
   ka.kb_per_cta = l.k_len / BK;
@@ -1924,7 +1919,8 @@ cudaError_t launch_pair(const GemmLaunch& l, KArgs ka, cudaStream_t stream) {
   if constexpr (!CV) {
   if (l.workspace != nullptr && tiles % max_pairs != 0) {
     auto kern_sk = gemm_mxf8_pair<STAGES, true, PK>;
-    static const cudaError_t attr_err_sk = set_smem_attrs(kern_sk, C::SMEM_BYTES);
+    static PerDevice smem_set_sk;
+    const cudaError_t attr_err_sk = allow_smem(smem_set_sk, kern_sk, C::SMEM_BYTES);
     if (attr_err_sk != cudaSuccess) return attr_err_sk;
     const int resident = pair_clusters_resident<STAGES, PK>();
     const int sk_pairs = resident < max_pairs ? resident : max_pairs;

@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include "mxq_device.cuh"
+#include "mxq_internal.h"
 #include "mxq_moe_internal.h"
 #include "mxq_settle.h"
 #include "mxq_tma.h"
@@ -1037,8 +1038,8 @@ cudaError_t launch_gemm_mode(const mxq_mx_tensor& w, const void* act, int64_t ac
                              cudaStream_t stream) {
   using C = GemmCfg<MODE>;
   auto kern = experts_gemm_kernel<MODE>;
-  static const cudaError_t attr_err =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  static PerDevice smem_set;
+  const cudaError_t attr_err = allow_smem(smem_set, kern, C::SMEM_BYTES);
   if (attr_err != cudaSuccess) return attr_err;
   GemmMaps maps = {};
   if (!make_map(&maps.w, w.data, w.rows, K, w.ld, BM) || !make_sf_map(&maps.sfw, w.sf, w.rows / 128 * (K / 128), kSfKb) ||

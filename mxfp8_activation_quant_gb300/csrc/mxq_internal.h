@@ -6,11 +6,24 @@
 #include <cuda_runtime.h>
 
 #include "mxq.h"
+#include "mxq_per_device.h"
 
 namespace mxq {
 
 // CUDA error -> MXQ_OK / MXQ_ERR_CUDA; records the error name for mxq_last_error_string.
 mxq_status from_cuda(cudaError_t e);
+
+// Dynamic shared memory limit of a kernel on the current device; `set` is that kernel's own. The L1/shared
+// split stays the driver's choice: forcing the largest carveout lets a programmatic dependent's CTAs
+// (wo_b) sit beside wo_a's, where their early weight loads slow wo_a more than they save (measured
+// on the T <= 16 pair).
+template <typename K>
+cudaError_t allow_smem(PerDevice& set, K kern, int bytes) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return set.once(dev, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+}
 
 struct QuantizeLaunch {
   const void* x;
