@@ -36,7 +36,8 @@ typedef enum mxq_moe_scoring {
  *   (y_q, scales) = mxfp8_quantize(y)                             of that bf16 y, bit-identical
  * The sum is taken in fp32 and rounded once to the stream's type; the norm reads the rounded h. The
  * value of y is the formula's, rounded once to fp32 (the sum of squares, r and the products carry
- * their error terms), before it is rounded to bf16.
+ * their error terms), before it is rounded to bf16; rows whose sum of squares lies outside fp32 are
+ * taken in fp64. An infinity in h makes its own y NaN and the row's other y 0, a NaN the whole row.
  *
  *   x_bf16       [T, H] bf16, row stride ldx elements.
  *   residual     [T, H] of residual_type (MXQ_TYPE_BF16 or MXQ_TYPE_FP32), row stride ldr elements.

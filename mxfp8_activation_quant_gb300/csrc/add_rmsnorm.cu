@@ -16,7 +16,10 @@
 // and r are held as unevaluated sums of two floats (error-free sums and products, Dekker 1971, Knuth
 // 4.2.2); (h r) gamma is taken in fp32, within 4 ulp, and only where that lies within 4 ulp of a bf16
 // midpoint (one value in 7000) it is taken again with its error terms. 8192 x 5120: 57 us without and
-// 60.5 us with it.
+// 60.5 us with it. The two-float sum holds while it lies well inside fp32; a row whose sum of squares
+// does not (|h| above about 1e19, infinities and NaN, or next to nothing with an eps as small) is taken
+// in fp64 instead.
+#include <cfloat>
 #include <cuda_runtime.h>
 
 #include "mxq_device.cuh"
@@ -59,6 +62,16 @@ __device__ __forceinline__ void put(V* p, const V v, bool far) {
     __stcs(p, v);
   else
     *p = v;
+}
+
+// The codes and scales of 8 values of y; a warp holds 256 of a row, `in`: these are in it.
+__device__ __forceinline__ void store_codes(const AddRmsArgs& a, int64_t row, int64_t c, const uint4 y, int lane, bool in) {
+  uint32_t amax = absmax8(y);
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const uint32_t code = ue8m0_from_bf16_amax(amax);
+  if (in) put(reinterpret_cast<uint2*>(a.yq + row * a.H + c), quant8(y, ue8m0_inverse(code)), a.far);
+  store_unit_scales(a.q, row, c, code, lane);
 }
 
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
@@ -141,11 +154,55 @@ __device__ __forceinline__ uint32_t midpoint_min2(float y0, float y1, uint32_t l
   return __viaddmin_u16x2(low, 0x80048004u, least);  // - 0x7FFC in each half
 }
 
+// The sum of squares and n eps, at least: squares' errors below fp32's range then stay under 2^-43 of it.
+constexpr float kLeastSum = 8.3e-25f;  // 2^-80
+
 // (h r) g rounded once to fp32.
 __device__ __forceinline__ float rounded_once(float h, float2 r, float g) {
   const float p = __fmul_rn(h, r.x), pe = __fmaf_rn(h, r.y, __fmaf_rn(h, r.x, -p));
   const float q = __fmul_rn(p, g), qe = __fmaf_rn(pe, g, __fmaf_rn(p, g, -q));
   return __fadd_rn(q, qe);
+}
+
+// One row of the block in fp64, from the stream as it has just been stored (each thread reads what it wrote).
+template <bool F32, int NT>
+__device__ __noinline__ void row_f64(const AddRmsArgs& a, int64_t row) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ double red[NT / 32];
+  auto load = [&](int64_t i) {
+    const uint8_t* h = a.res_out + row * a.ldro_b;
+    return static_cast<double>(F32 ? reinterpret_cast<const float*>(h)[i]
+                                   : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(h)[i]) << 16));
+  };
+  double ss = 0.0;
+  for (int64_t c = 8 * tid; c < a.H; c += 8 * NT)
+    for (int i = 0; i < 8; ++i) {
+      const double h = load(c + i);
+      ss += h * h;
+    }
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (lane == 0) red[warp] = ss;
+  __syncthreads();
+  ss = 0.0;
+  for (int i = 0; i < NT / 32; ++i) ss += red[i];
+  const double r = 1.0 / sqrt(ss / static_cast<double>(a.h) + static_cast<double>(a.eps));
+  for (int64_t c0 = 0; c0 < a.H; c0 += 8 * NT) {  // (whole warps: the scales are gathered by shuffles)
+    const int64_t c = c0 + 8 * tid;
+    uint32_t yw[4] = {};
+    if (c < a.H) {
+      for (int i = 0; i < 4; ++i) {
+        float y[2];
+        for (int j = 0; j < 2; ++j) {
+          const float g = __uint_as_float(static_cast<uint32_t>(a.gamma[c + 2 * i + j]) << 16);
+          y[j] = static_cast<float>(load(c + 2 * i + j) * r * static_cast<double>(g));
+        }
+        yw[i] = bf16x2_rn(y[0], y[1]);
+      }
+    }
+    const uint4 y = make_uint4(yw[0], yw[1], yw[2], yw[3]);
+    if (a.y != nullptr && c < a.H) *reinterpret_cast<uint4*>(a.y + row * a.H + c) = y;
+    if (a.yq != nullptr) store_codes(a, row, c, y, lane, c < a.H);
+  }
 }
 
 // Blocks per SM that the registers have to leave room for, by the floats that a thread holds.
@@ -231,6 +288,11 @@ __global__ void __launch_bounds__(NT, (kMinBlocks<CPT, F32, NT>)) add_rmsnorm_ke
   ss = ss_lo = 0.f;
 #pragma unroll
   for (int i = 0; i < NT / 32; ++i) dd_add(ss, ss_lo, red[i].x, red[i].y);
+  const float size = fmaf(a.h, a.eps, ss);
+  if (vrow && !(size >= kLeastSum && size <= FLT_MAX)) {  // the same in every thread
+    row_f64<F32, NT>(a, row);
+    return;
+  }
   const float2 r = dd_rsqrt_mean(ss, ss_lo, a.h, a.eps);
   const F2 rr = pack2(r.x, r.x);
 
@@ -271,13 +333,7 @@ __global__ void __launch_bounds__(NT, (kMinBlocks<CPT, F32, NT>)) add_rmsnorm_ke
       y = make_uint4(yw[0], yw[1], yw[2], yw[3]);
       if (a.y != nullptr) put(reinterpret_cast<uint4*>(a.y + row * a.H + c), y, a.far);
     }
-    if (a.yq == nullptr) continue;
-    uint32_t amax = absmax8(y);
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const uint32_t code = ue8m0_from_bf16_amax(amax);
-    if (vrow && c < a.H) put(reinterpret_cast<uint2*>(a.yq + row * a.H + c), quant8(y, ue8m0_inverse(code)), a.far);
-    store_unit_scales(a.q, row, c, code, lane);
+    if (a.yq != nullptr) store_codes(a, row, c, y, lane, vrow && c < a.H);
   }
 }
 
