@@ -474,6 +474,13 @@ __device__ __forceinline__ void issue_quads(uint32_t dst, const CUtensorMap* tm,
   }
 }
 
+// silu(g) u. e^-|g| is taken as the square of e1 = e^(-|g| / 2): below zero silu(g) = g e1 e1 / (1 + e^-|g|)
+// then stays in range as far as the product with u does (g / (1 + e^-g) is 0 from -88 on).
+__device__ __forceinline__ float silu_times(float g, float u) {
+  const float e1 = __expf(-0.5f * fabsf(g)), a = g < 0.f ? e1 : 1.f;
+  return g * a * __fdividef(1.f, fmaf(e1, e1, 1.f)) * (a * u);
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(kThreads<MODE>, 1)
     experts_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
@@ -826,7 +833,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
                 const float a0 = __uint_as_float(acc[i][2 * c]), a1 = __uint_as_float(acc[i][2 * c + 1]);
                 const float o = __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 1);
                 const float g = up ? o : a0, u = up ? a1 : o;
-                const float h = __fdividef(g, 1.f + __expf(-g)) * u;
+                const float h = silu_times(g, u);
                 const int tok = t0 + 2 * c + up;
                 // 16-byte pieces of a 128-byte row are XOR-swizzled by the row
                 const uint32_t at = stage + tok * 128 + (((f >> 3) ^ (2 * (tok & 3))) << 4) + (f & 7) * 2;
