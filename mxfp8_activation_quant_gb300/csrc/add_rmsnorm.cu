@@ -337,19 +337,14 @@ __global__ void __launch_bounds__(NT, (kMinBlocks<CPT, F32, NT>)) add_rmsnorm_ke
   }
 }
 
-template <bool F32, int NT>
+// The kernel of the least of CPTS 8-element chunks per thread that holds a row.
+template <bool F32, int NT, int... CPTS>
 cudaError_t launch_nt(const AddRmsArgs& a, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(a.rows_total);
-  switch ((a.H / 8 + NT - 1) / NT) {  // 8-element chunks per thread
-    case 1: add_rmsnorm_kernel<1, F32, NT><<<grid, NT, 0, stream>>>(a); break;
-    case 2: add_rmsnorm_kernel<2, F32, NT><<<grid, NT, 0, stream>>>(a); break;
-    case 3: add_rmsnorm_kernel<3, F32, NT><<<grid, NT, 0, stream>>>(a); break;
-    case 4: add_rmsnorm_kernel<4, F32, NT><<<grid, NT, 0, stream>>>(a); break;
-    case 5: case 6: add_rmsnorm_kernel<6, F32, NT><<<grid, NT, 0, stream>>>(a); break;
-    case 7: case 8: add_rmsnorm_kernel<8, F32, NT><<<grid, NT, 0, stream>>>(a); break;
-    default: return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+  const int64_t need = (a.H / 8 + NT - 1) / NT;
+  bool done = false;
+  ((!done && need <= CPTS ? (add_rmsnorm_kernel<CPTS, F32, NT><<<grid, NT, 0, stream>>>(a), done = true) : false), ...);
+  return done ? cudaGetLastError() : cudaErrorInvalidValue;
 }
 
 // Threads per row. Few rows: a row is one block's latency, so 320 threads (1 x 5120 5.2 us, against 5.6
@@ -363,11 +358,11 @@ constexpr int64_t kFarBytes = int64_t(96) << 20;  // three quarters of L2
 template <bool F32>
 cudaError_t launch_type(const AddRmsArgs& a, cudaStream_t stream) {
   const int64_t chunks = a.H / 8;
-  if (a.rows_total <= kFewRows || chunks > 4 * 512) return launch_nt<F32, 320>(a, stream);
-  if (chunks <= 2 * 64) return launch_nt<F32, 64>(a, stream);
-  if (chunks <= 4 * 160) return launch_nt<F32, 160>(a, stream);
-  if (chunks <= 4 * 256) return launch_nt<F32, 256>(a, stream);
-  return chunks <= 4 * 320 ? launch_nt<F32, 320>(a, stream) : launch_nt<F32, 512>(a, stream);
+  if (a.rows_total <= kFewRows) return launch_nt<F32, 320, 1, 2, 3, 4, 6, 8>(a, stream);
+  if (chunks <= 2 * 64) return launch_nt<F32, 64, 1, 2>(a, stream);
+  if (chunks <= 4 * 160) return launch_nt<F32, 160, 1, 2, 3, 4>(a, stream);
+  if (chunks <= 4 * 256) return launch_nt<F32, 256, 3, 4>(a, stream);
+  return chunks <= 4 * 320 ? launch_nt<F32, 320, 4>(a, stream) : launch_nt<F32, 512, 3, 4>(a, stream);
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
