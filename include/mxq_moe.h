@@ -42,7 +42,8 @@ typedef enum mxq_moe_scoring {
  *   x_bf16       [T, H] bf16, row stride ldx elements.
  *   residual     [T, H] of residual_type (MXQ_TYPE_BF16 or MXQ_TYPE_FP32), row stride ldr elements.
  *   residual_out [T, H] of the same type, row stride ldro elements; may be `residual` itself with
- *                ldro == ldr (in place), must not overlap it otherwise.
+ *                ldro == ldr (in place), must not overlap it otherwise, nor x. (Column ranges of one
+ *                buffer do not overlap; with different row strides the whole spans count.)
  *   y_bf16       [T, H] bf16 out (row stride H), or NULL.
  *   y_q          [T, H] E4M3 out (row stride H bytes) and at least one scale output, or all NULL.
  * At least one of y_bf16 and y_q. Requires T >= 1, 32 <= H <= 16384, H % 32 == 0 (H % 128 == 0 for

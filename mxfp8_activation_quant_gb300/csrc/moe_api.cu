@@ -6,19 +6,11 @@
 
 #include "mxq_internal.h"
 #include "mxq_moe_internal.h"
+#include "mxq_overlap.h"
 
 namespace {
 
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// [rows, cols] of `elem` bytes at a and b with row strides in elements: whether the spans overlap
-bool spans_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t cols, int64_t elem_a,
-                   int64_t elem_b) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  const uintptr_t a1 = a0 + static_cast<uintptr_t>(((rows - 1) * lda + cols) * elem_a);
-  const uintptr_t b1 = b0 + static_cast<uintptr_t>(((rows - 1) * ldb + cols) * elem_b);
-  return a0 < b1 && b0 < a1;
-}
 
 mxq_status check_weights(const mxq_mx_tensor* t, int64_t rows, int64_t cols) {
   if (t == nullptr || t->data == nullptr || t->sf == nullptr) return MXQ_ERR_INVALID_ARG;
@@ -59,8 +51,8 @@ mxq_status add_rmsnorm_dual_out(const void* x_bf16, int64_t ldx, const void* res
     return MXQ_ERR_MISALIGNED;
   if ((ldx * 2) % 16 != 0 || (ldr * es) % 16 != 0 || (ldro * es) % 16 != 0) return MXQ_ERR_MISALIGNED;
   const bool in_place = residual_out == residual && ldro == ldr;
-  if (!in_place && spans_overlap(residual, ldr, residual_out, ldro, T, H, es, es)) return MXQ_ERR_INVALID_ARG;
-  if (spans_overlap(x_bf16, ldx, residual_out, ldro, T, H, 2, es)) return MXQ_ERR_INVALID_ARG;
+  if (!in_place && mxq::rows_overlap(residual, ldr * es, H * es, residual_out, ldro * es, H * es, T)) return MXQ_ERR_INVALID_ARG;
+  if (mxq::rows_overlap(x_bf16, ldx * 2, H * 2, residual_out, ldro * es, H * es, T)) return MXQ_ERR_INVALID_ARG;
   mxq::AddRmsnormLaunch l{x_bf16, ldx, residual, residual_type == MXQ_TYPE_FP32, ldr, gamma_bf16, eps, T, H,
                           residual_out, ldro, y_bf16, y_q, y_sf_packed_i32, y_sf_rowmajor, y_sf_128x4};
   return mxq::from_cuda(mxq::launch_add_rmsnorm(l, static_cast<cudaStream_t>(stream)));
