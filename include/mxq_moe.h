@@ -5,7 +5,8 @@
  *
  * The conventions, status codes, MXFP8 format and scale layouts are those of mxq.h: device
  * pointers owned by the caller, work enqueued on `stream`, argument errors detected on the host
- * before anything is launched, nothing allocated and nothing synchronized.
+ * before anything is launched, nothing allocated and nothing synchronized. Row strides are below 2^40;
+ * that of a single row is not looked at.
  *
  * No page describes these operators; they extend the chain of mxq.h so that activations stay
  * MXFP8 through the experts as they do through _o_proj.

@@ -10,6 +10,8 @@
 
 namespace {
 
+constexpr int64_t kMaxStride = int64_t(1) << 40;  // a tensor map's
+
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 mxq_status check_weights(const mxq_mx_tensor* t, int64_t rows, int64_t cols) {
@@ -17,7 +19,7 @@ mxq_status check_weights(const mxq_mx_tensor* t, int64_t rows, int64_t cols) {
   if (t->sf_layout != MXQ_SF_TILED_128X4) return MXQ_ERR_LAYOUT;
   if (t->rows != rows || t->cols != cols || t->ld < cols) return MXQ_ERR_UNSUPPORTED_SHAPE;
   if (!al16(t->data) || !al16(t->sf) || t->ld % 16 != 0) return MXQ_ERR_MISALIGNED;
-  if (t->ld >= (int64_t(1) << 40) || rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31))
+  if (t->ld >= kMaxStride || rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31))
     return MXQ_ERR_UNSUPPORTED_SHAPE;
   return MXQ_OK;
 }
@@ -41,9 +43,10 @@ mxq_status add_rmsnorm_dual_out(const void* x_bf16, int64_t ldx, const void* res
   const bool any_sf = y_sf_packed_i32 != nullptr || y_sf_rowmajor != nullptr || y_sf_128x4 != nullptr;
   if ((y_q != nullptr) != any_sf || (y_q == nullptr && y_bf16 == nullptr)) return MXQ_ERR_INVALID_ARG;
   if (T <= 0 || H <= 0 || !(eps >= 0.0f)) return MXQ_ERR_INVALID_ARG;
+  if (T == 1) ldx = ldr = ldro = H;  // a single row has no stride
   if (H % 32 != 0 || H > 16384 || ldx < H || ldr < H || ldro < H) return MXQ_ERR_UNSUPPORTED_SHAPE;
   if (y_sf_packed_i32 != nullptr && H % 128 != 0) return MXQ_ERR_UNSUPPORTED_SHAPE;
-  if (T >= (int64_t(1) << 31) || ldx >= (int64_t(1) << 31) || ldr >= (int64_t(1) << 31) || ldro >= (int64_t(1) << 31))
+  if (T >= (int64_t(1) << 31) || ldx >= kMaxStride || ldr >= kMaxStride || ldro >= kMaxStride)
     return MXQ_ERR_UNSUPPORTED_SHAPE;
   const int64_t es = residual_type == MXQ_TYPE_FP32 ? 4 : 2;
   if (!al16(x_bf16) || !al16(residual) || !al16(gamma_bf16) || !al16(residual_out) || !al16(y_bf16) || !al16(y_q) ||
@@ -66,9 +69,10 @@ mxq_status moe_route(const void* logits, int32_t logits_type, int64_t ldl, const
   if (scoring != MXQ_MOE_SIGMOID && scoring != MXQ_MOE_SOFTMAX) return MXQ_ERR_INVALID_ARG;
   if (T <= 0 || E <= 0 || k <= 0 || groups <= 0 || topk_groups <= 0 || topk_groups > groups) return MXQ_ERR_INVALID_ARG;
   if ((group_top != 1 && group_top != 2) || !(scale - scale == 0.0f)) return MXQ_ERR_INVALID_ARG;
+  if (T == 1) ldl = E;  // a single row has no stride
   if (E > 1024 || k > 32 || groups > 32 || E % groups != 0 || k > topk_groups * (E / groups) || ldl < E)
     return MXQ_ERR_UNSUPPORTED_SHAPE;
-  if (T >= (int64_t(1) << 31) || ldl >= (int64_t(1) << 31)) return MXQ_ERR_UNSUPPORTED_SHAPE;
+  if (T >= (int64_t(1) << 31) || ldl >= kMaxStride) return MXQ_ERR_UNSUPPORTED_SHAPE;
   const uintptr_t es = logits_type == MXQ_TYPE_FP32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) % es != 0 || reinterpret_cast<uintptr_t>(bias_f32) % 4 != 0 ||
       reinterpret_cast<uintptr_t>(ids_i32) % 4 != 0 || reinterpret_cast<uintptr_t>(weights_f32) % 4 != 0)
@@ -92,18 +96,20 @@ mxq_status moe_experts_mxfp8(const mxq_mx_tensor* x, const void* ids_i32, const 
     return MXQ_ERR_INVALID_ARG;
   if (T <= 0 || k <= 0 || E <= 0 || H <= 0 || I <= 0) return MXQ_ERR_INVALID_ARG;
   if (x->sf_layout != MXQ_SF_ROWMAJOR_U8 && x->sf_layout != MXQ_SF_TILED_128X4) return MXQ_ERR_LAYOUT;
-  if (!experts_shape_ok(T, k, E, H, I) || x->rows != T || x->cols != H || x->ld < H || x->ld >= (int64_t(1) << 31) ||
-      ldo < H || ldo >= (int64_t(1) << 31))
+  mxq_mx_tensor xt = *x;
+  if (T == 1) xt.ld = ldo = H;  // a single row has no stride
+  if (!experts_shape_ok(T, k, E, H, I) || xt.rows != T || xt.cols != H || xt.ld < H || xt.ld >= kMaxStride || ldo < H ||
+      ldo >= kMaxStride)
     return MXQ_ERR_UNSUPPORTED_SHAPE;
   mxq_status st = check_weights(w13, static_cast<int64_t>(E) * 2 * I, H);
   if (st != MXQ_OK) return st;
   if ((st = check_weights(w2, static_cast<int64_t>(E) * H, I)) != MXQ_OK) return st;
-  if (!al16(x->data) || !al16(x->sf) || x->ld % 16 != 0 || !al16(out_bf16) || (ldo * 2) % 16 != 0 ||
+  if (!al16(xt.data) || !al16(xt.sf) || xt.ld % 16 != 0 || !al16(out_bf16) || (ldo * 2) % 16 != 0 ||
       !al16(workspace) || !al16(status) || reinterpret_cast<uintptr_t>(ids_i32) % 4 != 0 ||
       reinterpret_cast<uintptr_t>(weights_f32) % 4 != 0)
     return MXQ_ERR_MISALIGNED;
   if (workspace_bytes < mxq::experts_workspace_bytes(T, k, E, H, I)) return MXQ_ERR_INVALID_ARG;
-  mxq::ExpertsLaunch l{x, static_cast<const int32_t*>(ids_i32), static_cast<const float*>(weights_f32), T, k, w13, w2,
+  mxq::ExpertsLaunch l{&xt, static_cast<const int32_t*>(ids_i32), static_cast<const float*>(weights_f32), T, k, w13, w2,
                        E, H, I, out_bf16, ldo, workspace, static_cast<int32_t*>(status)};
   return mxq::from_cuda(mxq::launch_experts(l, static_cast<cudaStream_t>(stream)));
 }
