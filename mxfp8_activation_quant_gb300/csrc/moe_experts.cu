@@ -52,10 +52,12 @@ struct __align__(128) ExpertRows {
   int32_t row0, tile0, step, next;
 };
 
-// Whether the token rows are copied in expert order before GEMM 1. Its loads of four rows at a time
-// keep up with the MMAs of small tiles only: at 97 tokens per expert (777 tokens, 64 experts, top 8,
-// 5120 -> 2 x 1024) reading x in place takes the call from 225 to 216 us, at 160 there is no difference,
-// and at 512 GEMM 1 takes 288 us in place and 231 us from copies that cost 26 us.
+// Whether the token rows are copied in expert order before GEMM 1. Reading them in place costs a gather of
+// four rows per load for every block of 256 weight rows, copying them H bytes a pair once. us of the call
+// in place / copied at 100, 160 and 400 tokens per expert: 5120 -> 2 x 1024 (64 experts, top 8) 228 / 230,
+// 267 / 269, 499 / 463; 7168 -> 2 x 512 (32, top 8) 99 / 103, 140 / 141, 264 / 259; 2048 -> 2 x 768 (32, top 4)
+// 46.0 / 44.7, 58.6 / 56.7, 99.5 / 95.2; 1024 -> 2 x 1024 35.9 / 34.0, 43.5 / 41.1, 77 / 72. So the sides cross
+// between 60 (narrow rows, many blocks) and 300; what the one number gives away is at most 6 %.
 inline bool copies_rows(int64_t P, int32_t E) { return P > static_cast<int64_t>(160) * E; }
 
 struct Layout {  // byte offsets into the workspace
@@ -259,9 +261,11 @@ struct RowsArgs {
   uint8_t* xp;
 };
 constexpr int kRowsThreads = 128;
-// Most scale words that plan copies itself (one token of 5120 in 8 places has 320; at 15360, 48 tokens,
-// the call takes 177 us so and 172 us with the kernel for rows).
-constexpr int64_t kScalesInPlan = 8192;
+// Most scale words that plan copies itself, in one block (one token of 5120 in 8 places has 320). us of the
+// call so / with the kernel for rows, 5120 -> 2 x 1024, 2048 -> 2 x 640 and 7168 -> 2 x 512: 320 words
+// 34.0 / 35.1, 64 17.8 / 18.9, 448 32.8 / 33.7; about 1500 equal (74.4 / 74.7, 38.0 / 38.1, 59.5 / 59.6); 5120
+// 139 / 136, 6144 42.4 / 38.7, 7168 71.1 / 66.7.
+constexpr int64_t kScalesInPlan = 2048;
 
 template <bool COPY>
 __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
