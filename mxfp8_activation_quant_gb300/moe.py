@@ -32,6 +32,8 @@ SIGNATURES = {
 }
 
 _bound = None
+# (looked up once; a torch without CUDA has neither, and no device tensor to call with)
+_device, _raw_stream = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _fns():
@@ -83,7 +85,7 @@ def add_rmsnorm_dual_out(x: torch.Tensor, residual: torch.Tensor, gamma: torch.T
         x.data_ptr(), ldx, residual.data_ptr(), _TYPES[st], ldr, gamma.data_ptr(), eps, T, H, residual_out.data_ptr(), ldo,
         None if y is None else _ptr(y), None if yq is None else _ptr(yq), None if sf_packed is None else _ptr(sf_packed),
         None if sf_rowmajor is None else _ptr(sf_rowmajor), None if sf_128x4 is None else _ptr(sf_128x4),
-        _stream(stream))
+        _raw_stream(_device()) if stream is None else _stream(stream))
     if status:
         _check(status, "add_rmsnorm_dual_out")
 
@@ -106,7 +108,7 @@ def moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, bi
     status = _fns().moe_route(
         logits.data_ptr(), _TYPES[logits.dtype], ldl, None if bias is None else _ptr(bias), T, E, k, _SCORING[scoring],
         groups, topk_groups, group_top, 1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(),
-        _stream(stream))
+        _raw_stream(_device()) if stream is None else _stream(stream))
     if status:
         _check(status, "moe_route")
 
