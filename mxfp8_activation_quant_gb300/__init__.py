@@ -1,8 +1,8 @@
 """GB300 (sm_103a) MXFP8 activation chain: standalone quantizer, the fused `_o_proj` pair
 (wo_a einsum writing MXFP8 z, wo_b MXFP8 GEMM consuming it), the RMSNorm dual-output producer,
-and the mixture-of-experts half of the layer (residual RMSNorm, router, experts' products),
-behind the C ABI in include/mxq.h and include/mxq_moe.h. The Python layer only marshals
-arguments."""
+the mixture-of-experts half of the layer (residual RMSNorm, router, experts' products), and the
+paged MXFP8 key-value cache with the attention that reads it, behind the C ABI in include/mxq.h,
+include/mxq_moe.h and include/mxq_kv.h. The Python layer only marshals arguments."""
 from ._lib import (  # noqa: F401
     MXFP8,
     SF_PACKED_I32_MN,
@@ -35,4 +35,11 @@ from .moe import (  # noqa: F401
     moe_experts_mxfp8,
     moe_route,
     moe_workspace_bytes,
+)
+from .kv import (  # noqa: F401
+    MXFP8Cache,
+    kv_read_bf16,
+    kv_write_mxfp8,
+    paged_attention_mxfp8,
+    paged_attention_workspace_bytes,
 )

@@ -1,0 +1,216 @@
+// Quantizing keys and values as they are written into a paged cache, and reading them back
+// (HBM-streaming kernels).
+//
+// Mapping: as the standalone quantizer's: 8 elements per lane, 4 lanes per 32-element group (amax with two
+// xor-shuffles), 16 lanes per 128-element scale word, and a warp owns a segment of kUnits x 256 columns
+// of a token's heads * dim row. Both bound by HBM: a write moves 2 + 33/32 bytes an element, a read the
+// same the other way. Keys and values go in one launch (grid.y), since a decode step's few tokens take less
+// than a launch does.
+#include <cuda_runtime.h>
+
+#include "mxq_device.cuh"
+#include "mxq_internal.h"
+#include "mxq_kv_internal.h"
+
+namespace mxq {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kUnits = 2;
+
+struct Tensor {
+  const uint16_t* rows;
+  int64_t ld, ldh;
+  uint8_t* data;
+  uint8_t* sf;
+  int64_t page, token, head, sf_page, sf_token, sf_head;
+  uint32_t dim, width;  // width = heads * dim
+  uint32_t chunks;      // warp segments per row
+};
+
+struct WriteArgs {
+  Tensor t[2];
+  const int32_t* slots;
+  int64_t T;
+  uint32_t page_size, slots_end;
+};
+
+struct ReadArgs {
+  Tensor t[2];
+  const int32_t* table;
+  int64_t ld_table, B, rows;
+  const int32_t* cu;
+  const int32_t* starts;
+  uint32_t page_size, pages, table_width;
+};
+
+Tensor tensor(const KvTensor& k) {
+  const mxq_kv_cache& c = k.c;
+  Tensor t;
+  t.rows = static_cast<const uint16_t*>(k.rows);
+  t.ld = k.ld;
+  t.ldh = k.ldh;
+  t.data = static_cast<uint8_t*>(c.data);
+  t.sf = static_cast<uint8_t*>(c.sf);
+  t.page = c.page_stride;
+  t.token = c.token_stride;
+  t.head = c.head_stride;
+  t.sf_page = c.sf_page_stride;
+  t.sf_token = c.sf_token_stride;
+  t.sf_head = c.sf_head_stride;
+  t.dim = static_cast<uint32_t>(c.dim);
+  t.width = static_cast<uint32_t>(c.heads) * t.dim;
+  t.chunks = (t.width + 256 * kUnits - 1) / (256 * kUnits);
+  return t;
+}
+
+__global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ WriteArgs a) {
+  const Tensor& t = a.t[blockIdx.y];
+  const int lane = threadIdx.x & 31;
+  const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t row = wid / t.chunks;
+  if (row >= a.T) return;
+  const uint32_t slot = static_cast<uint32_t>(a.slots[row]);
+  if (slot >= a.slots_end) return;  // (negative ones too)
+  const uint32_t page = slot / a.page_size, place = slot - page * a.page_size;
+  uint8_t* const data = t.data + page * t.page + place * t.token;
+  uint8_t* const sf = t.sf + page * t.sf_page + place * t.sf_token;
+  const uint32_t col0 = static_cast<uint32_t>(wid - row * t.chunks) * (256 * kUnits) + 8 * lane;
+
+  uint4 v[kUnits];
+  uint32_t h[kUnits], d[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const uint32_t c = col0 + 256 * u;
+    h[u] = c / t.dim;
+    d[u] = c - h[u] * t.dim;
+    v[u] = c < t.width ? ld_stream_u4(t.rows + row * t.ld + h[u] * t.ldh + d[u]) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const bool in = col0 + 256 * u < t.width;
+    uint32_t amax = absmax8(v[u]);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const uint32_t code = ue8m0_from_bf16_amax(amax);
+    if (in) *reinterpret_cast<uint2*>(data + h[u] * t.head + d[u]) = quant8(v[u], ue8m0_inverse(code));
+    uint8_t* const s = sf + h[u] * t.sf_head + (d[u] >> 5);
+    if (t.dim % 128 == 0) {  // 16 lanes lie in one head: whole words
+      uint32_t w = code;
+      w |= __shfl_down_sync(0xffffffffu, code, 4) << 8;
+      w |= __shfl_down_sync(0xffffffffu, code, 8) << 16;
+      w |= __shfl_down_sync(0xffffffffu, code, 12) << 24;
+      if (in && (lane & 15) == 0) *reinterpret_cast<uint32_t*>(s) = w;
+    } else if (in && (lane & 3) == 0) {
+      *s = static_cast<uint8_t>(code);
+    }
+  }
+}
+
+// 2^(b - 127) as fp32; byte 255 is NaN.
+__device__ __forceinline__ float ue8m0_value(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
+}
+
+// Four E4M3 bytes times s, as four bf16.
+__device__ __forceinline__ uint2 dequant4(uint32_t w, float s) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+  float f[4];
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f[0]), "=f"(f[1]) : "r"(lo));
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f[2]), "=f"(f[3]) : "r"(hi));
+  return make_uint2(bf16x2_rn(f[0] * s, f[1] * s), bf16x2_rn(f[2] * s, f[3] * s));
+}
+
+__global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_constant__ ReadArgs a) {
+  const Tensor& t = a.t[blockIdx.y];
+  const int lane = threadIdx.x & 31;
+  const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t row = wid / t.chunks;
+  if (row >= a.rows) return;
+  // the last b with cu[b] <= row: 32 candidates a step
+  int64_t b = 0, n = a.B + 1;
+  while (n > 1) {
+    const int64_t step = (n + 31) / 32, i = lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, i < n && a.cu[b + i] <= row);
+    if (le == 0) return;  // before the first row
+    const int64_t at = (__popc(le) - 1) * step;
+    b += at;
+    n = min(step, n - at);
+  }
+  if (b == a.B) return;  // behind the last row
+  const int64_t pos = row - a.cu[b] + (a.starts != nullptr ? a.starts[b] : 0);
+  uint32_t page = a.pages, place = 0;
+  if (pos >= 0 && pos < static_cast<int64_t>(a.table_width) * a.page_size) {
+    const uint32_t p = static_cast<uint32_t>(pos / a.page_size);
+    place = static_cast<uint32_t>(pos - static_cast<int64_t>(p) * a.page_size);
+    page = static_cast<uint32_t>(a.table[b * a.ld_table + p]);
+  }
+  const bool there = page < a.pages;
+  const uint8_t* const data = t.data + (there ? page * t.page + place * t.token : 0);
+  const uint8_t* const sf = t.sf + (there ? page * t.sf_page + place * t.sf_token : 0);
+  const uint32_t col0 = static_cast<uint32_t>(wid - row * t.chunks) * (256 * kUnits) + 8 * lane;
+  uint2 v[kUnits];
+  uint32_t s[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const uint32_t c = col0 + 256 * u, h = c / t.dim, d = c - h * t.dim;
+    const bool in = there && c < t.width;
+    v[u] = in ? *reinterpret_cast<const uint2*>(data + h * t.head + d) : make_uint2(0, 0);
+    s[u] = in ? sf[h * t.sf_head + (d >> 5)] : 0;
+  }
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const uint32_t c = col0 + 256 * u;
+    if (c >= t.width) continue;
+    const float f = ue8m0_value(s[u]);
+    const uint2 x = dequant4(v[u].x, f), y = dequant4(v[u].y, f);
+    *reinterpret_cast<uint4*>(const_cast<uint16_t*>(t.rows) + row * t.ld + c) = make_uint4(x.x, x.y, y.x, y.y);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const KvWriteLaunch& l, cudaStream_t stream) {
+  WriteArgs a{};
+  int64_t warps = 0;
+  for (int i = 0; i < l.tensors; ++i) {
+    a.t[i] = tensor(l.t[i]);
+    warps = warps > l.T * a.t[i].chunks ? warps : l.T * a.t[i].chunks;
+  }
+  a.slots = l.slots;
+  a.T = l.T;
+  a.page_size = static_cast<uint32_t>(l.t[0].c.page_size);
+  a.slots_end = static_cast<uint32_t>(l.t[0].c.pages * l.t[0].c.page_size);
+  const int64_t blocks = (warps + kWarps - 1) / kWarps;
+  if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  kv_write_kernel<<<dim3(static_cast<unsigned>(blocks), l.tensors), kWarps * 32, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_read(const KvReadLaunch& l, cudaStream_t stream) {
+  ReadArgs a{};
+  int64_t warps = 0;
+  for (int i = 0; i < l.tensors; ++i) {
+    a.t[i] = tensor(l.t[i]);
+    warps = warps > l.rows * a.t[i].chunks ? warps : l.rows * a.t[i].chunks;
+  }
+  a.table = l.table;
+  a.ld_table = l.ld_table;
+  a.table_width = static_cast<uint32_t>(l.table_width);
+  a.B = l.B;
+  a.rows = l.rows;
+  a.cu = l.cu;
+  a.starts = l.starts;
+  a.page_size = static_cast<uint32_t>(l.t[0].c.page_size);
+  a.pages = static_cast<uint32_t>(l.t[0].c.pages);
+  const int64_t blocks = (warps + kWarps - 1) / kWarps;
+  if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  kv_read_kernel<<<dim3(static_cast<unsigned>(blocks), l.tensors), kWarps * 32, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace mxq
