@@ -165,6 +165,7 @@ mxq_status paged_attention_mxfp8(const void* q_bf16, int64_t ldq, int64_t ldqh, 
   }
   if (!attention_shape_ok(B, q_heads, k.heads, k.dim) || k.page_size % 16 != 0) return MXQ_ERR_UNSUPPORTED_SHAPE;
   if ((st = check_table(block_table_i32, &ld_table, table_width, B)) != MXQ_OK) return st;
+  if (static_cast<int64_t>(table_width) * k.page_size > (int64_t(1) << 30)) return MXQ_ERR_UNSUPPORTED_SHAPE;
   if (q_heads == 1) ldqh = k.dim;
   if (B == 1) ldq = static_cast<int64_t>(q_heads) * ldqh;
   if (ldqh < k.dim || ldq < k.dim || ldq >= kMaxStride || ldqh >= kMaxStride) return MXQ_ERR_UNSUPPORTED_SHAPE;

@@ -1,5 +1,27 @@
 // Attention of one new token per sequence over a paged MXFP8 cache, split over the cache's length and
 // joined.
+//
+// One persistent CTA per SM takes an equal share of all (sequence, cache head, block of query heads)
+// items' tokens, in units of 64, in tiles of up to 128 tokens. For a tile:
+//   S^T[t, h] = K_t . q_h    tcgen05.mma kind::mxf8f6f4, block-scaled, M = 128 tokens: cache rows go from TMA
+//                            straight into the MMA. bf16 has 8 significant bits and E4M3 4, so q = hi + lo, both
+//                            MXFP8 (lo's scales 2^-4 of hi's): N = 2 GP columns, added where S is read.
+//   P = exp2(S - ref)        ref: a running reference within 2^8 of the running maximum (moved, with O and the
+//                            sums, only when a score passes it by more), so P fits fp16 and a tile
+//                            needs no maximum of its own
+//   O^T[d, h] += V^T P^T     kind::f16, M = 128 features a panel: ldmatrix transposes the E4M3 bytes, registers make
+//                            them fp16 with their scales relative to the segment's pivot 2^E, and they
+//                            are stored to TMEM as the A operand. (Dequantized rows in shared memory would
+//                            cost 128 KB written and read a tile of 512 features, which alone takes
+//                            2048 of the 2800 cycles in which HBM delivers the tile.)
+// fp16 holds code * 2^(b - E) exactly for b in [E - 15, E + 7]: a tile with a scale above raises E (O is
+// rescaled with ref), one with a nonzero scale below takes P and V as bf16.
+//
+// Warps: 0 TMA, 1 MMA, 2-3 scales, 4-11 queries and softmax (two a TMEM lane quarter, half of the heads each),
+// 12-19 V^T and the outputs (two a quarter; 64 of the tile's tokens each, half of the heads each).
+//
+// A CTA that holds an item from start to end writes its outputs; the others' normalised parts go to the
+// workspace (at most two a CTA), and join_kernel adds them up in the order of the CTAs.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -12,177 +34,1051 @@
 namespace mxq {
 namespace {
 
-constexpr int kTile = 32;   // tokens per step
-constexpr int kHeads = 8;   // query heads per block
-constexpr int kThreads = 256;
+constexpr int kUnit = 64;         // tokens of the unit of work; a TMA box has no more
+constexpr int kTile = 128;        // tokens of a tile
+constexpr int kThreads = 640;
+constexpr int kPanel = 128 * 128; // bytes of 128 features of a tile
+constexpr int kMaxHeads = 64;     // query heads of an item
+constexpr int kSoftThreads = 256;
+constexpr float kLowRef = -1e30f; // ref before the first token
+constexpr float kSlack = 8.0f;
 
-struct Cache {
-  const uint8_t* data;
-  const uint8_t* sf;
-  int64_t page, token, head, sf_page, sf_token, sf_head;
-};
+// TMEM columns: O from 0, then S, the scales and V^T. With two S buffers (O then ends by column 128) K's scales
+// have two too, so that a tile's are not overwritten before its products are done.
+constexpr uint32_t kColS = 256, kColSfK = 384, kColSfK1 = 240, kColSfQ = 400, kColV = 416;
+constexpr int kVSlots = 3;
+
 struct Args {
   const uint16_t* q;
   int64_t ldq, ldqh;
-  Cache k, v;
-  bool shared;
+  const uint8_t* k_sf;
+  const uint8_t* v_sf;  // null: the keys'
+  int64_t k_sf_page, k_sf_token, k_sf_head, v_sf_page, v_sf_token, v_sf_head;
   const int32_t* table;
   int64_t ld_table;
   uint32_t table_width, page_size, pages;
   const int32_t* lens;
-  int32_t B, H, kv, G, D, splits, blocks;
+  int32_t B, H, kv, G, D, panels;
+  int32_t blocks, block_heads;  // blocks of query heads per cache head, and their size
+  int32_t box;                  // tokens of a TMA box
+  int32_t ring, sf_bufs, p_bufs;
   float scale;
-  float* part;   // [B * H * splits][D + 2]
+  float* part;   // [2 * CTAs][GP][D]
+  float2* stat;  // [2 * CTAs][GP]: ref, sum
+  int2* owner;   // [CTAs]: 1 + the item whose first part is the CTA's last segment (0: none), the CTA of its last part
   uint16_t* o;
   uint8_t* oq;
   uint8_t* sf_rm;
-  uint32_t* sf_pk;
+  uint8_t* sf_pk;
   uint8_t* sf_tl;
   float* lse;
+  int32_t* status;
+  int32_t ctas;
 };
 
-__device__ __forceinline__ float code_value(uint32_t c) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(c));
-  float f;
-  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(h));
+// Shared memory, from the kernel's sizes. Panels on 1024-byte boundaries (their swizzle).
+struct Layout {
+  int q, p, ring, q_sf, sf, fin, misc, total;
+};
+struct Misc {
+  uint64_t ring_full[16], ring_empty[16], sf_full[4], sf_empty[4], s_full[2], s_empty[2], p_full[2], p_empty[2], v_full[kVSlots],
+      v_empty[kVSlots], q_full, q_empty, o_full, o_empty, fin_full[2], fin_empty[2], done;
+  alignas(16) float ref[kMaxHeads];
+  float fac[kMaxHeads];
+  int32_t red[kMaxHeads];
+  int64_t sums[kThreads / 32];
+  int32_t sf_red[2][4];
+  int64_t w0, w1, total, ctas;
+  int32_t b0, sub0, u0;
+  uint32_t tmem;
+  volatile int32_t dead;
+};
+// A buffer of scales: K atoms [panels][512], V table [4 panels][128] of 16 bits, then this.
+struct TileInfo {
+  uint32_t valid[4];
+  int32_t pivot, wide;
+  int32_t pad[2];
+};
+// A finished segment's sums and references.
+struct Fin {
+  float sum[4][kMaxHeads];
+  float ref[kMaxHeads];
+  int32_t pivot;
+  int32_t pad[3];
+};
+__host__ __device__ inline int sf_buf_bytes(int panels) { return panels * (512 + 1024) + static_cast<int>(sizeof(TileInfo)); }
+__host__ __device__ inline Layout layout_of(int gp, int panels, int ring, int sf_bufs, int p_bufs) {
+  Layout l;
+  l.q = 0;
+  l.p = l.q + panels * gp * 256;
+  l.ring = l.p + p_bufs * kPanel;
+  l.q_sf = l.ring + ring * kPanel;
+  l.sf = l.q_sf + panels * 512;
+  l.fin = l.sf + sf_bufs * sf_buf_bytes(panels);
+  l.misc = l.fin + 2 * static_cast<int>(sizeof(Fin));
+  l.total = l.misc + static_cast<int>(sizeof(Misc));
+  return l;
+}
+
+// ---- PTX ----------------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* desc, uint32_t bar, int32_t x, int32_t y, int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          dst),
+      "l"(desc), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+// Two 16 x 16 byte matrices transposed; lanes 0-15 and 16-31 give their rows' addresses. Lane l gets, of each,
+// columns l / 4 and 8 + l / 4, rows 4 (l % 4) .. + 3 a register.
+__device__ __forceinline__ void ldmatrix_b8_trans_x2(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// 16 lanes x 32 columns: lane l holds rows l / 4 and 8 + l / 4 of columns 4 i + l % 4 in r[2 i] and r[2 i + 1].
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// fp32 accumulator, A and B both fp16 or both bf16, B with N contiguous (MN-major).
+__device__ __forceinline__ constexpr uint32_t idesc_f16_mn(uint32_t N, bool bf16) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (1u << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two E4M3 bytes (the low or the high half of w) as fp16x2.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f16x2_f32(uint32_t w) {
+  float2 f;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(w));
   return f;
 }
-__device__ __forceinline__ float scale_value(uint32_t b) { return __uint_as_float(b == 0 ? 0x00400000u : b << 23); }
+__device__ __forceinline__ uint32_t f16x2_rn(float first, float second) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(second), "f"(first));
+  return r;
+}
+// A named barrier among `count` threads that also tells whether any of them said so.
+__device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t count, bool said) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(id), "r"(count), "r"(said ? 1u : 0u) : "memory");
+  return r != 0;
+}
+// 2^(b - 127) as fp32, b in [0, 254].
+__device__ __forceinline__ float pow2_byte(uint32_t b) { return __uint_as_float(b == 0 ? 0x00400000u : b << 23); }
+// Floats as integers of the same order (no NaN).
+__device__ __forceinline__ int32_t ordered(float f) {
+  const int32_t i = __float_as_int(f);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float of_ordered(int32_t i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
-__global__ void __launch_bounds__(kThreads) split_kernel(const Args a) {
-  extern __shared__ float sm[];
-  float* q = sm;                    // [8][D]
-  float* x = q + kHeads * a.D;      // [32][D]
-  float* p = x + kTile * a.D;       // [8][32]
-  __shared__ float m[kHeads], l[kHeads], f[kHeads];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / (a.kv * a.blocks), kv = blockIdx.x / a.blocks % a.kv, h0 = blockIdx.x % a.blocks * kHeads;
-  const int nh = min(kHeads, a.G - h0), head0 = kv * a.G + h0;
-  const int64_t len = max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.lens[b]), static_cast<int64_t>(a.table_width) * a.page_size));
-  const int64_t tiles = (len + kTile - 1) / kTile;
-  const int64_t t0 = tiles * blockIdx.y / a.splits * kTile, t1 = min(len, tiles * (blockIdx.y + 1) / a.splits * kTile);
-  for (int i = tid; i < kHeads * a.D; i += kThreads) {
-    const int h = i / a.D;
-    q[i] = h < nh ? __uint_as_float(static_cast<uint32_t>(a.q[b * a.ldq + (head0 + h) * a.ldqh + i % a.D]) << 16) : 0.f;
+// ---- work -----------------------------------------------------------------------------------
+__device__ __forceinline__ int32_t length_of(const Args& a, int32_t len) {
+  const int64_t cap = static_cast<int64_t>(a.table_width) * a.page_size;
+  return len <= 0 ? 0 : static_cast<int32_t>(cap < len ? cap : len);
+}
+// A sequence without tokens is one unit, which writes its zeros.
+__device__ __forceinline__ int32_t units_of(int32_t len) { return len <= 0 ? 1 : (len - 1) / kUnit + 1; }
+
+// Walks a CTA's segments: runs of units of one item. An item is (sequence b, sub = cache head * blocks + block).
+struct Segments {
+  const Args& a;
+  int64_t left;
+  int32_t b, sub, u, len, units, next_len;
+  // the current segment
+  int32_t seg_b, seg_sub, seg_len, u0, u1, seg_units;
+
+  __device__ Segments(const Args& args, const Misc& m) : a(args), left(m.w1 - m.w0), b(m.b0), sub(m.sub0), u(m.u0) {
+    len = left > 0 ? length_of(a, a.lens[b]) : 0;
+    units = units_of(len);
+    next_len = left > 0 && b + 1 < a.B ? a.lens[b + 1] : 0;
   }
-  if (tid < kHeads) m[tid] = -INFINITY, l[tid] = 0.f;
-  float o[kHeads][2] = {};
-  __syncthreads();
-  for (int64_t t = t0; t < t1; t += kTile) {
-    for (int which = 0; which < 2; ++which) {
-      const Cache& c = which == 0 ? a.k : a.v;
-      if (which == 0 || !a.shared) {
-        for (int i = tid; i < kTile * a.D; i += kThreads) {
-          const int64_t pos = t + i / a.D;
-          const int d = i % a.D;
-          float v = 0.f;
-          if (pos < t1) {
-            const uint32_t page = a.table[b * a.ld_table + pos / a.page_size], at = pos % a.page_size;
-            if (page < a.pages)
-              v = code_value(c.data[page * c.page + at * c.token + kv * c.head + d]) *
-                  scale_value(c.sf[page * c.sf_page + at * c.sf_token + kv * c.sf_head + d / 32]);
-          }
-          x[i] = v;
-        }
-        __syncthreads();
-      }
-      if (which == 0) {
-        for (int i = warp; i < kHeads * kTile; i += kThreads / 32) {
-          const int h = i / kTile, r = i % kTile;
-          float s = 0.f;
-          for (int d = lane; d < a.D; d += 32) s = fmaf(q[h * a.D + d], x[r * a.D + d], s);
-          for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-          const int64_t pos = t + r;
-          const bool there = pos < t1 && static_cast<uint32_t>(a.table[b * a.ld_table + pos / a.page_size]) < a.pages;
-          if (lane == 0) p[i] = there ? s * a.scale : -INFINITY;
-        }
-        __syncthreads();
-        if (warp < kHeads) {  // one warp per head
-          const float s = p[warp * kTile + lane];
-          float mx = s;
-          for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          const float mn = fmaxf(m[warp], mx);
-          const float e = s == -INFINITY ? 0.f : expf(s - mn);
-          float sum = e;
-          for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-          p[warp * kTile + lane] = e;
-          __syncwarp();
-          if (lane == 0) {
-            f[warp] = m[warp] == -INFINITY ? 0.f : expf(m[warp] - mn);
-            l[warp] = l[warp] * f[warp] + sum;
-            m[warp] = mn;
-          }
-        }
-        __syncthreads();
+  __device__ bool next() {
+    if (left <= 0) return false;
+    if (u == units) {
+      u = 0;
+      if (++sub == a.kv * a.blocks) {
+        sub = 0;
+        ++b;
+        len = length_of(a, next_len);
+        units = units_of(len);
+        next_len = b + 1 < a.B ? a.lens[b + 1] : 0;
       }
     }
+    seg_b = b;
+    seg_sub = sub;
+    seg_len = len;
+    seg_units = units;
+    u0 = u;
+    const int64_t take = units - u < left ? units - u : left;
+    u1 = u0 + static_cast<int32_t>(take);
+    u = u1;
+    left -= take;
+    return true;
+  }
+  __device__ int tiles() const { return (u1 - u0 + 1) / 2; }
+  __device__ int32_t start(int tile) const { return (u0 + 2 * tile) * kUnit; }
+  // tokens of a tile (0 only in a sequence without any)
+  __device__ int32_t tokens(int tile) const {
+    const int32_t e = min(u1 * kUnit, seg_len), n = e - start(tile);
+    return n < kTile ? (n < 0 ? 0 : n) : kTile;
+  }
+  __device__ bool whole() const { return u0 == 0 && u1 == seg_units; }
+  __device__ int head0() const { return seg_sub / a.blocks * a.G + seg_sub % a.blocks * a.block_heads; }
+  __device__ int heads() const { return min(a.block_heads, a.G - seg_sub % a.blocks * a.block_heads); }
+};
+
+// Position in a ring of n barriers: the slot and the parity of its current use.
+struct Ring {
+  int n, slot = 0;
+  uint32_t phase = 0;
+  __device__ explicit Ring(int count) : n(count) {}
+  __device__ void next() {
+    if (++slot == n) slot = 0, phase ^= 1;
+  }
+};
+
+__device__ __forceinline__ void report_timeout(int32_t* status) {
+  if (status != nullptr) atomicCAS(status, 0, MXQ_ERR_TIMEOUT);
+}
+// A bounded wait; once one has run out nothing waits any more (results are void, every loop still ends).
+__device__ __forceinline__ void wait_bar(Misc& m, const Args& a, uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return;
+  if (m.dead) return;
+  if (!mbar_wait_bounded(bar, parity)) {
+    m.dead = 1;
+    report_timeout(a.status);
+  }
+}
+
+template <int GP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ Args a) {
+  constexpr int HPT = GP / 2;             // heads of a softmax or output thread
+  constexpr int SB = GP == 64 ? 1 : 2;    // S buffers in TMEM
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const Layout lay = layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs);
+  Misc& m = *reinterpret_cast<Misc*>(smem + lay.misc);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool shared_kv = a.v_sf == nullptr;
+  const int NP = a.panels, S = a.kv * a.blocks;
+  const int ring_k = shared_kv ? a.ring : a.ring / 2, ring_v = shared_kv ? a.ring : a.ring - ring_k;
+  const int sf_bytes = sf_buf_bytes(NP);
+#define BAR(x) smem_u32(&m.x)
+
+  pdl_launch_dependents();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&m.tmem), 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < a.ring; ++i) {
+      mbar_init(BAR(ring_full[i]), 1);
+      mbar_init(BAR(ring_empty[i]), shared_kv ? 9 : i < ring_k ? 1 : 8);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(BAR(sf_full[i]), 2), mbar_init(BAR(sf_empty[i]), 17);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(s_full[i]), 1), mbar_init(BAR(s_empty[i]), 8);
+      mbar_init(BAR(p_full[i]), 8), mbar_init(BAR(p_empty[i]), 1);
+      mbar_init(BAR(fin_full[i]), 8), mbar_init(BAR(fin_empty[i]), 8);
+    }
+    for (int i = 0; i < kVSlots; ++i) mbar_init(BAR(v_full[i]), 4), mbar_init(BAR(v_empty[i]), 1);
+    mbar_init(BAR(q_full), 8), mbar_init(BAR(q_empty), 1);
+    mbar_init(BAR(o_full), 1), mbar_init(BAR(o_empty), 8);
+    mbar_init(BAR(done), 1);
+    fence_mbar_init();
+    m.dead = 0;
+    m.w0 = m.w1 = 0;
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  if (tid < kMaxHeads) m.red[tid] = INT32_MIN;
+
+  // The CTA's share: a scan of the sequences' units, a run of sequences per thread.
+  {
+    const int32_t per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    int64_t sum = 0;
+    for (int32_t b = b0; b < b1; ++b) sum += units_of(length_of(a, a.lens[b]));
+    int64_t inc = sum;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int d = tid + j * kThreads;
-      if (d < a.D)
-        for (int h = 0; h < kHeads; ++h) {
-          float acc = o[h][j] * f[h];
-          for (int r = 0; r < kTile; ++r) acc = fmaf(p[h * kTile + r], x[r * a.D + d], acc);
-          o[h][j] = acc;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) m.sums[warp] = inc;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += m.sums[w];
+      total += m.sums[w];
+    }
+    before += inc - sum;
+    total *= S;
+    // (no share is empty among the CTAs that have one: the parts of an item lie in consecutive CTAs)
+    const int64_t ctas = total < a.ctas ? total : a.ctas;
+    const int64_t w0 = total * blockIdx.x / ctas, w1 = total * (blockIdx.x + 1) / ctas;
+    if (blockIdx.x < ctas && before * S <= w0 && w0 < (before + sum) * S) {  // one thread
+      int64_t at = w0 - before * S;
+      int32_t b = b0, units = units_of(length_of(a, a.lens[b]));
+      while (at >= static_cast<int64_t>(units) * S) {
+        at -= static_cast<int64_t>(units) * S;
+        units = units_of(length_of(a, a.lens[++b]));
+      }
+      m.b0 = b;
+      m.sub0 = static_cast<int32_t>(at / units);
+      m.u0 = static_cast<int32_t>(at % units);
+      m.w0 = w0;
+      m.w1 = w1;
+      m.total = total;
+      m.ctas = ctas;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = m.tmem;
+
+  if (warp == 0) {
+    // ---- TMA: a panel of a tile's rows per ring slot, a lane per box ----
+    Segments seg(a, m);
+    Ring rk(ring_k), rv(ring_v);
+    int used_k = 0, used_v = 0;
+    while (seg.next()) {
+      const int tiles = seg.tiles(), kvh = seg.seg_sub / a.blocks;
+      const int32_t* row = a.table + seg.seg_b * a.ld_table;
+      auto page_of = [&](int tile) {  // the page of this lane's box
+        const int32_t t = seg.start(tile) + lane * a.box;
+        return tile < tiles && lane * a.box < seg.tokens(tile) ? row[static_cast<uint32_t>(t) / a.page_size] : 0;
+      };
+      int32_t page = page_of(0);
+      for (int i = 0; i < tiles; ++i) {
+        const int32_t next_page = page_of(i + 1);
+        const int32_t t = seg.start(i) + lane * a.box, n = seg.tokens(i);
+        const int boxes = (n + a.box - 1) / a.box;
+        const int32_t place = static_cast<int32_t>(static_cast<uint32_t>(t) % a.page_size);
+        for (int half = 0; half < (shared_kv ? 1 : 2); ++half) {
+          Ring& r = half == 0 ? rk : rv;
+          const int slot0 = half == 0 ? 0 : ring_k;
+          for (int p = 0; p < NP; ++p) {
+            const int s = slot0 + r.slot;
+            wait_bar(m, a, BAR(ring_empty[s]), r.phase ^ 1);
+            if (__any_sync(0xffffffffu, m.dead)) break;
+            if (lane == 0) mbar_arrive_expect_tx(BAR(ring_full[s]), boxes * a.box * 128);
+            __syncwarp();
+            if (lane < boxes)
+              tma_load_4d(sbase + lay.ring + s * kPanel + lane * a.box * 128, half == 0 ? &map_k : &map_v, BAR(ring_full[s]),
+                          p * 128, place, kvh, page);
+            r.next();
+            (half == 0 ? used_k : used_v) += 1;
+          }
+          if (__any_sync(0xffffffffu, m.dead)) break;
         }
+        if (__any_sync(0xffffffffu, m.dead)) break;
+        page = next_page;
+      }
+      if (__any_sync(0xffffffffu, m.dead)) break;
+    }
+    // every load in flight lands before the CTA leaves
+    for (int half = 0; half < (shared_kv ? 1 : 2); ++half) {
+      const int n = half == 0 ? ring_k : ring_v, used = half == 0 ? used_k : used_v;
+      for (int i = max(0, used - n); i < used; ++i)
+        if (!mbar_wait_bounded(BAR(ring_full[(half == 0 ? 0 : ring_k) + i % n]), (i / n) & 1)) report_timeout(a.status);
+    }
+  } else if (warp == 1) {
+    // ---- MMA ----
+    if (lane == 0) {
+      Segments seg(a, m);
+      Ring rk(ring_k), sf(a.sf_bufs), s(SB), pr(a.p_bufs), vr(kVSlots), one(1);
+      Ring o_ring(1);
+      bool have = seg.next();
+      int wide_next = 0;
+      auto issue_qk = [&](bool first, bool last) {
+        if (first) {
+          wait_bar(m, a, BAR(q_full), one.phase);
+          tc_fence_after();
+          for (int p = 0; p < NP; ++p) tc_cp_sf_atom(tmem + kColSfQ + 4 * p, sdesc_sf_atom(sbase + lay.q_sf + 512 * p));
+        }
+        wait_bar(m, a, BAR(sf_full[sf.slot]), sf.phase);
+        wait_bar(m, a, BAR(s_empty[s.slot]), s.phase ^ 1);
+        tc_fence_after();
+        const uint32_t sf_at = sbase + lay.sf + sf.slot * sf_bytes;
+        wide_next = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1536)->wide;
+        const uint32_t d = tmem + kColS + s.slot * 2 * GP, sfk = tmem + (s.slot == 0 ? kColSfK : kColSfK1);
+        for (int p = 0; p < NP; ++p) {
+          wait_bar(m, a, BAR(ring_full[rk.slot]), rk.phase);
+          tc_fence_after();
+          tc_cp_sf_atom(sfk + 4 * p, sdesc_sf_atom(sf_at + 512 * p));
+          const uint64_t ad = sdesc_kmajor_sw128(sbase + lay.ring + rk.slot * kPanel);
+          const uint64_t bd = sdesc_kmajor_sw128(sbase + lay.q + p * GP * 256);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc_mxf8(128, 2 * GP, k, k), sfk + 4 * p, tmem + kColSfQ + 4 * p,
+                        (p | k) != 0 ? 1u : 0u);
+          tc_commit(BAR(ring_empty[rk.slot]));
+          rk.next();
+        }
+        tc_commit(BAR(s_full[s.slot]));
+        tc_commit(BAR(sf_empty[sf.slot]));
+        if (last) {
+          tc_commit(BAR(q_empty));
+          one.next();
+        }
+        sf.next();
+        s.next();
+      };
+      if (have) issue_qk(true, seg.tiles() == 1);
+      while (have) {
+        const int tiles = seg.tiles();
+        for (int i = 0; i < tiles; ++i) {
+          const int wide = wide_next, halves = seg.tokens(i) > 64 ? 2 : 1;
+          if (i + 1 < tiles) issue_qk(false, i + 2 == tiles);
+          if (i == 0) wait_bar(m, a, BAR(o_empty), o_ring.phase ^ 1);
+          wait_bar(m, a, BAR(p_full[pr.slot]), pr.phase);
+          tc_fence_after();
+          const uint32_t idesc = wide != 0 ? idesc_f16_mn(GP, true) : idesc_f16_mn(GP, false);
+          for (int p = 0; p < NP; ++p)
+            for (int h = 0; h < halves; ++h) {
+              wait_bar(m, a, BAR(v_full[vr.slot]), vr.phase);
+              tc_fence_after();
+              const uint64_t bd = sdesc(sbase + lay.p + pr.slot * kPanel + h * 64 * 128, 1024, 1024, 2);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma_f16_ts(tmem + p * GP, tmem + kColV + 32 * vr.slot + 8 * k, bd + 128 * k, idesc, (i | h | k) != 0 ? 1u : 0u);
+              tc_commit(BAR(v_empty[vr.slot]));
+              vr.next();
+            }
+          tc_commit(BAR(p_empty[pr.slot]));
+          pr.next();
+        }
+        tc_commit(BAR(o_full));
+        o_ring.next();
+        have = seg.next();
+        if (have) issue_qk(true, seg.tiles() == 1);
+      }
+      tc_commit(BAR(done));
+      if (!mbar_wait_bounded(BAR(done), 0)) report_timeout(a.status);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---- scales: K atoms, V table, the tokens that take part, the pivot ----
+    const int w = warp - 2;
+    Segments seg(a, m);
+    Ring sf(a.sf_bufs);
+    uint32_t parity = 0;
+    while (seg.next()) {
+      const int tiles = seg.tiles(), kvh = seg.seg_sub / a.blocks;
+      const int32_t* row = a.table + seg.seg_b * a.ld_table;
+      int32_t pivot = 0;
+      // lane: tokens 64 w + lane and 32 on
+      uint32_t page[2], kw[2][4], vw[2][4];
+      auto pages_of = [&](int tile, uint32_t (&pg)[2]) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int32_t r = 64 * w + 32 * j + lane;
+          pg[j] = tile < tiles && r < seg.tokens(tile)
+                      ? static_cast<uint32_t>(row[static_cast<uint32_t>(seg.start(tile) + r) / a.page_size]) : 0xFFFFFFFFu;
+        }
+      };
+      auto words_of = [&](int tile, const uint32_t (&pg)[2], uint32_t (&kk)[2][4], uint32_t (&vv)[2][4]) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const bool ok = pg[j] < a.pages;
+          const uint32_t at = static_cast<uint32_t>(seg.start(tile) + 64 * w + 32 * j + lane) % a.page_size;
+          const uint32_t* ks = reinterpret_cast<const uint32_t*>(a.k_sf + (ok ? pg[j] * a.k_sf_page + at * a.k_sf_token + kvh * a.k_sf_head : 0));
+          const uint32_t* vs = reinterpret_cast<const uint32_t*>(a.v_sf + (ok ? pg[j] * a.v_sf_page + at * a.v_sf_token + kvh * a.v_sf_head : 0));
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            kk[j][p] = ok && p < NP ? ks[p] : 0;
+            vv[j][p] = shared_kv ? kk[j][p] : ok && p < NP ? vs[p] : 0;
+          }
+        }
+      };
+      uint32_t next_page[2];
+      pages_of(0, page);
+      pages_of(1, next_page);
+      words_of(0, page, kw, vw);
+      for (int i = 0; i < tiles; ++i) {
+        uint32_t nkw[2][4], nvw[2][4], far_page[2];
+        words_of(i + 1, next_page, nkw, nvw);
+        pages_of(i + 2, far_page);
+        const bool ok[2] = {page[0] < a.pages, page[1] < a.pages};
+        uint32_t hi = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int p = 0; p < 4; ++p) hi = __vmaxu4(hi, vw[j][p]);
+        hi = max(max(hi & 0xFF, (hi >> 8) & 0xFF), max((hi >> 16) & 0xFF, hi >> 24));
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        const uint32_t v0 = __ballot_sync(0xffffffffu, ok[0]), v1 = __ballot_sync(0xffffffffu, ok[1]);
+        if (lane == 0) m.sf_red[parity][w] = static_cast<int32_t>(hi);
+        named_barrier(1, 64);
+        const int32_t top = max(m.sf_red[parity][0], m.sf_red[parity][1]);
+        if (top > pivot + 7) pivot = top;
+        bool low = false;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const int32_t b = (vw[j][p] >> (8 * g)) & 0xFF;
+              low |= b != 0 && b < pivot - 15;
+            }
+        low = __any_sync(0xffffffffu, low);
+        if (lane == 0) m.sf_red[parity][2 + w] = low;
+        wait_bar(m, a, BAR(sf_empty[sf.slot]), sf.phase ^ 1);
+        named_barrier(1, 64);
+        const bool wide = (m.sf_red[parity][2] | m.sf_red[parity][3]) != 0;
+        parity ^= 1;
+        uint8_t* const buf = smem + lay.sf + sf.slot * sf_bytes;
+        uint16_t* const tab = reinterpret_cast<uint16_t*>(buf + NP * 512);
+        TileInfo* const info = reinterpret_cast<TileInfo*>(buf + NP * 1536);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          if (p >= NP) break;
+          *reinterpret_cast<uint2*>(buf + p * 512 + lane * 16 + w * 8) = make_uint2(kw[0][p], kw[1][p]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const int32_t e = static_cast<int32_t>((vw[j][p] >> (8 * g)) & 0xFF) - pivot;
+              uint32_t x;  // 2^e, e <= 7
+              if (wide) x = e >= -126 ? (e + 127) << 7 : e >= -133 ? 0x80u >> (-126 - e) : 0;
+              else x = e >= -14 ? (e + 15) << 10 : e >= -24 ? 0x400u >> (-14 - e) : 0;
+              tab[(4 * p + g) * 128 + 64 * w + 32 * j + lane] = static_cast<uint16_t>(ok[j] ? x : 0);
+            }
+        }
+        if (lane == 0) {
+          info->valid[2 * w] = v0;
+          info->valid[2 * w + 1] = v1;
+          if (w == 0) info->pivot = pivot, info->wide = wide;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(sf_full[sf.slot]));
+        sf.next();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          page[j] = next_page[j];
+          next_page[j] = far_page[j];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) kw[j][p] = nkw[j][p], vw[j][p] = nvw[j][p];
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ---- queries and softmax ----
+    const int quarter = warp & 3, h0 = (warp - 4) / 4 * HPT, st = tid - 128;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    const float c = a.scale * 1.4426950408889634f;
+    const int t = 32 * quarter + lane;
+    // the row of P of this thread's token: tokens 4 j + i of 16 are rows 2 j + i (i < 2) and 6 + 2 j + i
+    const int prow = (t & ~15) + ((t >> 2) & 3) * 2 + (t & 1) + ((t & 2) << 2);
+    Segments seg(a, m);
+    Ring sf(a.sf_bufs), s(SB), pr(a.p_bufs), one(1), fin(2);
+    while (seg.next()) {
+      const int tiles = seg.tiles(), heads = seg.heads();
+      // q as hi + lo: 8 values a lane, 4 lanes a group
+      wait_bar(m, a, BAR(q_empty), one.phase ^ 1);
+      one.next();
+      {
+        const uint16_t* q = a.q + seg.seg_b * a.ldq + seg.head0() * a.ldqh;
+        const int chunks = a.D / 8;
+#pragma unroll 4
+        for (int i = st; i < GP * chunks; i += kSoftThreads) {
+          const int h = i / chunks, d = (i - h * chunks) * 8;
+          const uint4 x = h < heads ? *reinterpret_cast<const uint4*>(q + h * a.ldqh + d) : make_uint4(0, 0, 0, 0);
+          uint32_t amax = absmax8(x);
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          const uint32_t code = ue8m0_from_bf16_amax(amax), low = code >= 4 ? code - 4 : 0;
+          const float inv = ue8m0_inverse(code), up = __uint_as_float((127 + code - low) << 23);
+          const uint2 hi = quant8(x, inv);
+          uint2 lo;
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, hs[2] = {hi.x, hi.y};
+          uint32_t ls[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t c0, c1;
+            e4m3x4_f16(hs[j], c0, c1);
+            const float2 f0 = f16x2_f32(c0), f1 = f16x2_f32(c1);
+            ls[j] = e4m3x2((bf16_lo(xs[2 * j]) * inv - f0.x) * up, (bf16_hi(xs[2 * j]) * inv - f0.y) * up) |
+                    (e4m3x2((bf16_lo(xs[2 * j + 1]) * inv - f1.x) * up, (bf16_hi(xs[2 * j + 1]) * inv - f1.y) * up) << 16);
+          }
+          lo.x = ls[0], lo.y = ls[1];
+          const int p = d >> 7, col = d & 127;
+          uint8_t* const panel = smem + lay.q + p * GP * 256;
+          const int at = (((col >> 4) ^ (h & 7)) << 4) + (col & 8);  // (GP is a multiple of 8: both rows swizzle alike)
+          *reinterpret_cast<uint2*>(panel + h * 128 + at) = hi;
+          *reinterpret_cast<uint2*>(panel + (GP + h) * 128 + at) = lo;
+          if ((lane & 3) == 0) {
+            uint8_t* const atom = smem + lay.q_sf + p * 512;
+            atom[(h & 31) * 16 + (h >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(code);
+            const int r = GP + h;
+            atom[(r & 31) * 16 + (r >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(low);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(q_full));
+      float l[HPT];
+#pragma unroll
+      for (int i = 0; i < HPT; ++i) l[i] = 0.f;
+      int32_t pivot = 0;
+      // (the last segment's references were read before this barrier)
+      named_barrier(2, kSoftThreads);
+      if (st < GP) m.ref[st] = kLowRef;
+      named_barrier(2, kSoftThreads);
+      for (int i = 0; i < tiles; ++i) {
+        float x[HPT];
+        wait_bar(m, a, BAR(s_full[s.slot]), s.phase);
+        tc_fence_after();
+        const uint32_t sc = t_lane + kColS + s.slot * 2 * GP + h0;
+#pragma unroll
+        for (int j = 0; j < HPT; j += 8) {
+          uint32_t hi[8], lo[8];
+          tmem_ld_x8(sc + j, hi);
+          tmem_ld_x8(sc + GP + j, lo);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[j + k] = (__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(s_empty[s.slot]));
+        s.next();
+        wait_bar(m, a, BAR(sf_full[sf.slot]), sf.phase);
+        const TileInfo* const info = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1536);
+        const bool valid = (info->valid[quarter] >> lane) & 1;
+        const int32_t new_pivot = info->pivot;
+        const bool wide = info->wide != 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(sf_empty[sf.slot]));
+        sf.next();
+        float over = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < HPT; j += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j]);
+          over = fmaxf(fmaxf(over, fmaxf(x[j] - r.x, x[j + 1] - r.y)), fmaxf(x[j + 2] - r.z, x[j + 3] - r.w));
+        }
+        if (named_barrier_or(2, kSoftThreads, (valid && over > kSlack) || new_pivot != pivot)) {
+          // new references: the largest scores so far
+#pragma unroll
+          for (int j = 0; j < HPT; ++j) {
+            const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered(x[j]) : INT32_MIN);
+            if (lane == 0) atomicMax(&m.red[h0 + j], top);
+          }
+          named_barrier(2, kSoftThreads);
+          if (st < GP) {
+            const float old = m.ref[st], top = m.red[st] == INT32_MIN ? kLowRef : of_ordered(m.red[st]), now = fmaxf(old, top);
+            m.ref[st] = now;
+            m.fac[st] = ex2(old - now);
+            m.red[st] = INT32_MIN;
+          }
+          named_barrier(2, kSoftThreads);
+#pragma unroll
+          for (int j = 0; j < HPT; ++j) l[j] *= m.fac[h0 + j];
+          if (i > 0) {
+            // every product so far is in O, and the next waits for P
+            const int prev = pr.slot == 0 ? a.p_bufs - 1 : pr.slot - 1;
+            wait_bar(m, a, BAR(p_empty[prev]), pr.slot == 0 ? pr.phase ^ 1 : pr.phase);
+            tc_fence_after();
+            const int down = pivot - new_pivot;  // <= 0
+            const float pf = down < -126 ? 0.f : __uint_as_float((127 + down) << 23);
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+              for (int j = 0; j < HPT; j += 8) {
+                uint32_t r[8];
+                tmem_ld_x8(t_lane + p * GP + h0 + j, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * m.fac[h0 + j + k] * pf);
+                tmem_st_x8(t_lane + p * GP + h0 + j, r);
+              }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          pivot = new_pivot;
+        }
+        wait_bar(m, a, BAR(p_empty[pr.slot]), pr.phase ^ 1);
+        uint8_t* const row = smem + lay.p + pr.slot * kPanel + prow * 128;
+#pragma unroll
+        for (int j = 0; j < HPT; j += 8) {
+          float e[8];
+          const float4 r0 = *reinterpret_cast<const float4*>(&m.ref[h0 + j]), r1 = *reinterpret_cast<const float4*>(&m.ref[h0 + j + 4]);
+          const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            e[k] = valid ? ex2(x[j + k] - r[k]) : 0.f;
+            l[j + k] += e[k];
+          }
+          uint4 v;
+          if (wide) v = make_uint4(bf16x2_rn(e[0], e[1]), bf16x2_rn(e[2], e[3]), bf16x2_rn(e[4], e[5]), bf16x2_rn(e[6], e[7]));
+          else v = make_uint4(f16x2_rn(e[0], e[1]), f16x2_rn(e[2], e[3]), f16x2_rn(e[4], e[5]), f16x2_rn(e[6], e[7]));
+          *reinterpret_cast<uint4*>(row + ((((h0 + j) >> 3) ^ (prow & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(p_full[pr.slot]));
+        pr.next();
+      }
+      // sums over the quarter's tokens: halves of the heads change hands at each step
+      Fin& f = *reinterpret_cast<Fin*>(smem + lay.fin + fin.slot * sizeof(Fin));
+      wait_bar(m, a, BAR(fin_empty[fin.slot]), fin.phase ^ 1);
+#pragma unroll
+      for (int o = 16, n = HPT; o > 0; o >>= 1) {
+        if (n > 1) {
+          n >>= 1;
+#pragma unroll
+          for (int j = 0; j < n; ++j) {
+            const bool up = (lane & o) != 0;
+            const float keep = up ? l[j + n] : l[j], give = up ? l[j] : l[j + n];
+            l[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        } else {
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+        }
+      }
+      constexpr int kShare = 32 / HPT;  // lanes that hold the same head
+      if (lane % kShare == 0) f.sum[quarter][h0 + lane / kShare] = l[0];
+      if (quarter == 0 && lane < HPT) f.ref[h0 + lane] = m.ref[h0 + lane];
+      if (st == 0) f.pivot = pivot;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(fin_full[fin.slot]));
+      fin.next();
+    }
+  } else {
+    // ---- V^T and the outputs ----
+    const int quarter = warp & 3, set = (warp - 12) / 4, h0 = set * HPT;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    Segments seg(a, m);
+    Ring rv(ring_v), sf(a.sf_bufs), fin(2), o_ring(1);
+    const int slot0 = shared_kv ? 0 : ring_k;
+    uint32_t chunk = 0;
+    int2 owner = make_int2(0, 0);
+    while (seg.next()) {
+      const int tiles = seg.tiles();
+      for (int i = 0; i < tiles; ++i) {
+        const int halves = seg.tokens(i) > 64 ? 2 : 1;
+        wait_bar(m, a, BAR(sf_full[sf.slot]), sf.phase);
+        const uint8_t* const buf = smem + lay.sf + sf.slot * sf_bytes;
+        const TileInfo* const info = reinterpret_cast<const TileInfo*>(buf + NP * 1536);
+        const bool wide = info->wide != 0;
+        const uint32_t valid0 = info->valid[2 * set], valid1 = info->valid[2 * set + 1];
+        const bool full = (valid0 & valid1) == 0xFFFFFFFFu;
+        for (int p = 0; p < NP; ++p) {
+          const int s = slot0 + rv.slot;
+          wait_bar(m, a, BAR(ring_full[s]), rv.phase);
+          if (set < halves) {
+            const uint32_t ci = chunk + p * halves + set, vs = ci % kVSlots, vphase = (ci / kVSlots) & 1;
+            const uint32_t panel = sbase + lay.ring + s * kPanel;
+            const uint16_t* const tab = reinterpret_cast<const uint16_t*>(buf + NP * 512) + (4 * p + quarter) * 128 + 64 * set;
+            uint32_t w0[16], w1[16];  // features 0-15 and 16-31 of the quarter's 32
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int t = 64 * set + 16 * k + (lane & 15), c16 = 2 * quarter + (lane >> 4);
+              uint32_t r[4];
+              ldmatrix_b8_trans_x2(panel + t * 128 + ((c16 ^ (t & 7)) << 4), r);
+              const uint2 sc = *reinterpret_cast<const uint2*>(tab + 16 * k + 4 * (lane & 3));
+              if (!full) {  // tokens that take no part may be NaN
+                const uint32_t bits = ((k < 2 ? valid0 : valid1) >> (16 * (k & 1) + 4 * (lane & 3))) & 15;
+                const uint32_t mask = ((bits * 0x00204081u) & 0x01010101u) * 0xFFu;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[j] &= mask;
+              }
+              uint32_t lo[4], hi[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) e4m3x4_f16(r[j], lo[j], hi[j]);
+              if (!wide) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) lo[j] = hmul2(lo[j], sc.x), hi[j] = hmul2(hi[j], sc.y);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float2 fl = f16x2_f32(lo[j]), fh = f16x2_f32(hi[j]);
+                  lo[j] = bf16x2_rn(fl.x * bf16_lo(sc.x), fl.y * bf16_hi(sc.x));
+                  hi[j] = bf16x2_rn(fh.x * bf16_lo(sc.y), fh.y * bf16_hi(sc.y));
+                }
+              }
+              w0[4 * k] = lo[0], w0[4 * k + 1] = lo[1], w0[4 * k + 2] = hi[0], w0[4 * k + 3] = hi[1];
+              w1[4 * k] = lo[2], w1[4 * k + 1] = lo[3], w1[4 * k + 2] = hi[2], w1[4 * k + 3] = hi[3];
+            }
+            wait_bar(m, a, BAR(v_empty[vs]), vphase ^ 1);
+            tc_fence_after();
+            const uint32_t dst = t_lane + kColV + 32 * vs;
+            tmem_st_16x128b_x8(dst, w0);
+            tmem_st_16x128b_x8(dst + (16u << 16), w1);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(v_full[vs]));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(ring_empty[s]));
+          rv.next();
+        }
+        chunk += NP * halves;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(sf_empty[sf.slot]));
+        sf.next();
+      }
+      // outputs: this thread's feature 128 p + 32 quarter + lane of its heads
+      wait_bar(m, a, BAR(fin_full[fin.slot]), fin.phase);
+      wait_bar(m, a, BAR(o_full), o_ring.phase);
+      tc_fence_after();
+      const Fin& f = *reinterpret_cast<const Fin*>(smem + lay.fin + fin.slot * sizeof(Fin));
+      const float unit = pow2_byte(f.pivot);
+      const bool whole = seg.whole();
+      const int heads = seg.heads(), head0 = seg.head0();
+      const int part = 2 * blockIdx.x + (seg.u0 == 0 ? 1 : 0);
+      if (!whole && seg.u0 == 0) {  // the item's first part, and this CTA's last segment
+        const int64_t end = m.w1 + seg.seg_units - seg.u1;  // behind the item's last unit
+        owner = make_int2(1 + seg.seg_b * S + seg.seg_sub, static_cast<int>((end * m.ctas + m.total - 1) / m.total - 1));
+      }
+      const int64_t groups = static_cast<int64_t>(a.H) * a.D / 32, b4 = (static_cast<int64_t>(a.B) + 3) / 4 * 4;
+      for (int p = 0; p < NP; ++p) {
+#pragma unroll 1
+        for (int j = 0; j < HPT; j += 8) {
+          if (h0 + j >= heads) break;
+          uint32_t r[8];
+          tmem_ld_x8(t_lane + p * GP + h0 + j, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int h = h0 + j + k;
+            if (h >= heads) break;
+            const float sum = f.sum[0][h] + f.sum[1][h] + f.sum[2][h] + f.sum[3][h];
+            const float v = sum > 0.f ? __uint_as_float(r[k]) * (1.0f / sum) * unit : 0.f;
+            const int d = 128 * p + 32 * quarter + lane;
+            if (!whole) {
+              a.part[(static_cast<int64_t>(part) * GP + h) * a.D + d] = v;
+              if (d == 0) a.stat[part * GP + h] = make_float2(f.ref[h], sum);
+            } else {
+              const int64_t row = seg.seg_b;
+              const int head = head0 + h;
+              const uint32_t y = bf16x2_rn(v, 0.f) & 0xFFFFu;
+              const int64_t at = (row * a.H + head) * a.D + d;
+              if (a.o != nullptr) a.o[at] = static_cast<uint16_t>(y);
+              if (a.oq != nullptr) {
+                const uint32_t code = ue8m0_from_bf16_amax(__reduce_max_sync(0xffffffffu, y & 0x7FFFu));
+                a.oq[at] = static_cast<uint8_t>(e4m3x2(bf16_lo(y) * ue8m0_inverse(code), 0.f));
+                const int64_t g = (static_cast<int64_t>(head) * a.D + d) >> 5;
+                if (lane == 0) {
+                  if (a.sf_rm != nullptr) a.sf_rm[row * groups + g] = static_cast<uint8_t>(code);
+                  if (a.sf_pk != nullptr) a.sf_pk[(g / 4 * b4 + row) * 4 + g % 4] = static_cast<uint8_t>(code);
+                  if (a.sf_tl != nullptr) a.sf_tl[tiled128x4_word_offset(row, g / 4, groups / 4) + g % 4] = static_cast<uint8_t>(code);
+                }
+              }
+              if (a.lse != nullptr && d == 0)
+                a.lse[row * a.H + head] = sum > 0.f ? (f.ref[h] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(o_empty)), mbar_arrive(BAR(fin_empty[fin.slot]));
+      o_ring.next();
+      fin.next();
+    }
+    if (tid == 12 * 32) a.owner[blockIdx.x] = owner;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+#undef BAR
+}
+
+// Adds the parts of the items that more than one CTA held: a block takes 128 features of one head, a warp
+// every eighth part, added in fixed order. Also the scale layouts' padding rows.
+constexpr int kJoinThreads = 256;
+constexpr int kMaxCtas = 512;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int gp) {
+  __shared__ int16_t owners[kMaxCtas];
+  __shared__ int count;
+  __shared__ float weight[kMaxCtas];
+  __shared__ float4 acc[kJoinThreads / 32][32];
+  __shared__ float tops[kJoinThreads / 32], sums[kJoinThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t words = static_cast<int64_t>(a.H) * a.D / 128, b4 = (static_cast<int64_t>(a.B) + 3) / 4 * 4,
+                b128 = (static_cast<int64_t>(a.B) + 127) / 128 * 128;
+  for (int64_t i = blockIdx.x * kJoinThreads + tid; i < words * (b128 - a.B); i += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
+    const int64_t row = a.B + i / words, w = i % words;
+    if (a.sf_pk != nullptr && row < b4) *reinterpret_cast<uint32_t*>(a.sf_pk + (w * b4 + row) * 4) = 0;
+    if (a.sf_tl != nullptr) *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(row, w, words)) = 0;
+  }
+  if (tid == 0) count = 0;
+  pdl_wait_primary();
+  __syncthreads();
+  if (warp == 0)
+    for (int i = 0; i < a.ctas; i += 32) {
+      const bool is = i + lane < a.ctas && a.owner[i + lane].x != 0;
+      const uint32_t all = __ballot_sync(0xffffffffu, is);
+      if (is) owners[count + __popc(all & ((1u << lane) - 1))] = static_cast<int16_t>(i + lane);
+      __syncwarp();
+      if (lane == 0) count += __popc(all);
+      __syncwarp();
+    }
+  __syncthreads();
+  const int S = a.kv * a.blocks, per = a.block_heads * a.panels;
+  for (int64_t i = blockIdx.x; i < static_cast<int64_t>(count) * per; i += gridDim.x) {
+    const int j0 = owners[i / per], h = static_cast<int>(i % per) / a.panels, p = static_cast<int>(i % per) % a.panels;
+    const int2 own = a.owner[j0];
+    const int item = own.x - 1, parts = own.y - j0 + 1, b = item / S, sub = item % S;
+    if (h >= min(a.block_heads, a.G - sub % a.blocks * a.block_heads)) continue;  // block-uniform
+    const int head = sub / a.blocks * a.G + sub % a.blocks * a.block_heads + h;
+    // part k: the first CTA's last segment, the others' first
+    auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * j0 + 1 : 2 * (j0 + k)); };
+    float top = kLowRef;
+    for (int k = tid; k < parts; k += kJoinThreads) top = fmaxf(top, a.stat[slot(k) * gp + h].x);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, tops[w]);
+    float sum = 0.f;
+    for (int k = tid; k < parts; k += kJoinThreads) {
+      const float2 s = a.stat[slot(k) * gp + h];
+      weight[k] = s.y * ex2(s.x - top);
+      sum += weight[k];
+    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+    for (int w = 0; w < kJoinThreads / 32; ++w) sum += sums[w];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = warp; k < parts; k += kJoinThreads / 32) {
+      const float4 x = *reinterpret_cast<const float4*>(a.part + (slot(k) * gp + h) * a.D + 128 * p + 4 * lane);
+      const float w = weight[k];
+      v.x = fmaf(w, x.x, v.x), v.y = fmaf(w, x.y, v.y), v.z = fmaf(w, x.z, v.z), v.w = fmaf(w, x.w, v.w);
+    }
+    acc[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0) {
+      for (int w = 1; w < kJoinThreads / 32; ++w) {
+        const float4 x = acc[w][lane];
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+      const uint2 y = make_uint2(bf16x2_rn(v.x * inv, v.y * inv), bf16x2_rn(v.z * inv, v.w * inv));
+      const int64_t at = (static_cast<int64_t>(b) * a.H + head) * a.D + 128 * p + 4 * lane;
+      if (a.o != nullptr) *reinterpret_cast<uint2*>(a.o + at) = y;
+      if (a.oq != nullptr) {
+        uint32_t amax = max(absmax_bf16x2(y.x), absmax_bf16x2(y.y));
+        for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const uint32_t code = ue8m0_from_bf16_amax(amax);
+        const float s = ue8m0_inverse(code);
+        *reinterpret_cast<uint32_t*>(a.oq + at) = e4m3x2(bf16_lo(y.x) * s, bf16_hi(y.x) * s) | (e4m3x2(bf16_lo(y.y) * s, bf16_hi(y.y) * s) << 16);
+        uint32_t w = code;
+        w |= __shfl_down_sync(0xffffffffu, code, 8) << 8;
+        w |= __shfl_down_sync(0xffffffffu, code, 16) << 16;
+        w |= __shfl_down_sync(0xffffffffu, code, 24) << 24;
+        const int64_t word = static_cast<int64_t>(head) * a.panels + p;
+        if (lane == 0) {
+          if (a.sf_rm != nullptr) *reinterpret_cast<uint32_t*>(a.sf_rm + (b * words + word) * 4) = w;
+          if (a.sf_pk != nullptr) *reinterpret_cast<uint32_t*>(a.sf_pk + (word * b4 + b) * 4) = w;
+          if (a.sf_tl != nullptr) *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(b, word, words)) = w;
+        }
+      }
+      if (a.lse != nullptr && p == 0 && lane == 0)
+        a.lse[static_cast<int64_t>(b) * a.H + head] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
     __syncthreads();
   }
-  for (int h = 0; h < nh; ++h) {
-    float* out = a.part + ((static_cast<int64_t>(b) * a.H + head0 + h) * a.splits + blockIdx.y) * (a.D + 2);
-    if (tid == 0) out[0] = m[h], out[1] = l[h];
-    for (int j = 0; j < 2; ++j)
-      if (tid + j * kThreads < a.D) out[2 + tid + j * kThreads] = o[h][j];
-  }
 }
 
-// One warp per (row, 32 elements of o); rows past the batch write the scale layouts' padding.
-__global__ void __launch_bounds__(128) join_kernel(const Args a) {
-  const int64_t groups = static_cast<int64_t>(a.H) * a.D / 32, w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t row = w / groups, g = w % groups;
-  const int lane = threadIdx.x & 31;
-  const int64_t B4 = (a.B + 3) / 4 * 4, B128 = (static_cast<int64_t>(a.B) + 127) / 128 * 128;
-  if (row >= B128) return;
-  uint32_t code = 0;
-  if (row < a.B) {
-    const int h = g * 32 / a.D, d = g * 32 % a.D + lane;
-    const float* part = a.part + (row * a.H + h) * a.splits * (a.D + 2);
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, part[s * (a.D + 2)]);
-    for (int s = 0; s < a.splits; ++s) {
-      const float* q = part + s * (a.D + 2);
-      const float f = q[0] == -INFINITY ? 0.f : expf(q[0] - m);
-      l = fmaf(q[1], f, l);
-      o = fmaf(q[2 + d], f, o);
-    }
-    const uint32_t y = bf16x2_rn(l > 0.f ? o / l : 0.f, 0.f) & 0xFFFFu;
-    code = ue8m0_from_bf16_amax(__reduce_max_sync(0xffffffffu, y & 0x7FFFu));
-    const int64_t at = row * a.H * a.D + g * 32 + lane;
-    if (a.o != nullptr) a.o[at] = static_cast<uint16_t>(y);
-    if (a.oq != nullptr) a.oq[at] = static_cast<uint8_t>(e4m3x2(bf16_lo(y) * ue8m0_inverse(code), 0.f));
-    if (a.lse != nullptr && d == 0) a.lse[row * a.H + h] = l > 0.f ? m + logf(l) : -INFINITY;
-  }
-  if (lane != 0) return;
-  if (a.sf_rm != nullptr && row < a.B) a.sf_rm[row * groups + g] = code;
-  if (a.sf_pk != nullptr && row < B4) reinterpret_cast<uint8_t*>(a.sf_pk)[(g / 4 * B4 + row) * 4 + g % 4] = code;
-  if (a.sf_tl != nullptr) a.sf_tl[tiled128x4_word_offset(row, g / 4, groups / 4) + g % 4] = code;
+// ---- host -----------------------------------------------------------------------------------
+constexpr int kSmemLimit = 227 * 1024;
+
+int padded_heads(int block_heads) { return block_heads <= 16 ? 16 : block_heads <= 32 ? 32 : 64; }
+
+// A cache as a 4-D tensor (feature, place, head, page) in boxes of 128 features x `box` places.
+bool make_cache_map(CUtensorMap* m, const mxq_kv_cache& c, int box) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.heads),
+                        static_cast<cuuint64_t>(c.pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride), static_cast<cuuint64_t>(c.head_stride),
+                           static_cast<cuuint64_t>(c.page_stride)};
+  cuuint32_t boxes[4] = {128u, static_cast<cuuint32_t>(box), 1u, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.data, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-Cache cache_of(const mxq_kv_cache& c) {
-  return {static_cast<const uint8_t*>(c.data), static_cast<const uint8_t*>(c.sf), c.page_stride, c.token_stride, c.head_stride,
-          c.sf_page_stride, c.sf_token_stride, c.sf_head_stride};
-}
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
-int splits_of(int64_t B, int32_t q_heads, int32_t kv_heads) {
-  const int64_t blocks = B * kv_heads * ((q_heads / kv_heads + kHeads - 1) / kHeads);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, 608 / blocks)));
+template <int GP>
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, Args a, cudaStream_t stream) {
+  a.p_bufs = a.panels * GP >= 256 ? 1 : 2;
+  a.sf_bufs = a.panels <= 2 ? 4 : 2;
+  const int fixed = layout_of(GP, a.panels, 0, a.sf_bufs, a.p_bufs).total;
+  a.ring = std::min(16, (kSmemLimit - fixed) / kPanel);
+  static PerDevice set;
+  cudaError_t e = allow_smem(set, attention_kernel<GP>, kSmemLimit);
+  if (e != cudaSuccess) return e;
+  attention_kernel<GP><<<a.ctas, kThreads, layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs).total, stream>>>(mk, mv, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * num_sms()));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel, a, GP);
 }
 
 }  // namespace
 
 int64_t paged_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim) {
-  return (B * q_heads * splits_of(B, q_heads, kv_heads) * (dim + 2) * 4 + 15) / 16 * 16;
+  (void)B;
+  const int G = q_heads / kv_heads, blocks = (G + kMaxHeads - 1) / kMaxHeads, gp = padded_heads((G + blocks - 1) / blocks);
+  const int64_t ctas = std::min(kMaxCtas, num_sms());
+  return align256(2 * ctas * gp * dim * 4) + align256(2 * ctas * gp * 8) + align256(ctas * 8);
 }
 
 cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t stream) {
@@ -191,9 +1087,16 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
   a.q = static_cast<const uint16_t*>(l.q);
   a.ldq = l.ldq;
   a.ldqh = l.ldqh;
-  a.k = cache_of(k);
-  a.v = cache_of(l.v != nullptr ? *l.v : k);
-  a.shared = l.v == nullptr;
+  a.k_sf = static_cast<const uint8_t*>(k.sf);
+  a.k_sf_page = k.sf_page_stride;
+  a.k_sf_token = k.sf_token_stride;
+  a.k_sf_head = k.sf_head_stride;
+  if (l.v != nullptr) {
+    a.v_sf = static_cast<const uint8_t*>(l.v->sf);
+    a.v_sf_page = l.v->sf_page_stride;
+    a.v_sf_token = l.v->sf_token_stride;
+    a.v_sf_head = l.v->sf_head_stride;
+  }
   a.table = l.table;
   a.ld_table = l.ld_table;
   a.table_width = static_cast<uint32_t>(l.table_width);
@@ -205,25 +1108,31 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
   a.kv = k.heads;
   a.G = l.q_heads / k.heads;
   a.D = k.dim;
-  a.blocks = (a.G + kHeads - 1) / kHeads;
-  a.splits = splits_of(l.B, l.q_heads, k.heads);
+  a.panels = k.dim / 128;
+  a.blocks = (a.G + kMaxHeads - 1) / kMaxHeads;
+  a.block_heads = (a.G + a.blocks - 1) / a.blocks;
+  a.box = std::min(kUnit, k.page_size & -k.page_size);
   a.scale = l.scale;
-  a.part = static_cast<float*>(l.workspace);
   a.o = static_cast<uint16_t*>(l.o);
   a.oq = static_cast<uint8_t*>(l.o_q);
   a.sf_rm = static_cast<uint8_t*>(l.sf_rowmajor);
-  a.sf_pk = static_cast<uint32_t*>(l.sf_packed);
+  a.sf_pk = static_cast<uint8_t*>(l.sf_packed);
   a.sf_tl = static_cast<uint8_t*>(l.sf_tiled);
   a.lse = l.lse;
-  const int bytes = ((kHeads + kTile) * a.D + kHeads * kTile) * 4;
-  static PerDevice set;
-  cudaError_t e = allow_smem(set, split_kernel, ((kHeads + kTile) * 512 + kHeads * kTile) * 4);
-  if (e != cudaSuccess) return e;
-  split_kernel<<<dim3(static_cast<unsigned>(a.B * a.kv * a.blocks), a.splits), kThreads, bytes, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t warps = (l.B + 127) / 128 * 128 * a.H * a.D / 32;
-  join_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  a.status = l.status;
+  const int gp = padded_heads(a.block_heads);
+  const int64_t ctas = std::min(kMaxCtas, num_sms());
+  const int64_t most = l.B * a.kv * a.blocks * ((static_cast<int64_t>(l.table_width) * k.page_size + kUnit - 1) / kUnit);
+  a.ctas = static_cast<int32_t>(std::min(ctas, most));
+  uint8_t* const ws = static_cast<uint8_t*>(l.workspace);
+  a.part = reinterpret_cast<float*>(ws);
+  a.stat = reinterpret_cast<float2*>(ws + align256(2 * ctas * gp * a.D * 4));
+  a.owner = reinterpret_cast<int2*>(ws + align256(2 * ctas * gp * a.D * 4) + align256(2 * ctas * gp * 8));
+  CUtensorMap mk, mv;
+  if (!make_cache_map(&mk, k, a.box)) return cudaErrorInvalidValue;
+  if (l.v == nullptr) mv = mk;
+  else if (!make_cache_map(&mv, *l.v, a.box)) return cudaErrorInvalidValue;
+  return gp == 16 ? launch<16>(mk, mv, a, stream) : gp == 32 ? launch<32>(mk, mv, a, stream) : launch<64>(mk, mv, a, stream);
 }
 
 }  // namespace mxq
