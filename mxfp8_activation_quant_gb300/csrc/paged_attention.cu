@@ -57,10 +57,12 @@ struct Args {
   const int32_t* table;
   int64_t ld_table;
   uint32_t table_width, page_size, pages;
+  uint32_t page_mul, page_shift;  // t / page_size = umulhi(t, page_mul) >> page_shift for t < 2^30
   const int32_t* lens;
   int32_t B, H, kv, G, D, panels;
   int32_t blocks, block_heads;  // blocks of query heads per cache head, and their size
-  int32_t box;                  // tokens of a TMA box
+  int32_t box, box_shift;       // tokens of a TMA box, a power of two
+  int32_t sf_vec;               // bytes of a copy of scales
   int32_t ring, sf_bufs, p_bufs;
   float scale;
   float* part;   // [2 * CTAs][GP][D]
@@ -78,22 +80,22 @@ struct Args {
 
 // Shared memory, from the kernel's sizes. Panels on 1024-byte boundaries (their swizzle).
 struct Layout {
-  int q, p, ring, q_sf, sf, fin, misc, total;
+  int q, p, ring, q_sf, sf, stage, fin, misc, total;
 };
 struct Misc {
   uint64_t ring_full[16], ring_empty[16], sf_full[4], sf_empty[4], s_full[2], s_empty[2], p_full[2], p_empty[2], v_full[kVSlots],
       v_empty[kVSlots], q_full, q_empty, o_full, o_empty, fin_full[2], fin_empty[2], done;
   alignas(16) float ref[kMaxHeads];
-  float fac[kMaxHeads];
+  alignas(16) float fac[kMaxHeads];
   int32_t red[kMaxHeads];
   int64_t sums[kThreads / 32];
   int32_t sf_red[2][4];
-  int64_t w0, w1, total, ctas;
-  int32_t b0, sub0, u0;
+  int64_t w0, w1, per_cta, rest;
+  int32_t b0, kvh0, blk0, u0;
   uint32_t tmem;
   volatile int32_t dead;
 };
-// A buffer of scales: K atoms [panels][512], V table [4 panels][128] of 16 bits, then this.
+// A buffer of scales: K atoms [panels][512], V bytes [panels][128 tokens][4 groups], then this.
 struct TileInfo {
   uint32_t valid[4];
   int32_t pivot, wide;
@@ -106,15 +108,16 @@ struct Fin {
   int32_t pivot;
   int32_t pad[3];
 };
-__host__ __device__ inline int sf_buf_bytes(int panels) { return panels * (512 + 1024) + static_cast<int>(sizeof(TileInfo)); }
-__host__ __device__ inline Layout layout_of(int gp, int panels, int ring, int sf_bufs, int p_bufs) {
+__host__ __device__ inline int sf_buf_bytes(int panels) { return panels * 1024 + static_cast<int>(sizeof(TileInfo)); }
+__host__ __device__ inline Layout layout_of(int gp, int panels, bool shared_kv, int ring, int sf_bufs, int p_bufs) {
   Layout l;
   l.q = 0;
   l.p = l.q + panels * gp * 256;
   l.ring = l.p + p_bufs * kPanel;
   l.q_sf = l.ring + ring * kPanel;
   l.sf = l.q_sf + panels * 512;
-  l.fin = l.sf + sf_bufs * sf_buf_bytes(panels);
+  l.stage = l.sf + sf_bufs * sf_buf_bytes(panels);
+  l.fin = l.stage + 2 * (shared_kv ? 1 : 2) * 2048;
   l.misc = l.fin + 2 * static_cast<int>(sizeof(Fin));
   l.total = l.misc + static_cast<int>(sizeof(Misc));
   return l;
@@ -152,6 +155,10 @@ __device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit operands.
@@ -191,6 +198,21 @@ __device__ __forceinline__ uint32_t f16x2_rn(float first, float second) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(second), "f"(first));
   return r;
 }
+// 4 NP bytes of scales in pieces of `vec` (4, 8 or 16) bytes.
+__device__ __forceinline__ void cp_async_scales(uint32_t dst, const uint8_t* src, int NP, int vec) {
+  if (vec == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  } else if (vec == 8) {
+#pragma unroll 1
+    for (int i = 0; i < 4 * NP; i += 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + i), "l"(src + i) : "memory");
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 4 * NP; i += 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + i), "l"(src + i) : "memory");
+  }
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 // A named barrier among `count` threads that also tells whether any of them said so.
 __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t count, bool said) {
   uint32_t r;
@@ -199,8 +221,24 @@ __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t count, bo
       : "=r"(r) : "r"(id), "r"(count), "r"(said ? 1u : 0u) : "memory");
   return r != 0;
 }
+// What four E4M3 values leave of four bf16 (two words) times inv, times up, as E4M3.
+__device__ __forceinline__ uint32_t rest4(uint32_t x01, uint32_t x23, uint32_t codes, float inv, float up) {
+  uint32_t c0, c1;
+  e4m3x4_f16(codes, c0, c1);
+  const float2 f0 = f16x2_f32(c0), f1 = f16x2_f32(c1);
+  return e4m3x2((bf16_lo(x01) * inv - f0.x) * up, (bf16_hi(x01) * inv - f0.y) * up) |
+         (e4m3x2((bf16_lo(x23) * inv - f1.x) * up, (bf16_hi(x23) * inv - f1.y) * up) << 16);
+}
+// ln of sum * 2^ref
+__device__ __forceinline__ float lse_of(float ref, float sum) {
+  return sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
 // 2^(b - 127) as fp32, b in [0, 254].
 __device__ __forceinline__ float pow2_byte(uint32_t b) { return __uint_as_float(b == 0 ? 0x00400000u : b << 23); }
+// 2^e as fp32, e <= 127 (0 below the smallest subnormal).
+__device__ __forceinline__ float pow2_of(int32_t e) {
+  return __uint_as_float(e >= -126 ? static_cast<uint32_t>(e + 127) << 23 : e >= -149 ? 0x400000u >> (-127 - e) : 0u);
+}
 // Floats as integers of the same order (no NaN).
 __device__ __forceinline__ int32_t ordered(float f) {
   const int32_t i = __float_as_int(f);
@@ -208,60 +246,87 @@ __device__ __forceinline__ int32_t ordered(float f) {
 }
 __device__ __forceinline__ float of_ordered(int32_t i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
+// Sums of l[0 .. N) over the warp's lanes: halves of the values change hands at each step, until lane i has that of
+// value i / (32 / N) in l[0].
+template <int O, int N, int M>
+__device__ __forceinline__ void fold_sums(float (&l)[M], int lane) {
+  if constexpr (N > 1) {
+    const bool up = (lane & O) != 0;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const float first = l[j], second = l[j + N / 2];
+      l[j] = (up ? second : first) + __shfl_xor_sync(0xffffffffu, up ? first : second, O);
+    }
+  } else {
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], O);
+  }
+  if constexpr (O > 1) fold_sums<O / 2, (N > 1 ? N / 2 : 1)>(l, lane);
+}
+
+// a / b for 0 <= a, 0 < b, in 32 bits where that does (a 64-bit division is a long subroutine).
+__device__ __forceinline__ int64_t divide(int64_t a, int32_t b) {
+  return a >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 // ---- work -----------------------------------------------------------------------------------
 __device__ __forceinline__ int32_t length_of(const Args& a, int32_t len) {
   const int64_t cap = static_cast<int64_t>(a.table_width) * a.page_size;
   return len <= 0 ? 0 : static_cast<int32_t>(cap < len ? cap : len);
 }
+__device__ __forceinline__ uint32_t page_index(const Args& a, uint32_t t) { return __umulhi(t, a.page_mul) >> a.page_shift; }
 // A sequence without tokens is one unit, which writes its zeros.
 __device__ __forceinline__ int32_t units_of(int32_t len) { return len <= 0 ? 1 : (len - 1) / kUnit + 1; }
 
-// Walks a CTA's segments: runs of units of one item. An item is (sequence b, sub = cache head * blocks + block).
+// Walks a CTA's segments: runs of units of one item. An item is (sequence, cache head, block of query heads).
 struct Segments {
   const Args& a;
   int64_t left;
-  int32_t b, sub, u, len, units, next_len;
+  int32_t next_len, b, k, blk_, u, len, units;
   // the current segment
-  int32_t seg_b, seg_sub, seg_len, u0, u1, seg_units;
+  int32_t seg_b, kvh, blk, seg_len, u0, u1, seg_units;
 
-  __device__ Segments(const Args& args, const Misc& m) : a(args), left(m.w1 - m.w0), b(m.b0), sub(m.sub0), u(m.u0) {
+  __device__ __forceinline__ Segments(const Args& args, const Misc& m)
+      : a(args), left(m.w1 - m.w0), b(m.b0), k(m.kvh0), blk_(m.blk0), u(m.u0) {
     len = left > 0 ? length_of(a, a.lens[b]) : 0;
     units = units_of(len);
     next_len = left > 0 && b + 1 < a.B ? a.lens[b + 1] : 0;
   }
-  __device__ bool next() {
+  __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
     if (u == units) {
       u = 0;
-      if (++sub == a.kv * a.blocks) {
-        sub = 0;
-        ++b;
-        len = length_of(a, next_len);
-        units = units_of(len);
-        next_len = b + 1 < a.B ? a.lens[b + 1] : 0;
+      if (++blk_ == a.blocks) {
+        blk_ = 0;
+        if (++k == a.kv) {
+          k = 0;
+          ++b;
+          len = length_of(a, next_len);
+          units = units_of(len);
+          next_len = b + 1 < a.B ? a.lens[b + 1] : 0;
+        }
       }
     }
     seg_b = b;
-    seg_sub = sub;
+    kvh = k;
+    blk = blk_;
     seg_len = len;
     seg_units = units;
     u0 = u;
-    const int64_t take = units - u < left ? units - u : left;
-    u1 = u0 + static_cast<int32_t>(take);
+    u1 = u + static_cast<int32_t>(units - u < left ? units - u : left);
+    left -= u1 - u;
     u = u1;
-    left -= take;
     return true;
   }
-  __device__ int tiles() const { return (u1 - u0 + 1) / 2; }
-  __device__ int32_t start(int tile) const { return (u0 + 2 * tile) * kUnit; }
+  __device__ __forceinline__ int tiles() const { return (u1 - u0 + 1) >> 1; }
+  __device__ __forceinline__ int32_t start(int tile) const { return (u0 + 2 * tile) * kUnit; }
   // tokens of a tile (0 only in a sequence without any)
-  __device__ int32_t tokens(int tile) const {
-    const int32_t e = min(u1 * kUnit, seg_len), n = e - start(tile);
-    return n < kTile ? (n < 0 ? 0 : n) : kTile;
+  __device__ __forceinline__ int32_t tokens(int tile) const {
+    const int32_t n = min(u1 * kUnit, seg_len) - start(tile);
+    return max(0, min(kTile, n));
   }
-  __device__ bool whole() const { return u0 == 0 && u1 == seg_units; }
-  __device__ int head0() const { return seg_sub / a.blocks * a.G + seg_sub % a.blocks * a.block_heads; }
-  __device__ int heads() const { return min(a.block_heads, a.G - seg_sub % a.blocks * a.block_heads); }
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == seg_units; }
+  __device__ __forceinline__ int head0() const { return kvh * a.G + blk * a.block_heads; }
+  __device__ __forceinline__ int heads() const { return min(a.block_heads, a.G - blk * a.block_heads); }
 };
 
 // Position in a ring of n barriers: the slot and the parity of its current use.
@@ -274,16 +339,18 @@ struct Ring {
   }
 };
 
-__device__ __forceinline__ void report_timeout(int32_t* status) {
-  if (status != nullptr) atomicCAS(status, 0, MXQ_ERR_TIMEOUT);
-}
-// A bounded wait; once one has run out nothing waits any more (results are void, every loop still ends).
-__device__ __forceinline__ void wait_bar(Misc& m, const Args& a, uint32_t bar, uint32_t parity) {
+// A bounded wait; once one has run out nothing waits any more (results are void, every loop still ends, and the
+// status word is written at the end). Small on purpose: it is inlined thirty times, and the roles' loops have to fit the
+// instruction cache together.
+__device__ __forceinline__ void wait_bar(Misc& m, uint32_t bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return;
-  if (m.dead) return;
-  if (!mbar_wait_bounded(bar, parity)) {
-    m.dead = 1;
-    report_timeout(a.status);
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (m.dead != 0 || globaltimer_ns() - t0 > kWaitLimitNs) {
+      m.dead = 1;
+      return;
+    }
   }
 }
 
@@ -294,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int HPT = GP / 2;             // heads of a softmax or output thread
   constexpr int SB = GP == 64 ? 1 : 2;    // S buffers in TMEM
   extern __shared__ __align__(1024) uint8_t smem[];
-  const Layout lay = layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs);
+  const Layout lay = layout_of(GP, a.panels, a.v_sf == nullptr, a.ring, a.sf_bufs, a.p_bufs);
   Misc& m = *reinterpret_cast<Misc*>(smem + lay.misc);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -310,16 +377,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < a.ring; ++i) {
       mbar_init(BAR(ring_full[i]), 1);
       mbar_init(BAR(ring_empty[i]), shared_kv ? 9 : i < ring_k ? 1 : 8);
     }
+#pragma unroll 1
     for (int i = 0; i < 4; ++i) mbar_init(BAR(sf_full[i]), 2), mbar_init(BAR(sf_empty[i]), 17);
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(s_full[i]), 1), mbar_init(BAR(s_empty[i]), 8);
       mbar_init(BAR(p_full[i]), 8), mbar_init(BAR(p_empty[i]), 1);
       mbar_init(BAR(fin_full[i]), 8), mbar_init(BAR(fin_empty[i]), 8);
     }
+#pragma unroll 1
     for (int i = 0; i < kVSlots; ++i) mbar_init(BAR(v_full[i]), 4), mbar_init(BAR(v_empty[i]), 1);
     mbar_init(BAR(q_full), 8), mbar_init(BAR(q_empty), 1);
     mbar_init(BAR(o_full), 1), mbar_init(BAR(o_empty), 8);
@@ -336,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     const int32_t per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int64_t sum = 0;
+#pragma unroll 1
     for (int32_t b = b0; b < b1; ++b) sum += units_of(length_of(a, a.lens[b]));
     int64_t inc = sum;
 #pragma unroll
@@ -346,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) m.sums[warp] = inc;
     __syncthreads();
     int64_t before = 0, total = 0;
+#pragma unroll 4
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += m.sums[w];
       total += m.sums[w];
@@ -353,22 +426,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     before += inc - sum;
     total *= S;
     // (no share is empty among the CTAs that have one: the parts of an item lie in consecutive CTAs)
-    const int64_t ctas = total < a.ctas ? total : a.ctas;
-    const int64_t w0 = total * blockIdx.x / ctas, w1 = total * (blockIdx.x + 1) / ctas;
-    if (blockIdx.x < ctas && before * S <= w0 && w0 < (before + sum) * S) {  // one thread
+    const int64_t per_cta = total < a.ctas ? 1 : divide(total, a.ctas), rest = total < a.ctas ? 0 : total - per_cta * a.ctas;
+    const int64_t w0 = per_cta * blockIdx.x + min(static_cast<int64_t>(blockIdx.x), rest);
+    if (w0 < total && before * S <= w0 && w0 < (before + sum) * S) {  // one thread
       int64_t at = w0 - before * S;
       int32_t b = b0, units = units_of(length_of(a, a.lens[b]));
+#pragma unroll 1
       while (at >= static_cast<int64_t>(units) * S) {
         at -= static_cast<int64_t>(units) * S;
         units = units_of(length_of(a, a.lens[++b]));
       }
+      const uint32_t sub = static_cast<uint32_t>(divide(at, units));  // (below S)
       m.b0 = b;
-      m.sub0 = static_cast<int32_t>(at / units);
-      m.u0 = static_cast<int32_t>(at % units);
+      m.kvh0 = static_cast<int32_t>(sub / a.blocks);
+      m.blk0 = static_cast<int32_t>(sub % a.blocks);
+      m.u0 = static_cast<int32_t>(at - static_cast<int64_t>(sub) * units);
       m.w0 = w0;
-      m.w1 = w1;
-      m.total = total;
-      m.ctas = ctas;
+      m.w1 = w0 + per_cta + (blockIdx.x < rest ? 1 : 0);
+      m.per_cta = per_cta;
+      m.rest = rest;
     }
   }
   tc_fence_before();
@@ -381,25 +457,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segments seg(a, m);
     Ring rk(ring_k), rv(ring_v);
     int used_k = 0, used_v = 0;
+#pragma unroll 1
     while (seg.next()) {
-      const int tiles = seg.tiles(), kvh = seg.seg_sub / a.blocks;
+      const int tiles = seg.tiles(), kvh = seg.kvh;
       const int32_t* row = a.table + seg.seg_b * a.ld_table;
       auto page_of = [&](int tile) {  // the page of this lane's box
         const int32_t t = seg.start(tile) + lane * a.box;
-        return tile < tiles && lane * a.box < seg.tokens(tile) ? row[static_cast<uint32_t>(t) / a.page_size] : 0;
+        return tile < tiles && lane * a.box < seg.tokens(tile) ? row[page_index(a, t)] : 0;
       };
       int32_t page = page_of(0);
+#pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
         const int32_t next_page = page_of(i + 1);
         const int32_t t = seg.start(i) + lane * a.box, n = seg.tokens(i);
-        const int boxes = (n + a.box - 1) / a.box;
-        const int32_t place = static_cast<int32_t>(static_cast<uint32_t>(t) % a.page_size);
+        const int boxes = (n + a.box - 1) >> a.box_shift;
+        const int32_t place = t - static_cast<int32_t>(page_index(a, t) * a.page_size);
+#pragma unroll 1
         for (int half = 0; half < (shared_kv ? 1 : 2); ++half) {
           Ring& r = half == 0 ? rk : rv;
           const int slot0 = half == 0 ? 0 : ring_k;
+#pragma unroll 1
           for (int p = 0; p < NP; ++p) {
             const int s = slot0 + r.slot;
-            wait_bar(m, a, BAR(ring_empty[s]), r.phase ^ 1);
+            wait_bar(m, BAR(ring_empty[s]), r.phase ^ 1);
             if (__any_sync(0xffffffffu, m.dead)) break;
             if (lane == 0) mbar_arrive_expect_tx(BAR(ring_full[s]), boxes * a.box * 128);
             __syncwarp();
@@ -417,193 +497,211 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (__any_sync(0xffffffffu, m.dead)) break;
     }
     // every load in flight lands before the CTA leaves
+#pragma unroll 1
     for (int half = 0; half < (shared_kv ? 1 : 2); ++half) {
       const int n = half == 0 ? ring_k : ring_v, used = half == 0 ? used_k : used_v;
+#pragma unroll 1
       for (int i = max(0, used - n); i < used; ++i)
-        if (!mbar_wait_bounded(BAR(ring_full[(half == 0 ? 0 : ring_k) + i % n]), (i / n) & 1)) report_timeout(a.status);
+        if (!mbar_wait_bounded(BAR(ring_full[(half == 0 ? 0 : ring_k) + i % n]), (i / n) & 1)) m.dead = 1;
     }
   } else if (warp == 1) {
     // ---- MMA ----
-    if (lane == 0) {
+    // A tile's scores are issued before the products of the tile before it, so that the tensor cores have work while
+    // its probabilities are made; at a segment's first tile after them, because its queries come late.
+    if (elect_one()) {
       Segments seg(a, m);
-      Ring rk(ring_k), sf(a.sf_bufs), s(SB), pr(a.p_bufs), vr(kVSlots), one(1);
-      Ring o_ring(1);
-      bool have = seg.next();
-      int wide_next = 0;
-      auto issue_qk = [&](bool first, bool last) {
-        if (first) {
-          wait_bar(m, a, BAR(q_full), one.phase);
-          tc_fence_after();
-          for (int p = 0; p < NP; ++p) tc_cp_sf_atom(tmem + kColSfQ + 4 * p, sdesc_sf_atom(sbase + lay.q_sf + 512 * p));
-        }
-        wait_bar(m, a, BAR(sf_full[sf.slot]), sf.phase);
-        wait_bar(m, a, BAR(s_empty[s.slot]), s.phase ^ 1);
-        tc_fence_after();
-        const uint32_t sf_at = sbase + lay.sf + sf.slot * sf_bytes;
-        wide_next = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1536)->wide;
-        const uint32_t d = tmem + kColS + s.slot * 2 * GP, sfk = tmem + (s.slot == 0 ? kColSfK : kColSfK1);
-        for (int p = 0; p < NP; ++p) {
-          wait_bar(m, a, BAR(ring_full[rk.slot]), rk.phase);
-          tc_fence_after();
-          tc_cp_sf_atom(sfk + 4 * p, sdesc_sf_atom(sf_at + 512 * p));
-          const uint64_t ad = sdesc_kmajor_sw128(sbase + lay.ring + rk.slot * kPanel);
-          const uint64_t bd = sdesc_kmajor_sw128(sbase + lay.q + p * GP * 256);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc_mxf8(128, 2 * GP, k, k), sfk + 4 * p, tmem + kColSfQ + 4 * p,
-                        (p | k) != 0 ? 1u : 0u);
-          tc_commit(BAR(ring_empty[rk.slot]));
-          rk.next();
-        }
-        tc_commit(BAR(s_full[s.slot]));
-        tc_commit(BAR(sf_empty[sf.slot]));
-        if (last) {
-          tc_commit(BAR(q_empty));
-          one.next();
-        }
-        sf.next();
-        s.next();
-      };
-      if (have) issue_qk(true, seg.tiles() == 1);
-      while (have) {
-        const int tiles = seg.tiles();
-        for (int i = 0; i < tiles; ++i) {
-          const int wide = wide_next, halves = seg.tokens(i) > 64 ? 2 : 1;
-          if (i + 1 < tiles) issue_qk(false, i + 2 == tiles);
-          if (i == 0) wait_bar(m, a, BAR(o_empty), o_ring.phase ^ 1);
-          wait_bar(m, a, BAR(p_full[pr.slot]), pr.phase);
-          tc_fence_after();
-          const uint32_t idesc = wide != 0 ? idesc_f16_mn(GP, true) : idesc_f16_mn(GP, false);
-          for (int p = 0; p < NP; ++p)
-            for (int h = 0; h < halves; ++h) {
-              wait_bar(m, a, BAR(v_full[vr.slot]), vr.phase);
+      Ring rk(ring_k), sf(a.sf_bufs), s(SB), pr(a.p_bufs), vr(kVSlots), q_ring(1), o_ring(1);
+      int tiles = 0, tile = 0;                              // of the next scores
+      bool prev = false, prev_first = false, prev_last = false;  // the products not issued yet
+      int prev_halves = 0, prev_wide = 0;
+      bool more = seg.next();
+      if (more) tiles = seg.tiles();
+      while (more || prev) {
+        const bool scores_first = more && tile > 0;
+        int halves = 0, wide = 0;
+#pragma unroll 1
+        for (int step = 0; step < 2; ++step) {
+          if ((step == 0) == scores_first) {
+            if (!more) continue;
+            if (tile == 0) {
+              wait_bar(m, BAR(q_full), q_ring.phase);
+              q_ring.next();
               tc_fence_after();
-              const uint64_t bd = sdesc(sbase + lay.p + pr.slot * kPanel + h * 64 * 128, 1024, 1024, 2);
+#pragma unroll 1
+              for (int p = 0; p < NP; ++p) tc_cp_sf_atom(tmem + kColSfQ + 4 * p, sdesc_sf_atom(sbase + lay.q_sf + 512 * p));
+            }
+            wait_bar(m, BAR(sf_full[0]) + 8 * sf.slot, sf.phase);
+            wait_bar(m, BAR(s_empty[0]) + 8 * s.slot, s.phase ^ 1);
+            tc_fence_after();
+            halves = seg.tokens(tile) > 64 ? 2 : 1;
+            wide = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1024)->wide;
+            const uint32_t sf_at = sbase + lay.sf + sf.slot * sf_bytes;
+            const uint32_t d = tmem + kColS + s.slot * 2 * GP, sfk = tmem + (s.slot == 0 ? kColSfK : kColSfK1);
+#pragma unroll 1
+            for (int p = 0; p < NP; ++p) {
+              wait_bar(m, BAR(ring_full[0]) + 8 * rk.slot, rk.phase);
+              tc_fence_after();
+              tc_cp_sf_atom(sfk + 4 * p, sdesc_sf_atom(sf_at + 512 * p));
+              const uint64_t ad = sdesc_kmajor_sw128(sbase + lay.ring + rk.slot * kPanel);
+              const uint64_t bd = sdesc_kmajor_sw128(sbase + lay.q + p * GP * 256);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                tc_mma_f16_ts(tmem + p * GP, tmem + kColV + 32 * vr.slot + 8 * k, bd + 128 * k, idesc, (i | h | k) != 0 ? 1u : 0u);
-              tc_commit(BAR(v_empty[vr.slot]));
+                tc_mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc_mxf8(128, 2 * GP, k, k), sfk + 4 * p, tmem + kColSfQ + 4 * p,
+                            (p | k) != 0 ? 1u : 0u);
+              tc_commit(BAR(ring_empty[0]) + 8 * rk.slot);
+              rk.next();
+            }
+            tc_commit(BAR(s_full[0]) + 8 * s.slot);
+            tc_commit(BAR(sf_empty[0]) + 8 * sf.slot);
+            if (tile + 1 == tiles) tc_commit(BAR(q_empty));
+            sf.next();
+            s.next();
+          } else if (prev) {
+            if (prev_first) {
+              wait_bar(m, BAR(o_empty), o_ring.phase ^ 1);
+              o_ring.next();
+            }
+            wait_bar(m, BAR(p_full[0]) + 8 * pr.slot, pr.phase);
+            tc_fence_after();
+            const uint32_t idesc = prev_wide != 0 ? idesc_f16_mn(GP, true) : idesc_f16_mn(GP, false);
+            const uint64_t p_desc = sdesc(sbase + lay.p + pr.slot * kPanel, 1024, 1024, 2);
+#pragma unroll 1
+            for (int c = 0; c < NP * prev_halves; ++c) {
+              const int p = prev_halves == 2 ? c >> 1 : c, h = prev_halves == 2 ? c & 1 : 0;
+              wait_bar(m, BAR(v_full[0]) + 8 * vr.slot, vr.phase);
+              tc_fence_after();
+              const uint64_t bd = p_desc + h * 512;
+              const uint32_t more_of_it = !prev_first || h != 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma_f16_ts(tmem + p * GP, tmem + kColV + 32 * vr.slot + 8 * k, bd + 128 * k, idesc, k != 0 ? 1u : more_of_it);
+              tc_commit(BAR(v_empty[0]) + 8 * vr.slot);
               vr.next();
             }
-          tc_commit(BAR(p_empty[pr.slot]));
-          pr.next();
+            tc_commit(BAR(p_empty[0]) + 8 * pr.slot);
+            pr.next();
+            if (prev_last) tc_commit(BAR(o_full));
+            prev = false;
+          }
         }
-        tc_commit(BAR(o_full));
-        o_ring.next();
-        have = seg.next();
-        if (have) issue_qk(true, seg.tiles() == 1);
+        if (more) {
+          prev = true;
+          prev_first = tile == 0;
+          prev_last = tile + 1 == tiles;
+          prev_halves = halves;
+          prev_wide = wide;
+          if (++tile == tiles) {
+            tile = 0;
+            more = seg.next();
+            if (more) tiles = seg.tiles();
+          }
+        }
       }
       tc_commit(BAR(done));
-      if (!mbar_wait_bounded(BAR(done), 0)) report_timeout(a.status);
+      if (!mbar_wait_bounded(BAR(done), 0)) m.dead = 1;
     }
     __syncwarp();
   } else if (warp < 4) {
-    // ---- scales: K atoms, V table, the tokens that take part, the pivot ----
-    const int w = warp - 2;
+    // ---- scales: K atoms, V bytes, the tokens that take part, the pivot ----
+    // lane: tokens 64 w + lane and 32 on. Their scales come by cp.async, a tile ahead, into a place of the lane's own.
+    const int w = warp - 2, kinds = shared_kv ? 1 : 2;
     Segments seg(a, m);
     Ring sf(a.sf_bufs);
     uint32_t parity = 0;
-    while (seg.next()) {
-      const int tiles = seg.tiles(), kvh = seg.seg_sub / a.blocks;
-      const int32_t* row = a.table + seg.seg_b * a.ld_table;
-      int32_t pivot = 0;
-      // lane: tokens 64 w + lane and 32 on
-      uint32_t page[2], kw[2][4], vw[2][4];
-      auto pages_of = [&](int tile, uint32_t (&pg)[2]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int32_t r = 64 * w + 32 * j + lane;
-          pg[j] = tile < tiles && r < seg.tokens(tile)
-                      ? static_cast<uint32_t>(row[static_cast<uint32_t>(seg.start(tile) + r) / a.page_size]) : 0xFFFFFFFFu;
-        }
-      };
-      auto words_of = [&](int tile, const uint32_t (&pg)[2], uint32_t (&kk)[2][4], uint32_t (&vv)[2][4]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const bool ok = pg[j] < a.pages;
-          const uint32_t at = static_cast<uint32_t>(seg.start(tile) + 64 * w + 32 * j + lane) % a.page_size;
-          const uint32_t* ks = reinterpret_cast<const uint32_t*>(a.k_sf + (ok ? pg[j] * a.k_sf_page + at * a.k_sf_token + kvh * a.k_sf_head : 0));
-          const uint32_t* vs = reinterpret_cast<const uint32_t*>(a.v_sf + (ok ? pg[j] * a.v_sf_page + at * a.v_sf_token + kvh * a.v_sf_head : 0));
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            kk[j][p] = ok && p < NP ? ks[p] : 0;
-            vv[j][p] = shared_kv ? kk[j][p] : ok && p < NP ? vs[p] : 0;
+    const uint32_t stage0 = lay.stage + (64 * w + lane) * 16;  // [tile parity][kind][token] of 16 bytes
+    auto fetch = [&](int tile, int tiles, uint32_t (&pg)[2], int kvh, const int32_t* row) {
+      const int32_t n = tile < tiles ? seg.tokens(tile) : 0;
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j) {
+        const int32_t r = 64 * w + 32 * j + lane;
+        uint32_t g = 0xFFFFFFFFu;
+        if (r < n) {
+          const uint32_t t = static_cast<uint32_t>(seg.start(tile) + r), i = page_index(a, t), at = t - i * a.page_size;
+          g = static_cast<uint32_t>(row[i]);
+          if (g < a.pages) {
+            const uint32_t dst = sbase + stage0 + 512 * j + (tile & 1) * kinds * 2048;
+            cp_async_scales(dst, a.k_sf + g * a.k_sf_page + at * a.k_sf_token + kvh * a.k_sf_head, NP, a.sf_vec);
+            if (!shared_kv) cp_async_scales(dst + 2048, a.v_sf + g * a.v_sf_page + at * a.v_sf_token + kvh * a.v_sf_head, NP, a.sf_vec);
           }
         }
-      };
-      uint32_t next_page[2];
-      pages_of(0, page);
-      pages_of(1, next_page);
-      words_of(0, page, kw, vw);
+        if (j == 0) pg[0] = g;
+        else pg[1] = g;
+      }
+      cp_async_commit();
+    };
+#pragma unroll 1
+    while (seg.next()) {
+      const int tiles = seg.tiles(), kvh = seg.kvh;
+      const int32_t* row = a.table + seg.seg_b * a.ld_table;
+      int32_t pivot = 0;
+      uint32_t page[2], next_page[2];
+      fetch(0, tiles, page, kvh, row);
+#pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
-        uint32_t nkw[2][4], nvw[2][4], far_page[2];
-        words_of(i + 1, next_page, nkw, nvw);
-        pages_of(i + 2, far_page);
+        fetch(i + 1, tiles, next_page, kvh, row);
+        cp_async_wait_1();
         const bool ok[2] = {page[0] < a.pages, page[1] < a.pages};
+        const uint32_t* const kw = reinterpret_cast<const uint32_t*>(smem + stage0 + (i & 1) * kinds * 2048);
+        const uint32_t* const vw = kw + (kinds - 1) * 512;
         uint32_t hi = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int p = 0; p < 4; ++p) hi = __vmaxu4(hi, vw[j][p]);
-        hi = max(max(hi & 0xFF, (hi >> 8) & 0xFF), max((hi >> 16) & 0xFF, hi >> 24));
-        hi = __reduce_max_sync(0xffffffffu, hi);
+          if (ok[j])
+#pragma unroll 1
+            for (int p = 0; p < NP; ++p) {
+              const uint32_t x = vw[p + 128 * j];
+              hi = __vmaxu2(hi, __vmaxu2(x & 0x00FF00FFu, (x >> 8) & 0x00FF00FFu));
+            }
+        hi = __reduce_max_sync(0xffffffffu, max(hi & 0xFFFFu, hi >> 16));
         const uint32_t v0 = __ballot_sync(0xffffffffu, ok[0]), v1 = __ballot_sync(0xffffffffu, ok[1]);
         if (lane == 0) m.sf_red[parity][w] = static_cast<int32_t>(hi);
+        wait_bar(m, BAR(sf_empty[0]) + 8 * sf.slot, sf.phase ^ 1);
         named_barrier(1, 64);
         const int32_t top = max(m.sf_red[parity][0], m.sf_red[parity][1]);
         if (top > pivot + 7) pivot = top;
-        bool low = false;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int32_t b = (vw[j][p] >> (8 * g)) & 0xFF;
-              low |= b != 0 && b < pivot - 15;
-            }
-        low = __any_sync(0xffffffffu, low);
-        if (lane == 0) m.sf_red[parity][2 + w] = low;
-        wait_bar(m, a, BAR(sf_empty[sf.slot]), sf.phase ^ 1);
-        named_barrier(1, 64);
-        const bool wide = (m.sf_red[parity][2] | m.sf_red[parity][3]) != 0;
-        parity ^= 1;
+        // bytes t = max(0, b - pivot + 15): 2^(b - pivot) is fp16 with exponent field t, and 4 t its upper byte
+        const uint32_t down = static_cast<uint32_t>((15 - pivot) & 0xFFFF) * 0x10001u;
         uint8_t* const buf = smem + lay.sf + sf.slot * sf_bytes;
-        uint16_t* const tab = reinterpret_cast<uint16_t*>(buf + NP * 512);
-        TileInfo* const info = reinterpret_cast<TileInfo*>(buf + NP * 1536);
+        TileInfo* const info = reinterpret_cast<TileInfo*>(buf + NP * 1024);
+        uint32_t low = 0;
+#pragma unroll 1
+        for (int p = 0; p < NP; ++p) {
+          const uint32_t k0 = ok[0] ? kw[p] : 0, k1 = ok[1] ? kw[p + 128] : 0;
+          *reinterpret_cast<uint2*>(buf + p * 512 + lane * 16 + w * 8) = make_uint2(k0, k1);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          if (p >= NP) break;
-          *reinterpret_cast<uint2*>(buf + p * 512 + lane * 16 + w * 8) = make_uint2(kw[0][p], kw[1][p]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int32_t e = static_cast<int32_t>((vw[j][p] >> (8 * g)) & 0xFF) - pivot;
-              uint32_t x;  // 2^e, e <= 7
-              if (wide) x = e >= -126 ? (e + 127) << 7 : e >= -133 ? 0x80u >> (-126 - e) : 0;
-              else x = e >= -14 ? (e + 15) << 10 : e >= -24 ? 0x400u >> (-14 - e) : 0;
-              tab[(4 * p + g) * 128 + 64 * w + 32 * j + lane] = static_cast<uint16_t>(ok[j] ? x : 0);
-            }
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t x = ok[j] ? vw[p + 128 * j] : 0, e = x & 0x00FF00FFu, o = (x >> 8) & 0x00FF00FFu;
+            const uint32_t te = __viaddmax_s16x2(e, down, 0), to = __viaddmax_s16x2(o, down, 0);
+            // nonzero scales that fp16 does not hold
+            low |= (__vminu2(e, 0x00010001u) & ~__vminu2(te, 0x00010001u)) | (__vminu2(o, 0x00010001u) & ~__vminu2(to, 0x00010001u));
+            *reinterpret_cast<uint32_t*>(buf + NP * 512 + (p * 128 + 64 * w + 32 * j + lane) * 4) = (te << 2) | (to << 10);
+          }
         }
+        if (named_barrier_or(1, 64, low != 0)) {  // bf16: the bytes themselves
+#pragma unroll 1
+          for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              *reinterpret_cast<uint32_t*>(buf + NP * 512 + (p * 128 + 64 * w + 32 * j + lane) * 4) = ok[j] ? vw[p + 128 * j] : 0;
+          if (lane == 0 && w == 0) info->wide = 1;
+        } else if (lane == 0 && w == 0) {
+          info->wide = 0;
+        }
+        parity ^= 1;
         if (lane == 0) {
           info->valid[2 * w] = v0;
           info->valid[2 * w + 1] = v1;
-          if (w == 0) info->pivot = pivot, info->wide = wide;
+          if (w == 0) info->pivot = pivot;
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(sf_full[sf.slot]));
+        if (lane == 0) mbar_arrive(BAR(sf_full[0]) + 8 * sf.slot);
         sf.next();
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          page[j] = next_page[j];
-          next_page[j] = far_page[j];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) kw[j][p] = nkw[j][p], vw[j][p] = nvw[j][p];
-        }
+        page[0] = next_page[0];
+        page[1] = next_page[1];
       }
     }
+    cp_async_wait_0();
   } else if (warp < 12) {
     // ---- queries and softmax ----
     const int quarter = warp & 3, h0 = (warp - 4) / 4 * HPT, st = tid - 128;
@@ -614,46 +712,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int prow = (t & ~15) + ((t >> 2) & 3) * 2 + (t & 1) + ((t & 2) << 2);
     Segments seg(a, m);
     Ring sf(a.sf_bufs), s(SB), pr(a.p_bufs), one(1), fin(2);
+#pragma unroll 1
     while (seg.next()) {
       const int tiles = seg.tiles(), heads = seg.heads();
       // q as hi + lo: 8 values a lane, 4 lanes a group
-      wait_bar(m, a, BAR(q_empty), one.phase ^ 1);
+      wait_bar(m, BAR(q_empty), one.phase ^ 1);
       one.next();
       {
-        const uint16_t* q = a.q + seg.seg_b * a.ldq + seg.head0() * a.ldqh;
-        const int chunks = a.D / 8;
-#pragma unroll 4
-        for (int i = st; i < GP * chunks; i += kSoftThreads) {
-          const int h = i / chunks, d = (i - h * chunks) * 8;
-          const uint4 x = h < heads ? *reinterpret_cast<const uint4*>(q + h * a.ldqh + d) : make_uint4(0, 0, 0, 0);
-          uint32_t amax = absmax8(x);
-          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          const uint32_t code = ue8m0_from_bf16_amax(amax), low = code >= 4 ? code - 4 : 0;
-          const float inv = ue8m0_inverse(code), up = __uint_as_float((127 + code - low) << 23);
-          const uint2 hi = quant8(x, inv);
-          uint2 lo;
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, hs[2] = {hi.x, hi.y};
-          uint32_t ls[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t c0, c1;
-            e4m3x4_f16(hs[j], c0, c1);
-            const float2 f0 = f16x2_f32(c0), f1 = f16x2_f32(c1);
-            ls[j] = e4m3x2((bf16_lo(xs[2 * j]) * inv - f0.x) * up, (bf16_hi(xs[2 * j]) * inv - f0.y) * up) |
-                    (e4m3x2((bf16_lo(xs[2 * j + 1]) * inv - f1.x) * up, (bf16_hi(xs[2 * j + 1]) * inv - f1.y) * up) << 16);
-          }
-          lo.x = ls[0], lo.y = ls[1];
-          const int p = d >> 7, col = d & 127;
+        const uint16_t* q = a.q + seg.seg_b * a.ldq + seg.head0() * a.ldqh + (st & 15) * 8;
+        const int col = (st & 15) * 8;
+#pragma unroll 1
+        for (int p = 0; p < NP; ++p) {  // 16 lanes a head's 128 features
           uint8_t* const panel = smem + lay.q + p * GP * 256;
-          const int at = (((col >> 4) ^ (h & 7)) << 4) + (col & 8);  // (GP is a multiple of 8: both rows swizzle alike)
-          *reinterpret_cast<uint2*>(panel + h * 128 + at) = hi;
-          *reinterpret_cast<uint2*>(panel + (GP + h) * 128 + at) = lo;
-          if ((lane & 3) == 0) {
-            uint8_t* const atom = smem + lay.q_sf + p * 512;
-            atom[(h & 31) * 16 + (h >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(code);
-            const int r = GP + h;
-            atom[(r & 31) * 16 + (r >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(low);
+          uint8_t* const atom = smem + lay.q_sf + p * 512;
+          uint4 xs[GP / 16];
+#pragma unroll
+          for (int u = 0; u < GP / 16; ++u) {
+            const int h = (st >> 4) + 16 * u;
+            xs[u] = h < heads ? ld_stream_u4(q + h * a.ldqh + 128 * p) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int u = 0; u < GP / 16; ++u) {
+            const int h = (st >> 4) + 16 * u, r = GP + h;
+            const uint4 x = xs[u];
+            uint32_t amax = absmax8(x);
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const uint32_t code = ue8m0_from_bf16_amax(amax), low = code >= 4 ? code - 4 : 0;
+            const float inv = ue8m0_inverse(code), up = __uint_as_float((127 + code - low) << 23);
+            const uint2 hi = quant8(x, inv);
+            const uint2 lo = make_uint2(rest4(x.x, x.y, hi.x, inv, up), rest4(x.z, x.w, hi.y, inv, up));
+            const int at = (((col >> 4) ^ (h & 7)) << 4) + (col & 8);  // (GP is a multiple of 8: both rows swizzle alike)
+            *reinterpret_cast<uint2*>(panel + h * 128 + at) = hi;
+            *reinterpret_cast<uint2*>(panel + r * 128 + at) = lo;
+            if ((lane & 3) == 0) {
+              atom[(h & 31) * 16 + (h >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(code);
+              atom[(r & 31) * 16 + (r >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(low);
+            }
           }
         }
       }
@@ -668,26 +763,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_barrier(2, kSoftThreads);
       if (st < GP) m.ref[st] = kLowRef;
       named_barrier(2, kSoftThreads);
+#pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
         float x[HPT];
-        wait_bar(m, a, BAR(s_full[s.slot]), s.phase);
+        wait_bar(m, BAR(s_full[s.slot]), s.phase);
         tc_fence_after();
         const uint32_t sc = t_lane + kColS + s.slot * 2 * GP + h0;
 #pragma unroll
-        for (int j = 0; j < HPT; j += 8) {
-          uint32_t hi[8], lo[8];
-          tmem_ld_x8(sc + j, hi);
-          tmem_ld_x8(sc + GP + j, lo);
+        for (int j = 0; j < HPT; j += 16) {
+          constexpr int n = HPT < 16 ? 8 : 16;
+          uint32_t hi[n], lo[n];
+          if constexpr (n == 8) tmem_ld_x8(sc + j, hi), tmem_ld_x8(sc + GP + j, lo);
+          else tmem_ld_x16(sc + j, hi), tmem_ld_x16(sc + GP + j, lo);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[j + k] = (__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c;
+          for (int k = 0; k < n; ++k) x[j + k] = (__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(s_empty[s.slot]));
-        s.next();
-        wait_bar(m, a, BAR(sf_full[sf.slot]), sf.phase);
-        const TileInfo* const info = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1536);
+        wait_bar(m, BAR(sf_full[sf.slot]), sf.phase);
+        const TileInfo* const info = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1024);
         const bool valid = (info->valid[quarter] >> lane) & 1;
         const int32_t new_pivot = info->pivot;
         const bool wide = info->wide != 0;
@@ -701,11 +794,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           over = fmaxf(fmaxf(over, fmaxf(x[j] - r.x, x[j + 1] - r.y)), fmaxf(x[j + 2] - r.z, x[j + 3] - r.w));
         }
         if (named_barrier_or(2, kSoftThreads, (valid && over > kSlack) || new_pivot != pivot)) {
-          // new references: the largest scores so far
+          // new references: the largest scores so far (seldom but at a segment's start; compact, S read again)
+#pragma unroll 1
+          for (int j = 0; j < HPT; j += 8) {
+            uint32_t hi[8], lo[8];
+            tmem_ld_x8(sc + j, hi);
+            tmem_ld_x8(sc + GP + j, lo);
+            tmem_ld_wait();
+            int32_t mine = INT32_MIN;  // lane k: head k's
 #pragma unroll
-          for (int j = 0; j < HPT; ++j) {
-            const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered(x[j]) : INT32_MIN);
-            if (lane == 0) atomicMax(&m.red[h0 + j], top);
+            for (int k = 0; k < 8; ++k) {
+              const float y = (__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c;
+              const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered(y) : INT32_MIN);
+              mine = lane == k ? top : mine;
+            }
+            if (lane < 8) atomicMax(&m.red[h0 + j + lane], mine);
           }
           named_barrier(2, kSoftThreads);
           if (st < GP) {
@@ -716,30 +819,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           named_barrier(2, kSoftThreads);
 #pragma unroll
-          for (int j = 0; j < HPT; ++j) l[j] *= m.fac[h0 + j];
+          for (int j = 0; j < HPT; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&m.fac[h0 + j]);
+            l[j] *= f.x, l[j + 1] *= f.y, l[j + 2] *= f.z, l[j + 3] *= f.w;
+          }
           if (i > 0) {
             // every product so far is in O, and the next waits for P
             const int prev = pr.slot == 0 ? a.p_bufs - 1 : pr.slot - 1;
-            wait_bar(m, a, BAR(p_empty[prev]), pr.slot == 0 ? pr.phase ^ 1 : pr.phase);
+            wait_bar(m, BAR(p_empty[0]) + 8 * prev, pr.slot == 0 ? pr.phase ^ 1 : pr.phase);
             tc_fence_after();
             const int down = pivot - new_pivot;  // <= 0
             const float pf = down < -126 ? 0.f : __uint_as_float((127 + down) << 23);
-            for (int p = 0; p < NP; ++p)
+#pragma unroll 1
+            for (int q = 0; q < NP * (HPT / 8); ++q) {
+              const int j = q % (HPT / 8) * 8;
+              const uint32_t col = t_lane + q / (HPT / 8) * GP + h0 + j;
+              uint32_t r[8];
+              tmem_ld_x8(col, r);
+              tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < HPT; j += 8) {
-                uint32_t r[8];
-                tmem_ld_x8(t_lane + p * GP + h0 + j, r);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * m.fac[h0 + j + k] * pf);
-                tmem_st_x8(t_lane + p * GP + h0 + j, r);
-              }
+              for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * m.fac[h0 + j + k] * pf);
+              tmem_st_x8(col, r);
+            }
             tmem_st_wait();
-            tc_fence_before();
           }
           pivot = new_pivot;
         }
-        wait_bar(m, a, BAR(p_empty[pr.slot]), pr.phase ^ 1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(s_empty[0]) + 8 * s.slot);
+        s.next();
+        wait_bar(m, BAR(p_empty[pr.slot]), pr.phase ^ 1);
         uint8_t* const row = smem + lay.p + pr.slot * kPanel + prow * 128;
 #pragma unroll
         for (int j = 0; j < HPT; j += 8) {
@@ -762,23 +872,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(BAR(p_full[pr.slot]));
         pr.next();
       }
-      // sums over the quarter's tokens: halves of the heads change hands at each step
+      // sums over the quarter's tokens
       Fin& f = *reinterpret_cast<Fin*>(smem + lay.fin + fin.slot * sizeof(Fin));
-      wait_bar(m, a, BAR(fin_empty[fin.slot]), fin.phase ^ 1);
-#pragma unroll
-      for (int o = 16, n = HPT; o > 0; o >>= 1) {
-        if (n > 1) {
-          n >>= 1;
-#pragma unroll
-          for (int j = 0; j < n; ++j) {
-            const bool up = (lane & o) != 0;
-            const float keep = up ? l[j + n] : l[j], give = up ? l[j] : l[j + n];
-            l[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-          }
-        } else {
-          l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
-        }
-      }
+      wait_bar(m, BAR(fin_empty[fin.slot]), fin.phase ^ 1);
+      fold_sums<16, HPT>(l, lane);
       constexpr int kShare = 32 / HPT;  // lanes that hold the same head
       if (lane % kShare == 0) f.sum[quarter][h0 + lane / kShare] = l[0];
       if (quarter == 0 && lane < HPT) f.ref[h0 + lane] = m.ref[h0 + lane];
@@ -795,63 +892,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring rv(ring_v), sf(a.sf_bufs), fin(2), o_ring(1);
     const int slot0 = shared_kv ? 0 : ring_k;
     uint32_t chunk = 0;
+    const uint32_t pick = static_cast<uint32_t>(quarter) * 0x1010u | 0x4000u;
     int2 owner = make_int2(0, 0);
+#pragma unroll 1
     while (seg.next()) {
       const int tiles = seg.tiles();
+#pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
         const int halves = seg.tokens(i) > 64 ? 2 : 1;
-        wait_bar(m, a, BAR(sf_full[sf.slot]), sf.phase);
+        wait_bar(m, BAR(sf_full[sf.slot]), sf.phase);
         const uint8_t* const buf = smem + lay.sf + sf.slot * sf_bytes;
-        const TileInfo* const info = reinterpret_cast<const TileInfo*>(buf + NP * 1536);
+        const TileInfo* const info = reinterpret_cast<const TileInfo*>(buf + NP * 1024);
         const bool wide = info->wide != 0;
+        const int32_t pivot = info->pivot;
         const uint32_t valid0 = info->valid[2 * set], valid1 = info->valid[2 * set + 1];
         const bool full = (valid0 & valid1) == 0xFFFFFFFFu;
+#pragma unroll 1
         for (int p = 0; p < NP; ++p) {
           const int s = slot0 + rv.slot;
-          wait_bar(m, a, BAR(ring_full[s]), rv.phase);
+          wait_bar(m, BAR(ring_full[s]), rv.phase);
           if (set < halves) {
-            const uint32_t ci = chunk + p * halves + set, vs = ci % kVSlots, vphase = (ci / kVSlots) & 1;
+            const uint32_t ci = chunk + p * halves + set, use = ci / kVSlots, vs = ci - use * kVSlots, vphase = use & 1;
             const uint32_t panel = sbase + lay.ring + s * kPanel;
-            const uint16_t* const tab = reinterpret_cast<const uint16_t*>(buf + NP * 512) + (4 * p + quarter) * 128 + 64 * set;
-            uint32_t w0[16], w1[16];  // features 0-15 and 16-31 of the quarter's 32
+            // the scale bytes of four tokens a lane
+            const uint8_t* const tab = buf + NP * 512 + (p * 128 + 64 * set + 4 * (lane & 3)) * 4;
+            const int t = 64 * set + (lane & 15), c16 = 2 * quarter + (lane >> 4);
+            const uint32_t rows = panel + t * 128 + ((c16 ^ (t & 7)) << 4);
+            const uint32_t dst = t_lane + kColV + 32 * vs;
+            if (!wide) {
+              uint32_t r[4][4];
+              uint4 sw[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int t = 64 * set + 16 * k + (lane & 15), c16 = 2 * quarter + (lane >> 4);
-              uint32_t r[4];
-              ldmatrix_b8_trans_x2(panel + t * 128 + ((c16 ^ (t & 7)) << 4), r);
-              const uint2 sc = *reinterpret_cast<const uint2*>(tab + 16 * k + 4 * (lane & 3));
-              if (!full) {  // tokens that take no part may be NaN
-                const uint32_t bits = ((k < 2 ? valid0 : valid1) >> (16 * (k & 1) + 4 * (lane & 3))) & 15;
-                const uint32_t mask = ((bits * 0x00204081u) & 0x01010101u) * 0xFFu;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) r[j] &= mask;
+              for (int k = 0; k < 4; ++k) {
+                ldmatrix_b8_trans_x2(rows + k * 2048, r[k]);
+                sw[k] = *reinterpret_cast<const uint4*>(tab + k * 64);
               }
-              uint32_t lo[4], hi[4];
+              if (!full) {  // tokens that take no part may be NaN
 #pragma unroll
-              for (int j = 0; j < 4; ++j) e4m3x4_f16(r[j], lo[j], hi[j]);
-              if (!wide) {
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t bits = ((k < 2 ? valid0 : valid1) >> (16 * (k & 1) + 4 * (lane & 3))) & 15;
+                  const uint32_t mask = ((bits * 0x00204081u) & 0x01010101u) * 0xFFu;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) lo[j] = hmul2(lo[j], sc.x), hi[j] = hmul2(hi[j], sc.y);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float2 fl = f16x2_f32(lo[j]), fh = f16x2_f32(hi[j]);
-                  lo[j] = bf16x2_rn(fl.x * bf16_lo(sc.x), fl.y * bf16_hi(sc.x));
-                  hi[j] = bf16x2_rn(fh.x * bf16_lo(sc.y), fh.y * bf16_hi(sc.y));
+                  for (int j = 0; j < 4; ++j) r[k][j] &= mask;
                 }
               }
-              w0[4 * k] = lo[0], w0[4 * k + 1] = lo[1], w0[4 * k + 2] = hi[0], w0[4 * k + 3] = hi[1];
-              w1[4 * k] = lo[2], w1[4 * k + 1] = lo[3], w1[4 * k + 2] = hi[2], w1[4 * k + 3] = hi[3];
+              uint32_t w0[16], w1[16];  // features 0-15 and 16-31 of the quarter's 32
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                // this quarter's group: each byte to the top of an fp16
+                const uint32_t s01 = __byte_perm(sw[k].x, sw[k].y, pick) & 0xFF00FF00u, s23 = __byte_perm(sw[k].z, sw[k].w, pick) & 0xFF00FF00u;
+                uint32_t lo[4], hi[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  e4m3x4_f16(r[k][j], lo[j], hi[j]);
+                  lo[j] = hmul2(lo[j], s01), hi[j] = hmul2(hi[j], s23);
+                }
+                w0[4 * k] = lo[0], w0[4 * k + 1] = lo[1], w0[4 * k + 2] = hi[0], w0[4 * k + 3] = hi[1];
+                w1[4 * k] = lo[2], w1[4 * k + 1] = lo[3], w1[4 * k + 2] = hi[2], w1[4 * k + 3] = hi[3];
+              }
+              wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
+              tc_fence_after();
+              tmem_st_16x128b_x8(dst, w0);
+              tmem_st_16x128b_x8(dst + (16u << 16), w1);
+            } else {  // the scales span more than fp16 holds: bf16
+              wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int k = 0; k < 4; ++k) {
+                uint32_t r[4];
+                ldmatrix_b8_trans_x2(rows + k * 2048, r);
+                const uint4 sw = *reinterpret_cast<const uint4*>(tab + k * 64);
+                const uint32_t bits = ((k < 2 ? valid0 : valid1) >> (16 * (k & 1) + 4 * (lane & 3))) & 15;
+                const uint32_t mask = ((bits * 0x00204081u) & 0x01010101u) * 0xFFu;
+                const float f0 = pow2_of(((sw.x >> (8 * quarter)) & 0xFF) - pivot), f1 = pow2_of(((sw.y >> (8 * quarter)) & 0xFF) - pivot),
+                            f2 = pow2_of(((sw.z >> (8 * quarter)) & 0xFF) - pivot), f3 = pow2_of(((sw.w >> (8 * quarter)) & 0xFF) - pivot);
+                uint32_t lo[4], hi[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  e4m3x4_f16(r[j] & mask, lo[j], hi[j]);
+                  const float2 fl = f16x2_f32(lo[j]), fh = f16x2_f32(hi[j]);
+                  lo[j] = bf16x2_rn(fl.x * f0, fl.y * f1);
+                  hi[j] = bf16x2_rn(fh.x * f2, fh.y * f3);
+                }
+                tmem_st_16x128b_x2(dst + 8 * k, lo[0], lo[1], hi[0], hi[1]);
+                tmem_st_16x128b_x2(dst + (16u << 16) + 8 * k, lo[2], lo[3], hi[2], hi[3]);
+              }
             }
-            wait_bar(m, a, BAR(v_empty[vs]), vphase ^ 1);
-            tc_fence_after();
-            const uint32_t dst = t_lane + kColV + 32 * vs;
-            tmem_st_16x128b_x8(dst, w0);
-            tmem_st_16x128b_x8(dst + (16u << 16), w1);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(v_full[vs]));
+            if (lane == 0) mbar_arrive(BAR(v_full[0]) + 8 * vs);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(ring_empty[s]));
@@ -863,55 +993,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         sf.next();
       }
       // outputs: this thread's feature 128 p + 32 quarter + lane of its heads
-      wait_bar(m, a, BAR(fin_full[fin.slot]), fin.phase);
-      wait_bar(m, a, BAR(o_full), o_ring.phase);
+      wait_bar(m, BAR(fin_full[fin.slot]), fin.phase);
+      wait_bar(m, BAR(o_full), o_ring.phase);
       tc_fence_after();
       const Fin& f = *reinterpret_cast<const Fin*>(smem + lay.fin + fin.slot * sizeof(Fin));
-      const float unit = pow2_byte(f.pivot);
+      // lane: the sum of head lane % HPT, its inverse in the values' unit, and its reference
+      const int my = h0 + lane % HPT;
+      const float sum = f.sum[0][my] + f.sum[1][my] + f.sum[2][my] + f.sum[3][my], ref = f.ref[my];
+      const float inv = sum > 0.f ? 1.0f / sum : 0.f, unit = pow2_byte(f.pivot);
       const bool whole = seg.whole();
       const int heads = seg.heads(), head0 = seg.head0();
       const int part = 2 * blockIdx.x + (seg.u0 == 0 ? 1 : 0);
       if (!whole && seg.u0 == 0) {  // the item's first part, and this CTA's last segment
-        const int64_t end = m.w1 + seg.seg_units - seg.u1;  // behind the item's last unit
-        owner = make_int2(1 + seg.seg_b * S + seg.seg_sub, static_cast<int>((end * m.ctas + m.total - 1) / m.total - 1));
+        const int64_t last = m.w1 + seg.seg_units - seg.u1 - 1, more = (m.per_cta + 1) * m.rest;  // the item's last unit
+        const int64_t cta = last < more ? last / (m.per_cta + 1) : m.rest + (last - more) / m.per_cta;
+        owner = make_int2(1 + (seg.seg_b * a.kv + seg.kvh) * a.blocks + seg.blk, static_cast<int>(cta));
       }
-      const int64_t groups = static_cast<int64_t>(a.H) * a.D / 32, b4 = (static_cast<int64_t>(a.B) + 3) / 4 * 4;
-      for (int p = 0; p < NP; ++p) {
+      if (quarter == 0 && lane < HPT && my < heads) {
+        if (!whole) a.stat[part * GP + my] = make_float2(ref, sum);
+        else if (a.lse != nullptr)
+          a.lse[static_cast<int64_t>(seg.seg_b) * a.H + head0 + my] = lse_of(ref, sum);
+      }
+      const int64_t row = seg.seg_b;
 #pragma unroll 1
-        for (int j = 0; j < HPT; j += 8) {
-          if (h0 + j >= heads) break;
-          uint32_t r[8];
-          tmem_ld_x8(t_lane + p * GP + h0 + j, r);
-          tmem_ld_wait();
+      for (int i = 0; i < NP * (HPT / 8); ++i) {
+        const int p = i / (HPT / 8), j = i % (HPT / 8) * 8, n = min(8, heads - h0 - j);  // heads h0 + j ..
+        if (n <= 0) continue;
+        uint32_t r[8];
+        tmem_ld_x8(t_lane + p * GP + h0 + j, r);
+        tmem_ld_wait();
+        const int d = 128 * p + 32 * quarter + lane;
+        if (!whole) {
+          float* out = a.part + (static_cast<int64_t>(part) * GP + h0 + j) * a.D + d;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int h = h0 + j + k;
-            if (h >= heads) break;
-            const float sum = f.sum[0][h] + f.sum[1][h] + f.sum[2][h] + f.sum[3][h];
-            const float v = sum > 0.f ? __uint_as_float(r[k]) * (1.0f / sum) * unit : 0.f;
-            const int d = 128 * p + 32 * quarter + lane;
-            if (!whole) {
-              a.part[(static_cast<int64_t>(part) * GP + h) * a.D + d] = v;
-              if (d == 0) a.stat[part * GP + h] = make_float2(f.ref[h], sum);
-            } else {
-              const int64_t row = seg.seg_b;
-              const int head = head0 + h;
-              const uint32_t y = bf16x2_rn(v, 0.f) & 0xFFFFu;
-              const int64_t at = (row * a.H + head) * a.D + d;
-              if (a.o != nullptr) a.o[at] = static_cast<uint16_t>(y);
-              if (a.oq != nullptr) {
-                const uint32_t code = ue8m0_from_bf16_amax(__reduce_max_sync(0xffffffffu, y & 0x7FFFu));
-                a.oq[at] = static_cast<uint8_t>(e4m3x2(bf16_lo(y) * ue8m0_inverse(code), 0.f));
-                const int64_t g = (static_cast<int64_t>(head) * a.D + d) >> 5;
-                if (lane == 0) {
-                  if (a.sf_rm != nullptr) a.sf_rm[row * groups + g] = static_cast<uint8_t>(code);
-                  if (a.sf_pk != nullptr) a.sf_pk[(g / 4 * b4 + row) * 4 + g % 4] = static_cast<uint8_t>(code);
-                  if (a.sf_tl != nullptr) a.sf_tl[tiled128x4_word_offset(row, g / 4, groups / 4) + g % 4] = static_cast<uint8_t>(code);
-                }
-              }
-              if (a.lse != nullptr && d == 0)
-                a.lse[row * a.H + head] = sum > 0.f ? (f.ref[h] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          for (int k = 0; k < 8; ++k, out += a.D) {
+            const float v = __uint_as_float(r[k]) * __shfl_sync(0xffffffffu, inv, j + k) * unit;
+            if (k < n) *out = v;
+          }
+        } else {
+          int64_t at = (row * a.H + head0 + h0 + j) * a.D + d;
+          uint32_t mine = 0;  // lane k: the scale byte of head k
+#pragma unroll
+          for (int k = 0; k < 8; ++k, at += a.D) {
+            const uint32_t y = bf16x2_rn(__uint_as_float(r[k]) * __shfl_sync(0xffffffffu, inv, j + k) * unit, 0.f) & 0xFFFFu;
+            if (a.o != nullptr && k < n) a.o[at] = static_cast<uint16_t>(y);
+            if (a.oq != nullptr) {
+              const uint32_t code = ue8m0_from_bf16_amax(__reduce_max_sync(0xffffffffu, y & 0x7FFFu));
+              if (k < n) a.oq[at] = static_cast<uint8_t>(e4m3x2(bf16_lo(y) * ue8m0_inverse(code), 0.f));
+              mine = lane == k ? code : mine;
             }
+          }
+          if (a.oq != nullptr && lane < n) {
+            const int64_t word = static_cast<int64_t>(head0 + h0 + j + lane) * NP + p, words = static_cast<int64_t>(a.H) * NP;
+            if (a.sf_rm != nullptr) a.sf_rm[(row * words + word) * 4 + quarter] = static_cast<uint8_t>(mine);
+            if (a.sf_pk != nullptr) a.sf_pk[(word * ((a.B + 3) / 4 * 4) + row) * 4 + quarter] = static_cast<uint8_t>(mine);
+            if (a.sf_tl != nullptr) a.sf_tl[tiled128x4_word_offset(row, word, words) + quarter] = static_cast<uint8_t>(mine);
           }
         }
       }
@@ -926,105 +1062,172 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (tid == 0 && m.dead != 0 && a.status != nullptr) atomicCAS(a.status, 0, MXQ_ERR_TIMEOUT);
 #undef BAR
 }
 
-// Adds the parts of the items that more than one CTA held: a block takes 128 features of one head, a warp
-// every eighth part, added in fixed order. Also the scale layouts' padding rows.
-constexpr int kJoinThreads = 256;
+// Adds the parts of the items that more than one CTA held, always in the CTAs' order of a warp's share. Work is
+// 128 features of one head of an item. With few items, which then have many parts, a block takes each and its warps
+// every eighth part; with many a warp does (64 ragged sequences of 64 x 512: 150 -> XX us). Also the scale
+// layouts' padding rows.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxCtas = 512;
+constexpr int kFewItems = 32;
+
+struct JoinWork {
+  int j0, h, p, parts, b, head;
+};
+__device__ __forceinline__ JoinWork join_work(const Args& a, const int16_t* owners, int64_t i) {
+  const int per = a.block_heads * a.panels, S = a.kv * a.blocks;
+  JoinWork w;
+  w.j0 = owners[i / per];
+  w.h = static_cast<int>(i % per) / a.panels;
+  w.p = static_cast<int>(i % per) % a.panels;
+  const int2 own = a.owner[w.j0];
+  const int item = own.x - 1, sub = item % S, h0 = sub % a.blocks * a.block_heads;
+  w.parts = w.h < min(a.block_heads, a.G - h0) ? own.y - w.j0 + 1 : 0;
+  w.b = item / S;
+  w.head = sub / a.blocks * a.G + h0 + w.h;
+  return w;
+}
+// Part k: the first CTA's last segment, the others' first.
+__device__ __forceinline__ int64_t join_slot(const JoinWork& w, int k) { return k == 0 ? 2 * w.j0 + 1 : 2 * (w.j0 + k); }
+
+// A warp's features 4 lane .. + 3, already divided by the sum.
+__device__ __forceinline__ void join_store(const Args& a, const JoinWork& w, float4 v, float lse, int lane) {
+  const int64_t words = static_cast<int64_t>(a.H) * a.D / 128, b4 = (static_cast<int64_t>(a.B) + 3) / 4 * 4;
+  const uint2 y = make_uint2(bf16x2_rn(v.x, v.y), bf16x2_rn(v.z, v.w));
+  const int64_t at = (static_cast<int64_t>(w.b) * a.H + w.head) * a.D + 128 * w.p + 4 * lane;
+  if (a.o != nullptr) *reinterpret_cast<uint2*>(a.o + at) = y;
+  if (a.oq != nullptr) {
+    uint32_t amax = max(absmax_bf16x2(y.x), absmax_bf16x2(y.y));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const uint32_t code = ue8m0_from_bf16_amax(amax);
+    const float s = ue8m0_inverse(code);
+    *reinterpret_cast<uint32_t*>(a.oq + at) = e4m3x2(bf16_lo(y.x) * s, bf16_hi(y.x) * s) | (e4m3x2(bf16_lo(y.y) * s, bf16_hi(y.y) * s) << 16);
+    uint32_t c = code;
+    c |= __shfl_down_sync(0xffffffffu, code, 8) << 8;
+    c |= __shfl_down_sync(0xffffffffu, code, 16) << 16;
+    c |= __shfl_down_sync(0xffffffffu, code, 24) << 24;
+    const int64_t word = static_cast<int64_t>(w.head) * a.panels + w.p;
+    if (lane == 0) {
+      if (a.sf_rm != nullptr) *reinterpret_cast<uint32_t*>(a.sf_rm + (w.b * words + word) * 4) = c;
+      if (a.sf_pk != nullptr) *reinterpret_cast<uint32_t*>(a.sf_pk + (word * b4 + w.b) * 4) = c;
+      if (a.sf_tl != nullptr) *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(w.b, word, words)) = c;
+    }
+  }
+  if (a.lse != nullptr && w.p == 0 && lane == 0) a.lse[static_cast<int64_t>(w.b) * a.H + w.head] = lse;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ void join_add(float4& v, float w, const float* x) {
+  const float4 f = *reinterpret_cast<const float4*>(x);
+  v.x = fmaf(w, f.x, v.x), v.y = fmaf(w, f.y, v.y), v.z = fmaf(w, f.z, v.z), v.w = fmaf(w, f.w, v.w);
+}
+
+
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int gp) {
   __shared__ int16_t owners[kMaxCtas];
   __shared__ int count;
   __shared__ float weight[kMaxCtas];
-  __shared__ float4 acc[kJoinThreads / 32][32];
-  __shared__ float tops[kJoinThreads / 32], sums[kJoinThreads / 32];
+  __shared__ float4 acc[kJoinWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t words = static_cast<int64_t>(a.H) * a.D / 128, b4 = (static_cast<int64_t>(a.B) + 3) / 4 * 4,
                 b128 = (static_cast<int64_t>(a.B) + 127) / 128 * 128;
-  for (int64_t i = blockIdx.x * kJoinThreads + tid; i < words * (b128 - a.B); i += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
-    const int64_t row = a.B + i / words, w = i % words;
-    if (a.sf_pk != nullptr && row < b4) *reinterpret_cast<uint32_t*>(a.sf_pk + (w * b4 + row) * 4) = 0;
-    if (a.sf_tl != nullptr) *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(row, w, words)) = 0;
-  }
-  if (tid == 0) count = 0;
+  if (a.sf_pk != nullptr || a.sf_tl != nullptr)
+#pragma unroll 1
+    for (int64_t i = blockIdx.x * kJoinThreads + tid; i < words * (b128 - a.B); i += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
+      const int64_t row = a.B + i / words, w = i % words;
+      if (a.sf_pk != nullptr && row < b4) *reinterpret_cast<uint32_t*>(a.sf_pk + (w * b4 + row) * 4) = 0;
+      if (a.sf_tl != nullptr) *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(row, w, words)) = 0;
+    }
   pdl_wait_primary();
-  __syncthreads();
-  if (warp == 0)
+  if (warp == 0) {
+    int n = 0;
+#pragma unroll 1
     for (int i = 0; i < a.ctas; i += 32) {
       const bool is = i + lane < a.ctas && a.owner[i + lane].x != 0;
       const uint32_t all = __ballot_sync(0xffffffffu, is);
-      if (is) owners[count + __popc(all & ((1u << lane) - 1))] = static_cast<int16_t>(i + lane);
-      __syncwarp();
-      if (lane == 0) count += __popc(all);
-      __syncwarp();
+      if (is) owners[n + __popc(all & ((1u << lane) - 1))] = static_cast<int16_t>(i + lane);
+      n += __popc(all);
     }
+    if (lane == 0) count = n;
+  }
   __syncthreads();
-  const int S = a.kv * a.blocks, per = a.block_heads * a.panels;
-  for (int64_t i = blockIdx.x; i < static_cast<int64_t>(count) * per; i += gridDim.x) {
-    const int j0 = owners[i / per], h = static_cast<int>(i % per) / a.panels, p = static_cast<int>(i % per) % a.panels;
-    const int2 own = a.owner[j0];
-    const int item = own.x - 1, parts = own.y - j0 + 1, b = item / S, sub = item % S;
-    if (h >= min(a.block_heads, a.G - sub % a.blocks * a.block_heads)) continue;  // block-uniform
-    const int head = sub / a.blocks * a.G + sub % a.blocks * a.block_heads + h;
-    // part k: the first CTA's last segment, the others' first
-    auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * j0 + 1 : 2 * (j0 + k)); };
-    float top = kLowRef;
-    for (int k = tid; k < parts; k += kJoinThreads) top = fmaxf(top, a.stat[slot(k) * gp + h].x);
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-    for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, tops[w]);
-    float sum = 0.f;
-    for (int k = tid; k < parts; k += kJoinThreads) {
-      const float2 s = a.stat[slot(k) * gp + h];
-      weight[k] = s.y * ex2(s.x - top);
-      sum += weight[k];
+  const int64_t total = static_cast<int64_t>(count) * a.block_heads * a.panels;
+  if (count > kFewItems) {
+#pragma unroll 1
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp; i < total; i += static_cast<int64_t>(gridDim.x) * kJoinWarps) {
+      const JoinWork w = join_work(a, owners, i);
+      if (w.parts == 0) continue;
+      float top = kLowRef;
+#pragma unroll 1
+      for (int k = lane; k < w.parts; k += 32) top = fmaxf(top, a.stat[join_slot(w, k) * gp + w.h].x);
+      top = warp_max(top);
+      float sum = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int k0 = 0; k0 < w.parts; k0 += 32) {
+        float mine = 0.f;
+        if (k0 + lane < w.parts) {
+          const float2 s = a.stat[join_slot(w, k0 + lane) * gp + w.h];
+          mine = s.y * ex2(s.x - top);
+        }
+        sum += mine;
+#pragma unroll 2
+        for (int k = 0; k < min(32, w.parts - k0); ++k)
+          join_add(v, __shfl_sync(0xffffffffu, mine, k), a.part + (join_slot(w, k0 + k) * gp + w.h) * a.D + 128 * w.p + 4 * lane);
+      }
+      sum = warp_sum(sum);
+      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+      join_store(a, w, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv), lse_of(top, sum), lane);
     }
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) sums[warp] = sum;
+    return;
+  }
+#pragma unroll 1
+  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+    const JoinWork w = join_work(a, owners, i);
+    if (w.parts == 0) continue;  // block-uniform
+    // every warp looks over all the statistics; the weights are the same whoever writes them
+    float top = kLowRef;
+#pragma unroll 1
+    for (int k = lane; k < w.parts; k += 32) top = fmaxf(top, a.stat[join_slot(w, k) * gp + w.h].x);
+    top = warp_max(top);
+    float sum = 0.f;
+#pragma unroll 1
+    for (int k = lane; k < w.parts; k += 32) {
+      const float2 s = a.stat[join_slot(w, k) * gp + w.h];
+      const float x = s.y * ex2(s.x - top);
+      if (warp == 0) weight[k] = x;
+      sum += x;
+    }
+    sum = warp_sum(sum);
     __syncthreads();
-    sum = 0.f;
-    for (int w = 0; w < kJoinThreads / 32; ++w) sum += sums[w];
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = warp; k < parts; k += kJoinThreads / 32) {
-      const float4 x = *reinterpret_cast<const float4*>(a.part + (slot(k) * gp + h) * a.D + 128 * p + 4 * lane);
-      const float w = weight[k];
-      v.x = fmaf(w, x.x, v.x), v.y = fmaf(w, x.y, v.y), v.z = fmaf(w, x.z, v.z), v.w = fmaf(w, x.w, v.w);
-    }
+    for (int k = warp; k < w.parts; k += kJoinWarps)
+      join_add(v, weight[k], a.part + (join_slot(w, k) * gp + w.h) * a.D + 128 * w.p + 4 * lane);
     acc[warp][lane] = v;
     __syncthreads();
     if (warp == 0) {
-      for (int w = 1; w < kJoinThreads / 32; ++w) {
-        const float4 x = acc[w][lane];
+#pragma unroll 1
+      for (int k = 1; k < kJoinWarps; ++k) {
+        const float4 x = acc[k][lane];
         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
       }
       const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-      const uint2 y = make_uint2(bf16x2_rn(v.x * inv, v.y * inv), bf16x2_rn(v.z * inv, v.w * inv));
-      const int64_t at = (static_cast<int64_t>(b) * a.H + head) * a.D + 128 * p + 4 * lane;
-      if (a.o != nullptr) *reinterpret_cast<uint2*>(a.o + at) = y;
-      if (a.oq != nullptr) {
-        uint32_t amax = max(absmax_bf16x2(y.x), absmax_bf16x2(y.y));
-        for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const uint32_t code = ue8m0_from_bf16_amax(amax);
-        const float s = ue8m0_inverse(code);
-        *reinterpret_cast<uint32_t*>(a.oq + at) = e4m3x2(bf16_lo(y.x) * s, bf16_hi(y.x) * s) | (e4m3x2(bf16_lo(y.y) * s, bf16_hi(y.y) * s) << 16);
-        uint32_t w = code;
-        w |= __shfl_down_sync(0xffffffffu, code, 8) << 8;
-        w |= __shfl_down_sync(0xffffffffu, code, 16) << 16;
-        w |= __shfl_down_sync(0xffffffffu, code, 24) << 24;
-        const int64_t word = static_cast<int64_t>(head) * a.panels + p;
-        if (lane == 0) {
-          if (a.sf_rm != nullptr) *reinterpret_cast<uint32_t*>(a.sf_rm + (b * words + word) * 4) = w;
-          if (a.sf_pk != nullptr) *reinterpret_cast<uint32_t*>(a.sf_pk + (word * b4 + b) * 4) = w;
-          if (a.sf_tl != nullptr) *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(b, word, words)) = w;
-        }
-      }
-      if (a.lse != nullptr && p == 0 && lane == 0)
-        a.lse[static_cast<int64_t>(b) * a.H + head] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      join_store(a, w, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv), lse_of(top, sum), lane);
     }
-    __syncthreads();
+    __syncthreads();  // (the weights and sums of the next)
   }
 }
 
@@ -1051,14 +1254,14 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 template <int GP>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, Args a, cudaStream_t stream) {
-  a.p_bufs = a.panels * GP >= 256 ? 1 : 2;
+  a.p_bufs = 2;
   a.sf_bufs = a.panels <= 2 ? 4 : 2;
-  const int fixed = layout_of(GP, a.panels, 0, a.sf_bufs, a.p_bufs).total;
+  const int fixed = layout_of(GP, a.panels, a.v_sf == nullptr, 0, a.sf_bufs, a.p_bufs).total;
   a.ring = std::min(16, (kSmemLimit - fixed) / kPanel);
   static PerDevice set;
   cudaError_t e = allow_smem(set, attention_kernel<GP>, kSmemLimit);
   if (e != cudaSuccess) return e;
-  attention_kernel<GP><<<a.ctas, kThreads, layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs).total, stream>>>(mk, mv, a);
+  attention_kernel<GP><<<a.ctas, kThreads, layout_of(GP, a.panels, a.v_sf == nullptr, a.ring, a.sf_bufs, a.p_bufs).total, stream>>>(mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * num_sms()));
@@ -1112,6 +1315,11 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
   a.blocks = (a.G + kMaxHeads - 1) / kMaxHeads;
   a.block_heads = (a.G + a.blocks - 1) / a.blocks;
   a.box = std::min(kUnit, k.page_size & -k.page_size);
+  a.box_shift = __builtin_ctz(a.box);
+  // 2^(31 + s) / d rounded up, s = floor(log2 d): off by less than d < 2^(s + 1), which t < 2^30 times stays below 2^(31 + s)
+  const int s = 31 - __builtin_clz(k.page_size);
+  a.page_mul = static_cast<uint32_t>((uint64_t(1) << (31 + s)) / k.page_size + 1);
+  a.page_shift = s - 1;
   a.scale = l.scale;
   a.o = static_cast<uint16_t*>(l.o);
   a.oq = static_cast<uint8_t*>(l.o_q);
@@ -1120,6 +1328,12 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
   a.sf_tl = static_cast<uint8_t*>(l.sf_tiled);
   a.lse = l.lse;
   a.status = l.status;
+  // scales are copied in the largest pieces that every row starts on a multiple of
+  auto vec_of = [&](const mxq_kv_cache& c) {
+    const uint64_t all = reinterpret_cast<uintptr_t>(c.sf) | c.sf_page_stride | c.sf_token_stride | c.sf_head_stride;
+    return all % 16 == 0 && a.panels == 4 ? 16 : all % 8 == 0 && a.panels % 2 == 0 ? 8 : 4;
+  };
+  a.sf_vec = std::min(vec_of(k), vec_of(l.v != nullptr ? *l.v : k));
   const int gp = padded_heads(a.block_heads);
   const int64_t ctas = std::min(kMaxCtas, num_sms());
   const int64_t most = l.B * a.kv * a.blocks * ((static_cast<int64_t>(l.table_width) * k.page_size + kUnit - 1) / kUnit);
