@@ -97,7 +97,7 @@ MXQ_API mxq_status kv_read_bf16(const mxq_kv_cache* k_cache, const mxq_kv_cache*
  *   status: optional device status word (mxq_status_bytes()).
  * At least one of o_bf16 and o_q. Requires dim in {128, 256, 384, 512}, page_size % 16 == 0, q_heads a multiple
  * of heads, q_heads <= 4096, 1 <= B <= 65536 / heads, table_width >= 1, table_width * page_size <= 2^30, a finite
- * scale. Two launches; the results do not depend on timing.
+ * scale. Three launches; the results do not depend on timing.
  */
 MXQ_API int64_t mxq_paged_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim);
 

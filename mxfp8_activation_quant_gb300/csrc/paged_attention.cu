@@ -17,7 +17,7 @@
 // fp16 holds code * 2^(b - E) exactly for b in [E - 15, E + 7]: a tile with a scale above raises E (O is
 // rescaled with ref), one with a nonzero scale below takes P and V as bf16.
 //
-// Warps: 0 TMA, 1 MMA, 2-3 scales, 4-11 queries and softmax (two a TMEM lane quarter, half of the heads each),
+// Warps: 0 TMA, 1 MMA, 2-3 scales, 4-11 softmax (two a TMEM lane quarter, half of the heads each),
 // 12-19 V^T and the outputs (two a quarter; 64 of the tile's tokens each, half of the heads each).
 //
 // A CTA that holds an item from start to end writes its outputs; the others' normalised parts go to the
@@ -65,6 +65,7 @@ struct Args {
   int32_t sf_vec;               // bytes of a copy of scales
   int32_t ring, sf_bufs, p_bufs;
   float scale;
+  uint8_t* q_ws; // [items][panels][2 GP x 128] swizzled, [panels][512] scale atoms
   float* part;   // [2 * CTAs][GP][D]
   float2* stat;  // [2 * CTAs][GP]: ref, sum
   int2* owner;   // [CTAs]: 1 + the item whose first part is the CTA's last segment (0: none), the CTA of its last part
@@ -354,6 +355,48 @@ __device__ __forceinline__ void wait_bar(Misc& m, uint32_t bar, uint32_t parity)
   }
 }
 
+// q as hi + lo, an item's panels as the kernel's shared memory holds them (rows of 128 bytes, swizzled; hi heads, then
+// lo heads; then the scale atoms), so that they come by bulk copies. One block a panel: 8 values a lane, 16 lanes a head.
+// In the attention kernel itself this took 5 us an item of 64 x 512, with loads that nothing overlaps.
+constexpr int kQThreads = 256;
+template <int GP>
+__global__ void __launch_bounds__(kQThreads) query_kernel(const __grid_constant__ Args a) {
+  pdl_launch_dependents();
+  const uint32_t item = blockIdx.x / a.panels, p = blockIdx.x - item * a.panels;
+  const uint32_t bk = item / a.blocks, blk = item - bk * a.blocks, b = bk / a.kv, kvh = bk - b * a.kv;
+  const int heads = min(a.block_heads, a.G - static_cast<int>(blk) * a.block_heads), head0 = kvh * a.G + blk * a.block_heads;
+  const int tid = threadIdx.x, col = (tid & 15) * 8;
+  const uint16_t* const q = a.q + b * a.ldq + head0 * a.ldqh + 128 * p + col;
+  uint8_t* const out = a.q_ws + static_cast<int64_t>(item) * (a.panels * (GP * 256 + 512));
+  uint8_t* const panel = out + p * GP * 256;
+  uint8_t* const atom = out + a.panels * GP * 256 + p * 512;
+  uint4 xs[GP / 16];
+#pragma unroll
+  for (int u = 0; u < GP / 16; ++u) {
+    const int h = (tid >> 4) + 16 * u;
+    xs[u] = h < heads ? ld_stream_u4(q + h * a.ldqh) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < GP / 16; ++u) {
+    const int h = (tid >> 4) + 16 * u, r = GP + h;
+    const uint4 x = xs[u];
+    uint32_t amax = absmax8(x);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const uint32_t code = ue8m0_from_bf16_amax(amax), low = code >= 4 ? code - 4 : 0;
+    const float inv = ue8m0_inverse(code), up = __uint_as_float((127 + code - low) << 23);
+    const uint2 hi = quant8(x, inv);
+    const uint2 lo = make_uint2(rest4(x.x, x.y, hi.x, inv, up), rest4(x.z, x.w, hi.y, inv, up));
+    const int at = (((col >> 4) ^ (h & 7)) << 4) + (col & 8);  // (GP is a multiple of 8: both rows swizzle alike)
+    *reinterpret_cast<uint2*>(panel + h * 128 + at) = hi;
+    *reinterpret_cast<uint2*>(panel + r * 128 + at) = lo;
+    if ((tid & 3) == 0) {
+      atom[(h & 31) * 16 + (h >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(code);
+      atom[(r & 31) * 16 + (r >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(low);
+    }
+  }
+}
+
 template <int GP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -392,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 #pragma unroll 1
     for (int i = 0; i < kVSlots; ++i) mbar_init(BAR(v_full[i]), 4), mbar_init(BAR(v_empty[i]), 1);
-    mbar_init(BAR(q_full), 8), mbar_init(BAR(q_empty), 1);
+    mbar_init(BAR(q_full), 1), mbar_init(BAR(q_empty), 1);
     mbar_init(BAR(o_full), 1), mbar_init(BAR(o_empty), 8);
     mbar_init(BAR(done), 1);
     fence_mbar_init();
@@ -609,23 +652,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring sf(a.sf_bufs);
     uint32_t parity = 0;
     const uint32_t stage0 = lay.stage + (64 * w + lane) * 16;  // [tile parity][kind][token] of 16 bytes
-    auto fetch = [&](int tile, int tiles, uint32_t (&pg)[2], int kvh, const int32_t* row) {
-      const int32_t n = tile < tiles ? seg.tokens(tile) : 0;
+    // the pages of this lane's tokens of a tile (no page: 2^32 - 1)
+    auto pages_of = [&](int tile, int tiles, const int32_t* row, uint32_t& p0, uint32_t& p1) {
+      const int32_t n = tile < tiles ? seg.tokens(tile) : 0, r = 64 * w + lane;
+      const uint32_t t = static_cast<uint32_t>(seg.start(tile) + r);
+      p0 = r < n ? static_cast<uint32_t>(row[page_index(a, t)]) : 0xFFFFFFFFu;
+      p1 = r + 32 < n ? static_cast<uint32_t>(row[page_index(a, t + 32)]) : 0xFFFFFFFFu;
+    };
+    auto fetch = [&](int tile, uint32_t p0, uint32_t p1, int kvh) {
 #pragma unroll 1
       for (int j = 0; j < 2; ++j) {
-        const int32_t r = 64 * w + 32 * j + lane;
-        uint32_t g = 0xFFFFFFFFu;
-        if (r < n) {
-          const uint32_t t = static_cast<uint32_t>(seg.start(tile) + r), i = page_index(a, t), at = t - i * a.page_size;
-          g = static_cast<uint32_t>(row[i]);
-          if (g < a.pages) {
-            const uint32_t dst = sbase + stage0 + 512 * j + (tile & 1) * kinds * 2048;
-            cp_async_scales(dst, a.k_sf + g * a.k_sf_page + at * a.k_sf_token + kvh * a.k_sf_head, NP, a.sf_vec);
-            if (!shared_kv) cp_async_scales(dst + 2048, a.v_sf + g * a.v_sf_page + at * a.v_sf_token + kvh * a.v_sf_head, NP, a.sf_vec);
-          }
+        const uint32_t g = j == 0 ? p0 : p1;
+        if (g < a.pages) {
+          const uint32_t t = static_cast<uint32_t>(seg.start(tile) + 64 * w + 32 * j + lane), at = t - page_index(a, t) * a.page_size;
+          const uint32_t dst = sbase + stage0 + 512 * j + (tile & 1) * kinds * 2048;
+          cp_async_scales(dst, a.k_sf + g * a.k_sf_page + at * a.k_sf_token + kvh * a.k_sf_head, NP, a.sf_vec);
+          if (!shared_kv) cp_async_scales(dst + 2048, a.v_sf + g * a.v_sf_page + at * a.v_sf_token + kvh * a.v_sf_head, NP, a.sf_vec);
         }
-        if (j == 0) pg[0] = g;
-        else pg[1] = g;
       }
       cp_async_commit();
     };
@@ -635,10 +678,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* row = a.table + seg.seg_b * a.ld_table;
       int32_t pivot = 0;
       uint32_t page[2], next_page[2];
-      fetch(0, tiles, page, kvh, row);
+      pages_of(0, tiles, row, page[0], page[1]);
+      pages_of(1, tiles, row, next_page[0], next_page[1]);
+      fetch(0, page[0], page[1], kvh);
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
-        fetch(i + 1, tiles, next_page, kvh, row);
+        uint32_t far_page[2];
+        pages_of(i + 2, tiles, row, far_page[0], far_page[1]);
+        fetch(i + 1, next_page[0], next_page[1], kvh);
         cp_async_wait_1();
         const bool ok[2] = {page[0] < a.pages, page[1] < a.pages};
         const uint32_t* const kw = reinterpret_cast<const uint32_t*>(smem + stage0 + (i & 1) * kinds * 2048);
@@ -697,13 +744,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(sf_full[0]) + 8 * sf.slot);
         sf.next();
-        page[0] = next_page[0];
-        page[1] = next_page[1];
+        page[0] = next_page[0], page[1] = next_page[1];
+        next_page[0] = far_page[0], next_page[1] = far_page[1];
       }
     }
     cp_async_wait_0();
   } else if (warp < 12) {
-    // ---- queries and softmax ----
+    // ---- softmax ----
     const int quarter = warp & 3, h0 = (warp - 4) / 4 * HPT, st = tid - 128;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const float c = a.scale * 1.4426950408889634f;
@@ -712,49 +759,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int prow = (t & ~15) + ((t >> 2) & 3) * 2 + (t & 1) + ((t & 2) << 2);
     Segments seg(a, m);
     Ring sf(a.sf_bufs), s(SB), pr(a.p_bufs), one(1), fin(2);
+    bool first = true;
 #pragma unroll 1
     while (seg.next()) {
       const int tiles = seg.tiles(), heads = seg.heads();
-      // q as hi + lo: 8 values a lane, 4 lanes a group
-      wait_bar(m, BAR(q_empty), one.phase ^ 1);
-      one.next();
-      {
-        const uint16_t* q = a.q + seg.seg_b * a.ldq + seg.head0() * a.ldqh + (st & 15) * 8;
-        const int col = (st & 15) * 8;
-#pragma unroll 1
-        for (int p = 0; p < NP; ++p) {  // 16 lanes a head's 128 features
-          uint8_t* const panel = smem + lay.q + p * GP * 256;
-          uint8_t* const atom = smem + lay.q_sf + p * 512;
-          uint4 xs[GP / 16];
-#pragma unroll
-          for (int u = 0; u < GP / 16; ++u) {
-            const int h = (st >> 4) + 16 * u;
-            xs[u] = h < heads ? ld_stream_u4(q + h * a.ldqh + 128 * p) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int u = 0; u < GP / 16; ++u) {
-            const int h = (st >> 4) + 16 * u, r = GP + h;
-            const uint4 x = xs[u];
-            uint32_t amax = absmax8(x);
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const uint32_t code = ue8m0_from_bf16_amax(amax), low = code >= 4 ? code - 4 : 0;
-            const float inv = ue8m0_inverse(code), up = __uint_as_float((127 + code - low) << 23);
-            const uint2 hi = quant8(x, inv);
-            const uint2 lo = make_uint2(rest4(x.x, x.y, hi.x, inv, up), rest4(x.z, x.w, hi.y, inv, up));
-            const int at = (((col >> 4) ^ (h & 7)) << 4) + (col & 8);  // (GP is a multiple of 8: both rows swizzle alike)
-            *reinterpret_cast<uint2*>(panel + h * 128 + at) = hi;
-            *reinterpret_cast<uint2*>(panel + r * 128 + at) = lo;
-            if ((lane & 3) == 0) {
-              atom[(h & 31) * 16 + (h >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(code);
-              atom[(r & 31) * 16 + (r >> 5) * 4 + (col >> 5)] = static_cast<uint8_t>(low);
-            }
-          }
-        }
+      if (st == 0) {  // this item's queries, once the last scores of the one before are done
+        wait_bar(m, BAR(q_empty), one.phase ^ 1);
+        const uint8_t* const q = a.q_ws + ((static_cast<int64_t>(seg.seg_b) * a.kv + seg.kvh) * a.blocks + seg.blk) * (NP * (GP * 256 + 512));
+        if (first) pdl_wait_primary();
+        first = false;
+        mbar_arrive_expect_tx(BAR(q_full), NP * (GP * 256 + 512));
+        bulk_load(sbase + lay.q, q, NP * GP * 256, BAR(q_full));
+        bulk_load(sbase + lay.q_sf, q + NP * GP * 256, NP * 512, BAR(q_full));
+        one.next();
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(q_full));
       float l[HPT];
 #pragma unroll
       for (int i = 0; i < HPT; ++i) l[i] = 0.f;
@@ -884,6 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(BAR(fin_full[fin.slot]));
       fin.next();
     }
+    if (st == 0 && !first && !mbar_wait_bounded(BAR(q_full), one.phase ^ 1)) m.dead = 1;  // (no copy outlives the CTA)
   } else {
     // ---- V^T and the outputs ----
     const int quarter = warp & 3, set = (warp - 12) / 4, h0 = set * HPT;
@@ -1066,38 +1085,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef BAR
 }
 
-// Adds the parts of the items that more than one CTA held, always in the CTAs' order of a warp's share. Work is
-// 128 features of one head of an item. With few items, which then have many parts, a block takes each and its warps
-// every eighth part; with many a warp does (64 ragged sequences of 64 x 512: 150 -> XX us). Also the scale
-// layouts' padding rows.
+// Adds the parts of the items that more than one CTA held, always in the CTAs' order of a warp's share. With few
+// items, which then have many parts, a block takes 128 features of a head and its warps every eighth part; with
+// many a warp takes a head. Also the scale layouts' padding rows.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxCtas = 512;
 constexpr int kFewItems = 32;
 
 struct JoinWork {
-  int j0, h, p, parts, b, head;
+  int j0, h, parts, b, head;
 };
-__device__ __forceinline__ JoinWork join_work(const Args& a, const int16_t* owners, int64_t i) {
-  const int per = a.block_heads * a.panels, S = a.kv * a.blocks;
+__device__ __forceinline__ JoinWork join_work(const Args& a, const int16_t* owners, uint32_t owner, int h) {
   JoinWork w;
-  w.j0 = owners[i / per];
-  w.h = static_cast<int>(i % per) / a.panels;
-  w.p = static_cast<int>(i % per) % a.panels;
+  w.j0 = owners[owner];
+  w.h = h;
   const int2 own = a.owner[w.j0];
-  const int item = own.x - 1, sub = item % S, h0 = sub % a.blocks * a.block_heads;
-  w.parts = w.h < min(a.block_heads, a.G - h0) ? own.y - w.j0 + 1 : 0;
-  w.b = item / S;
-  w.head = sub / a.blocks * a.G + h0 + w.h;
+  const uint32_t item = own.x - 1, k = item / a.blocks, blk = item - k * a.blocks;
+  w.b = k / a.kv;
+  const int kvh = k - w.b * a.kv, h0 = blk * a.block_heads;
+  w.parts = h < min(a.block_heads, a.G - h0) ? own.y - w.j0 + 1 : 0;
+  w.head = kvh * a.G + h0 + h;
   return w;
 }
 // Part k: the first CTA's last segment, the others' first.
-__device__ __forceinline__ int64_t join_slot(const JoinWork& w, int k) { return k == 0 ? 2 * w.j0 + 1 : 2 * (w.j0 + k); }
+__device__ __forceinline__ int join_slot(const JoinWork& w, int k) { return k == 0 ? 2 * w.j0 + 1 : 2 * (w.j0 + k); }
 
-// A warp's features 4 lane .. + 3, already divided by the sum.
-__device__ __forceinline__ void join_store(const Args& a, const JoinWork& w, float4 v, float lse, int lane) {
-  const int64_t words = static_cast<int64_t>(a.H) * a.D / 128, b4 = (static_cast<int64_t>(a.B) + 3) / 4 * 4;
-  const uint2 y = make_uint2(bf16x2_rn(v.x, v.y), bf16x2_rn(v.z, v.w));
-  const int64_t at = (static_cast<int64_t>(w.b) * a.H + w.head) * a.D + 128 * w.p + 4 * lane;
+// A warp's features 128 p + 4 lane .. + 3.
+__device__ __forceinline__ void join_store(const Args& a, const JoinWork& w, int p, float4 v, float inv, int lane) {
+  const uint2 y = make_uint2(bf16x2_rn(v.x * inv, v.y * inv), bf16x2_rn(v.z * inv, v.w * inv));
+  const int64_t at = (static_cast<int64_t>(w.b) * a.H + w.head) * a.D + 128 * p + 4 * lane;
   if (a.o != nullptr) *reinterpret_cast<uint2*>(a.o + at) = y;
   if (a.oq != nullptr) {
     uint32_t amax = max(absmax_bf16x2(y.x), absmax_bf16x2(y.y));
@@ -1110,14 +1126,13 @@ __device__ __forceinline__ void join_store(const Args& a, const JoinWork& w, flo
     c |= __shfl_down_sync(0xffffffffu, code, 8) << 8;
     c |= __shfl_down_sync(0xffffffffu, code, 16) << 16;
     c |= __shfl_down_sync(0xffffffffu, code, 24) << 24;
-    const int64_t word = static_cast<int64_t>(w.head) * a.panels + w.p;
     if (lane == 0) {
+      const int64_t words = static_cast<int64_t>(a.H) * a.panels, word = static_cast<int64_t>(w.head) * a.panels + p;
       if (a.sf_rm != nullptr) *reinterpret_cast<uint32_t*>(a.sf_rm + (w.b * words + word) * 4) = c;
-      if (a.sf_pk != nullptr) *reinterpret_cast<uint32_t*>(a.sf_pk + (word * b4 + w.b) * 4) = c;
+      if (a.sf_pk != nullptr) *reinterpret_cast<uint32_t*>(a.sf_pk + (word * ((a.B + 3) / 4 * 4) + w.b) * 4) = c;
       if (a.sf_tl != nullptr) *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(w.b, word, words)) = c;
     }
   }
-  if (a.lse != nullptr && w.p == 0 && lane == 0) a.lse[static_cast<int64_t>(w.b) * a.H + w.head] = lse;
 }
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -1129,11 +1144,9 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-__device__ __forceinline__ void join_add(float4& v, float w, const float* x) {
-  const float4 f = *reinterpret_cast<const float4*>(x);
+__device__ __forceinline__ void join_add(float4& v, float w, const float4 f) {
   v.x = fmaf(w, f.x, v.x), v.y = fmaf(w, f.y, v.y), v.z = fmaf(w, f.z, v.z), v.w = fmaf(w, f.w, v.w);
 }
-
 
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int gp) {
   __shared__ int16_t owners[kMaxCtas];
@@ -1141,15 +1154,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   __shared__ float weight[kMaxCtas];
   __shared__ float4 acc[kJoinWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t words = static_cast<int64_t>(a.H) * a.D / 128, b4 = (static_cast<int64_t>(a.B) + 3) / 4 * 4,
-                b128 = (static_cast<int64_t>(a.B) + 127) / 128 * 128;
-  if (a.sf_pk != nullptr || a.sf_tl != nullptr)
+  if (a.sf_pk != nullptr || a.sf_tl != nullptr) {  // a word column per block and a row per thread
+    const int words = a.H * a.panels, b4 = (a.B + 3) / 4 * 4, b128 = (a.B + 127) / 128 * 128, row = a.B + tid;
+    if (row < b128)
 #pragma unroll 1
-    for (int64_t i = blockIdx.x * kJoinThreads + tid; i < words * (b128 - a.B); i += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
-      const int64_t row = a.B + i / words, w = i % words;
-      if (a.sf_pk != nullptr && row < b4) *reinterpret_cast<uint32_t*>(a.sf_pk + (w * b4 + row) * 4) = 0;
-      if (a.sf_tl != nullptr) *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(row, w, words)) = 0;
-    }
+      for (int w = blockIdx.x; w < words; w += gridDim.x) {
+        if (a.sf_pk != nullptr && row < b4) *reinterpret_cast<uint32_t*>(a.sf_pk + (static_cast<int64_t>(w) * b4 + row) * 4) = 0;
+        if (a.sf_tl != nullptr) *reinterpret_cast<uint32_t*>(a.sf_tl + tiled128x4_word_offset(row, w, words)) = 0;
+      }
+  }
   pdl_wait_primary();
   if (warp == 0) {
     int n = 0;
@@ -1163,18 +1176,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (lane == 0) count = n;
   }
   __syncthreads();
-  const int64_t total = static_cast<int64_t>(count) * a.block_heads * a.panels;
+  const int heads = count * a.block_heads, NP = a.panels;
   if (count > kFewItems) {
 #pragma unroll 1
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp; i < total; i += static_cast<int64_t>(gridDim.x) * kJoinWarps) {
-      const JoinWork w = join_work(a, owners, i);
+    for (int i = blockIdx.x * kJoinWarps + warp; i < heads; i += gridDim.x * kJoinWarps) {
+      const JoinWork w = join_work(a, owners, static_cast<uint32_t>(i) / a.block_heads, static_cast<uint32_t>(i) % a.block_heads);
       if (w.parts == 0) continue;
-      float top = kLowRef;
+      float top = kLowRef, sum = 0.f;
 #pragma unroll 1
       for (int k = lane; k < w.parts; k += 32) top = fmaxf(top, a.stat[join_slot(w, k) * gp + w.h].x);
       top = warp_max(top);
-      float sum = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 v[4] = {};
 #pragma unroll 1
       for (int k0 = 0; k0 < w.parts; k0 += 32) {
         float mine = 0.f;
@@ -1183,26 +1195,35 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
           mine = s.y * ex2(s.x - top);
         }
         sum += mine;
+        const int n = min(32, w.parts - k0);
 #pragma unroll 2
-        for (int k = 0; k < min(32, w.parts - k0); ++k)
-          join_add(v, __shfl_sync(0xffffffffu, mine, k), a.part + (join_slot(w, k0 + k) * gp + w.h) * a.D + 128 * w.p + 4 * lane);
+        for (int k = 0; k < n; ++k) {
+          const float4* x = reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(join_slot(w, k0 + k)) * gp + w.h) * a.D) + lane;
+          const float f = __shfl_sync(0xffffffffu, mine, k);
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            if (p < NP) join_add(v[p], f, x[32 * p]);
+        }
       }
       sum = warp_sum(sum);
       const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-      join_store(a, w, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv), lse_of(top, sum), lane);
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        if (p < NP) join_store(a, w, p, v[p], inv, lane);
+      if (a.lse != nullptr && lane == 0) a.lse[static_cast<int64_t>(w.b) * a.H + w.head] = lse_of(top, sum);
     }
     return;
   }
 #pragma unroll 1
-  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-    const JoinWork w = join_work(a, owners, i);
+  for (int i = blockIdx.x; i < heads * NP; i += gridDim.x) {
+    const int h = i / NP, p = i - h * NP;
+    const JoinWork w = join_work(a, owners, static_cast<uint32_t>(h) / a.block_heads, static_cast<uint32_t>(h) % a.block_heads);
     if (w.parts == 0) continue;  // block-uniform
-    // every warp looks over all the statistics; the weights are the same whoever writes them
-    float top = kLowRef;
+    // every warp looks over all the statistics
+    float top = kLowRef, sum = 0.f;
 #pragma unroll 1
     for (int k = lane; k < w.parts; k += 32) top = fmaxf(top, a.stat[join_slot(w, k) * gp + w.h].x);
     top = warp_max(top);
-    float sum = 0.f;
 #pragma unroll 1
     for (int k = lane; k < w.parts; k += 32) {
       const float2 s = a.stat[join_slot(w, k) * gp + w.h];
@@ -1215,17 +1236,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = warp; k < w.parts; k += kJoinWarps)
-      join_add(v, weight[k], a.part + (join_slot(w, k) * gp + w.h) * a.D + 128 * w.p + 4 * lane);
+      join_add(v, weight[k], *reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(join_slot(w, k)) * gp + w.h) * a.D + 128 * p + 4 * lane));
     acc[warp][lane] = v;
     __syncthreads();
     if (warp == 0) {
-#pragma unroll 1
-      for (int k = 1; k < kJoinWarps; ++k) {
-        const float4 x = acc[k][lane];
-        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-      }
-      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-      join_store(a, w, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv), lse_of(top, sum), lane);
+#pragma unroll
+      for (int k = 1; k < kJoinWarps; ++k) join_add(v, 1.0f, acc[k][lane]);
+      join_store(a, w, p, v, sum > 0.f ? 1.0f / sum : 0.f, lane);
+      if (a.lse != nullptr && p == 0 && lane == 0) a.lse[static_cast<int64_t>(w.b) * a.H + w.head] = lse_of(top, sum);
     }
     __syncthreads();  // (the weights and sums of the next)
   }
@@ -1252,6 +1270,22 @@ bool make_cache_map(CUtensorMap* m, const mxq_kv_cache& c, int box) {
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
+// Launches `kern` so that it may start before the kernel ahead of it ends.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), unsigned grid, int threads, int bytes, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <int GP>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, Args a, cudaStream_t stream) {
   a.p_bufs = 2;
@@ -1261,27 +1295,33 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, Args a, cudaStr
   static PerDevice set;
   cudaError_t e = allow_smem(set, attention_kernel<GP>, kSmemLimit);
   if (e != cudaSuccess) return e;
-  attention_kernel<GP><<<a.ctas, kThreads, layout_of(GP, a.panels, a.v_sf == nullptr, a.ring, a.sf_bufs, a.p_bufs).total, stream>>>(mk, mv, a);
+  query_kernel<GP><<<static_cast<unsigned>(a.B * a.kv * a.blocks * a.panels), kQThreads, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * num_sms()));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, a, GP);
+  const int bytes = layout_of(GP, a.panels, a.v_sf == nullptr, a.ring, a.sf_bufs, a.p_bufs).total;
+  if ((e = launch_behind(attention_kernel<GP>, a.ctas, kThreads, bytes, stream, mk, mv, a)) != cudaSuccess) return e;
+  return launch_behind(join_kernel, 2 * num_sms(), kJoinThreads, 0, stream, a, GP);
+}
+
+// The workspace: parts, statistics, owners, queries.
+struct Space {
+  int64_t ctas, gp, stat, owner, q, total;
+};
+Space space_of(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim) {
+  const int G = q_heads / kv_heads, blocks = (G + kMaxHeads - 1) / kMaxHeads;
+  Space s;
+  s.gp = padded_heads((G + blocks - 1) / blocks);
+  s.ctas = std::min(kMaxCtas, num_sms());
+  s.stat = align256(2 * s.ctas * s.gp * dim * 4);
+  s.owner = s.stat + align256(2 * s.ctas * s.gp * 8);
+  s.q = s.owner + align256(s.ctas * 8);
+  s.total = s.q + B * kv_heads * blocks * (dim / 128) * (s.gp * 256 + 512);
+  return s;
 }
 
 }  // namespace
 
 int64_t paged_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim) {
-  (void)B;
-  const int G = q_heads / kv_heads, blocks = (G + kMaxHeads - 1) / kMaxHeads, gp = padded_heads((G + blocks - 1) / blocks);
-  const int64_t ctas = std::min(kMaxCtas, num_sms());
-  return align256(2 * ctas * gp * dim * 4) + align256(2 * ctas * gp * 8) + align256(ctas * 8);
+  return space_of(B, q_heads, kv_heads, dim).total;
 }
 
 cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t stream) {
@@ -1334,19 +1374,19 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
     return all % 16 == 0 && a.panels == 4 ? 16 : all % 8 == 0 && a.panels % 2 == 0 ? 8 : 4;
   };
   a.sf_vec = std::min(vec_of(k), vec_of(l.v != nullptr ? *l.v : k));
-  const int gp = padded_heads(a.block_heads);
-  const int64_t ctas = std::min(kMaxCtas, num_sms());
+  const Space sp = space_of(l.B, l.q_heads, k.heads, k.dim);
   const int64_t most = l.B * a.kv * a.blocks * ((static_cast<int64_t>(l.table_width) * k.page_size + kUnit - 1) / kUnit);
-  a.ctas = static_cast<int32_t>(std::min(ctas, most));
+  a.ctas = static_cast<int32_t>(std::min(sp.ctas, most));
   uint8_t* const ws = static_cast<uint8_t*>(l.workspace);
   a.part = reinterpret_cast<float*>(ws);
-  a.stat = reinterpret_cast<float2*>(ws + align256(2 * ctas * gp * a.D * 4));
-  a.owner = reinterpret_cast<int2*>(ws + align256(2 * ctas * gp * a.D * 4) + align256(2 * ctas * gp * 8));
+  a.stat = reinterpret_cast<float2*>(ws + sp.stat);
+  a.owner = reinterpret_cast<int2*>(ws + sp.owner);
+  a.q_ws = ws + sp.q;
   CUtensorMap mk, mv;
   if (!make_cache_map(&mk, k, a.box)) return cudaErrorInvalidValue;
   if (l.v == nullptr) mv = mk;
   else if (!make_cache_map(&mv, *l.v, a.box)) return cudaErrorInvalidValue;
-  return gp == 16 ? launch<16>(mk, mv, a, stream) : gp == 32 ? launch<32>(mk, mv, a, stream) : launch<64>(mk, mv, a, stream);
+  return sp.gp == 16 ? launch<16>(mk, mv, a, stream) : sp.gp == 32 ? launch<32>(mk, mv, a, stream) : launch<64>(mk, mv, a, stream);
 }
 
 }  // namespace mxq
