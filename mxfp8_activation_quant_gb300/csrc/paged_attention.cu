@@ -17,7 +17,7 @@
 // fp16 holds code * 2^(b - E) exactly for b in [E - 15, E + 7]: a tile with a scale above raises E (O is
 // rescaled with ref), one with a nonzero scale below takes P and V as bf16.
 //
-// Warps: 0 TMA, 1 MMA, 2-3 scales, 4-11 softmax (two a TMEM lane quarter, half of the heads each),
+// Warps: 0 loads, 1 and 2 MMAs (scores, outputs), 3 the scales' check, 4-11 softmax (two a TMEM lane quarter, half of the heads each),
 // 12-19 V^T and the outputs (two a quarter; 64 of the tile's tokens each, half of the heads each).
 //
 // A CTA that holds an item from start to end writes its outputs; the others' normalised parts go to the
@@ -62,7 +62,6 @@ struct Args {
   int32_t B, H, kv, G, D, panels;
   int32_t blocks, block_heads;  // blocks of query heads per cache head, and their size
   int32_t box, box_shift;       // tokens of a TMA box, a power of two
-  int32_t sf_vec;               // bytes of a copy of scales
   int32_t ring, sf_bufs, p_bufs;
   float scale;
   uint8_t* q_ws; // [items][panels][2 GP x 128] swizzled, [panels][512] scale atoms
@@ -81,16 +80,17 @@ struct Args {
 
 // Shared memory, from the kernel's sizes. Panels on 1024-byte boundaries (their swizzle).
 struct Layout {
-  int q, p, ring, q_sf, sf, stage, fin, misc, total;
+  int q, p, ring, q_sf, sf, fin, misc, total;
 };
+constexpr int kMaxSfBufs = 6;
 struct Misc {
-  uint64_t ring_full[16], ring_empty[16], sf_full[4], sf_empty[4], s_full[2], s_empty[2], p_full[2], p_empty[2], v_full[kVSlots],
+  uint64_t ring_full[16], ring_empty[16], sf_raw[kMaxSfBufs], sf_full[kMaxSfBufs], sf_empty[kMaxSfBufs], s_full[2], s_empty[2], p_full[2], p_empty[2], v_full[kVSlots],
       v_empty[kVSlots], q_full, q_empty, o_full, o_empty, fin_full[2], fin_empty[2], done;
   alignas(16) float ref[kMaxHeads];
   alignas(16) float fac[kMaxHeads];
   int32_t red[kMaxHeads];
   int64_t sums[kThreads / 32];
-  int32_t sf_red[2][4];
+  int32_t p_wide[2];  // whether the probabilities are bf16
   int64_t w0, w1, per_cta, rest;
   int32_t b0, kvh0, blk0, u0;
   uint32_t tmem;
@@ -100,7 +100,8 @@ struct Misc {
 struct TileInfo {
   uint32_t valid[4];
   int32_t pivot, wide;
-  int32_t pad[2];
+  uint32_t there;  // bit l: tokens 4 l .. 4 l + 3 are on a page of the cache
+  int32_t tokens;
 };
 // A finished segment's sums and references.
 struct Fin {
@@ -110,15 +111,14 @@ struct Fin {
   int32_t pad[3];
 };
 __host__ __device__ inline int sf_buf_bytes(int panels) { return panels * 1024 + static_cast<int>(sizeof(TileInfo)); }
-__host__ __device__ inline Layout layout_of(int gp, int panels, bool shared_kv, int ring, int sf_bufs, int p_bufs) {
+__host__ __device__ inline Layout layout_of(int gp, int panels, int ring, int sf_bufs, int p_bufs) {
   Layout l;
   l.q = 0;
   l.p = l.q + panels * gp * 256;
   l.ring = l.p + p_bufs * kPanel;
   l.q_sf = l.ring + ring * kPanel;
   l.sf = l.q_sf + panels * 512;
-  l.stage = l.sf + sf_bufs * sf_buf_bytes(panels);
-  l.fin = l.stage + 2 * (shared_kv ? 1 : 2) * 2048;
+  l.fin = l.sf + sf_bufs * sf_buf_bytes(panels);
   l.misc = l.fin + 2 * static_cast<int>(sizeof(Fin));
   l.total = l.misc + static_cast<int>(sizeof(Misc));
   return l;
@@ -199,21 +199,14 @@ __device__ __forceinline__ uint32_t f16x2_rn(float first, float second) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(second), "f"(first));
   return r;
 }
-// 4 NP bytes of scales in pieces of `vec` (4, 8 or 16) bytes.
-__device__ __forceinline__ void cp_async_scales(uint32_t dst, const uint8_t* src, int NP, int vec) {
-  if (vec == 16) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  } else if (vec == 8) {
-#pragma unroll 1
-    for (int i = 0; i < 4 * NP; i += 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + i), "l"(src + i) : "memory");
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < 4 * NP; i += 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + i), "l"(src + i) : "memory");
-  }
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_wait_1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_wait_0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// An arrival on `bar` (counted in its number) once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // A named barrier among `count` threads that also tells whether any of them said so.
 __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t count, bool said) {
   uint32_t r;
@@ -404,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int HPT = GP / 2;             // heads of a softmax or output thread
   constexpr int SB = GP == 64 ? 1 : 2;    // S buffers in TMEM
   extern __shared__ __align__(1024) uint8_t smem[];
-  const Layout lay = layout_of(GP, a.panels, a.v_sf == nullptr, a.ring, a.sf_bufs, a.p_bufs);
+  const Layout lay = layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs);
   Misc& m = *reinterpret_cast<Misc*>(smem + lay.misc);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -426,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(ring_empty[i]), shared_kv ? 9 : i < ring_k ? 1 : 8);
     }
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) mbar_init(BAR(sf_full[i]), 2), mbar_init(BAR(sf_empty[i]), 17);
+    for (int i = 0; i < kMaxSfBufs; ++i) mbar_init(BAR(sf_raw[i]), 33), mbar_init(BAR(sf_full[i]), 1), mbar_init(BAR(sf_empty[i]), 17);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(s_full[i]), 1), mbar_init(BAR(s_empty[i]), 8);
@@ -437,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kVSlots; ++i) mbar_init(BAR(v_full[i]), 4), mbar_init(BAR(v_empty[i]), 1);
     mbar_init(BAR(q_full), 1), mbar_init(BAR(q_empty), 1);
     mbar_init(BAR(o_full), 1), mbar_init(BAR(o_empty), 8);
-    mbar_init(BAR(done), 1);
+    mbar_init(BAR(done), 2);
     fence_mbar_init();
     m.dead = 0;
     m.w0 = m.w1 = 0;
@@ -496,50 +489,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = m.tmem;
 
   if (warp == 0) {
-    // ---- TMA: a panel of a tile's rows per ring slot, a lane per box ----
+    // ---- loads: scales by cp.async, four tokens a lane; then a panel of rows per ring slot, a lane per box ----
+    // K's scale words go where the MMA's scale atoms have them, V's to a table of tokens.
     Segments seg(a, m);
-    Ring rk(ring_k), rv(ring_v);
+    Ring rk(ring_k), rv(ring_v), sf(a.sf_bufs);
     int used_k = 0, used_v = 0;
+    bool dead = false;
 #pragma unroll 1
-    while (seg.next()) {
+    while (!dead && seg.next()) {
       const int tiles = seg.tiles(), kvh = seg.kvh;
       const int32_t* row = a.table + seg.seg_b * a.ld_table;
-      auto page_of = [&](int tile) {  // the page of this lane's box
-        const int32_t t = seg.start(tile) + lane * a.box;
-        return tile < tiles && lane * a.box < seg.tokens(tile) ? row[page_index(a, t)] : 0;
+      auto page_of = [&](int tile) {  // the page of this lane's tokens (they lie on one); 2^32 - 1: none
+        return tile < tiles && 4 * lane < seg.tokens(tile) ? static_cast<uint32_t>(row[page_index(a, seg.start(tile) + 4 * lane)]) : 0xFFFFFFFFu;
       };
-      int32_t page = page_of(0);
+      uint32_t page = page_of(0);
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
-        const int32_t next_page = page_of(i + 1);
-        const int32_t t = seg.start(i) + lane * a.box, n = seg.tokens(i);
-        const int boxes = (n + a.box - 1) >> a.box_shift;
-        const int32_t place = t - static_cast<int32_t>(page_index(a, t) * a.page_size);
+        const uint32_t next_page = page_of(i + 1);
+        const int32_t t = seg.start(i), n = seg.tokens(i);
+        const uint32_t sf_at = sbase + lay.sf + sf.slot * sf_bytes;
+        wait_bar(m, BAR(sf_empty[0]) + 8 * sf.slot, sf.phase ^ 1);
+        const uint32_t there = __ballot_sync(0xffffffffu, page < a.pages);
+        if (page < a.pages) {
+          const uint32_t at = t + 4 * lane - page_index(a, t + 4 * lane) * a.page_size;
+          const uint8_t* ks = a.k_sf + page * a.k_sf_page + at * a.k_sf_token + kvh * a.k_sf_head;
+          const uint8_t* vs = shared_kv ? ks : a.v_sf + page * a.v_sf_page + at * a.v_sf_token + kvh * a.v_sf_head;
+          const int64_t v_step = shared_kv ? a.k_sf_token : a.v_sf_token;
+          // (tokens of the page behind the sequence's end are copied too, and not used)
+          uint32_t kd = sf_at + (lane & 7) * 64 + (lane >> 3) * 4, vd = sf_at + NP * 512 + lane * 16;
 #pragma unroll 1
-        for (int half = 0; half < (shared_kv ? 1 : 2); ++half) {
+          for (int p = 0; p < NP; ++p, ks += 4, vs += 4, kd += 512, vd += 512) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              cp_async_4(kd + 16 * k, ks + k * a.k_sf_token);
+              cp_async_4(vd + 4 * k, vs + k * v_step);
+            }
+          }
+        }
+        cp_async_arrive(BAR(sf_raw[0]) + 8 * sf.slot);
+        if (lane == 0) {
+          TileInfo* const info = reinterpret_cast<TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1024);
+          info->there = there;
+          info->tokens = n;
+          mbar_arrive(BAR(sf_raw[0]) + 8 * sf.slot);
+        }
+        sf.next();
+        const int boxes = (n + a.box - 1) >> a.box_shift;
+        const uint32_t box_page = __shfl_sync(0xffffffffu, page, (lane * a.box >> 2) & 31);
+        const int32_t place = t + lane * a.box - static_cast<int32_t>(page_index(a, t + lane * a.box) * a.page_size);
+#pragma unroll 1
+        for (int half = 0; half < (shared_kv ? 1 : 2) && !dead; ++half) {
           Ring& r = half == 0 ? rk : rv;
           const int slot0 = half == 0 ? 0 : ring_k;
 #pragma unroll 1
           for (int p = 0; p < NP; ++p) {
             const int s = slot0 + r.slot;
-            wait_bar(m, BAR(ring_empty[s]), r.phase ^ 1);
-            if (__any_sync(0xffffffffu, m.dead)) break;
-            if (lane == 0) mbar_arrive_expect_tx(BAR(ring_full[s]), boxes * a.box * 128);
+            wait_bar(m, BAR(ring_empty[0]) + 8 * s, r.phase ^ 1);
+            dead = __any_sync(0xffffffffu, m.dead);
+            if (dead) break;
+            if (lane == 0) mbar_arrive_expect_tx(BAR(ring_full[0]) + 8 * s, boxes * a.box * 128);
             __syncwarp();
             if (lane < boxes)
-              tma_load_4d(sbase + lay.ring + s * kPanel + lane * a.box * 128, half == 0 ? &map_k : &map_v, BAR(ring_full[s]),
-                          p * 128, place, kvh, page);
+              tma_load_4d(sbase + lay.ring + s * kPanel + lane * a.box * 128, half == 0 ? &map_k : &map_v, BAR(ring_full[0]) + 8 * s,
+                          p * 128, place, kvh, static_cast<int32_t>(box_page));
             r.next();
             (half == 0 ? used_k : used_v) += 1;
           }
-          if (__any_sync(0xffffffffu, m.dead)) break;
         }
-        if (__any_sync(0xffffffffu, m.dead)) break;
+        if (dead) break;
         page = next_page;
       }
-      if (__any_sync(0xffffffffu, m.dead)) break;
     }
     // every load in flight lands before the CTA leaves
+    cp_async_wait_all();
 #pragma unroll 1
     for (int half = 0; half < (shared_kv ? 1 : 2); ++half) {
       const int n = half == 0 ? ring_k : ring_v, used = half == 0 ? used_k : used_v;
@@ -548,207 +570,138 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_bounded(BAR(ring_full[(half == 0 ? 0 : ring_k) + i % n]), (i / n) & 1)) m.dead = 1;
     }
   } else if (warp == 1) {
-    // ---- MMA ----
-    // A tile's scores are issued before the products of the tile before it, so that the tensor cores have work while
-    // its probabilities are made; at a segment's first tile after them, because its queries come late.
+    // ---- the scores' MMAs ----
+    // (A thread of their own: a wait behind a commit takes the issuing thread about 250 cycles, eight of which a tile's
+    // other products need.)
     if (elect_one()) {
       Segments seg(a, m);
-      Ring rk(ring_k), sf(a.sf_bufs), s(SB), pr(a.p_bufs), vr(kVSlots), q_ring(1), o_ring(1);
-      int tiles = 0, tile = 0;                              // of the next scores
-      bool prev = false, prev_first = false, prev_last = false;  // the products not issued yet
-      int prev_halves = 0, prev_wide = 0;
-      bool more = seg.next();
-      if (more) tiles = seg.tiles();
-      while (more || prev) {
-        const bool scores_first = more && tile > 0;
-        int halves = 0, wide = 0;
+      Ring rk(ring_k), sf(a.sf_bufs), s(SB), q_ring(1);
 #pragma unroll 1
-        for (int step = 0; step < 2; ++step) {
-          if ((step == 0) == scores_first) {
-            if (!more) continue;
-            if (tile == 0) {
-              wait_bar(m, BAR(q_full), q_ring.phase);
-              q_ring.next();
-              tc_fence_after();
+      while (seg.next()) {
+        const int tiles = seg.tiles();
+        wait_bar(m, BAR(q_full), q_ring.phase);
+        q_ring.next();
+        tc_fence_after();
 #pragma unroll 1
-              for (int p = 0; p < NP; ++p) tc_cp_sf_atom(tmem + kColSfQ + 4 * p, sdesc_sf_atom(sbase + lay.q_sf + 512 * p));
-            }
-            wait_bar(m, BAR(sf_full[0]) + 8 * sf.slot, sf.phase);
-            wait_bar(m, BAR(s_empty[0]) + 8 * s.slot, s.phase ^ 1);
+        for (int p = 0; p < NP; ++p) tc_cp_sf_atom(tmem + kColSfQ + 4 * p, sdesc_sf_atom(sbase + lay.q_sf + 512 * p));
+#pragma unroll 1
+        for (int i = 0; i < tiles; ++i) {
+          wait_bar(m, BAR(sf_full[0]) + 8 * sf.slot, sf.phase);
+          wait_bar(m, BAR(s_empty[0]) + 8 * s.slot, s.phase ^ 1);
+          tc_fence_after();
+          const uint32_t sf_at = sbase + lay.sf + sf.slot * sf_bytes;
+          const uint32_t d = tmem + kColS + s.slot * 2 * GP, sfk = tmem + (s.slot == 0 ? kColSfK : kColSfK1);
+#pragma unroll 1
+          for (int p = 0; p < NP; ++p) {
+            wait_bar(m, BAR(ring_full[0]) + 8 * rk.slot, rk.phase);
             tc_fence_after();
-            halves = seg.tokens(tile) > 64 ? 2 : 1;
-            wide = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1024)->wide;
-            const uint32_t sf_at = sbase + lay.sf + sf.slot * sf_bytes;
-            const uint32_t d = tmem + kColS + s.slot * 2 * GP, sfk = tmem + (s.slot == 0 ? kColSfK : kColSfK1);
-#pragma unroll 1
-            for (int p = 0; p < NP; ++p) {
-              wait_bar(m, BAR(ring_full[0]) + 8 * rk.slot, rk.phase);
-              tc_fence_after();
-              tc_cp_sf_atom(sfk + 4 * p, sdesc_sf_atom(sf_at + 512 * p));
-              const uint64_t ad = sdesc_kmajor_sw128(sbase + lay.ring + rk.slot * kPanel);
-              const uint64_t bd = sdesc_kmajor_sw128(sbase + lay.q + p * GP * 256);
+            tc_cp_sf_atom(sfk + 4 * p, sdesc_sf_atom(sf_at + 512 * p));
+            const uint64_t ad = sdesc_kmajor_sw128(sbase + lay.ring + rk.slot * kPanel);
+            const uint64_t bd = sdesc_kmajor_sw128(sbase + lay.q + p * GP * 256);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tc_mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc_mxf8(128, 2 * GP, k, k), sfk + 4 * p, tmem + kColSfQ + 4 * p,
-                            (p | k) != 0 ? 1u : 0u);
-              tc_commit(BAR(ring_empty[0]) + 8 * rk.slot);
-              rk.next();
-            }
-            tc_commit(BAR(s_full[0]) + 8 * s.slot);
-            tc_commit(BAR(sf_empty[0]) + 8 * sf.slot);
-            if (tile + 1 == tiles) tc_commit(BAR(q_empty));
-            sf.next();
-            s.next();
-          } else if (prev) {
-            if (prev_first) {
-              wait_bar(m, BAR(o_empty), o_ring.phase ^ 1);
-              o_ring.next();
-            }
-            wait_bar(m, BAR(p_full[0]) + 8 * pr.slot, pr.phase);
+            for (int k = 0; k < 4; ++k)
+              tc_mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc_mxf8(128, 2 * GP, k, k), sfk + 4 * p, tmem + kColSfQ + 4 * p,
+                          (p | k) != 0 ? 1u : 0u);
+            tc_commit(BAR(ring_empty[0]) + 8 * rk.slot);
+            rk.next();
+          }
+          tc_commit(BAR(s_full[0]) + 8 * s.slot);
+          tc_commit(BAR(sf_empty[0]) + 8 * sf.slot);
+          if (i + 1 == tiles) tc_commit(BAR(q_empty));
+          sf.next();
+          s.next();
+        }
+      }
+      tc_commit(BAR(done));
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---- the output's MMAs ----
+    if (elect_one()) {
+      Segments seg(a, m);
+      Ring pr(a.p_bufs), vr(kVSlots), o_ring(1);
+#pragma unroll 1
+      while (seg.next()) {
+        const int tiles = seg.tiles();
+        wait_bar(m, BAR(o_empty), o_ring.phase ^ 1);
+        o_ring.next();
+#pragma unroll 1
+        for (int i = 0; i < tiles; ++i) {
+          const int both = seg.tokens(i) > 64 ? 1 : 0, chunks = NP << both;
+          wait_bar(m, BAR(p_full[0]) + 8 * pr.slot, pr.phase);
+          const uint32_t idesc = m.p_wide[pr.slot] != 0 ? idesc_f16_mn(GP, true) : idesc_f16_mn(GP, false);
+          const uint64_t p_desc = sdesc(sbase + lay.p + pr.slot * kPanel, 1024, 1024, 2);
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            const int p = c >> both, h = c & both;
+            wait_bar(m, BAR(v_full[0]) + 8 * vr.slot, vr.phase);
             tc_fence_after();
-            const uint32_t idesc = prev_wide != 0 ? idesc_f16_mn(GP, true) : idesc_f16_mn(GP, false);
-            const uint64_t p_desc = sdesc(sbase + lay.p + pr.slot * kPanel, 1024, 1024, 2);
-#pragma unroll 1
-            for (int c = 0; c < NP * prev_halves; ++c) {
-              const int p = prev_halves == 2 ? c >> 1 : c, h = prev_halves == 2 ? c & 1 : 0;
-              wait_bar(m, BAR(v_full[0]) + 8 * vr.slot, vr.phase);
-              tc_fence_after();
-              const uint64_t bd = p_desc + h * 512;
-              const uint32_t more_of_it = !prev_first || h != 0;
+            const uint64_t bd = p_desc + h * 512;
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tc_mma_f16_ts(tmem + p * GP, tmem + kColV + 32 * vr.slot + 8 * k, bd + 128 * k, idesc, k != 0 ? 1u : more_of_it);
-              tc_commit(BAR(v_empty[0]) + 8 * vr.slot);
-              vr.next();
-            }
-            tc_commit(BAR(p_empty[0]) + 8 * pr.slot);
-            pr.next();
-            if (prev_last) tc_commit(BAR(o_full));
-            prev = false;
+            for (int k = 0; k < 4; ++k)
+              tc_mma_f16_ts(tmem + p * GP, tmem + kColV + 32 * vr.slot + 8 * k, bd + 128 * k, idesc, (i | h | k) != 0 ? 1u : 0u);
+            tc_commit(BAR(v_empty[0]) + 8 * vr.slot);
+            vr.next();
           }
+          tc_commit(BAR(p_empty[0]) + 8 * pr.slot);
+          pr.next();
         }
-        if (more) {
-          prev = true;
-          prev_first = tile == 0;
-          prev_last = tile + 1 == tiles;
-          prev_halves = halves;
-          prev_wide = wide;
-          if (++tile == tiles) {
-            tile = 0;
-            more = seg.next();
-            if (more) tiles = seg.tiles();
-          }
-        }
+        tc_commit(BAR(o_full));
       }
       tc_commit(BAR(done));
       if (!mbar_wait_bounded(BAR(done), 0)) m.dead = 1;
     }
     __syncwarp();
-  } else if (warp < 4) {
-    // ---- scales: K atoms, V bytes, the tokens that take part, the pivot ----
-    // lane: tokens 64 w + lane and 32 on. Their scales come by cp.async, a tile ahead, into a place of the lane's own.
-    const int w = warp - 2, kinds = shared_kv ? 1 : 2;
+  } else if (warp == 3) {
+    // ---- a tile's tokens that take part, its pivot, and whether fp16 holds its scales ----
     Segments seg(a, m);
     Ring sf(a.sf_bufs);
-    uint32_t parity = 0;
-    const uint32_t stage0 = lay.stage + (64 * w + lane) * 16;  // [tile parity][kind][token] of 16 bytes
-    // the pages of this lane's tokens of a tile (no page: 2^32 - 1)
-    auto pages_of = [&](int tile, int tiles, const int32_t* row, uint32_t& p0, uint32_t& p1) {
-      const int32_t n = tile < tiles ? seg.tokens(tile) : 0, r = 64 * w + lane;
-      const uint32_t t = static_cast<uint32_t>(seg.start(tile) + r);
-      p0 = r < n ? static_cast<uint32_t>(row[page_index(a, t)]) : 0xFFFFFFFFu;
-      p1 = r + 32 < n ? static_cast<uint32_t>(row[page_index(a, t + 32)]) : 0xFFFFFFFFu;
-    };
-    auto fetch = [&](int tile, uint32_t p0, uint32_t p1, int kvh) {
-#pragma unroll 1
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t g = j == 0 ? p0 : p1;
-        if (g < a.pages) {
-          const uint32_t t = static_cast<uint32_t>(seg.start(tile) + 64 * w + 32 * j + lane), at = t - page_index(a, t) * a.page_size;
-          const uint32_t dst = sbase + stage0 + 512 * j + (tile & 1) * kinds * 2048;
-          cp_async_scales(dst, a.k_sf + g * a.k_sf_page + at * a.k_sf_token + kvh * a.k_sf_head, NP, a.sf_vec);
-          if (!shared_kv) cp_async_scales(dst + 2048, a.v_sf + g * a.v_sf_page + at * a.v_sf_token + kvh * a.v_sf_head, NP, a.sf_vec);
-        }
-      }
-      cp_async_commit();
-    };
 #pragma unroll 1
     while (seg.next()) {
-      const int tiles = seg.tiles(), kvh = seg.kvh;
-      const int32_t* row = a.table + seg.seg_b * a.ld_table;
+      const int tiles = seg.tiles();
       int32_t pivot = 0;
-      uint32_t page[2], next_page[2];
-      pages_of(0, tiles, row, page[0], page[1]);
-      pages_of(1, tiles, row, next_page[0], next_page[1]);
-      fetch(0, page[0], page[1], kvh);
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
-        uint32_t far_page[2];
-        pages_of(i + 2, tiles, row, far_page[0], far_page[1]);
-        fetch(i + 1, next_page[0], next_page[1], kvh);
-        cp_async_wait_1();
-        const bool ok[2] = {page[0] < a.pages, page[1] < a.pages};
-        const uint32_t* const kw = reinterpret_cast<const uint32_t*>(smem + stage0 + (i & 1) * kinds * 2048);
-        const uint32_t* const vw = kw + (kinds - 1) * 512;
-        uint32_t hi = 0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (ok[j])
-#pragma unroll 1
-            for (int p = 0; p < NP; ++p) {
-              const uint32_t x = vw[p + 128 * j];
-              hi = __vmaxu2(hi, __vmaxu2(x & 0x00FF00FFu, (x >> 8) & 0x00FF00FFu));
-            }
-        hi = __reduce_max_sync(0xffffffffu, max(hi & 0xFFFFu, hi >> 16));
-        const uint32_t v0 = __ballot_sync(0xffffffffu, ok[0]), v1 = __ballot_sync(0xffffffffu, ok[1]);
-        if (lane == 0) m.sf_red[parity][w] = static_cast<int32_t>(hi);
-        wait_bar(m, BAR(sf_empty[0]) + 8 * sf.slot, sf.phase ^ 1);
-        named_barrier(1, 64);
-        const int32_t top = max(m.sf_red[parity][0], m.sf_red[parity][1]);
-        if (top > pivot + 7) pivot = top;
-        // bytes t = max(0, b - pivot + 15): 2^(b - pivot) is fp16 with exponent field t, and 4 t its upper byte
-        const uint32_t down = static_cast<uint32_t>((15 - pivot) & 0xFFFF) * 0x10001u;
+        wait_bar(m, BAR(sf_raw[0]) + 8 * sf.slot, sf.phase);
         uint8_t* const buf = smem + lay.sf + sf.slot * sf_bytes;
         TileInfo* const info = reinterpret_cast<TileInfo*>(buf + NP * 1024);
-        uint32_t low = 0;
+        // lane: tokens 4 lane .. + 3
+        const int32_t n = info->tokens - 4 * lane;
+        const bool ok = (info->there >> lane) & 1;
+        const uint32_t mine = !ok || n <= 0 ? 0u : n >= 4 ? 15u : (1u << n) - 1;  // these of them take part
+        uint32_t hi = 0, lo = 0xFFFFFFFFu;  // largest byte, smallest nonzero byte - 1
 #pragma unroll 1
         for (int p = 0; p < NP; ++p) {
-          const uint32_t k0 = ok[0] ? kw[p] : 0, k1 = ok[1] ? kw[p + 128] : 0;
-          *reinterpret_cast<uint2*>(buf + p * 512 + lane * 16 + w * 8) = make_uint2(k0, k1);
+          uint4* const at = reinterpret_cast<uint4*>(buf + NP * 512 + p * 512 + lane * 16);
+          uint4 x = *at;
+          if (mine != 15u) {  // what takes no part is zero
+            x.x = mine & 1 ? x.x : 0, x.y = mine & 2 ? x.y : 0, x.z = mine & 4 ? x.z : 0, x.w = mine & 8 ? x.w : 0;
+            *at = x;
+          }
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t x = ok[j] ? vw[p + 128 * j] : 0, e = x & 0x00FF00FFu, o = (x >> 8) & 0x00FF00FFu;
-            const uint32_t te = __viaddmax_s16x2(e, down, 0), to = __viaddmax_s16x2(o, down, 0);
-            // nonzero scales that fp16 does not hold
-            low |= (__vminu2(e, 0x00010001u) & ~__vminu2(te, 0x00010001u)) | (__vminu2(o, 0x00010001u) & ~__vminu2(to, 0x00010001u));
-            *reinterpret_cast<uint32_t*>(buf + NP * 512 + (p * 128 + 64 * w + 32 * j + lane) * 4) = (te << 2) | (to << 10);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t e = xs[k] & 0x00FF00FFu, o = (xs[k] >> 8) & 0x00FF00FFu;
+            hi = __vimax3_u16x2(hi, e, o);
+            lo = __viaddmin_u16x2(e, 0xFFFFFFFFu, lo);
+            lo = __viaddmin_u16x2(o, 0xFFFFFFFFu, lo);
           }
         }
-        if (named_barrier_or(1, 64, low != 0)) {  // bf16: the bytes themselves
-#pragma unroll 1
-          for (int p = 0; p < NP; ++p)
+        const int32_t top = __reduce_max_sync(0xffffffffu, max(hi & 0xFFFFu, hi >> 16));
+        const int32_t least = __reduce_min_sync(0xffffffffu, min(lo & 0xFFFFu, lo >> 16)) + 1;  // (65536: none)
+        if (top > pivot + 7) pivot = top;
+        // token 32 w + 4 j + i: bit 4 j + i of word w
+        uint32_t word = mine << (4 * (lane & 7));
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              *reinterpret_cast<uint32_t*>(buf + NP * 512 + (p * 128 + 64 * w + 32 * j + lane) * 4) = ok[j] ? vw[p + 128 * j] : 0;
-          if (lane == 0 && w == 0) info->wide = 1;
-        } else if (lane == 0 && w == 0) {
-          info->wide = 0;
-        }
-        parity ^= 1;
-        if (lane == 0) {
-          info->valid[2 * w] = v0;
-          info->valid[2 * w + 1] = v1;
-          if (w == 0) info->pivot = pivot;
-        }
+        for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+        if ((lane & 7) == 0) info->valid[lane >> 3] = word;
+        if (lane == 0) info->pivot = pivot, info->wide = least < pivot - 14;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(sf_full[0]) + 8 * sf.slot);
         sf.next();
-        page[0] = next_page[0], page[1] = next_page[1];
-        next_page[0] = far_page[0], next_page[1] = far_page[1];
       }
     }
-    cp_async_wait_0();
   } else if (warp < 12) {
     // ---- softmax ----
     const int quarter = warp & 3, h0 = (warp - 4) / 4 * HPT, st = tid - 128;
@@ -884,10 +837,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           else v = make_uint4(f16x2_rn(e[0], e[1]), f16x2_rn(e[2], e[3]), f16x2_rn(e[4], e[5]), f16x2_rn(e[6], e[7]));
           *reinterpret_cast<uint4*>(row + ((((h0 + j) >> 3) ^ (prow & 7)) << 4)) = v;
         }
+        if (st == 0) m.p_wide[pr.slot] = wide;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(p_full[pr.slot]));
+        if (lane == 0) mbar_arrive(BAR(p_full[0]) + 8 * pr.slot);
         pr.next();
       }
       // sums over the quarter's tokens
@@ -911,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring rv(ring_v), sf(a.sf_bufs), fin(2), o_ring(1);
     const int slot0 = shared_kv ? 0 : ring_k;
     uint32_t chunk = 0;
-    const uint32_t pick = static_cast<uint32_t>(quarter) * 0x1010u | 0x4000u;
+    const uint32_t pick = static_cast<uint32_t>(quarter) * 0x0101u | 0x0400u;  // a byte of each word, to bytes 0 and 2 (1 and 3 are masked)
     int2 owner = make_int2(0, 0);
 #pragma unroll 1
     while (seg.next()) {
@@ -924,6 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileInfo* const info = reinterpret_cast<const TileInfo*>(buf + NP * 1024);
         const bool wide = info->wide != 0;
         const int32_t pivot = info->pivot;
+        const uint32_t down = static_cast<uint32_t>((15 - pivot) & 0xFFFF) * 0x10001u;
         const uint32_t valid0 = info->valid[2 * set], valid1 = info->valid[2 * set + 1];
         const bool full = (valid0 & valid1) == 0xFFFFFFFFu;
 #pragma unroll 1
@@ -958,8 +913,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t w0[16], w1[16];  // features 0-15 and 16-31 of the quarter's 32
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                // this quarter's group: each byte to the top of an fp16
-                const uint32_t s01 = __byte_perm(sw[k].x, sw[k].y, pick) & 0xFF00FF00u, s23 = __byte_perm(sw[k].z, sw[k].w, pick) & 0xFF00FF00u;
+                // this quarter's group: 2^(b - pivot) in fp16 has the exponent field b - pivot + 15
+                const uint32_t s01 = __viaddmax_s16x2(__byte_perm(sw[k].x, sw[k].y, pick) & 0x00FF00FFu, down, 0) << 10,
+                               s23 = __viaddmax_s16x2(__byte_perm(sw[k].z, sw[k].w, pick) & 0x00FF00FFu, down, 0) << 10;
                 uint32_t lo[4], hi[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -1265,7 +1221,8 @@ bool make_cache_map(CUtensorMap* m, const mxq_kv_cache& c, int box) {
   cuuint32_t boxes[4] = {128u, static_cast<cuuint32_t>(box), 1u, 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.data, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_SWIZZLE_128B, c.dim == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -1289,15 +1246,15 @@ cudaError_t launch_behind(void (*kern)(P...), unsigned grid, int threads, int by
 template <int GP>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, Args a, cudaStream_t stream) {
   a.p_bufs = 2;
-  a.sf_bufs = a.panels <= 2 ? 4 : 2;
-  const int fixed = layout_of(GP, a.panels, a.v_sf == nullptr, 0, a.sf_bufs, a.p_bufs).total;
+  a.sf_bufs = a.panels == 1 ? 6 : a.panels == 2 ? 4 : 3;
+  const int fixed = layout_of(GP, a.panels, 0, a.sf_bufs, a.p_bufs).total;
   a.ring = std::min(16, (kSmemLimit - fixed) / kPanel);
   static PerDevice set;
   cudaError_t e = allow_smem(set, attention_kernel<GP>, kSmemLimit);
   if (e != cudaSuccess) return e;
   query_kernel<GP><<<static_cast<unsigned>(a.B * a.kv * a.blocks * a.panels), kQThreads, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int bytes = layout_of(GP, a.panels, a.v_sf == nullptr, a.ring, a.sf_bufs, a.p_bufs).total;
+  const int bytes = layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs).total;
   if ((e = launch_behind(attention_kernel<GP>, a.ctas, kThreads, bytes, stream, mk, mv, a)) != cudaSuccess) return e;
   return launch_behind(join_kernel, 2 * num_sms(), kJoinThreads, 0, stream, a, GP);
 }
@@ -1368,12 +1325,6 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
   a.sf_tl = static_cast<uint8_t*>(l.sf_tiled);
   a.lse = l.lse;
   a.status = l.status;
-  // scales are copied in the largest pieces that every row starts on a multiple of
-  auto vec_of = [&](const mxq_kv_cache& c) {
-    const uint64_t all = reinterpret_cast<uintptr_t>(c.sf) | c.sf_page_stride | c.sf_token_stride | c.sf_head_stride;
-    return all % 16 == 0 && a.panels == 4 ? 16 : all % 8 == 0 && a.panels % 2 == 0 ? 8 : 4;
-  };
-  a.sf_vec = std::min(vec_of(k), vec_of(l.v != nullptr ? *l.v : k));
   const Space sp = space_of(l.B, l.q_heads, k.heads, k.dim);
   const int64_t most = l.B * a.kv * a.blocks * ((static_cast<int64_t>(l.table_width) * k.page_size + kUnit - 1) / kUnit);
   a.ctas = static_cast<int32_t>(std::min(sp.ctas, most));
