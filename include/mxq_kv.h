@@ -25,7 +25,8 @@ extern "C" {
  * of page p starts at data + p * page_stride + r * token_stride + h * head_stride, its scales at
  * sf + p * sf_page_stride + r * sf_token_stride + h * sf_head_stride (all in bytes), so both orders of
  * tokens and heads within a page can be had, and pages with other data between them. Rows of data start
- * on 16-byte boundaries; rows of scales on 4-byte boundaries where dim % 128 == 0. Rows must not overlap.
+ * on 16-byte boundaries; rows of scales on 4-byte boundaries where dim % 128 == 0, at strides below 2^31. Rows
+ * must not overlap.
  * Slot s is place s % page_size of page s / page_size.
  * dim % 32 == 0, 32 <= dim <= 1024, heads <= 1024, page_size <= 65536, pages * page_size < 2^31.
  */

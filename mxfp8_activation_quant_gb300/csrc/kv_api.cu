@@ -48,9 +48,10 @@ mxq_status check_cache(const mxq_kv_cache* in, mxq_kv_cache* out) {
     return MXQ_ERR_UNSUPPORTED_SHAPE;
   *out = *in;
   settle(out);
-  for (int64_t s : {out->page_stride, out->token_stride, out->head_stride, out->sf_page_stride, out->sf_token_stride,
-                    out->sf_head_stride})
+  for (int64_t s : {out->page_stride, out->token_stride, out->head_stride})
     if (s < 0 || s >= kMaxStride) return MXQ_ERR_UNSUPPORTED_SHAPE;
+  for (int64_t s : {out->sf_page_stride, out->sf_token_stride, out->sf_head_stride})
+    if (s < 0 || s >= (int64_t(1) << 31)) return MXQ_ERR_UNSUPPORTED_SHAPE;
   if (!al16(out->data) || !al4(out->sf) || out->page_stride % 16 != 0 || out->token_stride % 16 != 0 ||
       out->head_stride % 16 != 0)
     return MXQ_ERR_MISALIGNED;

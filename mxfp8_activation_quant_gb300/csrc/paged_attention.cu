@@ -17,14 +17,17 @@
 // fp16 holds code * 2^(b - E) exactly for b in [E - 15, E + 7]: a tile with a scale above raises E (O is
 // rescaled with ref), one with a nonzero scale below takes P and V as bf16.
 //
-// Warps: 0 loads, 1 and 2 MMAs (scores, outputs), 3 the scales' check, 4-11 softmax (two a TMEM lane quarter, half of the heads each),
-// 12-19 V^T and the outputs (two a quarter; 64 of the tile's tokens each, half of the heads each).
+// Warps: 0 the rows' loads, 1 and 2 MMAs (scores, outputs), 3 scales, 4-11 softmax (two a TMEM lane quarter, half of the heads each),
+// 12-19 V^T and the outputs (two a
+// quarter; 64 of the tile's tokens each, half of the heads each). Up to 8 heads the softmax takes four warps, and
+// warp 8 the scales' copies.
 //
 // A CTA that holds an item from start to end writes its outputs; the others' normalised parts go to the
 // workspace (at most two a CTA), and join_kernel adds them up in the order of the CTAs.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
@@ -36,10 +39,9 @@ namespace {
 
 constexpr int kUnit = 64;         // tokens of the unit of work; a TMA box has no more
 constexpr int kTile = 128;        // tokens of a tile
-constexpr int kThreads = 640;
+constexpr int kThreads = 640;  // (five warps a scheduler leave each thread 96 registers; a sixth anywhere, 80)
 constexpr int kPanel = 128 * 128; // bytes of 128 features of a tile
 constexpr int kMaxHeads = 64;     // query heads of an item
-constexpr int kSoftThreads = 256;
 constexpr float kLowRef = -1e30f; // ref before the first token
 constexpr float kSlack = 8.0f;
 
@@ -53,7 +55,7 @@ struct Args {
   int64_t ldq, ldqh;
   const uint8_t* k_sf;
   const uint8_t* v_sf;  // null: the keys'
-  int64_t k_sf_page, k_sf_token, k_sf_head, v_sf_page, v_sf_token, v_sf_head;
+  uint32_t k_sf_page, k_sf_token, k_sf_head, v_sf_page, v_sf_token, v_sf_head;  // (below 2^31)
   const int32_t* table;
   int64_t ld_table;
   uint32_t table_width, page_size, pages;
@@ -89,19 +91,20 @@ struct Misc {
   alignas(16) float ref[kMaxHeads];
   alignas(16) float fac[kMaxHeads];
   int32_t red[kMaxHeads];
-  int64_t sums[kThreads / 32];
+  int32_t sums[kThreads / 32];
   int32_t p_wide[2];  // whether the probabilities are bf16
-  int64_t w0, w1, per_cta, rest;
+  int32_t w0, w1, per_cta, rest;
   int32_t b0, kvh0, blk0, u0;
   uint32_t tmem;
   volatile int32_t dead;
 };
 // A buffer of scales: K atoms [panels][512], V bytes [panels][128 tokens][4 groups], then this.
+constexpr int kWide = 1, kLastTile = 2, kLastOfAll = 4;  // values in bf16; the segment's, and the CTA's, last tile
 struct TileInfo {
   uint32_t valid[4];
-  int32_t pivot, wide;
+  int32_t pivot, flags;
   uint32_t there;  // bit l: tokens 4 l .. 4 l + 3 are on a page of the cache
-  int32_t tokens;
+  int32_t pad;
 };
 // A finished segment's sums and references.
 struct Fin {
@@ -257,11 +260,7 @@ __device__ __forceinline__ void fold_sums(float (&l)[M], int lane) {
   if constexpr (O > 1) fold_sums<O / 2, (N > 1 ? N / 2 : 1)>(l, lane);
 }
 
-// a / b for 0 <= a, 0 < b, in 32 bits where that does (a 64-bit division is a long subroutine).
-__device__ __forceinline__ int64_t divide(int64_t a, int32_t b) {
-  return a >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
-}
-
+__device__ __forceinline__ int64_t wide_mul(uint32_t a, uint32_t b) { return static_cast<int64_t>(static_cast<uint64_t>(a) * b); }
 // ---- work -----------------------------------------------------------------------------------
 __device__ __forceinline__ int32_t length_of(const Args& a, int32_t len) {
   const int64_t cap = static_cast<int64_t>(a.table_width) * a.page_size;
@@ -274,8 +273,7 @@ __device__ __forceinline__ int32_t units_of(int32_t len) { return len <= 0 ? 1 :
 // Walks a CTA's segments: runs of units of one item. An item is (sequence, cache head, block of query heads).
 struct Segments {
   const Args& a;
-  int64_t left;
-  int32_t next_len, b, k, blk_, u, len, units;
+  int32_t left, next_len, b, k, blk_, u, len, units;
   // the current segment
   int32_t seg_b, kvh, blk, seg_len, u0, u1, seg_units;
 
@@ -306,7 +304,7 @@ struct Segments {
     seg_len = len;
     seg_units = units;
     u0 = u;
-    u1 = u + static_cast<int32_t>(units - u < left ? units - u : left);
+    u1 = u + min(units - u, left);
     left -= u1 - u;
     u = u1;
     return true;
@@ -333,20 +331,84 @@ struct Ring {
   }
 };
 
-// A bounded wait; once one has run out nothing waits any more (results are void, every loop still ends, and the
-// status word is written at the end). Small on purpose: it is inlined thirty times, and the roles' loops have to fit the
-// instruction cache together.
-__device__ __forceinline__ void wait_bar(Misc& m, uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = globaltimer_ns();
+// A bounded wait: tries that each last a microsecond at most, half a million of them; false once one has run out,
+// after which nothing waits any more (results are void, every loop still ends, and the status word is written at the
+// end). Small on purpose: it is inlined thirty times, and the roles' loops have to fit the instruction cache together
+// (with the library's usual wait, which reads a clock, they did not: 93 % hits, and its refills at 64 % of their peak).
+constexpr uint32_t kWaitTries = 1u << 19;
+__device__ __forceinline__ bool wait_bar(Misc& m, uint32_t bar, uint32_t parity) {
+  uint32_t tries = 0;
 #pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (m.dead != 0 || globaltimer_ns() - t0 > kWaitLimitNs) {
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (++tries > kWaitTries || m.dead != 0) {
       m.dead = 1;
-      return;
+      return false;
     }
   }
 }
+
+// Copies of scales, a tile at a time: four tokens a lane (they lie on one page). K's words go by cp.async where the
+// MMA's scale atoms have them, V's to a table of tokens.
+struct ScaleCopies {
+  const Args& a;
+  Misc& m;
+  Segments seg;
+  Ring sf;
+  const uint32_t kd0, vd0;
+  const int sf_bytes, lane;
+  int i = 0, tiles = 0;
+  uint32_t page = 0;
+  const int32_t* row = nullptr;
+  const uint8_t *k_base = nullptr, *v_base = nullptr;
+
+  __device__ __forceinline__ ScaleCopies(const Args& args, Misc& misc, uint32_t sf_smem, int bytes, int l)
+      : a(args), m(misc), seg(args, misc), sf(args.sf_bufs), kd0(sf_smem + (l & 7) * 64 + (l >> 3) * 4),
+        vd0(sf_smem + args.panels * 512 + l * 16), sf_bytes(bytes), lane(l) {}
+  __device__ __forceinline__ uint32_t page_of(int tile) const {  // (2^32 - 1: none)
+    return tile < tiles && 4 * lane < seg.tokens(tile) ? static_cast<uint32_t>(row[page_index(a, seg.start(tile) + 4 * lane)]) : 0xFFFFFFFFu;
+  }
+  __device__ __forceinline__ bool next(uint8_t* sf_area) {
+    if (i == tiles) {
+      if (!seg.next()) return false;
+      i = 0;
+      tiles = seg.tiles();
+      row = a.table + seg.seg_b * a.ld_table;
+      k_base = a.k_sf + wide_mul(seg.kvh, a.k_sf_head);
+      v_base = a.v_sf + wide_mul(seg.kvh, a.v_sf_head);
+      page = page_of(0);
+    }
+    const uint32_t next_page = page_of(i + 1);
+    const uint32_t raw = smem_u32(&m.sf_raw[0]) + 8 * sf.slot;
+    wait_bar(m, smem_u32(&m.sf_empty[0]) + 8 * sf.slot, sf.phase ^ 1);
+    const uint32_t there = __ballot_sync(0xffffffffu, page < a.pages);
+    if (page < a.pages) {
+      const bool shared_kv = a.v_sf == nullptr;
+      const uint32_t t = seg.start(i) + 4 * lane, at = t - page_index(a, t) * a.page_size, v_step = shared_kv ? a.k_sf_token : a.v_sf_token;
+      const uint8_t* ks = k_base + wide_mul(page, a.k_sf_page) + wide_mul(at, a.k_sf_token);
+      const uint8_t* vs = shared_kv ? ks : v_base + wide_mul(page, a.v_sf_page) + wide_mul(at, a.v_sf_token);
+      uint32_t kd = kd0 + sf.slot * sf_bytes, vd = vd0 + sf.slot * sf_bytes;
+      // (tokens of the page behind the sequence's end are copied too, and not used)
+#pragma unroll 1
+      for (int p = 0; p < a.panels; ++p, ks += 4, vs += 4, kd += 512, vd += 512) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          cp_async_4(kd + 16 * k, ks + wide_mul(k, a.k_sf_token));
+          cp_async_4(vd + 4 * k, vs + wide_mul(k, v_step));
+        }
+      }
+    }
+    cp_async_arrive(raw);
+    if (lane == 0) {
+      reinterpret_cast<TileInfo*>(sf_area + sf.slot * sf_bytes + a.panels * 1024)->there = there;
+      mbar_arrive(raw);
+    }
+    sf.next();
+    ++i;
+    page = next_page;
+    return true;
+  }
+};
 
 // q as hi + lo, an item's panels as the kernel's shared memory holds them (rows of 128 bytes, swizzled; hi heads, then
 // lo heads; then the scale atoms), so that they come by bulk copies. One block a panel: 8 values a lane, 16 lanes a head.
@@ -363,15 +425,17 @@ __global__ void __launch_bounds__(kQThreads) query_kernel(const __grid_constant_
   uint8_t* const out = a.q_ws + static_cast<int64_t>(item) * (a.panels * (GP * 256 + 512));
   uint8_t* const panel = out + p * GP * 256;
   uint8_t* const atom = out + a.panels * GP * 256 + p * 512;
-  uint4 xs[GP / 16];
+  constexpr int kRows = GP < 16 ? 1 : GP / 16;
+  uint4 xs[kRows];
 #pragma unroll
-  for (int u = 0; u < GP / 16; ++u) {
+  for (int u = 0; u < kRows; ++u) {
     const int h = (tid >> 4) + 16 * u;
     xs[u] = h < heads ? ld_stream_u4(q + h * a.ldqh) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
-  for (int u = 0; u < GP / 16; ++u) {
+  for (int u = 0; u < kRows; ++u) {
     const int h = (tid >> 4) + 16 * u, r = GP + h;
+    if (h >= GP) break;  // (whole warps)
     const uint4 x = xs[u];
     uint32_t amax = absmax8(x);
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
@@ -394,7 +458,11 @@ template <int GP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const __grid_constant__ Args a) {
-  constexpr int HPT = GP / 2;             // heads of a softmax or output thread
+  constexpr int GO = GP < 16 ? 16 : GP;   // columns of O a panel: an MMA has 16 at least
+  constexpr int HPT = GO / 2;             // heads of an output thread
+  constexpr int SW = GP == 8 ? 4 : 8;     // warps of the softmax, and a thread's heads
+  constexpr int SH = GP * 4 / SW;
+  constexpr bool kCopier = SW == 4;       // then another copies the scales
   constexpr int SB = GP == 64 ? 1 : 2;    // S buffers in TMEM
   extern __shared__ __align__(1024) uint8_t smem[];
   const Layout lay = layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs);
@@ -419,12 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(ring_empty[i]), shared_kv ? 9 : i < ring_k ? 1 : 8);
     }
 #pragma unroll 1
-    for (int i = 0; i < kMaxSfBufs; ++i) mbar_init(BAR(sf_raw[i]), 33), mbar_init(BAR(sf_full[i]), 1), mbar_init(BAR(sf_empty[i]), 17);
+    for (int i = 0; i < kMaxSfBufs; ++i) mbar_init(BAR(sf_raw[i]), 33), mbar_init(BAR(sf_full[i]), 1), mbar_init(BAR(sf_empty[i]), 9 + SW);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      mbar_init(BAR(s_full[i]), 1), mbar_init(BAR(s_empty[i]), 8);
-      mbar_init(BAR(p_full[i]), 8), mbar_init(BAR(p_empty[i]), 1);
-      mbar_init(BAR(fin_full[i]), 8), mbar_init(BAR(fin_empty[i]), 8);
+      mbar_init(BAR(s_full[i]), 1), mbar_init(BAR(s_empty[i]), SW);
+      mbar_init(BAR(p_full[i]), SW), mbar_init(BAR(p_empty[i]), 1);
+      mbar_init(BAR(fin_full[i]), SW), mbar_init(BAR(fin_empty[i]), 8);
     }
 #pragma unroll 1
     for (int i = 0; i < kVSlots; ++i) mbar_init(BAR(v_full[i]), 4), mbar_init(BAR(v_empty[i]), 1);
@@ -442,43 +510,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The CTA's share: a scan of the sequences' units, a run of sequences per thread.
   {
     const int32_t per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    int64_t sum = 0;
+    int32_t sum = 0;
 #pragma unroll 1
     for (int32_t b = b0; b < b1; ++b) sum += units_of(length_of(a, a.lens[b]));
-    int64_t inc = sum;
+    int32_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      const int32_t up = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += up;
     }
     if (lane == 31) m.sums[warp] = inc;
     __syncthreads();
-    int64_t before = 0, total = 0;
-#pragma unroll 4
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += m.sums[w];
-      total += m.sums[w];
-    }
-    before += inc - sum;
-    total *= S;
+    // (every warp sums the warps' sums, a lane each)
+    const int32_t theirs = lane < kThreads / 32 ? m.sums[lane] : 0;
+    const int32_t total = __reduce_add_sync(0xffffffffu, theirs) * S;
+    const int32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0) + inc - sum;
     // (no share is empty among the CTAs that have one: the parts of an item lie in consecutive CTAs)
-    const int64_t per_cta = total < a.ctas ? 1 : divide(total, a.ctas), rest = total < a.ctas ? 0 : total - per_cta * a.ctas;
-    const int64_t w0 = per_cta * blockIdx.x + min(static_cast<int64_t>(blockIdx.x), rest);
+    const int32_t per_cta = max(1, total / a.ctas), rest = total < a.ctas ? 0 : total - per_cta * a.ctas;
+    const int32_t w0 = per_cta * static_cast<int32_t>(blockIdx.x) + min(static_cast<int32_t>(blockIdx.x), rest);
     if (w0 < total && before * S <= w0 && w0 < (before + sum) * S) {  // one thread
-      int64_t at = w0 - before * S;
-      int32_t b = b0, units = units_of(length_of(a, a.lens[b]));
+      int32_t at = w0 - before * S, b = b0, units = units_of(length_of(a, a.lens[b]));
 #pragma unroll 1
-      while (at >= static_cast<int64_t>(units) * S) {
-        at -= static_cast<int64_t>(units) * S;
+      while (at >= units * S) {
+        at -= units * S;
         units = units_of(length_of(a, a.lens[++b]));
       }
-      const uint32_t sub = static_cast<uint32_t>(divide(at, units));  // (below S)
+      const int32_t sub = at / units;  // (below S)
       m.b0 = b;
-      m.kvh0 = static_cast<int32_t>(sub / a.blocks);
-      m.blk0 = static_cast<int32_t>(sub % a.blocks);
-      m.u0 = static_cast<int32_t>(at - static_cast<int64_t>(sub) * units);
+      m.kvh0 = sub / a.blocks;
+      m.blk0 = sub - m.kvh0 * a.blocks;
+      m.u0 = at - sub * units;
       m.w0 = w0;
-      m.w1 = w0 + per_cta + (blockIdx.x < rest ? 1 : 0);
+      m.w1 = w0 + per_cta + (static_cast<int32_t>(blockIdx.x) < rest ? 1 : 0);
       m.per_cta = per_cta;
       m.rest = rest;
     }
@@ -489,86 +552,78 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = m.tmem;
 
   if (warp == 0) {
-    // ---- loads: scales by cp.async, four tokens a lane; then a panel of rows per ring slot, a lane per box ----
-    // K's scale words go where the MMA's scale atoms have them, V's to a table of tokens.
-    Segments seg(a, m);
-    Ring rk(ring_k), rv(ring_v), sf(a.sf_bufs);
-    int used_k = 0, used_v = 0;
-    bool dead = false;
+    // ---- rows: a panel of a tile per ring slot ----
+    if (elect_one()) {
+      Segments seg(a, m);
+      Ring rk(ring_k), rv(ring_v);
+      int used_k = 0, used_v = 0;
+      const int kinds = shared_kv ? 1 : 2;
+      const bool two = a.box == kUnit;  // two boxes a tile: their pages are looked up a tile ahead
 #pragma unroll 1
-    while (!dead && seg.next()) {
-      const int tiles = seg.tiles(), kvh = seg.kvh;
-      const int32_t* row = a.table + seg.seg_b * a.ld_table;
-      auto page_of = [&](int tile) {  // the page of this lane's tokens (they lie on one); 2^32 - 1: none
-        return tile < tiles && 4 * lane < seg.tokens(tile) ? static_cast<uint32_t>(row[page_index(a, seg.start(tile) + 4 * lane)]) : 0xFFFFFFFFu;
-      };
-      uint32_t page = page_of(0);
+      while (m.dead == 0 && seg.next()) {
+        const int tiles = seg.tiles(), kvh = seg.kvh;
+        const int32_t* row = a.table + seg.seg_b * a.ld_table;
+        auto page_at = [&](int32_t t, int32_t& place) {  // the page and the place in it of a box
+          const uint32_t i = page_index(a, t);
+          place = t - static_cast<int32_t>(i * a.page_size);
+          return row[i];
+        };
+        int32_t page0 = 0, page1 = 0, place0 = 0, place1 = 0;
+        auto look_up = [&](int tile) {
+          const int32_t n = seg.tokens(tile), t = seg.start(tile);
+          if (n > 0) page0 = page_at(t, place0);
+          if (n > kUnit) page1 = page_at(t + kUnit, place1);
+        };
+        if (two) look_up(0);
 #pragma unroll 1
-      for (int i = 0; i < tiles; ++i) {
-        const uint32_t next_page = page_of(i + 1);
-        const int32_t t = seg.start(i), n = seg.tokens(i);
-        const uint32_t sf_at = sbase + lay.sf + sf.slot * sf_bytes;
-        wait_bar(m, BAR(sf_empty[0]) + 8 * sf.slot, sf.phase ^ 1);
-        const uint32_t there = __ballot_sync(0xffffffffu, page < a.pages);
-        if (page < a.pages) {
-          const uint32_t at = t + 4 * lane - page_index(a, t + 4 * lane) * a.page_size;
-          const uint8_t* ks = a.k_sf + page * a.k_sf_page + at * a.k_sf_token + kvh * a.k_sf_head;
-          const uint8_t* vs = shared_kv ? ks : a.v_sf + page * a.v_sf_page + at * a.v_sf_token + kvh * a.v_sf_head;
-          const int64_t v_step = shared_kv ? a.k_sf_token : a.v_sf_token;
-          // (tokens of the page behind the sequence's end are copied too, and not used)
-          uint32_t kd = sf_at + (lane & 7) * 64 + (lane >> 3) * 4, vd = sf_at + NP * 512 + lane * 16;
+        for (int i = 0; i < tiles; ++i) {
+          const int32_t t = seg.start(i), boxes = (seg.tokens(i) + a.box - 1) >> a.box_shift, bytes = boxes << a.box_shift << 7;
+          const int32_t p0 = page0, p1 = page1, at0 = place0, at1 = place1;
+          if (two && i + 1 < tiles) look_up(i + 1);
 #pragma unroll 1
-          for (int p = 0; p < NP; ++p, ks += 4, vs += 4, kd += 512, vd += 512) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              cp_async_4(kd + 16 * k, ks + k * a.k_sf_token);
-              cp_async_4(vd + 4 * k, vs + k * v_step);
+          for (int half = 0; half < kinds; ++half) {
+            const CUtensorMap* const map = half == 0 ? &map_k : &map_v;
+            const int slot0 = half == 0 ? 0 : ring_k;
+#pragma unroll 1
+            for (int p = 0; p < NP; ++p) {
+              const int s = slot0 + rk.slot;
+              const uint32_t full = BAR(ring_full[0]) + 8 * s;
+              uint32_t dst = sbase + lay.ring + s * kPanel;
+              if (!wait_bar(m, BAR(ring_empty[0]) + 8 * s, rk.phase ^ 1)) break;
+              mbar_arrive_expect_tx(full, bytes);
+              if (two) {
+                if (boxes > 0) tma_load_4d(dst, map, full, p * 128, at0, kvh, p0);
+                if (boxes > 1) tma_load_4d(dst + kUnit * 128, map, full, p * 128, at1, kvh, p1);
+              } else {
+#pragma unroll 1
+                for (int j = 0; j < boxes; ++j, dst += a.box << 7) {
+                  int32_t at;
+                  const int32_t page = page_at(t + (j << a.box_shift), at);
+                  tma_load_4d(dst, map, full, p * 128, at, kvh, page);
+                }
+              }
+              rk.next();
+              ++used_k;
+            }
+            if (kinds == 2) {  // (the values' ring and count; a reference to either would live in memory)
+              const Ring ring = rk;
+              const int used = used_k;
+              rk = rv, rv = ring;
+              used_k = used_v, used_v = used;
             }
           }
         }
-        cp_async_arrive(BAR(sf_raw[0]) + 8 * sf.slot);
-        if (lane == 0) {
-          TileInfo* const info = reinterpret_cast<TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1024);
-          info->there = there;
-          info->tokens = n;
-          mbar_arrive(BAR(sf_raw[0]) + 8 * sf.slot);
-        }
-        sf.next();
-        const int boxes = (n + a.box - 1) >> a.box_shift;
-        const uint32_t box_page = __shfl_sync(0xffffffffu, page, (lane * a.box >> 2) & 31);
-        const int32_t place = t + lane * a.box - static_cast<int32_t>(page_index(a, t + lane * a.box) * a.page_size);
+      }
+      // every load in flight lands before the CTA leaves
 #pragma unroll 1
-        for (int half = 0; half < (shared_kv ? 1 : 2) && !dead; ++half) {
-          Ring& r = half == 0 ? rk : rv;
-          const int slot0 = half == 0 ? 0 : ring_k;
+      for (int half = 0; half < kinds; ++half) {
+        const int n = half == 0 ? ring_k : ring_v, used = half == 0 ? used_k : used_v;
 #pragma unroll 1
-          for (int p = 0; p < NP; ++p) {
-            const int s = slot0 + r.slot;
-            wait_bar(m, BAR(ring_empty[0]) + 8 * s, r.phase ^ 1);
-            dead = __any_sync(0xffffffffu, m.dead);
-            if (dead) break;
-            if (lane == 0) mbar_arrive_expect_tx(BAR(ring_full[0]) + 8 * s, boxes * a.box * 128);
-            __syncwarp();
-            if (lane < boxes)
-              tma_load_4d(sbase + lay.ring + s * kPanel + lane * a.box * 128, half == 0 ? &map_k : &map_v, BAR(ring_full[0]) + 8 * s,
-                          p * 128, place, kvh, static_cast<int32_t>(box_page));
-            r.next();
-            (half == 0 ? used_k : used_v) += 1;
-          }
-        }
-        if (dead) break;
-        page = next_page;
+        for (int i = max(0, used - n); i < used; ++i)
+          if (!mbar_wait_bounded(BAR(ring_full[(half == 0 ? 0 : ring_k) + i % n]), (i / n) & 1)) m.dead = 1;
       }
     }
-    // every load in flight lands before the CTA leaves
-    cp_async_wait_all();
-#pragma unroll 1
-    for (int half = 0; half < (shared_kv ? 1 : 2); ++half) {
-      const int n = half == 0 ? ring_k : ring_v, used = half == 0 ? used_k : used_v;
-#pragma unroll 1
-      for (int i = max(0, used - n); i < used; ++i)
-        if (!mbar_wait_bounded(BAR(ring_full[(half == 0 ? 0 : ring_k) + i % n]), (i / n) & 1)) m.dead = 1;
-    }
+    __syncwarp();
   } else if (warp == 1) {
     // ---- the scores' MMAs ----
     // (A thread of their own: a wait behind a commit takes the issuing thread about 250 cycles, eight of which a tile's
@@ -576,9 +631,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       Segments seg(a, m);
       Ring rk(ring_k), sf(a.sf_bufs), s(SB), q_ring(1);
+      bool first = true;
 #pragma unroll 1
       while (seg.next()) {
         const int tiles = seg.tiles();
+        // this item's queries, once the last scores of the one before are done
+        wait_bar(m, BAR(q_empty), q_ring.phase ^ 1);
+        if (first) pdl_wait_primary();
+        first = false;
+        const uint8_t* const q = a.q_ws + ((static_cast<int64_t>(seg.seg_b) * a.kv + seg.kvh) * a.blocks + seg.blk) * (NP * (GP * 256 + 512));
+        mbar_arrive_expect_tx(BAR(q_full), NP * (GP * 256 + 512));
+        bulk_load(sbase + lay.q, q, NP * GP * 256, BAR(q_full));
+        bulk_load(sbase + lay.q_sf, q + NP * GP * 256, NP * 512, BAR(q_full));
         wait_bar(m, BAR(q_full), q_ring.phase);
         q_ring.next();
         tc_fence_after();
@@ -613,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_commit(BAR(done));
+      if (!first && !mbar_wait_bounded(BAR(q_full), q_ring.phase ^ 1)) m.dead = 1;  // (no copy outlives the CTA)
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -629,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < tiles; ++i) {
           const int both = seg.tokens(i) > 64 ? 1 : 0, chunks = NP << both;
           wait_bar(m, BAR(p_full[0]) + 8 * pr.slot, pr.phase);
-          const uint32_t idesc = m.p_wide[pr.slot] != 0 ? idesc_f16_mn(GP, true) : idesc_f16_mn(GP, false);
+          const uint32_t idesc = m.p_wide[pr.slot] != 0 ? idesc_f16_mn(GO, true) : idesc_f16_mn(GO, false);
           const uint64_t p_desc = sdesc(sbase + lay.p + pr.slot * kPanel, 1024, 1024, 2);
 #pragma unroll 1
           for (int c = 0; c < chunks; ++c) {
@@ -639,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t bd = p_desc + h * 512;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc_mma_f16_ts(tmem + p * GP, tmem + kColV + 32 * vr.slot + 8 * k, bd + 128 * k, idesc, (i | h | k) != 0 ? 1u : 0u);
+              tc_mma_f16_ts(tmem + p * GO, tmem + kColV + 32 * vr.slot + 8 * k, bd + 128 * k, idesc, (i | h | k) != 0 ? 1u : 0u);
             tc_commit(BAR(v_empty[0]) + 8 * vr.slot);
             vr.next();
           }
@@ -653,22 +718,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ---- a tile's tokens that take part, its pivot, and whether fp16 holds its scales ----
+    // ---- scales: the tokens that take part, the pivot, and whether fp16 holds them; four tokens a lane ----
     Segments seg(a, m);
     Ring sf(a.sf_bufs);
+    ScaleCopies copies(a, m, sbase + lay.sf, sf_bytes, lane);
+    // Without a warp for the copies they run two tiles ahead of the check; with three buffers right before it (a tile's
+    // scales would otherwise wait for the tile two before it, and its scores with them).
+    int more_copies = kCopier ? 0 : a.sf_bufs >= 4 ? 3 : 1;
 #pragma unroll 1
     while (seg.next()) {
       const int tiles = seg.tiles();
       int32_t pivot = 0;
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
-        wait_bar(m, BAR(sf_raw[0]) + 8 * sf.slot, sf.phase);
         uint8_t* const buf = smem + lay.sf + sf.slot * sf_bytes;
         TileInfo* const info = reinterpret_cast<TileInfo*>(buf + NP * 1024);
-        // lane: tokens 4 lane .. + 3
-        const int32_t n = info->tokens - 4 * lane;
+        const int32_t n = seg.tokens(i) - 4 * lane;
+        if constexpr (!kCopier) {
+#pragma unroll 1
+          do copies.next(smem + lay.sf);
+          while (--more_copies > 0);
+          more_copies = 1;
+        }
+        wait_bar(m, BAR(sf_raw[0]) + 8 * sf.slot, sf.phase);
         const bool ok = (info->there >> lane) & 1;
-        const uint32_t mine = !ok || n <= 0 ? 0u : n >= 4 ? 15u : (1u << n) - 1;  // these of them take part
+        const uint32_t mine = !ok || n <= 0 ? 0u : n >= 4 ? 15u : (1u << n) - 1;  // these of the lane's tokens take part
         uint32_t hi = 0, lo = 0xFFFFFFFFu;  // largest byte, smallest nonzero byte - 1
 #pragma unroll 1
         for (int p = 0; p < NP; ++p) {
@@ -687,62 +761,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             lo = __viaddmin_u16x2(o, 0xFFFFFFFFu, lo);
           }
         }
-        const int32_t top = __reduce_max_sync(0xffffffffu, max(hi & 0xFFFFu, hi >> 16));
-        const int32_t least = __reduce_min_sync(0xffffffffu, min(lo & 0xFFFFu, lo >> 16)) + 1;  // (65536: none)
-        if (top > pivot + 7) pivot = top;
-        // token 32 w + 4 j + i: bit 4 j + i of word w
-        uint32_t word = mine << (4 * (lane & 7));
+        int32_t top = static_cast<int32_t>(max(hi & 0xFFFFu, hi >> 16)), least = static_cast<int32_t>(min(lo & 0xFFFFu, lo >> 16)) + 1;
+        int32_t flags = i + 1 == tiles ? kLastTile | (seg.left == 0 ? kLastOfAll : 0) : 0;
+        if (__any_sync(0xffffffffu, mine != 15u || top > pivot + 7 || least < pivot - 14)) {  // seldom
+          top = __reduce_max_sync(0xffffffffu, top);
+          least = __reduce_min_sync(0xffffffffu, least);  // (65536: no nonzero one)
+          if (top > pivot + 7) pivot = top;
+          flags |= least < pivot - 14 ? kWide : 0;
+          // token 32 w + 4 j + i: bit 4 j + i of word w
+          uint32_t word = mine << (4 * (lane & 7));
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
-        if ((lane & 7) == 0) info->valid[lane >> 3] = word;
-        if (lane == 0) info->pivot = pivot, info->wide = least < pivot - 14;
+          for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+          if ((lane & 7) == 0) info->valid[lane >> 3] = word;
+        } else if (lane < 4) {
+          info->valid[lane] = 0xFFFFFFFFu;
+        }
+        if (lane == 0) info->pivot = pivot, info->flags = flags;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(sf_full[0]) + 8 * sf.slot);
         sf.next();
       }
     }
+    cp_async_wait_all();
+  } else if (kCopier && warp == 8) {
+    ScaleCopies copies(a, m, sbase + lay.sf, sf_bytes, lane);
+#pragma unroll 1
+    while (copies.next(smem + lay.sf)) {
+    }
+    cp_async_wait_all();
   } else if (warp < 12) {
     // ---- softmax ----
-    const int quarter = warp & 3, h0 = (warp - 4) / 4 * HPT, st = tid - 128;
+    const int quarter = warp & 3, h0 = (warp - 4) / 4 * SH, st = tid - 128;
+    const int hl = h0 + (st & 127), half_bar = 1 + (warp - 4) / 4;  // the warps of the same heads agree among themselves
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const float c = a.scale * 1.4426950408889634f;
     const int t = 32 * quarter + lane;
     // the row of P of this thread's token: tokens 4 j + i of 16 are rows 2 j + i (i < 2) and 6 + 2 j + i
     const int prow = (t & ~15) + ((t >> 2) & 3) * 2 + (t & 1) + ((t & 2) << 2);
-    Segments seg(a, m);
-    Ring sf(a.sf_bufs), s(SB), pr(a.p_bufs), one(1), fin(2);
-    bool first = true;
+    Ring sf(a.sf_bufs), s(SB), pr(a.p_bufs), fin(2);
+    bool more = m.w1 > m.w0 && warp < 4 + SW;
 #pragma unroll 1
-    while (seg.next()) {
-      const int tiles = seg.tiles(), heads = seg.heads();
-      if (st == 0) {  // this item's queries, once the last scores of the one before are done
-        wait_bar(m, BAR(q_empty), one.phase ^ 1);
-        const uint8_t* const q = a.q_ws + ((static_cast<int64_t>(seg.seg_b) * a.kv + seg.kvh) * a.blocks + seg.blk) * (NP * (GP * 256 + 512));
-        if (first) pdl_wait_primary();
-        first = false;
-        mbar_arrive_expect_tx(BAR(q_full), NP * (GP * 256 + 512));
-        bulk_load(sbase + lay.q, q, NP * GP * 256, BAR(q_full));
-        bulk_load(sbase + lay.q_sf, q + NP * GP * 256, NP * 512, BAR(q_full));
-        one.next();
-      }
-      float l[HPT];
+    while (more) {  // (the tiles say where a segment ends: its own count would cost registers)
+      float l[SH];
 #pragma unroll
-      for (int i = 0; i < HPT; ++i) l[i] = 0.f;
+      for (int i = 0; i < SH; ++i) l[i] = 0.f;
       int32_t pivot = 0;
       // (the last segment's references were read before this barrier)
-      named_barrier(2, kSoftThreads);
-      if (st < GP) m.ref[st] = kLowRef;
-      named_barrier(2, kSoftThreads);
-#pragma unroll 1
-      for (int i = 0; i < tiles; ++i) {
-        float x[HPT];
+      named_barrier(half_bar, 128);
+      if ((st & 127) < SH) m.ref[hl] = kLowRef;
+      named_barrier(half_bar, 128);
+      bool last, started = false;
+      do {
+        float x[SH];
         wait_bar(m, BAR(s_full[s.slot]), s.phase);
         tc_fence_after();
         const uint32_t sc = t_lane + kColS + s.slot * 2 * GP + h0;
 #pragma unroll
-        for (int j = 0; j < HPT; j += 16) {
-          constexpr int n = HPT < 16 ? 8 : 16;
+        for (int j = 0; j < SH; j += 16) {
+          constexpr int n = SH < 16 ? 8 : 16;
           uint32_t hi[n], lo[n];
           if constexpr (n == 8) tmem_ld_x8(sc + j, hi), tmem_ld_x8(sc + GP + j, lo);
           else tmem_ld_x16(sc + j, hi), tmem_ld_x16(sc + GP + j, lo);
@@ -754,20 +831,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileInfo* const info = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1024);
         const bool valid = (info->valid[quarter] >> lane) & 1;
         const int32_t new_pivot = info->pivot;
-        const bool wide = info->wide != 0;
+        const bool wide = (info->flags & kWide) != 0;
+        last = (info->flags & kLastTile) != 0;
+        more = (info->flags & kLastOfAll) == 0;
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(sf_empty[sf.slot]));
+        if (lane == 0) mbar_arrive(BAR(sf_empty[0]) + 8 * sf.slot);
         sf.next();
         float over = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < HPT; j += 4) {
+        for (int j = 0; j < SH; j += 4) {
           const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j]);
           over = fmaxf(fmaxf(over, fmaxf(x[j] - r.x, x[j + 1] - r.y)), fmaxf(x[j + 2] - r.z, x[j + 3] - r.w));
         }
-        if (named_barrier_or(2, kSoftThreads, (valid && over > kSlack) || new_pivot != pivot)) {
+        if (named_barrier_or(half_bar, 128, (valid && over > kSlack) || new_pivot != pivot)) {
           // new references: the largest scores so far (seldom but at a segment's start; compact, S read again)
 #pragma unroll 1
-          for (int j = 0; j < HPT; j += 8) {
+          for (int j = 0; j < SH; j += 8) {
             uint32_t hi[8], lo[8];
             tmem_ld_x8(sc + j, hi);
             tmem_ld_x8(sc + GP + j, lo);
@@ -781,20 +860,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane < 8) atomicMax(&m.red[h0 + j + lane], mine);
           }
-          named_barrier(2, kSoftThreads);
-          if (st < GP) {
-            const float old = m.ref[st], top = m.red[st] == INT32_MIN ? kLowRef : of_ordered(m.red[st]), now = fmaxf(old, top);
-            m.ref[st] = now;
-            m.fac[st] = ex2(old - now);
-            m.red[st] = INT32_MIN;
+          named_barrier(half_bar, 128);
+          if ((st & 127) < SH) {
+            const float old = m.ref[hl], top = m.red[hl] == INT32_MIN ? kLowRef : of_ordered(m.red[hl]), now = fmaxf(old, top);
+            m.ref[hl] = now;
+            m.fac[hl] = ex2(old - now);
+            m.red[hl] = INT32_MIN;
           }
-          named_barrier(2, kSoftThreads);
+          named_barrier(half_bar, 128);
 #pragma unroll
-          for (int j = 0; j < HPT; j += 4) {
+          for (int j = 0; j < SH; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(&m.fac[h0 + j]);
             l[j] *= f.x, l[j + 1] *= f.y, l[j + 2] *= f.z, l[j + 3] *= f.w;
           }
-          if (i > 0) {
+          if (started) {
             // every product so far is in O, and the next waits for P
             const int prev = pr.slot == 0 ? a.p_bufs - 1 : pr.slot - 1;
             wait_bar(m, BAR(p_empty[0]) + 8 * prev, pr.slot == 0 ? pr.phase ^ 1 : pr.phase);
@@ -802,9 +881,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int down = pivot - new_pivot;  // <= 0
             const float pf = down < -126 ? 0.f : __uint_as_float((127 + down) << 23);
 #pragma unroll 1
-            for (int q = 0; q < NP * (HPT / 8); ++q) {
-              const int j = q % (HPT / 8) * 8;
-              const uint32_t col = t_lane + q / (HPT / 8) * GP + h0 + j;
+            for (int q = 0; q < NP * (SH / 8); ++q) {
+              const int j = q % (SH / 8) * 8;
+              const uint32_t col = t_lane + q / (SH / 8) * GO + h0 + j;
               uint32_t r[8];
               tmem_ld_x8(col, r);
               tmem_ld_wait();
@@ -823,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_bar(m, BAR(p_empty[pr.slot]), pr.phase ^ 1);
         uint8_t* const row = smem + lay.p + pr.slot * kPanel + prow * 128;
 #pragma unroll
-        for (int j = 0; j < HPT; j += 8) {
+        for (int j = 0; j < SH; j += 8) {
           float e[8];
           const float4 r0 = *reinterpret_cast<const float4*>(&m.ref[h0 + j]), r1 = *reinterpret_cast<const float4*>(&m.ref[h0 + j + 4]);
           const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
@@ -843,20 +922,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(p_full[0]) + 8 * pr.slot);
         pr.next();
-      }
+        started = true;
+      } while (!last);
       // sums over the quarter's tokens
       Fin& f = *reinterpret_cast<Fin*>(smem + lay.fin + fin.slot * sizeof(Fin));
       wait_bar(m, BAR(fin_empty[fin.slot]), fin.phase ^ 1);
-      fold_sums<16, HPT>(l, lane);
-      constexpr int kShare = 32 / HPT;  // lanes that hold the same head
+      fold_sums<16, SH>(l, lane);
+      constexpr int kShare = 32 / SH;  // lanes that hold the same head
       if (lane % kShare == 0) f.sum[quarter][h0 + lane / kShare] = l[0];
-      if (quarter == 0 && lane < HPT) f.ref[h0 + lane] = m.ref[h0 + lane];
+      if (quarter == 0 && lane < SH) f.ref[h0 + lane] = m.ref[h0 + lane];
       if (st == 0) f.pivot = pivot;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(fin_full[fin.slot]));
       fin.next();
     }
-    if (st == 0 && !first && !mbar_wait_bounded(BAR(q_full), one.phase ^ 1)) m.dead = 1;  // (no copy outlives the CTA)
   } else {
     // ---- V^T and the outputs ----
     const int quarter = warp & 3, set = (warp - 12) / 4, h0 = set * HPT;
@@ -876,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_bar(m, BAR(sf_full[sf.slot]), sf.phase);
         const uint8_t* const buf = smem + lay.sf + sf.slot * sf_bytes;
         const TileInfo* const info = reinterpret_cast<const TileInfo*>(buf + NP * 1024);
-        const bool wide = info->wide != 0;
+        const bool wide = (info->flags & kWide) != 0;
         const int32_t pivot = info->pivot;
         const uint32_t down = static_cast<uint32_t>((15 - pivot) & 0xFFFF) * 0x10001u;
         const uint32_t valid0 = info->valid[2 * set], valid1 = info->valid[2 * set + 1];
@@ -980,9 +1059,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int heads = seg.heads(), head0 = seg.head0();
       const int part = 2 * blockIdx.x + (seg.u0 == 0 ? 1 : 0);
       if (!whole && seg.u0 == 0) {  // the item's first part, and this CTA's last segment
-        const int64_t last = m.w1 + seg.seg_units - seg.u1 - 1, more = (m.per_cta + 1) * m.rest;  // the item's last unit
-        const int64_t cta = last < more ? last / (m.per_cta + 1) : m.rest + (last - more) / m.per_cta;
-        owner = make_int2(1 + (seg.seg_b * a.kv + seg.kvh) * a.blocks + seg.blk, static_cast<int>(cta));
+        const int32_t last = m.w1 + seg.seg_units - seg.u1 - 1, more = (m.per_cta + 1) * m.rest;  // the item's last unit
+        const int32_t cta = last < more ? last / (m.per_cta + 1) : m.rest + (last - more) / m.per_cta;
+        owner = make_int2(1 + (seg.seg_b * a.kv + seg.kvh) * a.blocks + seg.blk, cta);
       }
       if (quarter == 0 && lane < HPT && my < heads) {
         if (!whole) a.stat[part * GP + my] = make_float2(ref, sum);
@@ -995,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p = i / (HPT / 8), j = i % (HPT / 8) * 8, n = min(8, heads - h0 - j);  // heads h0 + j ..
         if (n <= 0) continue;
         uint32_t r[8];
-        tmem_ld_x8(t_lane + p * GP + h0 + j, r);
+        tmem_ld_x8(t_lane + p * GO + h0 + j, r);
         tmem_ld_wait();
         const int d = 128 * p + 32 * quarter + lane;
         if (!whole) {
@@ -1208,7 +1287,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // ---- host -----------------------------------------------------------------------------------
 constexpr int kSmemLimit = 227 * 1024;
 
-int padded_heads(int block_heads) { return block_heads <= 16 ? 16 : block_heads <= 32 ? 32 : 64; }
+// SMs of the current device, asked for once per device.
+int cached_sms() {
+  static std::atomic<int> known[64];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms();
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) known[dev].store(n = num_sms(), std::memory_order_relaxed);
+  return n;
+}
+
+int padded_heads(int block_heads) { return block_heads <= 8 ? 8 : block_heads <= 16 ? 16 : block_heads <= 32 ? 32 : 64; }
 
 // A cache as a 4-D tensor (feature, place, head, page) in boxes of 128 features x `box` places.
 bool make_cache_map(CUtensorMap* m, const mxq_kv_cache& c, int box) {
@@ -1256,7 +1345,7 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, Args a, cudaStr
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int bytes = layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs).total;
   if ((e = launch_behind(attention_kernel<GP>, a.ctas, kThreads, bytes, stream, mk, mv, a)) != cudaSuccess) return e;
-  return launch_behind(join_kernel, 2 * num_sms(), kJoinThreads, 0, stream, a, GP);
+  return launch_behind(join_kernel, 2 * cached_sms(), kJoinThreads, 0, stream, a, GP);
 }
 
 // The workspace: parts, statistics, owners, queries.
@@ -1267,7 +1356,7 @@ Space space_of(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim) {
   const int G = q_heads / kv_heads, blocks = (G + kMaxHeads - 1) / kMaxHeads;
   Space s;
   s.gp = padded_heads((G + blocks - 1) / blocks);
-  s.ctas = std::min(kMaxCtas, num_sms());
+  s.ctas = std::min(kMaxCtas, cached_sms());
   s.stat = align256(2 * s.ctas * s.gp * dim * 4);
   s.owner = s.stat + align256(2 * s.ctas * s.gp * 8);
   s.q = s.owner + align256(s.ctas * 8);
@@ -1288,14 +1377,14 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
   a.ldq = l.ldq;
   a.ldqh = l.ldqh;
   a.k_sf = static_cast<const uint8_t*>(k.sf);
-  a.k_sf_page = k.sf_page_stride;
-  a.k_sf_token = k.sf_token_stride;
-  a.k_sf_head = k.sf_head_stride;
+  a.k_sf_page = static_cast<uint32_t>(k.sf_page_stride);
+  a.k_sf_token = static_cast<uint32_t>(k.sf_token_stride);
+  a.k_sf_head = static_cast<uint32_t>(k.sf_head_stride);
   if (l.v != nullptr) {
     a.v_sf = static_cast<const uint8_t*>(l.v->sf);
-    a.v_sf_page = l.v->sf_page_stride;
-    a.v_sf_token = l.v->sf_token_stride;
-    a.v_sf_head = l.v->sf_head_stride;
+    a.v_sf_page = static_cast<uint32_t>(l.v->sf_page_stride);
+    a.v_sf_token = static_cast<uint32_t>(l.v->sf_token_stride);
+    a.v_sf_head = static_cast<uint32_t>(l.v->sf_head_stride);
   }
   a.table = l.table;
   a.ld_table = l.ld_table;
@@ -1327,6 +1416,7 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
   a.status = l.status;
   const Space sp = space_of(l.B, l.q_heads, k.heads, k.dim);
   const int64_t most = l.B * a.kv * a.blocks * ((static_cast<int64_t>(l.table_width) * k.page_size + kUnit - 1) / kUnit);
+  if (most >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
   a.ctas = static_cast<int32_t>(std::min(sp.ctas, most));
   uint8_t* const ws = static_cast<uint8_t*>(l.workspace);
   a.part = reinterpret_cast<float*>(ws);
@@ -1337,7 +1427,7 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
   if (!make_cache_map(&mk, k, a.box)) return cudaErrorInvalidValue;
   if (l.v == nullptr) mv = mk;
   else if (!make_cache_map(&mv, *l.v, a.box)) return cudaErrorInvalidValue;
-  return sp.gp == 16 ? launch<16>(mk, mv, a, stream) : sp.gp == 32 ? launch<32>(mk, mv, a, stream) : launch<64>(mk, mv, a, stream);
+  return sp.gp == 8 ? launch<8>(mk, mv, a, stream) : sp.gp == 16 ? launch<16>(mk, mv, a, stream) : sp.gp == 32 ? launch<32>(mk, mv, a, stream) : launch<64>(mk, mv, a, stream);
 }
 
 }  // namespace mxq

@@ -10,6 +10,7 @@ The calls of a decode step around the attention; o leaves it as the operand of `
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -19,17 +20,13 @@ from . import _lib
 from ._lib import I32, I64, P, _check, _ptr, _stream
 
 _F32 = ctypes.c_float
-_device = getattr(torch._C, "_cuda_getDevice", None)  # (a torch without CUDA has none, and no device tensor to call with)
+# (looked up once; a torch without CUDA has neither, and no device tensor to call with)
+_device, _raw_stream = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-
-class KvCacheC(ctypes.Structure):
-    """The C struct mxq_kv_cache."""
-    _fields_ = [("data", P), ("sf", P), ("pages", I64), ("page_size", I32), ("heads", I32), ("dim", I32),
-                ("page_stride", I64), ("token_stride", I64), ("head_stride", I64),
-                ("sf_page_stride", I64), ("sf_token_stride", I64), ("sf_head_stride", I64)]
-
-
-_KVP = ctypes.POINTER(KvCacheC)
+# The C struct mxq_kv_cache as bytes: data, sf, pages, page_size, heads, dim, strides. (A few tokens take the GPU less
+# than a ctypes structure takes to be filled.)
+_CACHE = struct.Struct("@PPqiii4xqqqqqq")
+_KVP = ctypes.c_char_p
 
 SIGNATURES = {
     "kv_write_mxfp8": ([P, I64, I64, _KVP, P, I64, I64, _KVP, P, I64, P], ctypes.c_int),
@@ -56,11 +53,11 @@ def _fns():
     return lib
 
 
-def _here(t: torch.Tensor) -> None:
-    """The calls launch on the current device, so that is where their tensors have to be."""
-    _ptr(t)
-    if t.get_device() != _device():
-        raise ValueError("a tensor of another device than the current one")
+def _refuse(*tensors: Optional[torch.Tensor]) -> None:
+    """For a call whose tensors are not all on the current device, which is where it would launch."""
+    for t in tensors:
+        _ptr(t)
+    raise ValueError("a tensor of another device than the current one")
 
 
 @dataclass
@@ -71,13 +68,16 @@ class MXFP8Cache:
     data: torch.Tensor
     sf: torch.Tensor
 
-    def c(self) -> KvCacheC:
+    def c(self) -> bytes:
         d, s = self.data, self.sf
-        assert d.dtype is torch.uint8 and s.dtype is torch.uint8
         pages, page, heads, dim = d.shape
-        ds, ss = d.stride(), s.stride()
-        assert s.shape == (pages, page, heads, dim // 32) and ds[3] == 1 and (ss[3] == 1 or dim == 32)
-        return KvCacheC(_ptr(d), _ptr(s), pages, page, heads, dim, ds[0], ds[1], ds[2], ss[0], ss[1], ss[2])
+        d0, d1, d2, one = d.stride()
+        s0, s1, s2, one_s = s.stride()
+        assert d.dtype is torch.uint8 and s.dtype is torch.uint8
+        assert s.shape == (pages, page, heads, dim // 32) and one == 1 and (one_s == 1 or dim == 32)
+        if not (d.is_cuda and s.is_cuda and d.get_device() == s.get_device() == _device()):
+            _refuse(d, s)
+        return _CACHE.pack(d.data_ptr(), s.data_ptr(), pages, page, heads, dim, d0, d1, d2, s0, s1, s2)
 
     @staticmethod
     def empty(pages: int, page_size: int, heads: int, dim: int, device="cuda") -> "MXFP8Cache":
@@ -85,30 +85,24 @@ class MXFP8Cache:
                           torch.empty((pages, page_size, heads, dim // 32), dtype=torch.uint8, device=device))
 
 
-def _rows(x: torch.Tensor, cache: MXFP8Cache, T: int):
-    shape, st = x.shape, x.stride()
-    assert x.dtype is torch.bfloat16 and shape[0] == T and shape[1:] == cache.data.shape[2:] and st[2] == 1
-    return _ptr(x), st[0], st[1]
-
-
-def _table(t: torch.Tensor, B: int):
-    assert t.dtype is torch.int32 and t.dim() == 2 and t.shape[0] == B and (t.stride(1) == 1 or t.shape[1] == 1)
-    return _ptr(t), t.stride(0), t.shape[1]
-
-
 def kv_write_mxfp8(k: torch.Tensor, slots: torch.Tensor, k_cache: MXFP8Cache, v: Optional[torch.Tensor] = None,
                    v_cache: Optional[MXFP8Cache] = None, stream=None) -> None:
     """k bf16 [T, heads, dim] into the slots int32 [T] of the cache (-1: not written); v likewise."""
     T, = slots.shape
+    kt, kh, one = k.stride()
     assert slots.dtype is torch.int32 and slots.is_contiguous() and (v is None) == (v_cache is None)
-    kp, kt, kh = _rows(k, k_cache, T)
+    assert k.dtype is torch.bfloat16 and one == 1 and k.shape == (T, *k_cache.data.shape[2:])
     vp, vt, vh, vc = None, 0, 0, None
     if v is not None:
-        vp, vt, vh = _rows(v, v_cache, T)
-        vc = ctypes.byref(v_cache.c())
-    _here(k)
-    _check(_fns().kv_write_mxfp8(kp, kt, kh, ctypes.byref(k_cache.c()), vp, vt, vh, vc, _ptr(slots), T, _stream(stream)),
-           "kv_write_mxfp8")
+        vt, vh, one = v.stride()
+        assert v.dtype is torch.bfloat16 and one == 1 and v.shape == (T, *v_cache.data.shape[2:])
+        vp, vc = _ptr(v), v_cache.c()
+    if not (k.is_cuda and slots.is_cuda and k.get_device() == _device()):
+        _refuse(k, slots)
+    status = _fns().kv_write_mxfp8(k.data_ptr(), kt, kh, k_cache.c(), vp, vt, vh, vc, slots.data_ptr(), T,
+                                   _raw_stream(_device()) if stream is None else _stream(stream))
+    if status:
+        _check(status, "kv_write_mxfp8")
 
 
 def kv_read_bf16(k_cache: MXFP8Cache, block_table: torch.Tensor, cu_rows: torch.Tensor, k_out: torch.Tensor,
@@ -116,17 +110,26 @@ def kv_read_bf16(k_cache: MXFP8Cache, block_table: torch.Tensor, cu_rows: torch.
                  starts: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows cu_rows[b] .. cu_rows[b + 1] of k_out (and v_out), bf16 [rows, heads, dim], from the tokens of sequence
     b at starts[b] (0 without starts) and on; block_table int32 [B, width], cu_rows int32 [B + 1]."""
-    B = cu_rows.shape[0] - 1
-    assert cu_rows.dtype is torch.int32 and cu_rows.dim() == 1 and cu_rows.is_contiguous()
+    n, = cu_rows.shape
+    B, rows = n - 1, k_out.shape[0]
+    tb, width = block_table.shape
+    ldt, one = block_table.stride()
+    assert cu_rows.dtype is torch.int32 and cu_rows.is_contiguous()
+    assert block_table.dtype is torch.int32 and tb == B and (one == 1 or width == 1)
     assert starts is None or (starts.dtype is torch.int32 and starts.shape == (B,) and starts.is_contiguous())
     assert (v_out is None) == (v_cache is None)
-    rows = k_out.shape[0]
-    for x, c in ((k_out, k_cache),) + (() if v_out is None else ((v_out, v_cache),)):
-        assert x.dtype is torch.bfloat16 and x.is_contiguous() and x.shape[0] == rows and x.shape[1:] == c.data.shape[2:]
-    _here(k_out)
-    _check(_fns().kv_read_bf16(ctypes.byref(k_cache.c()), None if v_cache is None else ctypes.byref(v_cache.c()),
-                               *_table(block_table, B), _ptr(cu_rows), _ptr(starts), B, rows, _ptr(k_out), _ptr(v_out),
-                               _stream(stream)), "kv_read_bf16")
+    assert k_out.dtype is torch.bfloat16 and k_out.is_contiguous() and k_out.shape == (rows, *k_cache.data.shape[2:])
+    vp, vc = None, None
+    if v_out is not None:
+        assert v_out.dtype is torch.bfloat16 and v_out.is_contiguous() and v_out.shape == (rows, *v_cache.data.shape[2:])
+        vp, vc = _ptr(v_out), v_cache.c()
+    if not (k_out.is_cuda and block_table.is_cuda and cu_rows.is_cuda and k_out.get_device() == _device()):
+        _refuse(k_out, block_table, cu_rows)
+    status = _fns().kv_read_bf16(k_cache.c(), vc, block_table.data_ptr(), ldt, width, cu_rows.data_ptr(),
+                                 None if starts is None else _ptr(starts), B, rows, k_out.data_ptr(), vp,
+                                 _raw_stream(_device()) if stream is None else _stream(stream))
+    if status:
+        _check(status, "kv_read_bf16")
 
 
 def paged_attention_workspace_bytes(B: int, q_heads: int, kv_heads: int, dim: int) -> int:
@@ -146,10 +149,13 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
     workspace: None = allocated for this call on its stream, or a uint8 tensor of paged_attention_workspace_bytes(...)."""
     lib = _fns()
     B, H, D = q.shape
-    qs = q.stride()
-    kv = k_cache.data.shape[2]
-    assert q.dtype is torch.bfloat16 and k_cache.data.shape[3] == D and qs[2] == 1
+    ldq, ldqh, one = q.stride()
+    tb, width = block_table.shape
+    ldt, one_t = block_table.stride()
+    shape = k_cache.data.shape
+    assert q.dtype is torch.bfloat16 and shape[3] == D and one == 1
     assert seq_lens.dtype is torch.int32 and seq_lens.shape == (B,) and seq_lens.is_contiguous()
+    assert block_table.dtype is torch.int32 and tb == B and (one_t == 1 or width == 1)
     n = B * H * D
     assert out is None or (out.dtype is torch.bfloat16 and out.numel() == n and out.is_contiguous())
     assert out_q is None or (out_q.dtype is torch.uint8 and out_q.numel() == n and out_q.is_contiguous())
@@ -157,9 +163,11 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
     assert sf_rowmajor is None or sf_rowmajor.nbytes * 32 >= n
     assert sf_packed is None or sf_packed.nbytes * 32 >= -(-B // 4) * 4 * H * D
     assert sf_128x4 is None or sf_128x4.nbytes * 32 >= -(-B // 128) * 128 * H * D
-    _here(q)
+    if not (q.is_cuda and block_table.is_cuda and seq_lens.is_cuda and q.get_device() == _device()):
+        _refuse(q, block_table, seq_lens)
+    kc, vc = k_cache.c(), None if v_cache is None else v_cache.c()
     if workspace is None:
-        size = lib.mxq_paged_attention_workspace_bytes(B, H, kv, D)
+        size = lib.mxq_paged_attention_workspace_bytes(B, H, shape[2], D)
         if size:
             if stream is None:
                 workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
@@ -167,9 +175,12 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
                 s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
                 with torch.cuda.stream(s):
                     workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    _check(lib.paged_attention_mxfp8(_ptr(q), qs[0], qs[1], ctypes.byref(k_cache.c()),
-                                     None if v_cache is None else ctypes.byref(v_cache.c()), *_table(block_table, B),
-                                     _ptr(seq_lens), B, H, scale, _ptr(out), _ptr(out_q), _ptr(sf_packed),
-                                     _ptr(sf_rowmajor), _ptr(sf_128x4), _ptr(lse), _ptr(workspace),
-                                     0 if workspace is None else workspace.nbytes, _ptr(status), _stream(stream)),
-           "paged_attention_mxfp8")
+    code = lib.paged_attention_mxfp8(
+        q.data_ptr(), ldq, ldqh, kc, vc, block_table.data_ptr(), ldt, width, seq_lens.data_ptr(), B, H, scale,
+        None if out is None else _ptr(out), None if out_q is None else _ptr(out_q), None if sf_packed is None else _ptr(sf_packed),
+        None if sf_rowmajor is None else _ptr(sf_rowmajor), None if sf_128x4 is None else _ptr(sf_128x4),
+        None if lse is None else _ptr(lse), None if workspace is None else _ptr(workspace),
+        0 if workspace is None else workspace.nbytes, None if status is None else _ptr(status),
+        _raw_stream(_device()) if stream is None else _stream(stream))
+    if code:
+        _check(code, "paged_attention_mxfp8")

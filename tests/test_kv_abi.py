@@ -1,6 +1,5 @@
 """include/mxq_kv.h: every declared symbol is exported and bad arguments are refused on the host
 (these calls return before any CUDA work, so no GPU is needed)."""
-import ctypes
 import os
 import re
 
@@ -20,13 +19,13 @@ def lib():
 
 
 def cache(**kw):
-    from mxfp8_activation_quant_gb300.kv import KvCacheC
+    from mxfp8_activation_quant_gb300.kv import _CACHE
 
     a = dict(data=FAKE, sf=FAKE, pages=PAGES, page_size=PAGE, heads=HEADS, dim=D, page_stride=PAGE * HEADS * D,
              token_stride=HEADS * D, head_stride=D, sf_page_stride=PAGE * HEADS * D // 32,
              sf_token_stride=HEADS * D // 32, sf_head_stride=D // 32)
     a.update(kw)
-    return KvCacheC(*a.values())
+    return _CACHE.pack(*(v or 0 for v in a.values()))
 
 
 BAD_CACHES = [
@@ -42,7 +41,7 @@ BAD_CACHES = [
 
 
 def ref(c):
-    return ctypes.byref(c) if c is not None else None
+    return c  # (the struct's bytes, or None)
 
 
 def write(lib, kc=None, vc=None, k=FAKE, ldk=HEADS * D, ldkh=D, v=None, ldv=HEADS * D, ldvh=D, slots=FAKE, T=4):
