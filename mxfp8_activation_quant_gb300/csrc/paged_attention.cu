@@ -19,8 +19,8 @@
 //
 // Warps: 0 the rows' loads, 1 and 2 MMAs (scores, outputs), 3 scales, 4-11 softmax (two a TMEM lane quarter, half of the heads each),
 // 12-19 V^T and the outputs (two a
-// quarter; 64 of the tile's tokens each, half of the heads each). Up to 8 heads the softmax takes four warps, and
-// warp 8 the scales' copies.
+// quarter; 64 of the tile's tokens each, half of the heads each). Up to 8 heads the softmax takes four warps,
+// warp 8 the scales' copies and warp 9 the values' rows.
 //
 // A CTA that holds an item from start to end writes its outputs; the others' normalised parts go to the
 // workspace (at most two a CTA), and join_kernel adds them up in the order of the CTAs.
@@ -331,7 +331,7 @@ struct Ring {
   }
 };
 
-// A bounded wait: tries that each last a microsecond at most, half a million of them; false once one has run out,
+// A bounded wait: half a million tries, of about two microseconds each; false once one has run out,
 // after which nothing waits any more (results are void, every loop still ends, and the status word is written at the
 // end). Small on purpose: it is inlined thirty times, and the roles' loops have to fit the instruction cache together
 // (with the library's usual wait, which reads a clock, they did not: 93 % hits, and its refills at 64 % of their peak).
@@ -551,16 +551,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = m.tmem;
 
-  if (warp == 0) {
-    // ---- rows: a panel of a tile per ring slot ----
+  if (warp == 0 || (kCopier && warp == 9)) {
+    // ---- rows: a panel of a tile per ring slot (with warps to spare, the values' come from one of their own) ----
     if (elect_one()) {
       Segments seg(a, m);
-      Ring rk(ring_k), rv(ring_v);
-      int used_k = 0, used_v = 0;
-      const int kinds = shared_kv ? 1 : 2;
+      const int kind0 = warp == 0 ? 0 : 1, kinds = shared_kv ? 1 - kind0 : kCopier ? kind0 + 1 : 2;  // kinds [kind0, kinds)
+      Ring ring(kind0 == 0 ? ring_k : ring_v), other(ring_v);
+      int used = 0, other_used = 0;
       const bool two = a.box == kUnit;  // two boxes a tile: their pages are looked up a tile ahead
 #pragma unroll 1
-      while (m.dead == 0 && seg.next()) {
+      while (kind0 < kinds && m.dead == 0 && seg.next()) {
         const int tiles = seg.tiles(), kvh = seg.kvh;
         const int32_t* row = a.table + seg.seg_b * a.ld_table;
         auto page_at = [&](int32_t t, int32_t& place) {  // the page and the place in it of a box
@@ -581,46 +581,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t p0 = page0, p1 = page1, at0 = place0, at1 = place1;
           if (two && i + 1 < tiles) look_up(i + 1);
 #pragma unroll 1
-          for (int half = 0; half < kinds; ++half) {
-            const CUtensorMap* const map = half == 0 ? &map_k : &map_v;
-            const int slot0 = half == 0 ? 0 : ring_k;
+          for (int kind = kind0; kind < kinds; ++kind) {
+            const CUtensorMap* const map = kind == 0 ? &map_k : &map_v;
+            const int slot0 = kind == 0 ? 0 : ring_k;
 #pragma unroll 1
-            for (int p = 0; p < NP; ++p) {
-              const int s = slot0 + rk.slot;
+            for (int x = 0; x < 128 * NP; x += 128) {
+              const int s = slot0 + ring.slot;
               const uint32_t full = BAR(ring_full[0]) + 8 * s;
               uint32_t dst = sbase + lay.ring + s * kPanel;
-              if (!wait_bar(m, BAR(ring_empty[0]) + 8 * s, rk.phase ^ 1)) break;
+              if (!wait_bar(m, BAR(ring_empty[0]) + 8 * s, ring.phase ^ 1)) break;
               mbar_arrive_expect_tx(full, bytes);
               if (two) {
-                if (boxes > 0) tma_load_4d(dst, map, full, p * 128, at0, kvh, p0);
-                if (boxes > 1) tma_load_4d(dst + kUnit * 128, map, full, p * 128, at1, kvh, p1);
+                if (boxes > 0) tma_load_4d(dst, map, full, x, at0, kvh, p0);
+                if (boxes > 1) tma_load_4d(dst + kUnit * 128, map, full, x, at1, kvh, p1);
               } else {
 #pragma unroll 1
                 for (int j = 0; j < boxes; ++j, dst += a.box << 7) {
                   int32_t at;
                   const int32_t page = page_at(t + (j << a.box_shift), at);
-                  tma_load_4d(dst, map, full, p * 128, at, kvh, page);
+                  tma_load_4d(dst, map, full, x, at, kvh, page);
                 }
               }
-              rk.next();
-              ++used_k;
+              ring.next();
+              ++used;
             }
-            if (kinds == 2) {  // (the values' ring and count; a reference to either would live in memory)
-              const Ring ring = rk;
-              const int used = used_k;
-              rk = rv, rv = ring;
-              used_k = used_v, used_v = used;
+            if (!kCopier && kinds == 2) {  // (a reference to either ring would live in memory)
+              const Ring r = ring;
+              const int u = used;
+              ring = other, other = r;
+              used = other_used, other_used = u;
             }
           }
         }
       }
       // every load in flight lands before the CTA leaves
 #pragma unroll 1
-      for (int half = 0; half < kinds; ++half) {
-        const int n = half == 0 ? ring_k : ring_v, used = half == 0 ? used_k : used_v;
+      for (int kind = kind0; kind < kinds; ++kind) {
+        const int n = kind == 0 ? ring_k : ring_v, u = kind == kind0 ? used : other_used;
 #pragma unroll 1
-        for (int i = max(0, used - n); i < used; ++i)
-          if (!mbar_wait_bounded(BAR(ring_full[(half == 0 ? 0 : ring_k) + i % n]), (i / n) & 1)) m.dead = 1;
+        for (int i = max(0, u - n); i < u; ++i)
+          if (!mbar_wait_bounded(BAR(ring_full[(kind == 0 ? 0 : ring_k) + i % n]), (i / n) & 1)) m.dead = 1;
       }
     }
     __syncwarp();
