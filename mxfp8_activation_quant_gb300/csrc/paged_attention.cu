@@ -1069,24 +1069,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.lse[static_cast<int64_t>(seg.seg_b) * a.H + head0 + my] = lse_of(ref, sum);
       }
       const int64_t row = seg.seg_b;
+      const int mine = heads - h0;  // of this thread's heads there are so many
+      if (!whole) {
+        constexpr int CH = HPT < 16 ? 8 : 16;
 #pragma unroll 1
-      for (int i = 0; i < NP * (HPT / 8); ++i) {
-        const int p = i / (HPT / 8), j = i % (HPT / 8) * 8, n = min(8, heads - h0 - j);  // heads h0 + j ..
-        if (n <= 0) continue;
-        uint32_t r[8];
-        tmem_ld_x8(t_lane + p * GO + h0 + j, r);
-        tmem_ld_wait();
-        const int d = 128 * p + 32 * quarter + lane;
-        if (!whole) {
-          float* out = a.part + (static_cast<int64_t>(part) * GP + h0 + j) * a.D + d;
+        for (int i = 0; i < NP * (HPT / CH); ++i) {
+          const int p = i / (HPT / CH), j = i % (HPT / CH) * CH;
+          float* out = a.part + (static_cast<int64_t>(part) * GP + h0 + j) * a.D + 128 * p + 32 * quarter + lane;
+          uint32_t r[CH];
+          if constexpr (CH == 8) tmem_ld_x8(t_lane + p * GO + h0 + j, r);
+          else tmem_ld_x16(t_lane + p * GO + h0 + j, r);
+          tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 8; ++k, out += a.D) {
+          for (int k = 0; k < CH; ++k, out += a.D) {
             const float v = __uint_as_float(r[k]) * __shfl_sync(0xffffffffu, inv, j + k) * unit;
-            if (k < n) *out = v;
+            if (j + k < mine) *out = v;
           }
-        } else {
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < NP * (HPT / 8); ++i) {
+          const int p = i / (HPT / 8), j = i % (HPT / 8) * 8, n = mine - j;
+          if (n <= 0) continue;
+          uint32_t r[8];
+          tmem_ld_x8(t_lane + p * GO + h0 + j, r);
+          tmem_ld_wait();
+          const int d = 128 * p + 32 * quarter + lane;
           int64_t at = (row * a.H + head0 + h0 + j) * a.D + d;
-          uint32_t mine = 0;  // lane k: the scale byte of head k
+          uint32_t byte = 0;  // lane k: the scale byte of head k
 #pragma unroll
           for (int k = 0; k < 8; ++k, at += a.D) {
             const uint32_t y = bf16x2_rn(__uint_as_float(r[k]) * __shfl_sync(0xffffffffu, inv, j + k) * unit, 0.f) & 0xFFFFu;
@@ -1094,14 +1104,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.oq != nullptr) {
               const uint32_t code = ue8m0_from_bf16_amax(__reduce_max_sync(0xffffffffu, y & 0x7FFFu));
               if (k < n) a.oq[at] = static_cast<uint8_t>(e4m3x2(bf16_lo(y) * ue8m0_inverse(code), 0.f));
-              mine = lane == k ? code : mine;
+              byte = lane == k ? code : byte;
             }
           }
-          if (a.oq != nullptr && lane < n) {
+          if (a.oq != nullptr && lane < min(8, n)) {
             const int64_t word = static_cast<int64_t>(head0 + h0 + j + lane) * NP + p, words = static_cast<int64_t>(a.H) * NP;
-            if (a.sf_rm != nullptr) a.sf_rm[(row * words + word) * 4 + quarter] = static_cast<uint8_t>(mine);
-            if (a.sf_pk != nullptr) a.sf_pk[(word * ((a.B + 3) / 4 * 4) + row) * 4 + quarter] = static_cast<uint8_t>(mine);
-            if (a.sf_tl != nullptr) a.sf_tl[tiled128x4_word_offset(row, word, words) + quarter] = static_cast<uint8_t>(mine);
+            if (a.sf_rm != nullptr) a.sf_rm[(row * words + word) * 4 + quarter] = static_cast<uint8_t>(byte);
+            if (a.sf_pk != nullptr) a.sf_pk[(word * ((a.B + 3) / 4 * 4) + row) * 4 + quarter] = static_cast<uint8_t>(byte);
+            if (a.sf_tl != nullptr) a.sf_tl[tiled128x4_word_offset(row, word, words) + quarter] = static_cast<uint8_t>(byte);
           }
         }
       }
@@ -1183,11 +1193,12 @@ __device__ __forceinline__ void join_add(float4& v, float w, const float4 f) {
   v.x = fmaf(w, f.x, v.x), v.y = fmaf(w, f.y, v.y), v.z = fmaf(w, f.z, v.z), v.w = fmaf(w, f.w, v.w);
 }
 
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int gp) {
+__global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_constant__ Args a, int gp) {
   __shared__ int16_t owners[kMaxCtas];
-  __shared__ int count;
+  __shared__ uint32_t masks[kMaxCtas / 32];
   __shared__ float weight[kMaxCtas];
   __shared__ float4 acc[kJoinWarps][32];
+  __shared__ float tops[kJoinWarps], sums[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (a.sf_pk != nullptr || a.sf_tl != nullptr) {  // a word column per block and a row per thread
     const int words = a.H * a.panels, b4 = (a.B + 3) / 4 * 4, b128 = (a.B + 127) / 128 * 128, row = a.B + tid;
@@ -1199,16 +1210,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       }
   }
   pdl_wait_primary();
-  if (warp == 0) {
-    int n = 0;
-#pragma unroll 1
-    for (int i = 0; i < a.ctas; i += 32) {
-      const bool is = i + lane < a.ctas && a.owner[i + lane].x != 0;
-      const uint32_t all = __ballot_sync(0xffffffffu, is);
-      if (is) owners[n + __popc(all & ((1u << lane) - 1))] = static_cast<int16_t>(i + lane);
-      n += __popc(all);
-    }
-    if (lane == 0) count = n;
+  // the owners, in the same order in every block
+#pragma unroll
+  for (int u = 0; u < kMaxCtas / kJoinThreads; ++u) {
+    const int i = u * kJoinThreads + tid;
+    const uint32_t all = __ballot_sync(0xffffffffu, i < a.ctas && a.owner[i].x != 0);
+    if (lane == 0) masks[i >> 5] = all;
+  }
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxCtas / 32; ++k) {
+    const uint32_t all = masks[k];
+    if ((k & (kJoinWarps - 1)) == warp && (all >> lane & 1) != 0) owners[count + __popc(all & ((1u << lane) - 1))] = static_cast<int16_t>(32 * k + lane);
+    count += __popc(all);
   }
   __syncthreads();
   const int heads = count * a.block_heads, NP = a.panels;
@@ -1254,24 +1269,41 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const int h = i / NP, p = i - h * NP;
     const JoinWork w = join_work(a, owners, static_cast<uint32_t>(h) / a.block_heads, static_cast<uint32_t>(h) % a.block_heads);
     if (w.parts == 0) continue;  // block-uniform
-    // every warp looks over all the statistics
-    float top = kLowRef, sum = 0.f;
-#pragma unroll 1
-    for (int k = lane; k < w.parts; k += 32) top = fmaxf(top, a.stat[join_slot(w, k) * gp + w.h].x);
-    top = warp_max(top);
-#pragma unroll 1
-    for (int k = lane; k < w.parts; k += 32) {
-      const float2 s = a.stat[join_slot(w, k) * gp + w.h];
-      const float x = s.y * ex2(s.x - top);
-      if (warp == 0) weight[k] = x;
-      sum += x;
-    }
-    sum = warp_sum(sum);
+    // at most two parts a thread
+    const bool one = tid < w.parts, two = tid + kJoinThreads < w.parts;
+    const float2 none = make_float2(kLowRef, 0.f);
+    const float2 s0 = one ? a.stat[join_slot(w, tid) * gp + w.h] : none;
+    const float2 s1 = two ? a.stat[join_slot(w, tid + kJoinThreads) * gp + w.h] : none;
+    float top = warp_max(fmaxf(s0.x, s1.x));
+    if (lane == 0) tops[warp] = top;
     __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, tops[k]);
+    const float w0 = s0.y * ex2(s0.x - top), w1 = s1.y * ex2(s1.x - top);
+    if (one) weight[tid] = w0;
+    if (two) weight[tid + kJoinThreads] = w1;
+    const float part_sum = warp_sum(w0 + w1);
+    if (lane == 0) sums[warp] = part_sum;
+    __syncthreads();
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) sum += sums[k];
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = warp; k < w.parts; k += kJoinWarps)
-      join_add(v, weight[k], *reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(join_slot(w, k)) * gp + w.h) * a.D + 128 * p + 4 * lane));
+    const float* const x = a.part + w.h * a.D + 128 * p + 4 * lane;
+#pragma unroll 1
+    for (int k0 = warp; k0 < w.parts; k0 += 10 * kJoinWarps) {  // ten loads in flight
+      float4 f[10];
+#pragma unroll
+      for (int u = 0; u < 10; ++u) {
+        const int k = k0 + u * kJoinWarps;
+        f[u] = k < w.parts ? *reinterpret_cast<const float4*>(x + static_cast<int64_t>(join_slot(w, k)) * gp * a.D) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < 10; ++u) {
+        const int k = k0 + u * kJoinWarps;
+        join_add(v, k < w.parts ? weight[k] : 0.f, f[u]);
+      }
+    }
     acc[warp][lane] = v;
     __syncthreads();
     if (warp == 0) {
@@ -1345,7 +1377,7 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, Args a, cudaStr
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int bytes = layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs).total;
   if ((e = launch_behind(attention_kernel<GP>, a.ctas, kThreads, bytes, stream, mk, mv, a)) != cudaSuccess) return e;
-  return launch_behind(join_kernel, 2 * cached_sms(), kJoinThreads, 0, stream, a, GP);
+  return launch_behind(join_kernel, 4 * cached_sms(), kJoinThreads, 0, stream, a, GP);
 }
 
 // The workspace: parts, statistics, owners, queries.
