@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kUnits = 2;
+constexpr int64_t kManyRows = 4096;  // from here a warp reads four rows
 
 struct Tensor {
   const uint16_t* rows;
@@ -71,13 +72,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_cons
   const int64_t row = wid / t.chunks;
   if (row >= a.T) return;
   const uint32_t slot = static_cast<uint32_t>(a.slots[row]);
-  if (slot >= a.slots_end) return;  // (negative ones too)
-  const uint32_t page = slot / a.page_size, place = slot - page * a.page_size;
-  uint8_t* const data = t.data + page * t.page + place * t.token;
-  uint8_t* const sf = t.sf + page * t.sf_page + place * t.sf_token;
   const uint32_t col0 = static_cast<uint32_t>(wid - row * t.chunks) * (256 * kUnits) + 8 * lane;
 
-  uint4 v[kUnits];
+  uint4 v[kUnits];  // (asked for before the slot is looked at)
   uint32_t h[kUnits], d[kUnits];
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
@@ -86,6 +83,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_cons
     d[u] = c - h[u] * t.dim;
     v[u] = c < t.width ? ld_stream_u4(t.rows + row * t.ld + h[u] * t.ldh + d[u]) : make_uint4(0, 0, 0, 0);
   }
+  if (slot >= a.slots_end) return;  // (negative ones too)
+  const uint32_t page = slot / a.page_size, place = slot - page * a.page_size;
+  uint8_t* const data = t.data + page * t.page + place * t.token;
+  uint8_t* const sf = t.sf + page * t.sf_page + place * t.sf_token;
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
     const bool in = col0 + 256 * u < t.width;
@@ -125,50 +126,80 @@ __device__ __forceinline__ uint2 dequant4(uint32_t w, float s) {
   return make_uint2(bf16x2_rn(f[0] * s, f[1] * s), bf16x2_rn(f[2] * s, f[3] * s));
 }
 
+// A warp reads R consecutive rows; 32 / R lanes look up a row each, then all lanes take the rows' columns, 8 a lane.
+// Three loads depend on one another before a row's first byte (its sequence, its page, itself), so many rows want a
+// warp with four in flight: 40960 rows of 8 x 128, keys and values, 62.6 -> XX us.
+template <int R>
 __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int kLanes = 32 / R;
   const Tensor& t = a.t[blockIdx.y];
-  const int lane = threadIdx.x & 31;
-  const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t row = wid / t.chunks;
-  if (row >= a.rows) return;
-  // the last b with cu[b] <= row: 32 candidates a step
-  int64_t b = 0, n = a.B + 1;
-  while (n > 1) {
-    const int64_t step = (n + 31) / 32, i = lane * step;
-    const uint32_t le = __ballot_sync(0xffffffffu, i < n && a.cu[b + i] <= row);
-    if (le == 0) return;  // before the first row
-    const int64_t at = (__popc(le) - 1) * step;
-    b += at;
-    n = min(step, n - at);
+  const int lane = threadIdx.x & 31, sub = lane % kLanes;
+  const uint32_t group = (kLanes == 32 ? 0xffffffffu : (1u << kLanes) - 1) << (lane - sub);
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * R;
+  if (row0 >= a.rows) return;
+  const int64_t row = row0 + lane / kLanes;
+  // the last b with cu[b] <= row, kLanes candidates a step
+  int64_t b = -1, n = a.B + 1;
+  while (true) {
+    const int64_t step = (n + kLanes - 1) / kLanes, i = sub * step, at = b < 0 ? i : b + i;
+    const uint32_t le = __ballot_sync(0xffffffffu, i < n && a.cu[at] <= row) & group;
+    const int64_t k = (__popc(le) - 1) * step;  // (below zero: in front of the first row)
+    if (le != 0) {
+      b = (b < 0 ? 0 : b) + k;
+      n = min(step, n - k);
+    } else {
+      n = 1;
+    }
+    if (__all_sync(0xffffffffu, n <= 1)) break;
   }
-  if (b == a.B) return;  // behind the last row
-  const int64_t pos = row - a.cu[b] + (a.starts != nullptr ? a.starts[b] : 0);
-  uint32_t page = a.pages, place = 0;
-  if (pos >= 0 && pos < static_cast<int64_t>(a.table_width) * a.page_size) {
-    const uint32_t p = static_cast<uint32_t>(pos / a.page_size);
-    place = static_cast<uint32_t>(pos - static_cast<int64_t>(p) * a.page_size);
-    page = static_cast<uint32_t>(a.table[b * a.ld_table + p]);
+  // 0: not to be written, 1: zeros, 2: there
+  int state = row < a.rows && b >= 0 && b < a.B ? 1 : 0;
+  int64_t data_at = 0, sf_at = 0;
+  if (state != 0) {
+    const int64_t pos = row - a.cu[b] + (a.starts != nullptr ? a.starts[b] : 0);
+    if (pos >= 0 && pos < static_cast<int64_t>(a.table_width) * a.page_size) {
+      const uint32_t p = static_cast<uint32_t>(pos / a.page_size), place = static_cast<uint32_t>(pos - static_cast<int64_t>(p) * a.page_size);
+      const uint32_t page = static_cast<uint32_t>(a.table[b * a.ld_table + p]);
+      if (page < a.pages) {
+        state = 2;
+        data_at = page * t.page + place * t.token;
+        sf_at = page * t.sf_page + place * t.sf_token;
+      }
+    }
   }
-  const bool there = page < a.pages;
-  const uint8_t* const data = t.data + (there ? page * t.page + place * t.token : 0);
-  const uint8_t* const sf = t.sf + (there ? page * t.sf_page + place * t.sf_token : 0);
-  const uint32_t col0 = static_cast<uint32_t>(wid - row * t.chunks) * (256 * kUnits) + 8 * lane;
-  uint2 v[kUnits];
-  uint32_t s[kUnits];
+  int st[R];
+  const uint8_t *data[R], *sf[R];
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const uint32_t c = col0 + 256 * u, h = c / t.dim, d = c - h * t.dim;
-    const bool in = there && c < t.width;
-    v[u] = in ? *reinterpret_cast<const uint2*>(data + h * t.head + d) : make_uint2(0, 0);
-    s[u] = in ? sf[h * t.sf_head + (d >> 5)] : 0;
+  for (int r = 0; r < R; ++r) {
+    st[r] = __shfl_sync(0xffffffffu, state, r * kLanes);
+    data[r] = t.data + __shfl_sync(0xffffffffu, data_at, r * kLanes);
+    sf[r] = t.sf + __shfl_sync(0xffffffffu, sf_at, r * kLanes);
   }
+  for (uint32_t col0 = 8 * lane; col0 < (t.width + 255u & ~255u); col0 += 256 * kUnits) {
+    uint2 v[kUnits][R];
+    uint32_t s[kUnits][R];
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const uint32_t c = col0 + 256 * u;
-    if (c >= t.width) continue;
-    const float f = ue8m0_value(s[u]);
-    const uint2 x = dequant4(v[u].x, f), y = dequant4(v[u].y, f);
-    *reinterpret_cast<uint4*>(const_cast<uint16_t*>(t.rows) + row * t.ld + c) = make_uint4(x.x, x.y, y.x, y.y);
+    for (int u = 0; u < kUnits; ++u) {
+      const uint32_t c = col0 + 256 * u, h = c / t.dim, d = c - h * t.dim;
+      const int64_t da = h * t.head + d, sa = h * t.sf_head + (d >> 5);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bool in = st[r] == 2 && c < t.width;
+        v[u][r] = in ? *reinterpret_cast<const uint2*>(data[r] + da) : make_uint2(0, 0);
+        s[u][r] = in ? sf[r][sa] : 0;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const uint32_t c = col0 + 256 * u;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (c >= t.width || st[r] == 0) continue;
+        const float f = ue8m0_value(s[u][r]);
+        const uint2 x = dequant4(v[u][r].x, f), y = dequant4(v[u][r].y, f);
+        *reinterpret_cast<uint4*>(const_cast<uint16_t*>(t.rows) + (row0 + r) * t.ld + c) = make_uint4(x.x, x.y, y.x, y.y);
+      }
+    }
   }
 }
 
@@ -193,11 +224,7 @@ cudaError_t launch_kv_write(const KvWriteLaunch& l, cudaStream_t stream) {
 
 cudaError_t launch_kv_read(const KvReadLaunch& l, cudaStream_t stream) {
   ReadArgs a{};
-  int64_t warps = 0;
-  for (int i = 0; i < l.tensors; ++i) {
-    a.t[i] = tensor(l.t[i]);
-    warps = warps > l.rows * a.t[i].chunks ? warps : l.rows * a.t[i].chunks;
-  }
+  for (int i = 0; i < l.tensors; ++i) a.t[i] = tensor(l.t[i]);
   a.table = l.table;
   a.ld_table = l.ld_table;
   a.table_width = static_cast<uint32_t>(l.table_width);
@@ -207,9 +234,12 @@ cudaError_t launch_kv_read(const KvReadLaunch& l, cudaStream_t stream) {
   a.starts = l.starts;
   a.page_size = static_cast<uint32_t>(l.t[0].c.page_size);
   a.pages = static_cast<uint32_t>(l.t[0].c.pages);
-  const int64_t blocks = (warps + kWarps - 1) / kWarps;
+  const bool many = l.rows >= kManyRows;
+  const int64_t per = kWarps * (many ? 4 : 1), blocks = (l.rows + per - 1) / per;
   if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  kv_read_kernel<<<dim3(static_cast<unsigned>(blocks), l.tensors), kWarps * 32, 0, stream>>>(a);
+  const dim3 grid(static_cast<unsigned>(blocks), l.tensors);
+  if (many) kv_read_kernel<4><<<grid, kWarps * 32, 0, stream>>>(a);
+  else kv_read_kernel<1><<<grid, kWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

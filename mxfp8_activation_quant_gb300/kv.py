@@ -132,6 +132,30 @@ def kv_read_bf16(k_cache: MXFP8Cache, block_table: torch.Tensor, cu_rows: torch.
         _check(status, "kv_read_bf16")
 
 
+_workspaces: dict = {}
+
+
+def _workspace(size: int, stream) -> Optional[torch.Tensor]:
+    """The workspace kept for a stream, grown to `size` bytes where it is smaller; calls ordered on one stream may share
+    it. Under capture a call gets one from the graph's own pool, so that no graph depends on what is kept here."""
+    if size <= 0:
+        return None
+    device = _device()
+    raw = _raw_stream(device) if stream is None else _stream(stream)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(size, dtype=torch.uint8, device="cuda")
+    ws = _workspaces.get((device, raw))
+    if ws is None or ws.nbytes < size:
+        if stream is None:
+            ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        else:  # owned by the stream that uses it
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            with torch.cuda.stream(s):
+                ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        _workspaces[device, raw] = ws
+    return ws
+
+
 def paged_attention_workspace_bytes(B: int, q_heads: int, kv_heads: int, dim: int) -> int:
     """Bytes of the workspace of paged_attention_mxfp8 on the current device; 0 for an invalid shape."""
     return int(_fns().mxq_paged_attention_workspace_bytes(B, q_heads, kv_heads, dim))
@@ -146,7 +170,8 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
     out [B, q_heads, dim] and/or MXFP8 out_q [B, q_heads * dim] with any subset of the three scale layouts; lse
     fp32 [B, q_heads]. Without v_cache the values are the keys.
 
-    workspace: None = allocated for this call on its stream, or a uint8 tensor of paged_attention_workspace_bytes(...)."""
+    workspace: None = one that this module keeps for the stream (allocated for this call under stream capture), or a
+    uint8 tensor of paged_attention_workspace_bytes(...)."""
     lib = _fns()
     B, H, D = q.shape
     ldq, ldqh, one = q.stride()
@@ -167,14 +192,7 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
         _refuse(q, block_table, seq_lens)
     kc, vc = k_cache.c(), None if v_cache is None else v_cache.c()
     if workspace is None:
-        size = lib.mxq_paged_attention_workspace_bytes(B, H, shape[2], D)
-        if size:
-            if stream is None:
-                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-            else:  # owned by the stream that uses it
-                s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-                with torch.cuda.stream(s):
-                    workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        workspace = _workspace(lib.mxq_paged_attention_workspace_bytes(B, H, shape[2], D), stream)
     code = lib.paged_attention_mxfp8(
         q.data_ptr(), ldq, ldqh, kc, vc, block_table.data_ptr(), ldt, width, seq_lens.data_ptr(), B, H, scale,
         None if out is None else _ptr(out), None if out_q is None else _ptr(out_q), None if sf_packed is None else _ptr(sf_packed),
