@@ -45,10 +45,16 @@ constexpr int kMaxHeads = 64;     // query heads of an item
 constexpr float kLowRef = -1e30f; // ref before the first token
 constexpr float kSlack = 8.0f;
 
-// TMEM columns: O from 0, then S, the scales and V^T. With two S buffers (O then ends by column 128) K's scales
-// have two too, so that a tile's are not overwritten before its products are done.
-constexpr uint32_t kColS = 256, kColSfK = 384, kColSfK1 = 240, kColSfQ = 400, kColV = 416;
-constexpr int kVSlots = 3;
+// TMEM columns for GP heads: O from 0, S (one buffer of 64 heads, two of fewer, and as many of K's scales, so that a tile's are
+// not overwritten before its products are done), the queries' scales, and V^T in slots of 64 tokens x 128 features.
+template <int GP>
+struct Columns {
+  static constexpr int kBuffers = GP == 64 ? 1 : 2;
+  static constexpr uint32_t kS = GP == 64 ? 256 : GP == 32 ? 128 : 64, kSfK = kS + (GP < 16 ? 64 : kBuffers * 2 * GP),
+                            kSfQ = kSfK + 16 * kBuffers, kV = (kSfQ + 16 + 31) / 32 * 32;
+  static constexpr int kSlots = (512 - kV) / 32 < 8 ? (512 - kV) / 32 : 8;
+};
+constexpr int kMaxVSlots = 8;
 
 struct Args {
   const uint16_t* q;
@@ -86,8 +92,8 @@ struct Layout {
 };
 constexpr int kMaxSfBufs = 6;
 struct Misc {
-  uint64_t ring_full[16], ring_empty[16], sf_raw[kMaxSfBufs], sf_full[kMaxSfBufs], sf_empty[kMaxSfBufs], s_full[2], s_empty[2], p_full[2], p_empty[2], v_full[kVSlots],
-      v_empty[kVSlots], q_full, q_empty, o_full, o_empty, fin_full[2], fin_empty[2], done;
+  uint64_t ring_full[16], ring_empty[16], sf_raw[kMaxSfBufs], sf_full[kMaxSfBufs], sf_empty[kMaxSfBufs], s_full[2], s_empty[2], p_full[2], p_empty[2], v_full[kMaxVSlots],
+      v_empty[kMaxVSlots], q_full, q_empty, o_full, o_empty, fin_full[2], fin_empty[2], done;
   alignas(16) float ref[kMaxHeads];
   alignas(16) float fac[kMaxHeads];
   int32_t red[kMaxHeads];
@@ -225,6 +231,9 @@ __device__ __forceinline__ uint32_t rest4(uint32_t x01, uint32_t x23, uint32_t c
   const float2 f0 = f16x2_f32(c0), f1 = f16x2_f32(c1);
   return e4m3x2((bf16_lo(x01) * inv - f0.x) * up, (bf16_hi(x01) * inv - f0.y) * up) |
          (e4m3x2((bf16_lo(x23) * inv - f1.x) * up, (bf16_hi(x23) * inv - f1.y) * up) << 16);
+}
+__device__ __forceinline__ uint32_t fp16_fields(uint32_t bytes, uint32_t down) {
+  return (__viaddmax_s16x2(bytes & 0x00FF00FFu, down, 0) << 2) | (__viaddmax_s16x2((bytes >> 8) & 0x00FF00FFu, down, 0) << 10);
 }
 // ln of sum * 2^ref
 __device__ __forceinline__ float lse_of(float ref, float sum) {
@@ -463,7 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int SW = GP == 8 ? 4 : 8;     // warps of the softmax, and a thread's heads
   constexpr int SH = GP * 4 / SW;
   constexpr bool kCopier = SW == 4;       // then another copies the scales
-  constexpr int SB = GP == 64 ? 1 : 2;    // S buffers in TMEM
+  using Cols = Columns<GP>;
+  constexpr int SB = Cols::kBuffers, kVSlots = Cols::kSlots;
+  constexpr uint32_t kColS = Cols::kS, kColSfK = Cols::kSfK, kColSfQ = Cols::kSfQ, kColV = Cols::kV;
   extern __shared__ __align__(1024) uint8_t smem[];
   const Layout lay = layout_of(GP, a.panels, a.ring, a.sf_bufs, a.p_bufs);
   Misc& m = *reinterpret_cast<Misc*>(smem + lay.misc);
@@ -654,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bar(m, BAR(s_empty[0]) + 8 * s.slot, s.phase ^ 1);
           tc_fence_after();
           const uint32_t sf_at = sbase + lay.sf + sf.slot * sf_bytes;
-          const uint32_t d = tmem + kColS + s.slot * 2 * GP, sfk = tmem + (s.slot == 0 ? kColSfK : kColSfK1);
+          const uint32_t d = tmem + kColS + s.slot * 2 * GP, sfk = tmem + kColSfK + 16 * s.slot;
 #pragma unroll 1
           for (int p = 0; p < NP; ++p) {
             wait_bar(m, BAR(ring_full[0]) + 8 * rk.slot, rk.phase);
@@ -776,6 +787,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (lane < 4) {
           info->valid[lane] = 0xFFFFFFFFu;
         }
+        if ((flags & kWide) == 0) {  // the bytes become 4 max(0, b - pivot + 15): the exponent field of 2^(b - pivot) in fp16
+          const uint32_t down = static_cast<uint32_t>((15 - pivot) & 0xFFFF) * 0x10001u;
+#pragma unroll 1
+          for (int p = 0; p < NP; ++p) {
+            uint4* const at = reinterpret_cast<uint4*>(buf + NP * 512 + p * 512 + lane * 16);
+            const uint4 x = *at;
+            *at = make_uint4(fp16_fields(x.x, down), fp16_fields(x.y, down), fp16_fields(x.z, down), fp16_fields(x.w, down));
+          }
+        }
         if (lane == 0) info->pivot = pivot, info->flags = flags;
         fence_proxy_async_smem();
         __syncwarp();
@@ -795,7 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, h0 = (warp - 4) / 4 * SH, st = tid - 128;
     const int hl = h0 + (st & 127), half_bar = 1 + (warp - 4) / 4;  // the warps of the same heads agree among themselves
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    const float c = a.scale * 1.4426950408889634f;
+    // (a scale of zero becomes the smallest normal number: low times c has to be -infinity, which takes no part)
+    const float c0 = a.scale * 1.4426950408889634f, c = c0 == 0.f ? 1.1754944e-38f : c0, low = c < 0.f ? INFINITY : -INFINITY;
     const int t = 32 * quarter + lane;
     // the row of P of this thread's token: tokens 4 j + i of 16 are rows 2 j + i (i < 2) and 6 + 2 j + i
     const int prow = (t & ~15) + ((t >> 2) & 3) * 2 + (t & 1) + ((t & 2) << 2);
@@ -809,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int32_t pivot = 0;
       // (the last segment's references were read before this barrier)
       named_barrier(half_bar, 128);
-      if ((st & 127) < SH) m.ref[hl] = kLowRef;
+      if ((st & 127) < SH) m.ref[hl] = -kLowRef;
       named_barrier(half_bar, 128);
       bool last, started = false;
       do {
@@ -825,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else tmem_ld_x16(sc + j, hi), tmem_ld_x16(sc + GP + j, lo);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < n; ++k) x[j + k] = (__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c;
+          for (int k = 0; k < n; ++k) x[j + k] = __uint_as_float(hi[k]) + __uint_as_float(lo[k]);
         }
         wait_bar(m, BAR(sf_full[sf.slot]), sf.phase);
         const TileInfo* const info = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1024);
@@ -837,13 +858,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(sf_empty[0]) + 8 * sf.slot);
         sf.next();
+        if (!__all_sync(0xffffffffu, valid)) {  // (what takes no part may be NaN)
+#pragma unroll
+          for (int j = 0; j < SH; ++j) x[j] = valid ? x[j] : low;
+        }
         float over = -INFINITY;
 #pragma unroll
         for (int j = 0; j < SH; j += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j]);
-          over = fmaxf(fmaxf(over, fmaxf(x[j] - r.x, x[j + 1] - r.y)), fmaxf(x[j + 2] - r.z, x[j + 3] - r.w));
+          const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j]);  // (minus the references)
+          over = fmaxf(over, fmaxf(fmaf(x[j], c, r.x), fmaf(x[j + 1], c, r.y)));
+          over = fmaxf(over, fmaxf(fmaf(x[j + 2], c, r.z), fmaf(x[j + 3], c, r.w)));
         }
-        if (named_barrier_or(half_bar, 128, (valid && over > kSlack) || new_pivot != pivot)) {
+        if (named_barrier_or(half_bar, 128, over > kSlack || new_pivot != pivot)) {
           // new references: the largest scores so far (seldom but at a segment's start; compact, S read again)
 #pragma unroll 1
           for (int j = 0; j < SH; j += 8) {
@@ -862,8 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           named_barrier(half_bar, 128);
           if ((st & 127) < SH) {
-            const float old = m.ref[hl], top = m.red[hl] == INT32_MIN ? kLowRef : of_ordered(m.red[hl]), now = fmaxf(old, top);
-            m.ref[hl] = now;
+            const float old = -m.ref[hl], top = m.red[hl] == INT32_MIN ? kLowRef : of_ordered(m.red[hl]), now = fmaxf(old, top);
+            m.ref[hl] = -now;
             m.fac[hl] = ex2(old - now);
             m.red[hl] = INT32_MIN;
           }
@@ -908,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            e[k] = valid ? ex2(x[j + k] - r[k]) : 0.f;
+            e[k] = ex2(fmaf(x[j + k], c, r[k]));
             l[j + k] += e[k];
           }
           uint4 v;
@@ -930,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fold_sums<16, SH>(l, lane);
       constexpr int kShare = 32 / SH;  // lanes that hold the same head
       if (lane % kShare == 0) f.sum[quarter][h0 + lane / kShare] = l[0];
-      if (quarter == 0 && lane < SH) f.ref[h0 + lane] = m.ref[h0 + lane];
+      if (quarter == 0 && lane < SH) f.ref[h0 + lane] = -m.ref[h0 + lane];
       if (st == 0) f.pivot = pivot;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(fin_full[fin.slot]));
@@ -944,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring rv(ring_v), sf(a.sf_bufs), fin(2), o_ring(1);
     const int slot0 = shared_kv ? 0 : ring_k;
     uint32_t chunk = 0;
-    const uint32_t pick = static_cast<uint32_t>(quarter) * 0x0101u | 0x0400u;  // a byte of each word, to bytes 0 and 2 (1 and 3 are masked)
+    const uint32_t pick = static_cast<uint32_t>(quarter) * 0x1010u | 0x4000u;  // a byte of each word, to bytes 1 and 3 (0 and 2 are masked)
     int2 owner = make_int2(0, 0);
 #pragma unroll 1
     while (seg.next()) {
@@ -957,7 +983,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileInfo* const info = reinterpret_cast<const TileInfo*>(buf + NP * 1024);
         const bool wide = (info->flags & kWide) != 0;
         const int32_t pivot = info->pivot;
-        const uint32_t down = static_cast<uint32_t>((15 - pivot) & 0xFFFF) * 0x10001u;
         const uint32_t valid0 = info->valid[2 * set], valid1 = info->valid[2 * set + 1];
         const bool full = (valid0 & valid1) == 0xFFFFFFFFu;
 #pragma unroll 1
@@ -992,9 +1017,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t w0[16], w1[16];  // features 0-15 and 16-31 of the quarter's 32
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                // this quarter's group: 2^(b - pivot) in fp16 has the exponent field b - pivot + 15
-                const uint32_t s01 = __viaddmax_s16x2(__byte_perm(sw[k].x, sw[k].y, pick) & 0x00FF00FFu, down, 0) << 10,
-                               s23 = __viaddmax_s16x2(__byte_perm(sw[k].z, sw[k].w, pick) & 0x00FF00FFu, down, 0) << 10;
+                // this quarter's group: each byte to the top of an fp16
+                const uint32_t s01 = __byte_perm(sw[k].x, sw[k].y, pick) & 0xFF00FF00u, s23 = __byte_perm(sw[k].z, sw[k].w, pick) & 0xFF00FF00u;
                 uint32_t lo[4], hi[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -1089,29 +1113,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
 #pragma unroll 1
         for (int i = 0; i < NP * (HPT / 8); ++i) {
-          const int p = i / (HPT / 8), j = i % (HPT / 8) * 8, n = mine - j;
+          const int p = i / (HPT / 8), j = i % (HPT / 8) * 8, n = min(8, mine - j);
           if (n <= 0) continue;
           uint32_t r[8];
           tmem_ld_x8(t_lane + p * GO + h0 + j, r);
           tmem_ld_wait();
-          const int d = 128 * p + 32 * quarter + lane;
-          int64_t at = (row * a.H + head0 + h0 + j) * a.D + d;
-          uint32_t byte = 0;  // lane k: the scale byte of head k
+          const int64_t at = (row * a.H + head0 + h0 + j) * a.D + 128 * p + 32 * quarter + lane;
 #pragma unroll
-          for (int k = 0; k < 8; ++k, at += a.D) {
-            const uint32_t y = bf16x2_rn(__uint_as_float(r[k]) * __shfl_sync(0xffffffffu, inv, j + k) * unit, 0.f) & 0xFFFFu;
-            if (a.o != nullptr && k < n) a.o[at] = static_cast<uint16_t>(y);
-            if (a.oq != nullptr) {
-              const uint32_t code = ue8m0_from_bf16_amax(__reduce_max_sync(0xffffffffu, y & 0x7FFFu));
-              if (k < n) a.oq[at] = static_cast<uint8_t>(e4m3x2(bf16_lo(y) * ue8m0_inverse(code), 0.f));
+          for (int k = 0; k < 8; ++k) r[k] = bf16x2_rn(__uint_as_float(r[k]) * __shfl_sync(0xffffffffu, inv, j + k) * unit, 0.f);
+          if (a.o != nullptr) {
+            uint16_t* out = a.o + at;
+#pragma unroll
+            for (int k = 0; k < 8; ++k, out += a.D)
+              if (k < n) *out = static_cast<uint16_t>(r[k]);
+          }
+          if (a.oq != nullptr) {
+            uint8_t* out = a.oq + at;
+            uint32_t byte = 0;  // lane k: the scale byte of head k
+#pragma unroll
+            for (int k = 0; k < 8; ++k, out += a.D) {
+              const uint32_t code = ue8m0_from_bf16_amax(__reduce_max_sync(0xffffffffu, r[k] & 0x7FFFu));
+              if (k < n) *out = static_cast<uint8_t>(e4m3x2(bf16_lo(r[k]) * ue8m0_inverse(code), 0.f));
               byte = lane == k ? code : byte;
             }
-          }
-          if (a.oq != nullptr && lane < min(8, n)) {
-            const int64_t word = static_cast<int64_t>(head0 + h0 + j + lane) * NP + p, words = static_cast<int64_t>(a.H) * NP;
-            if (a.sf_rm != nullptr) a.sf_rm[(row * words + word) * 4 + quarter] = static_cast<uint8_t>(byte);
-            if (a.sf_pk != nullptr) a.sf_pk[(word * ((a.B + 3) / 4 * 4) + row) * 4 + quarter] = static_cast<uint8_t>(byte);
-            if (a.sf_tl != nullptr) a.sf_tl[tiled128x4_word_offset(row, word, words) + quarter] = static_cast<uint8_t>(byte);
+            if (lane < n) {
+              const int64_t word = static_cast<int64_t>(head0 + h0 + j + lane) * NP + p, words = static_cast<int64_t>(a.H) * NP;
+              if (a.sf_rm != nullptr) a.sf_rm[(row * words + word) * 4 + quarter] = static_cast<uint8_t>(byte);
+              if (a.sf_pk != nullptr) a.sf_pk[(word * ((a.B + 3) / 4 * 4) + row) * 4 + quarter] = static_cast<uint8_t>(byte);
+              if (a.sf_tl != nullptr) a.sf_tl[tiled128x4_word_offset(row, word, words) + quarter] = static_cast<uint8_t>(byte);
+            }
           }
         }
       }
