@@ -44,6 +44,7 @@ constexpr int kPanel = 128 * 128; // bytes of 128 features of a tile
 constexpr int kMaxHeads = 64;     // query heads of an item
 constexpr float kLowRef = -1e30f; // ref before the first token
 constexpr float kSlack = 8.0f;
+constexpr int32_t kNoScore = static_cast<int32_t>(0x807FFFFFu);  // ordered(-infinity)
 
 // TMEM columns for GP heads: O from 0, S (one buffer of 64 heads, two of fewer, and as many of K's scales, so that a tile's are
 // not overwritten before its products are done), the queries' scales, and V^T in slots of 64 tokens x 128 features.
@@ -279,7 +280,10 @@ __device__ __forceinline__ uint32_t page_index(const Args& a, uint32_t t) { retu
 // A sequence without tokens is one unit, which writes its zeros.
 __device__ __forceinline__ int32_t units_of(int32_t len) { return len <= 0 ? 1 : (len - 1) / kUnit + 1; }
 
-// Walks a CTA's segments: runs of units of one item. An item is (sequence, cache head, block of query heads).
+// Walks a CTA's segments: runs of units of one item. An item is (cache head, block of query heads, sequence), in that
+// order: CTAs that work at the same time then read the heads of the same tokens, which lie side by side, and
+// blocks of heads that share a cache head find it in L2 (128 sequences x 8 heads of 128, tokens before heads: 153 -> XX us
+// against sequences first).
 struct Segments {
   const Args& a;
   int32_t left, next_len, b, k, blk_, u, len, units;
@@ -290,22 +294,22 @@ struct Segments {
       : a(args), left(m.w1 - m.w0), b(m.b0), k(m.kvh0), blk_(m.blk0), u(m.u0) {
     len = left > 0 ? length_of(a, a.lens[b]) : 0;
     units = units_of(len);
-    next_len = left > 0 && b + 1 < a.B ? a.lens[b + 1] : 0;
+    next_len = left > 0 ? a.lens[b + 1 < a.B ? b + 1 : 0] : 0;
   }
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
     if (u == units) {
       u = 0;
-      if (++blk_ == a.blocks) {
-        blk_ = 0;
-        if (++k == a.kv) {
-          k = 0;
-          ++b;
-          len = length_of(a, next_len);
-          units = units_of(len);
-          next_len = b + 1 < a.B ? a.lens[b + 1] : 0;
+      if (++b == a.B) {
+        b = 0;
+        if (++blk_ == a.blocks) {
+          blk_ = 0;
+          ++k;
         }
       }
+      len = length_of(a, next_len);
+      units = units_of(len);
+      next_len = a.lens[b + 1 < a.B ? b + 1 : 0];
     }
     seg_b = b;
     kvh = k;
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
-  if (tid < kMaxHeads) m.red[tid] = INT32_MIN;
+  if (tid < kMaxHeads) m.red[tid] = kNoScore;
 
   // The CTA's share: a scan of the sequences' units, a run of sequences per thread.
   {
@@ -534,23 +538,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     // (every warp sums the warps' sums, a lane each)
     const int32_t theirs = lane < kThreads / 32 ? m.sums[lane] : 0;
-    const int32_t total = __reduce_add_sync(0xffffffffu, theirs) * S;
+    const int32_t once = __reduce_add_sync(0xffffffffu, theirs), total = once * S;  // the sequences', the items' units
     const int32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0) + inc - sum;
     // (no share is empty among the CTAs that have one: the parts of an item lie in consecutive CTAs)
     const int32_t per_cta = max(1, total / a.ctas), rest = total < a.ctas ? 0 : total - per_cta * a.ctas;
     const int32_t w0 = per_cta * static_cast<int32_t>(blockIdx.x) + min(static_cast<int32_t>(blockIdx.x), rest);
-    if (w0 < total && before * S <= w0 && w0 < (before + sum) * S) {  // one thread
-      int32_t at = w0 - before * S, b = b0, units = units_of(length_of(a, a.lens[b]));
+    const int32_t sub = w0 / once;
+    int32_t at = w0 - sub * once;
+    if (w0 < total && before <= at && at < before + sum) {  // one thread
+      at -= before;
+      int32_t b = b0, units = units_of(length_of(a, a.lens[b]));
 #pragma unroll 1
-      while (at >= units * S) {
-        at -= units * S;
+      while (at >= units) {
+        at -= units;
         units = units_of(length_of(a, a.lens[++b]));
       }
-      const int32_t sub = at / units;  // (below S)
       m.b0 = b;
       m.kvh0 = sub / a.blocks;
       m.blk0 = sub - m.kvh0 * a.blocks;
-      m.u0 = at - sub * units;
+      m.u0 = at;
       m.w0 = w0;
       m.w1 = w0 + per_cta + (static_cast<int32_t>(blockIdx.x) < rest ? 1 : 0);
       m.per_cta = per_cta;
@@ -862,44 +868,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < SH; ++j) x[j] = valid ? x[j] : low;
         }
-        float over = -INFINITY;
+        // Whether a score passes its reference by too much. A segment's first tile always sets the references, from S
+        // itself in a short loop; later S is given back before the question, for the next scores to be made meanwhile.
+        bool move = true;
+        if (started) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(s_empty[0]) + 8 * s.slot);
+          float over = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < SH; j += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j]);  // (minus the references)
-          over = fmaxf(over, fmaxf(fmaf(x[j], c, r.x), fmaf(x[j + 1], c, r.y)));
-          over = fmaxf(over, fmaxf(fmaf(x[j + 2], c, r.z), fmaf(x[j + 3], c, r.w)));
+          for (int j = 0; j < SH; j += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j]);  // (minus the references)
+            over = fmaxf(over, fmaxf(fmaf(x[j], c, r.x), fmaf(x[j + 1], c, r.y)));
+            over = fmaxf(over, fmaxf(fmaf(x[j + 2], c, r.z), fmaf(x[j + 3], c, r.w)));
+          }
+          move = named_barrier_or(half_bar, 128, over > kSlack || new_pivot != pivot);
         }
-        if (named_barrier_or(half_bar, 128, over > kSlack || new_pivot != pivot)) {
-          // new references: the largest scores so far (seldom but at a segment's start; compact, S read again)
+        if (move) {
+          // new references: the largest scores so far; lane k keeps head j + k's
+          if (!started) {
 #pragma unroll 1
-          for (int j = 0; j < SH; j += 8) {
-            uint32_t hi[8], lo[8];
-            tmem_ld_x8(sc + j, hi);
-            tmem_ld_x8(sc + GP + j, lo);
-            tmem_ld_wait();
-            int32_t mine = INT32_MIN;  // lane k: head k's
+            for (int j = 0; j < SH; j += 8) {
+              uint32_t hi[8], lo[8];
+              tmem_ld_x8(sc + j, hi);
+              tmem_ld_x8(sc + GP + j, lo);
+              tmem_ld_wait();
+              int32_t mine = kNoScore;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float y = (__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c;
-              const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered(y) : INT32_MIN);
+              for (int k = 0; k < 8; ++k) {
+                const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered((__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c) : kNoScore);
+                mine = lane == k ? top : mine;
+              }
+              if (lane < 8) atomicMax(&m.red[h0 + j + lane], mine);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(s_empty[0]) + 8 * s.slot);
+          } else {
+            int32_t mine = kNoScore;
+#pragma unroll
+            for (int k = 0; k < SH; ++k) {
+              const int32_t top = __reduce_max_sync(0xffffffffu, ordered(x[k] * c));
               mine = lane == k ? top : mine;
             }
-            if (lane < 8) atomicMax(&m.red[h0 + j + lane], mine);
+            if (lane < SH) atomicMax(&m.red[h0 + lane], mine);
           }
           named_barrier(half_bar, 128);
           if ((st & 127) < SH) {
-            const float old = -m.ref[hl], top = m.red[hl] == INT32_MIN ? kLowRef : of_ordered(m.red[hl]), now = fmaxf(old, top);
+            const float old = -m.ref[hl], now = fmaxf(old, fmaxf(kLowRef, of_ordered(m.red[hl])));
             m.ref[hl] = -now;
             m.fac[hl] = ex2(old - now);
-            m.red[hl] = INT32_MIN;
+            m.red[hl] = kNoScore;
           }
           named_barrier(half_bar, 128);
-#pragma unroll
-          for (int j = 0; j < SH; j += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&m.fac[h0 + j]);
-            l[j] *= f.x, l[j + 1] *= f.y, l[j + 2] *= f.z, l[j + 3] *= f.w;
-          }
           if (started) {
+#pragma unroll
+            for (int j = 0; j < SH; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&m.fac[h0 + j]);
+              l[j] *= f.x, l[j + 1] *= f.y, l[j + 2] *= f.z, l[j + 3] *= f.w;
+            }
             // every product so far is in O, and the next waits for P
             const int prev = pr.slot == 0 ? a.p_bufs - 1 : pr.slot - 1;
             wait_bar(m, BAR(p_empty[0]) + 8 * prev, pr.slot == 0 ? pr.phase ^ 1 : pr.phase);
@@ -921,9 +948,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           pivot = new_pivot;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(s_empty[0]) + 8 * s.slot);
         s.next();
         wait_bar(m, BAR(p_empty[pr.slot]), pr.phase ^ 1);
         uint8_t* const row = smem + lay.p + pr.slot * kPanel + prow * 128;
@@ -1085,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole && seg.u0 == 0) {  // the item's first part, and this CTA's last segment
         const int32_t last = m.w1 + seg.seg_units - seg.u1 - 1, more = (m.per_cta + 1) * m.rest;  // the item's last unit
         const int32_t cta = last < more ? last / (m.per_cta + 1) : m.rest + (last - more) / m.per_cta;
-        owner = make_int2(1 + (seg.seg_b * a.kv + seg.kvh) * a.blocks + seg.blk, cta);
+        owner = make_int2(1 + (seg.kvh * a.blocks + seg.blk) * a.B + seg.seg_b, cta);
       }
       if (quarter == 0 && lane < HPT && my < heads) {
         if (!whole) a.stat[part * GP + my] = make_float2(ref, sum);
@@ -1175,9 +1199,9 @@ __device__ __forceinline__ JoinWork join_work(const Args& a, const int16_t* owne
   w.j0 = owners[owner];
   w.h = h;
   const int2 own = a.owner[w.j0];
-  const uint32_t item = own.x - 1, k = item / a.blocks, blk = item - k * a.blocks;
-  w.b = k / a.kv;
-  const int kvh = k - w.b * a.kv, h0 = blk * a.block_heads;
+  const uint32_t item = own.x - 1, sub = item / a.B, kvh = sub / a.blocks;
+  w.b = item - sub * a.B;
+  const int h0 = (sub - kvh * a.blocks) * a.block_heads;
   w.parts = h < min(a.block_heads, a.G - h0) ? own.y - w.j0 + 1 : 0;
   w.head = kvh * a.G + h0 + h;
   return w;
