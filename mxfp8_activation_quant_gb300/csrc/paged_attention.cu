@@ -19,7 +19,7 @@
 //
 // Warps: 0 the rows' loads, 1 and 2 MMAs (scores, outputs), 3 scales, 4-11 softmax (two a TMEM lane quarter, half of the heads each),
 // 12-19 V^T and the outputs (two a
-// quarter; 64 of the tile's tokens each, half of the heads each). Up to 8 heads the softmax takes four warps,
+// quarter; every second panel each, half of the heads each). Up to 8 heads the softmax takes four warps,
 // warp 8 the scales' copies and warp 9 the values' rows.
 //
 // A CTA that holds an item from start to end writes its outputs; the others' normalised parts go to the
@@ -236,6 +236,22 @@ __device__ __forceinline__ uint32_t rest4(uint32_t x01, uint32_t x23, uint32_t c
 __device__ __forceinline__ uint32_t fp16_fields(uint32_t bytes, uint32_t down) {
   return (__viaddmax_s16x2(bytes & 0x00FF00FFu, down, 0) << 2) | (__viaddmax_s16x2((bytes >> 8) & 0x00FF00FFu, down, 0) << 10);
 }
+// Two fp32 at a time.
+__device__ __forceinline__ float2 add2(float a0, float a1, float b0, float b1) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c0, float c1) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\tfma.rn.f32x2 a, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b), "f"(c0), "f"(c1));
+  return r;
+}
+// Bytes of ones where the low four bits are set.
+__device__ __forceinline__ uint32_t byte_mask(uint32_t bits) { return (((bits & 15) * 0x00204081u) & 0x01010101u) * 0xFFu; }
 // ln of sum * 2^ref
 __device__ __forceinline__ float lse_of(float ref, float sum) {
   return sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
@@ -499,10 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int i = 0; i < a.ring; ++i) {
       mbar_init(BAR(ring_full[i]), 1);
-      mbar_init(BAR(ring_empty[i]), shared_kv ? 9 : i < ring_k ? 1 : 8);
+      mbar_init(BAR(ring_empty[i]), shared_kv ? 5 : i < ring_k ? 1 : 4);
     }
 #pragma unroll 1
-    for (int i = 0; i < kMaxSfBufs; ++i) mbar_init(BAR(sf_raw[i]), 33), mbar_init(BAR(sf_full[i]), 1), mbar_init(BAR(sf_empty[i]), 9 + SW);
+    for (int i = 0; i < kMaxSfBufs; ++i) mbar_init(BAR(sf_raw[i]), 33), mbar_init(BAR(sf_full[i]), 1), mbar_init(BAR(sf_empty[i]), 1 + SW + (NP > 1 ? 8 : 4));
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(s_full[i]), 1), mbar_init(BAR(s_empty[i]), SW);
@@ -821,8 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, h0 = (warp - 4) / 4 * SH, st = tid - 128;
     const int hl = h0 + (st & 127), half_bar = 1 + (warp - 4) / 4;  // the warps of the same heads agree among themselves
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    // (a scale of zero becomes the smallest normal number: low times c has to be -infinity, which takes no part)
-    const float c0 = a.scale * 1.4426950408889634f, c = c0 == 0.f ? 1.1754944e-38f : c0, low = c < 0.f ? INFINITY : -INFINITY;
+    const float c = a.scale * 1.4426950408889634f;
     const int t = 32 * quarter + lane;
     // the row of P of this thread's token: tokens 4 j + i of 16 are rows 2 j + i (i < 2) and 6 + 2 j + i
     const int prow = (t & ~15) + ((t >> 2) & 3) * 2 + (t & 1) + ((t & 2) << 2);
@@ -840,21 +855,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_barrier(half_bar, 128);
       bool last, started = false;
       do {
-        float x[SH];
-        wait_bar(m, BAR(s_full[s.slot]), s.phase);
+        wait_bar(m, BAR(s_full[0]) + 8 * s.slot, s.phase);
         tc_fence_after();
         const uint32_t sc = t_lane + kColS + s.slot * 2 * GP + h0;
-#pragma unroll
-        for (int j = 0; j < SH; j += 16) {
-          constexpr int n = SH < 16 ? 8 : 16;
-          uint32_t hi[n], lo[n];
-          if constexpr (n == 8) tmem_ld_x8(sc + j, hi), tmem_ld_x8(sc + GP + j, lo);
-          else tmem_ld_x16(sc + j, hi), tmem_ld_x16(sc + GP + j, lo);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < n; ++k) x[j + k] = __uint_as_float(hi[k]) + __uint_as_float(lo[k]);
-        }
-        wait_bar(m, BAR(sf_full[sf.slot]), sf.phase);
+        wait_bar(m, BAR(sf_full[0]) + 8 * sf.slot, sf.phase);
         const TileInfo* const info = reinterpret_cast<const TileInfo*>(smem + lay.sf + sf.slot * sf_bytes + NP * 1024);
         const bool valid = (info->valid[quarter] >> lane) & 1;
         const int32_t new_pivot = info->pivot;
@@ -864,36 +868,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(sf_empty[0]) + 8 * sf.slot);
         sf.next();
-        if (!__all_sync(0xffffffffu, valid)) {  // (what takes no part may be NaN)
-#pragma unroll
-          for (int j = 0; j < SH; ++j) x[j] = valid ? x[j] : low;
-        }
-        // Whether a score passes its reference by too much. A segment's first tile always sets the references, from S
-        // itself in a short loop; later S is given back before the question, for the next scores to be made meanwhile.
-        bool move = true;
-        if (started) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(s_empty[0]) + 8 * s.slot);
-          float over = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < SH; j += 4) {
-            const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j]);  // (minus the references)
-            over = fmaxf(over, fmaxf(fmaf(x[j], c, r.x), fmaf(x[j + 1], c, r.y)));
-            over = fmaxf(over, fmaxf(fmaf(x[j + 2], c, r.z), fmaf(x[j + 3], c, r.w)));
-          }
-          move = named_barrier_or(half_bar, 128, over > kSlack || new_pivot != pivot);
-        }
-        if (move) {
-          // new references: the largest scores so far; lane k keeps head j + k's
-          if (!started) {
+        // The probabilities with the references so far; where a score passes its reference by too much (a segment's first
+        // tile: they all do), or the pivot moves, the references move first, and S is read again.
+        float e[SH];
+        bool move = !started;
+        while (true) {
+          if (move) {
 #pragma unroll 1
             for (int j = 0; j < SH; j += 8) {
               uint32_t hi[8], lo[8];
               tmem_ld_x8(sc + j, hi);
               tmem_ld_x8(sc + GP + j, lo);
               tmem_ld_wait();
-              int32_t mine = kNoScore;
+              int32_t mine = kNoScore;  // lane k: the largest score of head j + k
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered((__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c) : kNoScore);
@@ -901,70 +888,88 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (lane < 8) atomicMax(&m.red[h0 + j + lane], mine);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(s_empty[0]) + 8 * s.slot);
-          } else {
-            int32_t mine = kNoScore;
-#pragma unroll
-            for (int k = 0; k < SH; ++k) {
-              const int32_t top = __reduce_max_sync(0xffffffffu, ordered(x[k] * c));
-              mine = lane == k ? top : mine;
+            named_barrier(half_bar, 128);
+            if ((st & 127) < SH) {
+              const float old = -m.ref[hl], now = fmaxf(old, fmaxf(kLowRef, of_ordered(m.red[hl])));
+              m.ref[hl] = -now;
+              m.fac[hl] = ex2(old - now);
+              m.red[hl] = kNoScore;
             }
-            if (lane < SH) atomicMax(&m.red[h0 + lane], mine);
-          }
-          named_barrier(half_bar, 128);
-          if ((st & 127) < SH) {
-            const float old = -m.ref[hl], now = fmaxf(old, fmaxf(kLowRef, of_ordered(m.red[hl])));
-            m.ref[hl] = -now;
-            m.fac[hl] = ex2(old - now);
-            m.red[hl] = kNoScore;
-          }
-          named_barrier(half_bar, 128);
-          if (started) {
+            named_barrier(half_bar, 128);
+            if (started) {
 #pragma unroll
-            for (int j = 0; j < SH; j += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&m.fac[h0 + j]);
-              l[j] *= f.x, l[j + 1] *= f.y, l[j + 2] *= f.z, l[j + 3] *= f.w;
-            }
-            // every product so far is in O, and the next waits for P
-            const int prev = pr.slot == 0 ? a.p_bufs - 1 : pr.slot - 1;
-            wait_bar(m, BAR(p_empty[0]) + 8 * prev, pr.slot == 0 ? pr.phase ^ 1 : pr.phase);
-            tc_fence_after();
-            const int down = pivot - new_pivot;  // <= 0
-            const float pf = down < -126 ? 0.f : __uint_as_float((127 + down) << 23);
+              for (int j = 0; j < SH; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&m.fac[h0 + j]);
+                l[j] *= f.x, l[j + 1] *= f.y, l[j + 2] *= f.z, l[j + 3] *= f.w;
+              }
+              // every product so far is in O, and the next waits for P
+              const int prev = pr.slot == 0 ? a.p_bufs - 1 : pr.slot - 1;
+              wait_bar(m, BAR(p_empty[0]) + 8 * prev, pr.slot == 0 ? pr.phase ^ 1 : pr.phase);
+              tc_fence_after();
+              const int down = pivot - new_pivot;  // <= 0
+              const float pf = down < -126 ? 0.f : __uint_as_float((127 + down) << 23);
 #pragma unroll 1
-            for (int q = 0; q < NP * (SH / 8); ++q) {
-              const int j = q % (SH / 8) * 8;
-              const uint32_t col = t_lane + q / (SH / 8) * GO + h0 + j;
-              uint32_t r[8];
-              tmem_ld_x8(col, r);
-              tmem_ld_wait();
+              for (int q = 0; q < NP * (SH / 8); ++q) {
+                const int j = q % (SH / 8) * 8;
+                const uint32_t col = t_lane + q / (SH / 8) * GO + h0 + j;
+                uint32_t r[8];
+                tmem_ld_x8(col, r);
+                tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * m.fac[h0 + j + k] * pf);
-              tmem_st_x8(col, r);
+                for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * m.fac[h0 + j + k] * pf);
+                tmem_st_x8(col, r);
+              }
+              tmem_st_wait();
             }
-            tmem_st_wait();
+            pivot = new_pivot;
           }
-          pivot = new_pivot;
+          constexpr int n = SH < 16 ? 8 : 16;
+#pragma unroll
+          for (int j = 0; j < SH; j += n) {
+            uint32_t hi[n], lo[n];
+            if constexpr (n == 8) tmem_ld_x8(sc + j, hi), tmem_ld_x8(sc + GP + j, lo);
+            else tmem_ld_x16(sc + j, hi), tmem_ld_x16(sc + GP + j, lo);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < n; k += 4) {
+              const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j + k]);  // (minus the references)
+              const float2 x0 = add2(__uint_as_float(hi[k]), __uint_as_float(hi[k + 1]), __uint_as_float(lo[k]), __uint_as_float(lo[k + 1]));
+              const float2 x1 = add2(__uint_as_float(hi[k + 2]), __uint_as_float(hi[k + 3]), __uint_as_float(lo[k + 2]), __uint_as_float(lo[k + 3]));
+              const float2 d0 = fma2(x0, c, r.x, r.y), d1 = fma2(x1, c, r.z, r.w);
+              e[j + k] = d0.x, e[j + k + 1] = d0.y, e[j + k + 2] = d1.x, e[j + k + 3] = d1.y;
+            }
+          }
+          if (!__all_sync(0xffffffffu, valid)) {  // (what takes no part may be NaN)
+#pragma unroll
+            for (int j = 0; j < SH; ++j) e[j] = valid ? e[j] : -INFINITY;
+          }
+          float over = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < SH; j += 2) over = fmaxf(over, fmaxf(e[j], e[j + 1]));
+#pragma unroll
+          for (int j = 0; j < SH; ++j) e[j] = ex2(e[j]);
+          if (move) break;
+          move = named_barrier_or(half_bar, 128, over > kSlack || new_pivot != pivot);
+          if (!move) break;
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(s_empty[0]) + 8 * s.slot);
         s.next();
-        wait_bar(m, BAR(p_empty[pr.slot]), pr.phase ^ 1);
+        wait_bar(m, BAR(p_empty[0]) + 8 * pr.slot, pr.phase ^ 1);
         uint8_t* const row = smem + lay.p + pr.slot * kPanel + prow * 128;
 #pragma unroll
         for (int j = 0; j < SH; j += 8) {
-          float e[8];
-          const float4 r0 = *reinterpret_cast<const float4*>(&m.ref[h0 + j]), r1 = *reinterpret_cast<const float4*>(&m.ref[h0 + j + 4]);
-          const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            e[k] = ex2(fmaf(x[j + k], c, r[k]));
-            l[j + k] += e[k];
-          }
+          const float* const f = e + j;
           uint4 v;
-          if (wide) v = make_uint4(bf16x2_rn(e[0], e[1]), bf16x2_rn(e[2], e[3]), bf16x2_rn(e[4], e[5]), bf16x2_rn(e[6], e[7]));
-          else v = make_uint4(f16x2_rn(e[0], e[1]), f16x2_rn(e[2], e[3]), f16x2_rn(e[4], e[5]), f16x2_rn(e[6], e[7]));
+          if (wide) v = make_uint4(bf16x2_rn(f[0], f[1]), bf16x2_rn(f[2], f[3]), bf16x2_rn(f[4], f[5]), bf16x2_rn(f[6], f[7]));
+          else v = make_uint4(f16x2_rn(f[0], f[1]), f16x2_rn(f[2], f[3]), f16x2_rn(f[4], f[5]), f16x2_rn(f[6], f[7]));
           *reinterpret_cast<uint4*>(row + ((((h0 + j) >> 3) ^ (prow & 7)) << 4)) = v;
+        }
+#pragma unroll
+        for (int j = 0; j < SH; j += 2) {
+          const float2 t2 = add2(l[j], l[j + 1], e[j], e[j + 1]);
+          l[j] = t2.x, l[j + 1] = t2.y;
         }
         if (st == 0) m.p_wide[pr.slot] = wide;
         fence_proxy_async_smem();
@@ -993,7 +998,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segments seg(a, m);
     Ring rv(ring_v), sf(a.sf_bufs), fin(2), o_ring(1);
     const int slot0 = shared_kv ? 0 : ring_k;
-    uint32_t chunk = 0;
+    int v_slot = 0, turn = 0;  // of the next panel's first chunk; whose the panel is
+    uint32_t v_phase = 0;
     const uint32_t pick = static_cast<uint32_t>(quarter) * 0x1010u | 0x4000u;  // a byte of each word, to bytes 1 and 3 (0 and 2 are masked)
     int2 owner = make_int2(0, 0);
 #pragma unroll 1
@@ -1002,96 +1008,104 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
         const int halves = seg.tokens(i) > 64 ? 2 : 1;
-        wait_bar(m, BAR(sf_full[sf.slot]), sf.phase);
-        const uint8_t* const buf = smem + lay.sf + sf.slot * sf_bytes;
-        const TileInfo* const info = reinterpret_cast<const TileInfo*>(buf + NP * 1024);
-        const bool wide = (info->flags & kWide) != 0;
-        const int32_t pivot = info->pivot;
-        const uint32_t valid0 = info->valid[2 * set], valid1 = info->valid[2 * set + 1];
-        const bool full = (valid0 & valid1) == 0xFFFFFFFFu;
+        if (NP > 1 || turn == set) {
+          wait_bar(m, BAR(sf_full[0]) + 8 * sf.slot, sf.phase);
+          const uint8_t* const buf = smem + lay.sf + sf.slot * sf_bytes;
+          const TileInfo* const info = reinterpret_cast<const TileInfo*>(buf + NP * 1024);
+          const bool wide = (info->flags & kWide) != 0;
+          const int32_t pivot = info->pivot;
+          // the scale bytes of four tokens a lane; the rows of its 16 tokens
+          const uint8_t* const tab0 = buf + NP * 512 + 16 * (lane & 3);
+          const uint32_t row_at = sbase + lay.ring + (lane & 15) * 128 + (((2 * quarter + (lane >> 4)) ^ (lane & 7)) << 4);
 #pragma unroll 1
-        for (int p = 0; p < NP; ++p) {
-          const int s = slot0 + rv.slot;
-          wait_bar(m, BAR(ring_full[s]), rv.phase);
-          if (set < halves) {
-            const uint32_t ci = chunk + p * halves + set, use = ci / kVSlots, vs = ci - use * kVSlots, vphase = use & 1;
-            const uint32_t panel = sbase + lay.ring + s * kPanel;
-            // the scale bytes of four tokens a lane
-            const uint8_t* const tab = buf + NP * 512 + (p * 128 + 64 * set + 4 * (lane & 3)) * 4;
-            const int t = 64 * set + (lane & 15), c16 = 2 * quarter + (lane >> 4);
-            const uint32_t rows = panel + t * 128 + ((c16 ^ (t & 7)) << 4);
-            const uint32_t dst = t_lane + kColV + 32 * vs;
-            if (!wide) {
-              uint32_t r[4][4];
-              uint4 sw[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                ldmatrix_b8_trans_x2(rows + k * 2048, r[k]);
-                sw[k] = *reinterpret_cast<const uint4*>(tab + k * 64);
-              }
-              if (!full) {  // tokens that take no part may be NaN
+          for (int p = 0; p < NP; ++p) {
+            const int s = slot0 + rv.slot;
+            int vs = v_slot;
+            uint32_t vphase = v_phase;
+            rv.next();
+            v_slot += halves;
+            if (v_slot >= kVSlots) v_slot -= kVSlots, v_phase ^= 1;
+            turn ^= 1;
+            if (turn == set) continue;  // (it was the other's)
+            wait_bar(m, BAR(ring_full[0]) + 8 * s, rv.slot == 0 ? rv.phase ^ 1 : rv.phase);
+#pragma unroll 1
+            for (int h = 0; h < halves; ++h) {
+              const uint32_t rows = row_at + s * kPanel + h * 8192, dst = t_lane + kColV + 32 * vs;
+              const uint8_t* const tab = tab0 + p * 512 + h * 256;
+              const uint32_t valid0 = info->valid[2 * h], valid1 = info->valid[2 * h + 1];
+              if (!wide) {
+                uint32_t r[4][4];
+                uint4 sw[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const uint32_t bits = ((k < 2 ? valid0 : valid1) >> (16 * (k & 1) + 4 * (lane & 3))) & 15;
-                  const uint32_t mask = ((bits * 0x00204081u) & 0x01010101u) * 0xFFu;
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) r[k][j] &= mask;
+                  ldmatrix_b8_trans_x2(rows + k * 2048, r[k]);
+                  sw[k] = *reinterpret_cast<const uint4*>(tab + k * 64);
                 }
-              }
-              uint32_t w0[16], w1[16];  // features 0-15 and 16-31 of the quarter's 32
+                if ((valid0 & valid1) != 0xFFFFFFFFu) {  // tokens that take no part may be NaN
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                // this quarter's group: each byte to the top of an fp16
-                const uint32_t s01 = __byte_perm(sw[k].x, sw[k].y, pick) & 0xFF00FF00u, s23 = __byte_perm(sw[k].z, sw[k].w, pick) & 0xFF00FF00u;
-                uint32_t lo[4], hi[4];
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t mask = byte_mask((k < 2 ? valid0 : valid1) >> (16 * (k & 1) + 4 * (lane & 3)));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  e4m3x4_f16(r[k][j], lo[j], hi[j]);
-                  lo[j] = hmul2(lo[j], s01), hi[j] = hmul2(hi[j], s23);
+                    for (int j = 0; j < 4; ++j) r[k][j] &= mask;
+                  }
                 }
-                w0[4 * k] = lo[0], w0[4 * k + 1] = lo[1], w0[4 * k + 2] = hi[0], w0[4 * k + 3] = hi[1];
-                w1[4 * k] = lo[2], w1[4 * k + 1] = lo[3], w1[4 * k + 2] = hi[2], w1[4 * k + 3] = hi[3];
-              }
-              wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
-              tc_fence_after();
-              tmem_st_16x128b_x8(dst, w0);
-              tmem_st_16x128b_x8(dst + (16u << 16), w1);
-            } else {  // the scales span more than fp16 holds: bf16
-              wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
-              tc_fence_after();
+                uint32_t w0[16], w1[16];  // features 0-15 and 16-31 of the quarter's 32
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  // this quarter's group: each byte to the top of an fp16
+                  const uint32_t s01 = __byte_perm(sw[k].x, sw[k].y, pick) & 0xFF00FF00u, s23 = __byte_perm(sw[k].z, sw[k].w, pick) & 0xFF00FF00u;
+                  uint32_t lo[4], hi[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    e4m3x4_f16(r[k][j], lo[j], hi[j]);
+                    lo[j] = hmul2(lo[j], s01), hi[j] = hmul2(hi[j], s23);
+                  }
+                  w0[4 * k] = lo[0], w0[4 * k + 1] = lo[1], w0[4 * k + 2] = hi[0], w0[4 * k + 3] = hi[1];
+                  w1[4 * k] = lo[2], w1[4 * k + 1] = lo[3], w1[4 * k + 2] = hi[2], w1[4 * k + 3] = hi[3];
+                }
+                wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
+                tc_fence_after();
+                tmem_st_16x128b_x8(dst, w0);
+                tmem_st_16x128b_x8(dst + (16u << 16), w1);
+              } else {  // the scales span more than fp16 holds: bf16
+                wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
+                tc_fence_after();
 #pragma unroll 1
-              for (int k = 0; k < 4; ++k) {
-                uint32_t r[4];
-                ldmatrix_b8_trans_x2(rows + k * 2048, r);
-                const uint4 sw = *reinterpret_cast<const uint4*>(tab + k * 64);
-                const uint32_t bits = ((k < 2 ? valid0 : valid1) >> (16 * (k & 1) + 4 * (lane & 3))) & 15;
-                const uint32_t mask = ((bits * 0x00204081u) & 0x01010101u) * 0xFFu;
-                const float f0 = pow2_of(((sw.x >> (8 * quarter)) & 0xFF) - pivot), f1 = pow2_of(((sw.y >> (8 * quarter)) & 0xFF) - pivot),
-                            f2 = pow2_of(((sw.z >> (8 * quarter)) & 0xFF) - pivot), f3 = pow2_of(((sw.w >> (8 * quarter)) & 0xFF) - pivot);
-                uint32_t lo[4], hi[4];
+                for (int k = 0; k < 4; ++k) {
+                  uint32_t r[4];
+                  ldmatrix_b8_trans_x2(rows + k * 2048, r);
+                  const uint4 sw = *reinterpret_cast<const uint4*>(tab + k * 64);
+                  const uint32_t mask = byte_mask((k < 2 ? valid0 : valid1) >> (16 * (k & 1) + 4 * (lane & 3)));
+                  const float f0 = pow2_of(((sw.x >> (8 * quarter)) & 0xFF) - pivot), f1 = pow2_of(((sw.y >> (8 * quarter)) & 0xFF) - pivot),
+                              f2 = pow2_of(((sw.z >> (8 * quarter)) & 0xFF) - pivot), f3 = pow2_of(((sw.w >> (8 * quarter)) & 0xFF) - pivot);
+                  uint32_t lo[4], hi[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  e4m3x4_f16(r[j] & mask, lo[j], hi[j]);
-                  const float2 fl = f16x2_f32(lo[j]), fh = f16x2_f32(hi[j]);
-                  lo[j] = bf16x2_rn(fl.x * f0, fl.y * f1);
-                  hi[j] = bf16x2_rn(fh.x * f2, fh.y * f3);
+                  for (int j = 0; j < 4; ++j) {
+                    e4m3x4_f16(r[j] & mask, lo[j], hi[j]);
+                    const float2 fl = f16x2_f32(lo[j]), fh = f16x2_f32(hi[j]);
+                    lo[j] = bf16x2_rn(fl.x * f0, fl.y * f1);
+                    hi[j] = bf16x2_rn(fh.x * f2, fh.y * f3);
+                  }
+                  tmem_st_16x128b_x2(dst + 8 * k, lo[0], lo[1], hi[0], hi[1]);
+                  tmem_st_16x128b_x2(dst + (16u << 16) + 8 * k, lo[2], lo[3], hi[2], hi[3]);
                 }
-                tmem_st_16x128b_x2(dst + 8 * k, lo[0], lo[1], hi[0], hi[1]);
-                tmem_st_16x128b_x2(dst + (16u << 16) + 8 * k, lo[2], lo[3], hi[2], hi[3]);
               }
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(BAR(v_full[0]) + 8 * vs);
+              if (++vs == kVSlots) vs = 0, vphase ^= 1;
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(v_full[0]) + 8 * vs);
+            if (lane == 0) mbar_arrive(BAR(ring_empty[0]) + 8 * s);  // (after the warp's last barrier)
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(ring_empty[s]));
+          if (lane == 0) mbar_arrive(BAR(sf_empty[0]) + 8 * sf.slot);
+        } else {
+          turn ^= 1;
           rv.next();
+          v_slot += halves;
+          if (v_slot >= kVSlots) v_slot -= kVSlots, v_phase ^= 1;
         }
-        chunk += NP * halves;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(sf_empty[sf.slot]));
         sf.next();
       }
       // outputs: this thread's feature 128 p + 32 quarter + lane of its heads
