@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmxq.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm_mxf8.cu", "noalloc.cu", "tma_maps.cu", "moe_api.cu", "add_rmsnorm.cu",
-           "moe_route.cu", "moe_experts.cu", "kv_api.cu", "kv_cache.cu", "paged_attention.cu"]
+           "moe_route.cu", "moe_experts.cu", "kv_api.cu", "kv_cache.cu", "paged_attention.cu",
+           "paged_attention_g8.cu", "paged_attention_g16.cu", "paged_attention_g32.cu", "paged_attention_g64.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          f"-I{INCLUDE}", f"-I{CSRC}"]
