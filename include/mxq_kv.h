@@ -26,7 +26,7 @@ extern "C" {
  * sf + p * sf_page_stride + r * sf_token_stride + h * sf_head_stride (all in bytes), so both orders of
  * tokens and heads within a page can be had, and pages with other data between them. Rows of data start
  * on 16-byte boundaries; rows of scales on 4-byte boundaries where dim % 128 == 0, at strides below 2^31. Rows
- * must not overlap.
+ * must not overlap (strides, taken from the smallest up, each at least the span of those below it).
  * Slot s is place s % page_size of page s / page_size.
  * dim % 32 == 0, 32 <= dim <= 1024, heads <= 1024, page_size <= 65536, pages * page_size < 2^31.
  */
@@ -85,7 +85,8 @@ MXQ_API mxq_status kv_read_bf16(const mxq_kv_cache* k_cache, const mxq_kv_cache*
  *
  * len_b = min(seq_lens[b], table_width * page_size); tokens on a page outside [0, pages) take no part. A
  * sequence without a token gives zeros and lse -inf. What the cache holds behind a sequence's end is not used,
- * NaN included.
+ * NaN included. NaN among a sequence's tokens reaches its own outputs only; that of a value's scale (byte 255) all
+ * features of its cache head's.
  *
  *   q_bf16   [B, q_heads, dim] bf16, row strides ldq (sequences) and ldqh (heads) in elements.
  *   v_cache  of k_cache's shape (strides may differ), or NULL.
@@ -97,8 +98,9 @@ MXQ_API mxq_status kv_read_bf16(const mxq_kv_cache* k_cache, const mxq_kv_cache*
  *            clearing; calls that overlap in time need separate workspaces.
  *   status: optional device status word (mxq_status_bytes()).
  * At least one of o_bf16 and o_q. Requires dim in {128, 256, 384, 512}, page_size % 16 == 0, q_heads a multiple
- * of heads, q_heads <= 4096, 1 <= B <= 65536 / heads, table_width >= 1, table_width * page_size <= 2^30, a finite
- * scale. Three launches; the results do not depend on timing.
+ * of heads, q_heads <= 4096, 1 <= B <= 65536 / heads, table_width >= 1, table_width * page_size <= 2^30,
+ * |scale| <= 1e38, and fewer than 2^30 pieces of 64 tokens: B * heads * ceil(q_heads / heads / 64) * ceil(table_width *
+ * page_size / 64). o_bf16 may be q_bf16. Three launches; the results do not depend on timing.
  */
 MXQ_API int64_t mxq_paged_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim);
 

@@ -155,7 +155,7 @@ mxq_status paged_attention_mxfp8(const void* q_bf16, int64_t ldq, int64_t ldqh, 
   if (q_bf16 == nullptr || seq_lens_i32 == nullptr || workspace == nullptr) return MXQ_ERR_INVALID_ARG;
   const bool scales = o_sf_packed_i32 != nullptr || o_sf_rowmajor != nullptr || o_sf_128x4 != nullptr;
   if ((o_bf16 == nullptr && o_q == nullptr) || (o_q != nullptr) != scales) return MXQ_ERR_INVALID_ARG;
-  if (B <= 0 || q_heads <= 0 || !(scale - scale == 0.0f)) return MXQ_ERR_INVALID_ARG;
+  if (B <= 0 || q_heads <= 0 || !(scale >= -1e38f && scale <= 1e38f)) return MXQ_ERR_INVALID_ARG;  // (times log2(e) it is finite too)
   mxq_kv_cache k, v;
   mxq_status st = check_cache(k_cache, &k);
   if (st != MXQ_OK) return st;
@@ -166,7 +166,9 @@ mxq_status paged_attention_mxfp8(const void* q_bf16, int64_t ldq, int64_t ldqh, 
   }
   if (!attention_shape_ok(B, q_heads, k.heads, k.dim) || k.page_size % 16 != 0) return MXQ_ERR_UNSUPPORTED_SHAPE;
   if ((st = check_table(block_table_i32, &ld_table, table_width, B)) != MXQ_OK) return st;
-  if (static_cast<int64_t>(table_width) * k.page_size > (int64_t(1) << 30)) return MXQ_ERR_UNSUPPORTED_SHAPE;
+  const int64_t places = static_cast<int64_t>(table_width) * k.page_size;
+  if (places > (int64_t(1) << 30) || mxq::paged_attention_units(B, q_heads, k.heads, places) >= (int64_t(1) << 30))
+    return MXQ_ERR_UNSUPPORTED_SHAPE;
   if (q_heads == 1) ldqh = k.dim;
   if (B == 1) ldq = static_cast<int64_t>(q_heads) * ldqh;
   if (ldqh < k.dim || ldq < k.dim || ldq >= kMaxStride || ldqh >= kMaxStride) return MXQ_ERR_UNSUPPORTED_SHAPE;

@@ -58,6 +58,8 @@ struct PagedAttentionLaunch {
   int32_t* status;
 };
 cudaError_t launch_paged_attention(const PagedAttentionLaunch& a, cudaStream_t stream);
+// Pieces of work, of 64 tokens, at tables of `places` tokens.
+int64_t paged_attention_units(int64_t B, int32_t q_heads, int32_t kv_heads, int64_t places);
 int64_t paged_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim);
 
 }  // namespace mxq

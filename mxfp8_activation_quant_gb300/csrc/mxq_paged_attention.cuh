@@ -44,7 +44,7 @@ constexpr int kTile = 128;        // tokens of a tile
 constexpr int kThreads = 640;  // (five warps a scheduler leave each thread 96 registers; a sixth anywhere, 80)
 constexpr int kPanel = 128 * 128; // bytes of 128 features of a tile
 constexpr int kMaxHeads = 64;     // query heads of an item
-constexpr float kLowRef = -1e30f; // ref before the first token
+constexpr float kLowRef = -3.4028235e38f;  // ref before the first token: the lowest finite number, so that every score is above
 constexpr float kSlack = 8.0f;
 constexpr int32_t kNoScore = static_cast<int32_t>(0x807FFFFFu);  // ordered(-infinity)
 
@@ -242,21 +242,22 @@ __device__ __forceinline__ float2 add2(float a0, float a1, float b0, float b1) {
       : "=f"(r.x), "=f"(r.y) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
   return r;
 }
-__device__ __forceinline__ float2 fma2(float2 a, float b, float c0, float c1) {
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
   float2 r;
-  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\tfma.rn.f32x2 a, a, b, c;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b), "f"(c0), "f"(c1));
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b));
   return r;
 }
 // Bytes of ones where the low four bits are set.
 __device__ __forceinline__ uint32_t byte_mask(uint32_t bits) { return (((bits & 15) * 0x00204081u) & 0x01010101u) * 0xFFu; }
 // ln of sum * 2^ref
 __device__ __forceinline__ float lse_of(float ref, float sum) {
-  return sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  return sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;  // (NaN stays NaN)
 }
-// 2^(b - 127) as fp32, b in [0, 254].
-__device__ __forceinline__ float pow2_byte(uint32_t b) { return __uint_as_float(b == 0 ? 0x00400000u : b << 23); }
+// 2^(b - 127) as fp32; byte 255 is NaN.
+__device__ __forceinline__ float pow2_byte(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
+}
 // 2^e as fp32, e <= 127 (0 below the smallest subnormal).
 __device__ __forceinline__ float pow2_of(int32_t e) {
   return __uint_as_float(e >= -126 ? static_cast<uint32_t>(e + 127) << 23 : e >= -149 ? 0x400000u >> (-127 - e) : 0u);
@@ -297,8 +298,8 @@ __device__ __forceinline__ int32_t units_of(int32_t len) { return len <= 0 ? 1 :
 
 // Walks a CTA's segments: runs of units of one item. An item is (cache head, block of query heads, sequence), in that
 // order: CTAs that work at the same time then read the heads of the same tokens, which lie side by side, and
-// blocks of heads that share a cache head find it in L2 (128 sequences x 8 heads of 128, tokens before heads: 153 -> XX us
-// against sequences first).
+// blocks of heads that share a cache head find it in L2 (128 sequences x 8 heads of 128, tokens before heads: 132 us;
+// with the sequences outermost, 150).
 struct Segments {
   const Args& a;
   int32_t left, next_len, b, k, blk_, u, len, units;
@@ -981,9 +982,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < n; k += 4) {
               const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j + k]);  // (minus the references)
-              const float2 x0 = add2(__uint_as_float(hi[k]), __uint_as_float(hi[k + 1]), __uint_as_float(lo[k]), __uint_as_float(lo[k + 1]));
-              const float2 x1 = add2(__uint_as_float(hi[k + 2]), __uint_as_float(hi[k + 3]), __uint_as_float(lo[k + 2]), __uint_as_float(lo[k + 3]));
-              const float2 d0 = fma2(x0, c, r.x, r.y), d1 = fma2(x1, c, r.z, r.w);
+              // (scaled as the references were, with a rounding of its own, so that the largest score's difference is 0
+              // however large it is)
+              const float2 x0 = mul2(add2(__uint_as_float(hi[k]), __uint_as_float(hi[k + 1]), __uint_as_float(lo[k]), __uint_as_float(lo[k + 1])), c);
+              const float2 x1 = mul2(add2(__uint_as_float(hi[k + 2]), __uint_as_float(hi[k + 3]), __uint_as_float(lo[k + 2]), __uint_as_float(lo[k + 3])), c);
+              const float2 d0 = add2(x0.x, x0.y, r.x, r.y), d1 = add2(x1.x, x1.y, r.z, r.w);
               e[j + k] = d0.x, e[j + k + 1] = d0.y, e[j + k + 2] = d1.x, e[j + k + 3] = d1.y;
             }
           }

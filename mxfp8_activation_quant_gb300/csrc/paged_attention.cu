@@ -251,6 +251,11 @@ int64_t paged_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_h
   return space_of(B, q_heads, kv_heads, dim).total;
 }
 
+int64_t paged_attention_units(int64_t B, int32_t q_heads, int32_t kv_heads, int64_t places) {
+  const int G = q_heads / kv_heads;
+  return B * kv_heads * ((G + kMaxHeads - 1) / kMaxHeads) * ((places + kUnit - 1) / kUnit);
+}
+
 cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t stream) {
   const mxq_kv_cache& k = *l.k;
   Args a{};
@@ -302,9 +307,8 @@ cudaError_t launch_paged_attention(const PagedAttentionLaunch& l, cudaStream_t s
   };
   a.sf_vec = std::min(vec_of(k), vec_of(l.v != nullptr ? *l.v : k));
   const Space sp = space_of(l.B, l.q_heads, k.heads, k.dim);
-  const int64_t most = l.B * a.kv * a.blocks * ((static_cast<int64_t>(l.table_width) * k.page_size + kUnit - 1) / kUnit);
-  if (most >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
-  a.ctas = static_cast<int32_t>(std::min(sp.ctas, most));
+  a.ctas = static_cast<int32_t>(
+      std::min(sp.ctas, paged_attention_units(l.B, l.q_heads, k.heads, static_cast<int64_t>(l.table_width) * k.page_size)));
   uint8_t* const ws = static_cast<uint8_t*>(l.workspace);
   a.part = reinterpret_cast<float*>(ws);
   a.stat = reinterpret_cast<float2*>(ws + sp.stat);

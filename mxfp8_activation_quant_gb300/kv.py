@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -133,26 +134,25 @@ def kv_read_bf16(k_cache: MXFP8Cache, block_table: torch.Tensor, cu_rows: torch.
 
 
 _workspaces: dict = {}
+_sharing = threading.Lock()  # held over a call with a kept workspace: two threads may call on one stream
 
 
 def _workspace(size: int, stream) -> Optional[torch.Tensor]:
     """The workspace kept for a stream, grown to `size` bytes where it is smaller; calls ordered on one stream may share
     it. Under capture a call gets one from the graph's own pool, so that no graph depends on what is kept here."""
+    if stream is not None:  # (memory is owned by the stream that uses it)
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(s):
+            return _workspace(size, None)
     if size <= 0:
         return None
-    device = _device()
-    raw = _raw_stream(device) if stream is None else _stream(stream)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(size, dtype=torch.uint8, device="cuda")
-    ws = _workspaces.get((device, raw))
+    device = _device()
+    key = device, _raw_stream(device)
+    ws = _workspaces.get(key)
     if ws is None or ws.nbytes < size:
-        if stream is None:
-            ws = torch.empty(size, dtype=torch.uint8, device="cuda")
-        else:  # owned by the stream that uses it
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-            with torch.cuda.stream(s):
-                ws = torch.empty(size, dtype=torch.uint8, device="cuda")
-        _workspaces[device, raw] = ws
+        ws = _workspaces[key] = torch.empty(size, dtype=torch.uint8, device="cuda")
     return ws
 
 
@@ -191,14 +191,17 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
     if not (q.is_cuda and block_table.is_cuda and seq_lens.is_cuda and q.get_device() == _device()):
         _refuse(q, block_table, seq_lens)
     kc, vc = k_cache.c(), None if v_cache is None else v_cache.c()
+    outs = (None if out is None else _ptr(out), None if out_q is None else _ptr(out_q), None if sf_packed is None else _ptr(sf_packed),
+            None if sf_rowmajor is None else _ptr(sf_rowmajor), None if sf_128x4 is None else _ptr(sf_128x4),
+            None if lse is None else _ptr(lse))
+    args = (q.data_ptr(), ldq, ldqh, kc, vc, block_table.data_ptr(), ldt, width, seq_lens.data_ptr(), B, H, scale, *outs)
+    status_at, raw = None if status is None else _ptr(status), _raw_stream(_device()) if stream is None else _stream(stream)
     if workspace is None:
-        workspace = _workspace(lib.mxq_paged_attention_workspace_bytes(B, H, shape[2], D), stream)
-    code = lib.paged_attention_mxfp8(
-        q.data_ptr(), ldq, ldqh, kc, vc, block_table.data_ptr(), ldt, width, seq_lens.data_ptr(), B, H, scale,
-        None if out is None else _ptr(out), None if out_q is None else _ptr(out_q), None if sf_packed is None else _ptr(sf_packed),
-        None if sf_rowmajor is None else _ptr(sf_rowmajor), None if sf_128x4 is None else _ptr(sf_128x4),
-        None if lse is None else _ptr(lse), None if workspace is None else _ptr(workspace),
-        0 if workspace is None else workspace.nbytes, None if status is None else _ptr(status),
-        _raw_stream(_device()) if stream is None else _stream(stream))
+        with _sharing:
+            ws = _workspace(lib.mxq_paged_attention_workspace_bytes(B, H, shape[2], D), stream)
+            code = lib.paged_attention_mxfp8(*args, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
+                                             status_at, raw)
+    else:
+        code = lib.paged_attention_mxfp8(*args, _ptr(workspace), workspace.nbytes, status_at, raw)
     if code:
         _check(code, "paged_attention_mxfp8")

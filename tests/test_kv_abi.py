@@ -168,3 +168,18 @@ def test_host_tensors_and_wrong_types_are_refused(lib):
         with pytest.raises(AssertionError):
             kv.paged_attention_mxfp8(q, c, table, lens, 0.1, out_q=torch.zeros(3, 2048, dtype=torch.uint8),
                                      **{name: torch.zeros(n - 4, dtype=torch.uint8)})
+
+
+def test_limits_of_lengths_strides_and_scale(lib):
+    c = cache()
+    assert attend(lib, c, B=1, width=2 ** 24 + 1, ldt=2 ** 25) == 2          # 2^30 + 64 places
+    wide = cache(pages=2 ** 20, page_size=16)
+    # pieces of 64 tokens: 512 sequences x 2 cache heads x 2^20 = 2^30; one sequence less passes (wsn = 0 then ends the call)
+    assert attend(lib, wide, B=512, width=2 ** 22, ldt=2 ** 22) == 2
+    assert attend(lib, wide, B=511, width=2 ** 22, ldt=2 ** 22, wsn=0) == 1
+    # and blocks of 64 query heads count: 65 a cache head are two
+    assert attend(lib, wide, B=256, H=130, ldq=130 * D, width=2 ** 22, ldt=2 ** 22) == 2
+    for s in (2e38, -2e38):
+        assert attend(lib, c, scale=s) == 1
+    assert attend(lib, c, scale=-1e38, wsn=0) == 1 and attend(lib, c, scale=1e38, lse=FAKE + 2) == 3
+    assert attend(lib, cache(sf_page_stride=2 ** 31)) == 2 and write(lib, cache(sf_page_stride=2 ** 31)) == 2
