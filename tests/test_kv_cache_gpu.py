@@ -189,3 +189,25 @@ def test_captured(mxq):
         starts.copy_(slots % 16)
         graph.replay()
         assert torch.equal(out, values(*quantized(mxq, x)).float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("T,heads,dim,two", [(32769, 1, 512, False), (16387, 5, 160, True), (33000, 1, 32, True)])
+def test_many_tokens(mxq, T, heads, dim, two):
+    """So many that a warp writes four: the last group is not full, some are not written, values of another width."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    pages = -(-T // 16) + 2
+    slots = torch.randperm(pages * 16, generator=g, device="cuda")[:T].to(torch.int32)
+    slots[torch.rand(T, generator=g, device="cuda") < 0.2] = -1
+    slots[T - 3:] = torch.tensor([-1, pages * 16, -(2 ** 31)], dtype=torch.int32)
+    pairs = [(rows(g, T, heads, dim), empty_cache(pages, 16, heads, dim))]
+    if two:
+        pairs.append((rows(g, T, 2, 64), empty_cache(pages, 16, 2, 64)))
+    caches = [mxq.MXFP8Cache(*c) for _, c in pairs]
+    mxq.kv_write_mxfp8(pairs[0][0], slots, caches[0], pairs[1][0] if two else None, caches[1] if two else None)
+    ok = (slots >= 0) & (slots < pages * 16)
+    for x, (q, sf) in pairs:
+        wq, ws = quantized(mxq, x)
+        want, wsf = torch.full_like(q, 0x7F), torch.full_like(sf, 0xFF)
+        want.view(-1, *q.shape[2:])[slots[ok].long()] = wq.view(x.shape)[ok]
+        wsf.view(-1, *sf.shape[2:])[slots[ok].long()] = ws.view(*x.shape[:2], -1)[ok]
+        assert torch.equal(q, want) and torch.equal(sf, wsf)
