@@ -50,10 +50,15 @@ constexpr int32_t kNoScore = static_cast<int32_t>(0x807FFFFFu);  // ordered(-inf
 
 // TMEM columns for GP heads: O from 0, S (one buffer of 64 heads, two of fewer, and as many of K's scales, so that a tile's are
 // not overwritten before its products are done), the queries' scales, and V^T in slots of 64 tokens x 128 features.
+// Of 64 heads the products with lo are added to those with hi in the tensor core (twice the MMAs of half the width, and five slots
+// for V^T instead of three: 64 latent sequences of 16384 x 256, 91.7 -> 84.0 us; of 512 features the same); their scales are rows 64 and on of the
+// queries', two columns further. Fewer heads' would start on an odd column or within one, where no MMA may read scales.
 template <int GP>
 struct Columns {
   static constexpr int kBuffers = GP == 64 ? 1 : 2;
-  static constexpr uint32_t kS = GP == 64 ? 256 : GP == 32 ? 128 : 64, kSfK = kS + (GP < 16 ? 64 : kBuffers * 2 * GP),
+  static constexpr bool kAdd = GP == 64;
+  static constexpr int kSWidth = kAdd ? GP : 2 * GP;
+  static constexpr uint32_t kS = GP == 64 ? 256 : GP == 32 ? 128 : 64, kSfK = kS + (GP < 16 ? 64 : kBuffers * kSWidth),
                             kSfQ = kSfK + 16 * kBuffers, kV = (kSfQ + 16 + 31) / 32 * 32;
   static constexpr int kSlots = (512 - kV) / 32 < 8 ? (512 - kV) / 32 : 8;
 };
@@ -375,6 +380,15 @@ __device__ __forceinline__ bool wait_bar(Misc& m, uint32_t bar, uint32_t parity)
       return false;
     }
   }
+}
+
+// Whether the phase of that parity is over, without a wait: the loops' next phases are tested while this one's work is issued
+// (128 sequences x 8 heads of 128: 130.4 -> 128.4 us; 64 sequences x 64 heads of 512 the same).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r) : "r"(bar), "r"(parity) : "memory");
+  return r != 0;
 }
 
 // Copies of scales, a tile at a time: four tokens a lane (they lie on one page), as they lie in the cache, to where the
@@ -753,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       Segments seg(a, m);
       Ring rk(ring_k), sf(Z::kSfBufs), s(SB), q_ring(1);
-      bool first = true;
+      bool first = true, ready = false;
 #pragma unroll 1
       while (seg.next()) {
         const int tiles = seg.tiles();
@@ -776,20 +790,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bar(m, BAR(s_empty[0]) + 8 * s.slot, s.phase ^ 1);
           tc_fence_after();
           const uint32_t sf_at = sbase + Z::kSf + sf.slot * sf_bytes;
-          const uint32_t d = tmem + kColS + s.slot * 2 * GP, sfk = tmem + kColSfK + 16 * s.slot;
+          const uint32_t d = tmem + kColS + s.slot * Cols::kSWidth, sfk = tmem + kColSfK + 16 * s.slot;
 #pragma unroll 1
           for (int p = 0; p < NP; ++p) {
-            wait_bar(m, BAR(ring_full[0]) + 8 * rk.slot, rk.phase);
+            if (!ready) wait_bar(m, BAR(ring_full[0]) + 8 * rk.slot, rk.phase);
             tc_fence_after();
+            const int slot = rk.slot;
+            rk.next();
+            ready = mbar_test(BAR(ring_full[0]) + 8 * rk.slot, rk.phase);
             tc_cp_sf_atom(sfk + 4 * p, sdesc_sf_atom(sf_at + 512 * p));
-            const uint64_t ad = sdesc_kmajor_sw128(sbase + Z::kRing + rk.slot * kPanel);
+            const uint64_t ad = sdesc_kmajor_sw128(sbase + Z::kRing + slot * kPanel);
             const uint64_t bd = sdesc_kmajor_sw128(sbase + Z::kQ + p * GP * 256);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc_mxf8(128, 2 * GP, k, k), sfk + 4 * p, tmem + kColSfQ + 4 * p,
+            for (int k = 0; k < 4; ++k) {
+              tc_mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc_mxf8(128, Cols::kSWidth, k, k), sfk + 4 * p, tmem + kColSfQ + 4 * p,
                           (p | k) != 0 ? 1u : 0u);
-            tc_commit(BAR(ring_empty[0]) + 8 * rk.slot);
-            rk.next();
+              if constexpr (Cols::kAdd)
+                tc_mma_mxf8(d, ad + 2 * k, bd + GP * 8 + 2 * k, idesc_mxf8(128, GP, k, k), sfk + 4 * p, tmem + kColSfQ + 4 * p + 2, 1u);
+            }
+            tc_commit(BAR(ring_empty[0]) + 8 * slot);
           }
           tc_commit(BAR(s_full[0]) + 8 * s.slot);
           tc_commit(BAR(sf_empty[0]) + 8 * sf.slot);
@@ -807,6 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       Segments seg(a, m);
       Ring pr(Z::kPBufs), vr(kVSlots), o_ring(1);
+      bool ready = false;
 #pragma unroll 1
       while (seg.next()) {
         const int tiles = seg.tiles();
@@ -821,14 +841,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < chunks; ++c) {
             const int p = c >> both, h = c & both;
-            wait_bar(m, BAR(v_full[0]) + 8 * vr.slot, vr.phase);
+            if (!ready) wait_bar(m, BAR(v_full[0]) + 8 * vr.slot, vr.phase);
             tc_fence_after();
+            const int slot = vr.slot;
+            vr.next();
+            ready = mbar_test(BAR(v_full[0]) + 8 * vr.slot, vr.phase);
             const uint64_t bd = p_desc + h * 512;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc_mma_f16_ts(tmem + p * GO, tmem + kColV + 32 * vr.slot + 8 * k, bd + 128 * k, idesc, (i | h | k) != 0 ? 1u : 0u);
-            tc_commit(BAR(v_empty[0]) + 8 * vr.slot);
-            vr.next();
+              tc_mma_f16_ts(tmem + p * GO, tmem + kColV + 32 * slot + 8 * k, bd + 128 * k, idesc, (i | h | k) != 0 ? 1u : 0u);
+            tc_commit(BAR(v_empty[0]) + 8 * slot);
           }
           tc_commit(BAR(p_empty[0]) + 8 * pr.slot);
           pr.next();
@@ -906,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       do {
         wait_bar(m, BAR(s_full[0]) + 8 * s.slot, s.phase);
         tc_fence_after();
-        const uint32_t sc = t_lane + kColS + s.slot * 2 * GP + h0;
+        const uint32_t sc = t_lane + kColS + s.slot * Cols::kSWidth + h0;
         wait_bar(m, BAR(sf_full[0]) + 8 * sf.slot, sf.phase);
         const TileInfo* const info = reinterpret_cast<const TileInfo*>(smem + Z::kSf + sf.slot * sf_bytes + NP * 1024);
         const bool valid = (info->valid[quarter] >> lane) & 1;
@@ -921,18 +943,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile: they all do), or the pivot moves, the references move first, and S is read again.
         float e[SH];
         bool move = !started;
+        const bool ready = mbar_test(BAR(p_empty[0]) + 8 * pr.slot, pr.phase ^ 1);
         while (true) {
           if (move) {
 #pragma unroll 1
             for (int j = 0; j < SH; j += 8) {
               uint32_t hi[8], lo[8];
               tmem_ld_x8(sc + j, hi);
-              tmem_ld_x8(sc + GP + j, lo);
+              if constexpr (!Cols::kAdd) tmem_ld_x8(sc + GP + j, lo);
               tmem_ld_wait();
               int32_t mine = kNoScore;  // lane k: the largest score of head j + k
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered((__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c) : kNoScore);
+                const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered((Cols::kAdd ? __uint_as_float(hi[k]) : __uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c) : kNoScore);
                 mine = lane == k ? top : mine;
               }
               if (lane < 8) atomicMax(&m.red[h0 + j + lane], mine);
@@ -976,16 +999,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < SH; j += n) {
             uint32_t hi[n], lo[n];
-            if constexpr (n == 8) tmem_ld_x8(sc + j, hi), tmem_ld_x8(sc + GP + j, lo);
-            else tmem_ld_x16(sc + j, hi), tmem_ld_x16(sc + GP + j, lo);
+            if constexpr (n == 8) tmem_ld_x8(sc + j, hi);
+            else tmem_ld_x16(sc + j, hi);
+            if constexpr (!Cols::kAdd) {
+              if constexpr (n == 8) tmem_ld_x8(sc + GP + j, lo);
+              else tmem_ld_x16(sc + GP + j, lo);
+            }
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < n; k += 4) {
               const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j + k]);  // (minus the references)
               // (scaled as the references were, with a rounding of its own, so that the largest score's difference is 0
               // however large it is)
-              const float2 x0 = mul2(add2(__uint_as_float(hi[k]), __uint_as_float(hi[k + 1]), __uint_as_float(lo[k]), __uint_as_float(lo[k + 1])), c);
-              const float2 x1 = mul2(add2(__uint_as_float(hi[k + 2]), __uint_as_float(hi[k + 3]), __uint_as_float(lo[k + 2]), __uint_as_float(lo[k + 3])), c);
+              float2 x0 = make_float2(__uint_as_float(hi[k]), __uint_as_float(hi[k + 1])), x1 = make_float2(__uint_as_float(hi[k + 2]), __uint_as_float(hi[k + 3]));
+              if constexpr (!Cols::kAdd) {
+                x0 = add2(x0.x, x0.y, __uint_as_float(lo[k]), __uint_as_float(lo[k + 1]));
+                x1 = add2(x1.x, x1.y, __uint_as_float(lo[k + 2]), __uint_as_float(lo[k + 3]));
+              }
+              x0 = mul2(x0, c), x1 = mul2(x1, c);
               const float2 d0 = add2(x0.x, x0.y, r.x, r.y), d1 = add2(x1.x, x1.y, r.z, r.w);
               e[j + k] = d0.x, e[j + k + 1] = d0.y, e[j + k + 2] = d1.x, e[j + k + 3] = d1.y;
             }
@@ -1007,7 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(s_empty[0]) + 8 * s.slot);
         s.next();
-        wait_bar(m, BAR(p_empty[0]) + 8 * pr.slot, pr.phase ^ 1);
+        if (!ready) wait_bar(m, BAR(p_empty[0]) + 8 * pr.slot, pr.phase ^ 1);
         uint8_t* const row = smem + Z::kP + pr.slot * kPanel + prow * 128;
 #pragma unroll
         for (int j = 0; j < SH; j += 8) {
@@ -1087,6 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!wide) {
                 uint32_t r[4][4];
                 uint4 sw[4];
+                const bool tested = mbar_test(BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   ldmatrix_b8_trans_x2(rows + k * 2048, r[k]);
@@ -1114,7 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   w0[4 * k] = lo[0], w0[4 * k + 1] = lo[1], w0[4 * k + 2] = hi[0], w0[4 * k + 3] = hi[1];
                   w1[4 * k] = lo[2], w1[4 * k + 1] = lo[3], w1[4 * k + 2] = hi[2], w1[4 * k + 3] = hi[3];
                 }
-                wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
+                if (!__all_sync(0xffffffffu, tested)) wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
                 tc_fence_after();
                 tmem_st_16x128b_x8(dst, w0);
                 tmem_st_16x128b_x8(dst + (16u << 16), w1);
