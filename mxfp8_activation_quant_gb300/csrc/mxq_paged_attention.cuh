@@ -17,13 +17,21 @@
 // fp16 holds code * 2^(b - E) exactly for b in [E - 15, E + 7]: a tile with a scale above raises E (O is
 // rescaled with ref), one with a nonzero scale below takes P and V as bf16.
 //
-// Warps: 0 the rows' loads, 1 and 2 MMAs (scores, outputs), 3 scales, 4-11 softmax (two a TMEM lane quarter, half of the heads each),
-// 12-19 V^T and the outputs (two a
-// quarter; every second panel each, half of the heads each). Up to 8 heads the softmax takes four warps,
-// warp 8 the scales' copies and warp 9 the values' rows.
+// Warps: 0 the rows' loads, 1 and 2 MMAs (scores, outputs), 3 scales, 4-11 softmax (two a TMEM lane quarter, half of the
+// heads each), 12-19 V^T (two a quarter; every second panel each) and the outputs (half of the heads each). Up to 8 heads the
+// softmax takes four warps, warp 8 the scales' copies and warp 9 the values' rows.
 //
 // A CTA that holds an item from start to end writes its outputs; the others' normalised parts go to the
 // workspace (at most two a CTA), and join_kernel adds them up in the order of the CTAs.
+//
+// Measured, the whole call (captured, GB300) and the algorithmic bytes' rate:
+//   128 sequences of 1024-4096 tokens, 8 cache heads x 8 query heads of 128: 129 us, 5400 GB/s (a copy: 6770). Bound by HBM;
+//     a tile of 128 tokens takes 0.92 us, of which its bytes need 0.74.
+//   64 sequences of 2048-8192 tokens, latent, 64 heads of 512: 78 us, 2300 GB/s; 1 sequence of 131072: 42 us. Bound by the
+//     instructions: 3000 a scheduler and tile (softmax, conversion of V; issue slots 45 % busy), the waits of the chain TMA ->
+//     scores -> softmax -> outputs between them, and their fetching: the roles' loops miss the instruction cache in one of
+//     ten requests. Tensor cores 31 % busy. About 18 us are the queries, the first tile and the join.
+// A kernel of fp32 FMAs over the same items, the first that was right, took 10900 and 30000 us.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -38,11 +46,10 @@
 namespace mxq {
 namespace paged {
 
-
 constexpr int kUnit = 64;         // tokens of the unit of work; a TMA box has no more
 constexpr int kTile = 128;        // tokens of a tile
-constexpr int kThreads = 640;  // (five warps a scheduler leave each thread 96 registers; a sixth anywhere, 80)
-constexpr int kPanel = 128 * 128; // bytes of 128 features of a tile
+constexpr int kThreads = 640;     // (five warps a scheduler leave each thread 96 registers; a sixth anywhere, 80)
+constexpr int kPanel = 128 * 128;  // bytes of 128 features of a tile
 constexpr int kMaxHeads = 64;     // query heads of an item
 constexpr float kLowRef = -3.4028235e38f;  // ref before the first token: the lowest finite number, so that every score is above
 constexpr float kSlack = 8.0f;
@@ -97,8 +104,9 @@ struct Args {
 constexpr int kMaxSfBufs = 6;
 // Shared memory besides the buffers.
 struct Misc {
-  uint64_t ring_full[16], ring_empty[16], sf_raw[kMaxSfBufs], sf_full[kMaxSfBufs], sf_empty[kMaxSfBufs], s_full[2], s_empty[2], p_full[2], p_empty[2], v_full[kMaxVSlots],
-      v_empty[kMaxVSlots], q_full, q_empty, o_full, o_empty, fin_full[2], fin_empty[2], done;
+  uint64_t ring_full[16], ring_empty[16], sf_raw[kMaxSfBufs], sf_full[kMaxSfBufs], sf_empty[kMaxSfBufs], s_full[2], s_empty[2],
+      p_full[2], p_empty[2], v_full[kMaxVSlots], v_empty[kMaxVSlots], q_full, q_empty, o_full, o_empty, fin_full[2],
+      fin_empty[2], done;
   alignas(16) float ref[kMaxHeads];
   alignas(16) float fac[kMaxHeads];
   int32_t red[kMaxHeads];
@@ -621,7 +629,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(ring_empty[i]), shared_kv ? 5 : i < ring_k ? 1 : 4);
     }
 #pragma unroll 1
-    for (int i = 0; i < kMaxSfBufs; ++i) mbar_init(BAR(sf_raw[i]), 33), mbar_init(BAR(sf_full[i]), 1), mbar_init(BAR(sf_empty[i]), 1 + SW + (NP > 1 ? 8 : 4));
+    for (int i = 0; i < kMaxSfBufs; ++i) {
+      mbar_init(BAR(sf_raw[i]), 33), mbar_init(BAR(sf_full[i]), 1);
+      mbar_init(BAR(sf_empty[i]), 1 + SW + (NP > 1 ? 8 : 4));
+    }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(s_full[i]), 1), mbar_init(BAR(s_empty[i]), SW);
@@ -955,7 +966,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               int32_t mine = kNoScore;  // lane k: the largest score of head j + k
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered((Cols::kAdd ? __uint_as_float(hi[k]) : __uint_as_float(hi[k]) + __uint_as_float(lo[k])) * c) : kNoScore);
+                const float x = Cols::kAdd ? __uint_as_float(hi[k]) : __uint_as_float(hi[k]) + __uint_as_float(lo[k]);
+                const int32_t top = __reduce_max_sync(0xffffffffu, valid ? ordered(x * c) : kNoScore);
                 mine = lane == k ? top : mine;
               }
               if (lane < 8) atomicMax(&m.red[h0 + j + lane], mine);
@@ -1011,7 +1023,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float4 r = *reinterpret_cast<const float4*>(&m.ref[h0 + j + k]);  // (minus the references)
               // (scaled as the references were, with a rounding of its own, so that the largest score's difference is 0
               // however large it is)
-              float2 x0 = make_float2(__uint_as_float(hi[k]), __uint_as_float(hi[k + 1])), x1 = make_float2(__uint_as_float(hi[k + 2]), __uint_as_float(hi[k + 3]));
+              float2 x0 = make_float2(__uint_as_float(hi[k]), __uint_as_float(hi[k + 1]));
+              float2 x1 = make_float2(__uint_as_float(hi[k + 2]), __uint_as_float(hi[k + 3]));
               if constexpr (!Cols::kAdd) {
                 x0 = add2(x0.x, x0.y, __uint_as_float(lo[k]), __uint_as_float(lo[k + 1]));
                 x1 = add2(x1.x, x1.y, __uint_as_float(lo[k + 2]), __uint_as_float(lo[k + 3]));
