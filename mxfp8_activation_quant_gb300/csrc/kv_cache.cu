@@ -17,8 +17,15 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kUnits = 2;
-constexpr int64_t kManyRows = 4096;    // from here a warp reads four rows
-constexpr int64_t kManyWarps = 32768;  // and from so many warps of one row it writes four
+constexpr int64_t kManyRows = 4096;  // from here a warp reads four rows
+
+// Division by a number known on the host: x / d = x * (floor(2^64 / d) + 1) >> 64 for x < 2^64 / d, since the product is off by
+// less than x / 2^64 < 1 / d. (d = 1: mul = 0.)
+struct Divisor {
+  uint64_t mul;
+};
+Divisor divisor(uint64_t d) { return {d == 1 ? 0 : ~uint64_t(0) / d + 1}; }
+__device__ __forceinline__ uint64_t operator/(uint64_t x, Divisor d) { return d.mul == 0 ? x : __umul64hi(x, d.mul); }
 
 struct Tensor {
   const uint16_t* rows;
@@ -28,6 +35,7 @@ struct Tensor {
   int64_t page, token, head, sf_page, sf_token, sf_head;
   uint32_t dim, width;  // width = heads * dim
   uint32_t chunks;      // warp segments per row
+  Divisor by_dim, by_chunks;
 };
 
 struct WriteArgs {
@@ -35,6 +43,7 @@ struct WriteArgs {
   const int32_t* slots;
   int64_t T;
   uint32_t page_size, slots_end;
+  Divisor by_page;
 };
 
 struct ReadArgs {
@@ -63,59 +72,52 @@ Tensor tensor(const KvTensor& k) {
   t.dim = static_cast<uint32_t>(c.dim);
   t.width = static_cast<uint32_t>(c.heads) * t.dim;
   t.chunks = (t.width + 256 * kUnits - 1) / (256 * kUnits);
+  t.by_dim = divisor(t.dim);
+  t.by_chunks = divisor(t.chunks);
   return t;
 }
 
-// A warp takes the same columns of R consecutive tokens: where the heads lie is worked out once for all of them, and their loads
-// are in flight together. Keys and values of 65536 tokens of 8 x 128, a token a warp 84.4 us (4820 GB/s), four 78.0 us (5220
-// GB/s); of 8192 tokens 11.8 us either way; 4096 latent rows of 512, 3.1 and 4.0 us: few rows want the more warps.
-template <int R>
+// A write's instructions count as much as its bytes: with the compiler's divisions (the 64-bit one by a row's warps above all) 8192
+// tokens of 8 x 128, keys and values, took 12.0 us, now 11.3 (4500 GB/s); 65536 tokens 84.4 and 79.2 (5140 GB/s).
 __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ WriteArgs a) {
   const Tensor& t = a.t[blockIdx.y];
   const int lane = threadIdx.x & 31;
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t group = wid / t.chunks, row0 = group * R;
-  if (row0 >= a.T) return;
-  const uint32_t col0 = static_cast<uint32_t>(wid - group * t.chunks) * (256 * kUnits) + 8 * lane;
+  const int64_t row = static_cast<uint64_t>(wid) / t.by_chunks;
+  if (row >= a.T) return;
+  const uint32_t slot = static_cast<uint32_t>(a.slots[row]);
+  const uint32_t col0 = static_cast<uint32_t>(wid - row * t.chunks) * (256 * kUnits) + 8 * lane;
 
-  uint32_t slot[R];
-  uint4 v[R][kUnits];  // (asked for before the slots are looked at)
+  uint4 v[kUnits];  // (asked for before the slot is looked at)
   uint32_t h[kUnits], d[kUnits];
-#pragma unroll
-  for (int r = 0; r < R; ++r) slot[r] = row0 + r < a.T ? static_cast<uint32_t>(a.slots[row0 + r]) : 0xFFFFFFFFu;
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
     const uint32_t c = col0 + 256 * u;
-    h[u] = c / t.dim;
+    h[u] = static_cast<uint32_t>(c / t.by_dim);
     d[u] = c - h[u] * t.dim;
-    const uint16_t* const x = t.rows + row0 * t.ld + h[u] * t.ldh + d[u];
-#pragma unroll
-    for (int r = 0; r < R; ++r) v[r][u] = c < t.width && row0 + r < a.T ? ld_stream_u4(x + r * t.ld) : make_uint4(0, 0, 0, 0);
+    v[u] = c < t.width ? ld_stream_u4(t.rows + row * t.ld + h[u] * t.ldh + d[u]) : make_uint4(0, 0, 0, 0);
   }
+  if (slot >= a.slots_end) return;  // (negative ones too)
+  const uint32_t page = static_cast<uint32_t>(slot / a.by_page), place = slot - page * a.page_size;
+  uint8_t* const data = t.data + page * t.page + place * t.token;
+  uint8_t* const sf = t.sf + page * t.sf_page + place * t.sf_token;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (slot[r] >= a.slots_end) continue;  // (negative ones too)
-    const uint32_t page = slot[r] / a.page_size, place = slot[r] - page * a.page_size;
-    uint8_t* const data = t.data + page * t.page + place * t.token;
-    uint8_t* const sf = t.sf + page * t.sf_page + place * t.sf_token;
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const bool in = col0 + 256 * u < t.width;
-      uint32_t amax = absmax8(v[r][u]);
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const uint32_t code = ue8m0_from_bf16_amax(amax);
-      if (in) *reinterpret_cast<uint2*>(data + h[u] * t.head + d[u]) = quant8(v[r][u], ue8m0_inverse(code));
-      uint8_t* const s = sf + h[u] * t.sf_head + (d[u] >> 5);
-      if (t.dim % 128 == 0) {  // 16 lanes lie in one head: whole words
-        uint32_t w = code;
-        w |= __shfl_down_sync(0xffffffffu, code, 4) << 8;
-        w |= __shfl_down_sync(0xffffffffu, code, 8) << 16;
-        w |= __shfl_down_sync(0xffffffffu, code, 12) << 24;
-        if (in && (lane & 15) == 0) *reinterpret_cast<uint32_t*>(s) = w;
-      } else if (in && (lane & 3) == 0) {
-        *s = static_cast<uint8_t>(code);
-      }
+  for (int u = 0; u < kUnits; ++u) {
+    const bool in = col0 + 256 * u < t.width;
+    uint32_t amax = absmax8(v[u]);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const uint32_t code = ue8m0_from_bf16_amax(amax);
+    if (in) *reinterpret_cast<uint2*>(data + h[u] * t.head + d[u]) = quant8(v[u], ue8m0_inverse(code));
+    uint8_t* const s = sf + h[u] * t.sf_head + (d[u] >> 5);
+    if (t.dim % 128 == 0) {  // 16 lanes lie in one head: whole words
+      uint32_t w = code;
+      w |= __shfl_down_sync(0xffffffffu, code, 4) << 8;
+      w |= __shfl_down_sync(0xffffffffu, code, 8) << 16;
+      w |= __shfl_down_sync(0xffffffffu, code, 12) << 24;
+      if (in && (lane & 15) == 0) *reinterpret_cast<uint32_t*>(s) = w;
+    } else if (in && (lane & 3) == 0) {
+      *s = static_cast<uint8_t>(code);
     }
   }
 }
@@ -224,17 +226,15 @@ cudaError_t launch_kv_write(const KvWriteLaunch& l, cudaStream_t stream) {
     a.t[i] = tensor(l.t[i]);
     chunks = chunks > a.t[i].chunks ? chunks : a.t[i].chunks;
   }
-  const bool many = l.T * chunks >= kManyWarps;
-  const int64_t warps = (many ? (l.T + 3) / 4 : l.T) * chunks;
+  const int64_t warps = l.T * chunks;
   a.slots = l.slots;
   a.T = l.T;
   a.page_size = static_cast<uint32_t>(l.t[0].c.page_size);
+  a.by_page = divisor(a.page_size);
   a.slots_end = static_cast<uint32_t>(l.t[0].c.pages * l.t[0].c.page_size);
   const int64_t blocks = (warps + kWarps - 1) / kWarps;
   if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks), l.tensors);
-  if (many) kv_write_kernel<4><<<grid, kWarps * 32, 0, stream>>>(a);
-  else kv_write_kernel<1><<<grid, kWarps * 32, 0, stream>>>(a);
+  kv_write_kernel<<<dim3(static_cast<unsigned>(blocks), l.tensors), kWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -193,7 +193,7 @@ def test_captured(mxq):
 
 @pytest.mark.parametrize("T,heads,dim,two", [(32769, 1, 512, False), (16387, 5, 160, True), (33000, 1, 32, True)])
 def test_many_tokens(mxq, T, heads, dim, two):
-    """So many that a warp writes four: the last group is not full, some are not written, values of another width."""
+    """Numbers of warps and slots past 2^15, some tokens not written, values of another width."""
     g = torch.Generator(device="cuda").manual_seed(T)
     pages = -(-T // 16) + 2
     slots = torch.randperm(pages * 16, generator=g, device="cuda")[:T].to(torch.int32)
