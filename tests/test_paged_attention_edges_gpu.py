@@ -214,3 +214,60 @@ def test_common_pages_within_a_sequence(mxq):  # noqa: F811
     c.table[0, 4:] = c.table[0, :4]
     fill(c.g, c.kq, c.ksf, c.table, c.lens, 116, 2)
     c.check(c.call())
+
+
+FIRST_CALL = """
+import torch
+import mxfp8_activation_quant_gb300 as m
+g = torch.Generator(device="cuda").manual_seed(1)
+c = m.MXFP8Cache.empty(5, 16, 1, 256)
+k = torch.randn((70, 1, 256), generator=g, device="cuda").to(torch.bfloat16)
+q = torch.randn((1, 9, 256), generator=g, device="cuda").to(torch.bfloat16)
+slots = torch.arange(70, dtype=torch.int32, device="cuda")
+table, seq = torch.arange(5, dtype=torch.int32, device="cuda").view(1, 5), torch.full((1,), 70, dtype=torch.int32, device="cuda")
+out, want = torch.zeros_like(q), torch.empty_like(q)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    m.kv_write_mxfp8(k, slots, c)
+    m.paged_attention_mxfp8(q, c, table, seq, 0.0625, out=out)
+graph.replay()
+m.paged_attention_mxfp8(q, c, table, seq, 0.0625, out=want)
+torch.cuda.synchronize()
+assert torch.equal(out, want) and bool(out.any())
+print("fine")
+"""
+
+
+def test_first_call_under_capture(mxq):  # noqa: F811
+    """A process whose first calls are captured ones: nothing has to be set up by an eager call."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("page", [16, 48, 64])
+def test_pages_that_end_inside_a_tile(mxq, page):  # noqa: F811
+    """Lengths around every multiple of 16 up to two tiles, one CTA's item next to another's, in 64 bits."""
+    lens = [n + d for n in range(16, 272, 16) for d in (-1, 0, 1)]
+    c = Case(mxq, lens, 1, 12, 384, False, page=page, seed=47)
+    out = c.call()
+    c.check(out)
+
+
+def test_a_longer_table_changes_nothing(mxq):  # noqa: F811
+    """Columns of the table behind a sequence's pages hold anything."""
+    c = Case(mxq, [300, 64, 1], 2, 8, 128, False, page=16, seed=48)
+    want = c.call()
+    wide = torch.full((3, 1000), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[:, ::2] = -(2 ** 31)
+    wide[:, :c.table.shape[1]] = c.table
+    for b, n in enumerate(c.lens):
+        wide[b, -(-n // 16):] = 7 if b == 1 else -9
+    c.table = wide
+    got = c.call()
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
