@@ -21,8 +21,10 @@ from . import _lib
 from ._lib import I32, I64, P, _check, _ptr, _stream
 
 _F32 = ctypes.c_float
+_U8, _I32, _BF16, _FP32 = torch.uint8, torch.int32, torch.bfloat16, torch.float32
 # (looked up once; a torch without CUDA has neither, and no device tensor to call with)
 _device, _raw_stream = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_capturing = torch.cuda.is_current_stream_capturing
 
 # The C struct mxq_kv_cache as bytes: data, sf, pages, page_size, heads, dim, strides. (A few tokens take the GPU less
 # than a ctypes structure takes to be filled.)
@@ -74,9 +76,10 @@ class MXFP8Cache:
         pages, page, heads, dim = d.shape
         d0, d1, d2, one = d.stride()
         s0, s1, s2, one_s = s.stride()
-        assert d.dtype is torch.uint8 and s.dtype is torch.uint8
+        assert d.dtype is _U8 and s.dtype is _U8
         assert s.shape == (pages, page, heads, dim // 32) and one == 1 and (one_s == 1 or dim == 32)
-        if not (d.is_cuda and s.is_cuda and d.get_device() == s.get_device() == _device()):
+        dev = d.get_device()
+        if dev < 0 or s.get_device() != dev or dev != _device():
             _refuse(d, s)
         return _CACHE.pack(d.data_ptr(), s.data_ptr(), pages, page, heads, dim, d0, d1, d2, s0, s1, s2)
 
@@ -91,17 +94,18 @@ def kv_write_mxfp8(k: torch.Tensor, slots: torch.Tensor, k_cache: MXFP8Cache, v:
     """k bf16 [T, heads, dim] into the slots int32 [T] of the cache (-1: not written); v likewise."""
     T, = slots.shape
     kt, kh, one = k.stride()
-    assert slots.dtype is torch.int32 and slots.is_contiguous() and (v is None) == (v_cache is None)
-    assert k.dtype is torch.bfloat16 and one == 1 and k.shape == (T, *k_cache.data.shape[2:])
+    assert slots.dtype is _I32 and slots.is_contiguous() and (v is None) == (v_cache is None)
+    assert k.dtype is _BF16 and one == 1 and k.shape == (T, *k_cache.data.shape[2:])
     vp, vt, vh, vc = None, 0, 0, None
     if v is not None:
         vt, vh, one = v.stride()
-        assert v.dtype is torch.bfloat16 and one == 1 and v.shape == (T, *v_cache.data.shape[2:])
+        assert v.dtype is _BF16 and one == 1 and v.shape == (T, *v_cache.data.shape[2:])
         vp, vc = _ptr(v), v_cache.c()
-    if not (k.is_cuda and slots.is_cuda and k.get_device() == _device()):
+    dev = k.get_device()
+    if dev < 0 or slots.get_device() != dev or dev != _device():
         _refuse(k, slots)
     status = _fns().kv_write_mxfp8(k.data_ptr(), kt, kh, k_cache.c(), vp, vt, vh, vc, slots.data_ptr(), T,
-                                   _raw_stream(_device()) if stream is None else _stream(stream))
+                                   _raw_stream(dev) if stream is None else _stream(stream))
     if status:
         _check(status, "kv_write_mxfp8")
 
@@ -115,20 +119,21 @@ def kv_read_bf16(k_cache: MXFP8Cache, block_table: torch.Tensor, cu_rows: torch.
     B, rows = n - 1, k_out.shape[0]
     tb, width = block_table.shape
     ldt, one = block_table.stride()
-    assert cu_rows.dtype is torch.int32 and cu_rows.is_contiguous()
-    assert block_table.dtype is torch.int32 and tb == B and (one == 1 or width == 1)
-    assert starts is None or (starts.dtype is torch.int32 and starts.shape == (B,) and starts.is_contiguous())
+    assert cu_rows.dtype is _I32 and cu_rows.is_contiguous()
+    assert block_table.dtype is _I32 and tb == B and (one == 1 or width == 1)
+    assert starts is None or (starts.dtype is _I32 and starts.shape == (B,) and starts.is_contiguous())
     assert (v_out is None) == (v_cache is None)
-    assert k_out.dtype is torch.bfloat16 and k_out.is_contiguous() and k_out.shape == (rows, *k_cache.data.shape[2:])
+    assert k_out.dtype is _BF16 and k_out.is_contiguous() and k_out.shape == (rows, *k_cache.data.shape[2:])
     vp, vc = None, None
     if v_out is not None:
-        assert v_out.dtype is torch.bfloat16 and v_out.is_contiguous() and v_out.shape == (rows, *v_cache.data.shape[2:])
+        assert v_out.dtype is _BF16 and v_out.is_contiguous() and v_out.shape == (rows, *v_cache.data.shape[2:])
         vp, vc = _ptr(v_out), v_cache.c()
-    if not (k_out.is_cuda and block_table.is_cuda and cu_rows.is_cuda and k_out.get_device() == _device()):
+    dev = k_out.get_device()
+    if dev < 0 or block_table.get_device() != dev or cu_rows.get_device() != dev or dev != _device():
         _refuse(k_out, block_table, cu_rows)
     status = _fns().kv_read_bf16(k_cache.c(), vc, block_table.data_ptr(), ldt, width, cu_rows.data_ptr(),
                                  None if starts is None else _ptr(starts), B, rows, k_out.data_ptr(), vp,
-                                 _raw_stream(_device()) if stream is None else _stream(stream))
+                                 _raw_stream(dev) if stream is None else _stream(stream))
     if status:
         _check(status, "kv_read_bf16")
 
@@ -137,23 +142,23 @@ _workspaces: dict = {}
 _sharing = threading.Lock()  # held over a call with a kept workspace: two threads may call on one stream
 
 
-def _workspace(size: int, stream) -> Optional[torch.Tensor]:
-    """The workspace kept for a stream, grown to `size` bytes where it is smaller; calls ordered on one stream may share
-    it. Under capture a call gets one from the graph's own pool, so that no graph depends on what is kept here."""
+def _workspace(dev: int, raw: int, size: int, stream):
+    """(address, bytes) of the workspace kept for a stream, grown to `size` bytes where it is smaller; calls ordered on one
+    stream may share it. Under capture a call gets one from the graph's own pool, so that no graph depends on what is kept here
+    (freed on return: the pool gives it to work behind this call's only)."""
+    if size <= 0:
+        return None, 0
     if stream is not None:  # (memory is owned by the stream that uses it)
         s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
         with torch.cuda.stream(s):
-            return _workspace(size, None)
-    if size <= 0:
-        return None
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(size, dtype=torch.uint8, device="cuda")
-    device = _device()
-    key = device, _raw_stream(device)
-    ws = _workspaces.get(key)
-    if ws is None or ws.nbytes < size:
-        ws = _workspaces[key] = torch.empty(size, dtype=torch.uint8, device="cuda")
-    return ws
+            return _workspace(dev, raw, size, None)
+    if _capturing():
+        return torch.empty(size, dtype=_U8, device="cuda").data_ptr(), size
+    ws = _workspaces.get((dev, raw))
+    if ws is None or ws[1] < size:
+        t = torch.empty(size, dtype=_U8, device="cuda")
+        ws = _workspaces[dev, raw] = t.data_ptr(), size, t
+    return ws[:2]
 
 
 def paged_attention_workspace_bytes(B: int, q_heads: int, kv_heads: int, dim: int) -> int:
@@ -178,29 +183,29 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
     tb, width = block_table.shape
     ldt, one_t = block_table.stride()
     shape = k_cache.data.shape
-    assert q.dtype is torch.bfloat16 and shape[3] == D and one == 1
-    assert seq_lens.dtype is torch.int32 and seq_lens.shape == (B,) and seq_lens.is_contiguous()
-    assert block_table.dtype is torch.int32 and tb == B and (one_t == 1 or width == 1)
+    assert q.dtype is _BF16 and shape[3] == D and one == 1
+    assert seq_lens.dtype is _I32 and seq_lens.shape == (B,) and seq_lens.is_contiguous()
+    assert block_table.dtype is _I32 and tb == B and (one_t == 1 or width == 1)
     n = B * H * D
-    assert out is None or (out.dtype is torch.bfloat16 and out.numel() == n and out.is_contiguous())
-    assert out_q is None or (out_q.dtype is torch.uint8 and out_q.numel() == n and out_q.is_contiguous())
-    assert lse is None or (lse.dtype is torch.float32 and lse.numel() == B * H and lse.is_contiguous())
+    assert out is None or (out.dtype is _BF16 and out.numel() == n and out.is_contiguous())
+    assert out_q is None or (out_q.dtype is _U8 and out_q.numel() == n and out_q.is_contiguous())
+    assert lse is None or (lse.dtype is _FP32 and lse.numel() == B * H and lse.is_contiguous())
     assert sf_rowmajor is None or sf_rowmajor.nbytes * 32 >= n
     assert sf_packed is None or sf_packed.nbytes * 32 >= -(-B // 4) * 4 * H * D
     assert sf_128x4 is None or sf_128x4.nbytes * 32 >= -(-B // 128) * 128 * H * D
-    if not (q.is_cuda and block_table.is_cuda and seq_lens.is_cuda and q.get_device() == _device()):
+    dev = q.get_device()
+    if dev < 0 or block_table.get_device() != dev or seq_lens.get_device() != dev or dev != _device():
         _refuse(q, block_table, seq_lens)
     kc, vc = k_cache.c(), None if v_cache is None else v_cache.c()
     outs = (None if out is None else _ptr(out), None if out_q is None else _ptr(out_q), None if sf_packed is None else _ptr(sf_packed),
             None if sf_rowmajor is None else _ptr(sf_rowmajor), None if sf_128x4 is None else _ptr(sf_128x4),
             None if lse is None else _ptr(lse))
     args = (q.data_ptr(), ldq, ldqh, kc, vc, block_table.data_ptr(), ldt, width, seq_lens.data_ptr(), B, H, scale, *outs)
-    status_at, raw = None if status is None else _ptr(status), _raw_stream(_device()) if stream is None else _stream(stream)
+    status_at, raw = None if status is None else _ptr(status), _raw_stream(dev) if stream is None else _stream(stream)
     if workspace is None:
         with _sharing:
-            ws = _workspace(lib.mxq_paged_attention_workspace_bytes(B, H, shape[2], D), stream)
-            code = lib.paged_attention_mxfp8(*args, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
-                                             status_at, raw)
+            at, size = _workspace(dev, raw, lib.mxq_paged_attention_workspace_bytes(B, H, shape[2], D), stream)
+            code = lib.paged_attention_mxfp8(*args, at, size, status_at, raw)
     else:
         code = lib.paged_attention_mxfp8(*args, _ptr(workspace), workspace.nbytes, status_at, raw)
     if code:
