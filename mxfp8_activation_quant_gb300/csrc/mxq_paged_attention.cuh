@@ -68,6 +68,9 @@ struct Columns {
   static constexpr uint32_t kS = GP == 64 ? 256 : GP == 32 ? 128 : 64, kSfK = kS + (GP < 16 ? 64 : kBuffers * kSWidth),
                             kSfQ = kSfK + 16 * kBuffers, kV = (kSfQ + 16 + 31) / 32 * 32;
   static constexpr int kSlots = (512 - kV) / 32 < 8 ? (512 - kV) / 32 : 8;
+  // A set of warps that is about to fill chunk c has filled one of c - 3 .. c - 1, so chunk c - 3 - kSlots is used up; its wait for
+  // chunk c - kSlots tells a phase from the next only if c - 2 kSlots is too.
+  static_assert(kSlots >= 3);
 };
 constexpr int kMaxVSlots = 8;
 
