@@ -271,3 +271,28 @@ def test_a_longer_table_changes_nothing(mxq):  # noqa: F811
     c.table = wide
     got = c.call()
     assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+
+
+@pytest.mark.parametrize("B,kv,G,D,page", [(65536, 1, 1, 128, 16), (64, 1024, 4, 128, 16), (3, 1, 4096, 256, 32), (1, 1024, 1, 512, 64)])
+def test_the_largest_batches_and_heads(mxq, B, kv, G, D, page):  # noqa: F811
+    """The most sequences, cache heads and query heads that a call takes; some sequences are checked in 64 bits."""
+    from kv_reference import attention
+
+    g = torch.Generator(device="cuda").manual_seed(B + kv)
+    pages = B + 1
+    shape = (pages, page, kv, D)
+    code = torch.randint(0, 254, shape, generator=g, device="cuda", dtype=torch.int16)
+    kq = (code + (code >= 127)).to(torch.uint8)
+    ksf = torch.randint(114, 119, (*shape[:3], D // 32), generator=g, device="cuda", dtype=torch.int16).to(torch.uint8)
+    table = torch.randperm(pages, generator=g, device="cuda")[:B].to(torch.int32).view(B, 1)
+    seq = torch.randint(0, page + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    seq[0] = page
+    q = torch.randn((B, kv * G, D), generator=g, device="cuda").to(torch.bfloat16)
+    out, lse, scale = torch.full_like(q, math.nan), torch.empty((B, kv * G), device="cuda"), 2.0 / (math.sqrt(D) * 70 * 2.0 ** -11)
+    mxq.paged_attention_mxfp8(q, mxq.MXFP8Cache(kq, ksf), table, seq, scale, out=out, lse=lse)
+    pick = sorted({0, B // 3, B // 2, B - 1})
+    o, l, tol, ltol = attention(q[pick], kq, ksf, None, None, table[pick], seq[pick].tolist(), scale)
+    got = out[pick].double()
+    assert bool(((got - o).abs() <= tol + 2.0 ** -8 * (o.abs() + tol) + 2.0 ** -133).all())
+    assert bool((torch.where(l.isinf(), 0.0, (lse[pick].double() - l).abs()) <= ltol).all())
+    assert torch.equal(lse.isinf(), (seq == 0)[:, None].expand_as(lse)) and not bool(out.isnan().any())
