@@ -41,6 +41,7 @@
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
 #include "mxq_kv_internal.h"
+#include "mxq_rings.h"
 #include "mxq_tma.h"
 
 namespace mxq {
@@ -145,7 +146,8 @@ struct Sizes {
                        kSfBytes = NP * 1024 + static_cast<int>(sizeof(TileInfo)), kFin = kSf + kSfBufs * kSfBytes,
                        kMisc = kFin + 2 * static_cast<int>(sizeof(Fin)), kRing = (kMisc + static_cast<int>(sizeof(Misc)) + 1023) / 1024 * 1024;
   static constexpr int kRoom = (kSmemLimit - kRing) / kPanel, kSlots = kRoom < 16 ? kRoom : 16, kTotal = kRing + kSlots * kPanel;
-  static_assert(kSlots >= 6 && kSfBufs <= kMaxSfBufs);
+  static constexpr int kValueSlots = value_ring(kSlots);  // of them, where the values are not the keys
+  static_assert(kSlots >= 6 && kSfBufs <= kMaxSfBufs && ring_ok(kSlots, Columns<GP>::kSlots) && ring_ok(kValueSlots, Columns<GP>::kSlots));
 };
 
 // ---- PTX ----------------------------------------------------------------------------------
@@ -617,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool shared_kv = a.v_sf == nullptr;
   const int S = a.kv * a.blocks;
-  const int ring_k = shared_kv ? Z::kSlots : Z::kSlots / 2, ring_v = shared_kv ? Z::kSlots : Z::kSlots - ring_k;
+  const int ring_v = shared_kv ? Z::kSlots : Z::kValueSlots, ring_k = shared_kv ? Z::kSlots : Z::kSlots - ring_v;
 #define BAR(x) smem_u32(&m.x)
 
   pdl_launch_dependents();

@@ -296,3 +296,22 @@ def test_the_largest_batches_and_heads(mxq, B, kv, G, D, page):  # noqa: F811
     assert bool(((got - o).abs() <= tol + 2.0 ** -8 * (o.abs() + tol) + 2.0 ** -133).all())
     assert bool((torch.where(l.isinf(), 0.0, (lse[pick].double() - l).abs()) <= ltol).all())
     assert torch.equal(lse.isinf(), (seq == 0)[:, None].expand_as(lse)) and not bool(out.isnan().any())
+
+
+@pytest.mark.parametrize("G,D", [(8, 384), (8, 512), (16, 256), (12, 384), (16, 512), (32, 256), (64, 512)])
+def test_values_of_their_own_at_length(mxq, G, D):  # noqa: F811
+    """Rings of keys and values apart, long enough that loads overtake one another: a value cache that holds what the keys do gives
+    what a latent call gives, but for the order of its sums (checked in 64 bits)."""
+    g = torch.Generator(device="cuda").manual_seed(D + G)
+    lens = [1 + (2711 * i) % 1500 for i in range(24)] + [1 + i for i in range(60)]
+    c = Case(mxq, lens, 2, G, D, False, page=64, seed=50)
+    c.vq.copy_(c.kq)
+    c.vsf.copy_(c.ksf)
+    out = c.call()
+    c.vq = c.vsf = None
+    want = c.call()
+    err = (out["out"].double() - want["out"].double()).norm() / want["out"].double().norm()
+    assert float(err) <= 2.0 ** -8 and not bool(out["out"].isnan().any())
+    pick = torch.randint(0, len(lens), (6,), generator=g, device="cuda").tolist()
+    c.q, c.table, c.lens = c.q[pick], c.table[pick], [lens[i] for i in pick]
+    c.check(dict(out=out["out"][pick], lse=out["lse"][pick]))
