@@ -18,7 +18,7 @@
 // rescaled with ref), one with a nonzero scale below takes P and V as bf16.
 //
 // Warps: 0 the rows' loads, 1 and 2 MMAs (scores, outputs), 3 scales, 4-11 softmax (two a TMEM lane quarter, half of the
-// heads each), 12-19 V^T (two a quarter; every second panel each) and the outputs (half of the heads each). Up to 8 heads the
+// heads each), 12-19 V^T (two a quarter; every second panel each) and the outputs (half of the heads each). Up to 16 heads the
 // softmax takes four warps, warp 8 the scales' copies and warp 9 the values' rows.
 //
 // A CTA that holds an item from start to end writes its outputs; the others' normalised parts go to the
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ Args a) {
   constexpr int GO = GP < 16 ? 16 : GP;   // columns of O a panel: an MMA has 16 at least
   constexpr int HPT = GO / 2;             // heads of an output thread
-  constexpr int SW = GP == 8 ? 4 : 8;     // warps of the softmax, and a thread's heads
+  constexpr int SW = GP <= 16 ? 4 : 8;    // warps of the softmax, and a thread's heads
   constexpr int SH = GP * 4 / SW;
   constexpr bool kCopier = SW == 4;       // then another copies the scales
   using Cols = Columns<GP>;
