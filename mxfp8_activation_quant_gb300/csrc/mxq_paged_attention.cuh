@@ -18,8 +18,8 @@
 // rescaled with ref), one with a nonzero scale below takes P and V as bf16.
 //
 // Warps: 0 the rows' loads, 1 and 2 MMAs (scores, outputs), 3 scales, 4-11 softmax (two a TMEM lane quarter, half of the
-// heads each), 12-19 V^T (two a quarter; every second panel each) and the outputs (half of the heads each). Up to 16 heads the
-// softmax takes four warps, warp 8 the scales' copies and warp 9 the values' rows.
+// heads each), 12-19 V^T (two a quarter; every second panel each) and the outputs (half of the heads each). Of few heads
+// the softmax takes four warps; warp 8 then copies the scales and warp 9 loads the values' rows.
 //
 // A CTA that holds an item from start to end writes its outputs; the others' normalised parts go to the
 // workspace (at most two a CTA), and join_kernel adds them up in the order of the CTAs.
@@ -605,7 +605,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ Args a) {
   constexpr int GO = GP < 16 ? 16 : GP;   // columns of O a panel: an MMA has 16 at least
   constexpr int HPT = GO / 2;             // heads of an output thread
-  constexpr int SW = GP <= 16 ? 4 : 8;    // warps of the softmax, and a thread's heads
+  // Warps of the softmax, and a thread's heads. With four of them others copy scales and load the values' rows: better where a tile's
+  // softmax is short beside its rows (4 cache heads x 64 sequences of 1024-4096, 16 heads of 128: 52.9 -> 47.7 us, 32 of 512: 137.2 -> 134.5;
+  // but 32 of 384: 107.7 -> 111.6, and 128 sequences x 8 cache heads, 32 of 128: 189 -> 237).
+  constexpr int SW = GP <= 16 || GP <= 8 * NP ? 4 : 8;
   constexpr int SH = GP * 4 / SW;
   constexpr bool kCopier = SW == 4;       // then another copies the scales
   using Cols = Columns<GP>;
