@@ -315,3 +315,18 @@ def test_values_of_their_own_at_length(mxq, G, D):  # noqa: F811
     pick = torch.randint(0, len(lens), (6,), generator=g, device="cuda").tolist()
     c.q, c.table, c.lens = c.q[pick], c.table[pick], [lens[i] for i in pick]
     c.check(dict(out=out["out"][pick], lse=out["lse"][pick]))
+
+
+def test_streams_by_object_and_by_handle(mxq):  # noqa: F811
+    """stream= as a Stream, as a raw handle and as the default stream's 0; each has a workspace that grows."""
+    small, large = Case(mxq, [40], 1, 8, 128, True, seed=51), two_cases(mxq)[1]
+    want = [c.call()["out"] for c in (small, large)]
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream, 0, torch.cuda.default_stream()):
+        for c, w in zip((small, large, small), (*want, want[0])):
+            k, v = c.caches()
+            out = torch.empty_like(c.q)
+            torch.cuda.synchronize()
+            mxq.paged_attention_mxfp8(c.q, k, c.table, c.seq, c.scale, v_cache=v, out=out, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(out, w)
