@@ -442,7 +442,7 @@ struct ScaleCopies {
       }
     } else {
       const uint32_t kd = buf + lane * 16 * NP, vd = kd + NP * 512;
-      if (vs != ks) copy_tokens(kd, ks, a.k_sf_token);
+      if (a.v_sf != nullptr) copy_tokens(kd, ks, a.k_sf_token);  // (as check_scales asks, whatever the addresses: two caches may share scales)
       copy_tokens(vd, vs, v_step);
     }
   }
