@@ -118,11 +118,13 @@ struct Misc {
   int32_t p_wide[2];  // whether the probabilities are bf16
   int32_t w0, w1, per_cta, rest;
   int32_t b0, kvh0, blk0, u0;
+  // the softmax's own walk over the segments, for each half of the heads: units left, sequence, first unit, length, tiles of the segment
+  int32_t left[2], b[2], u[2], len[2], tiles[2];
   uint32_t tmem;
   volatile int32_t dead;
 };
 // A buffer of scales: K atoms [panels][512], V bytes [panels][128 tokens][4 groups], then this.
-constexpr int kWide = 1, kLastTile = 2, kLastOfAll = 4;  // values in bf16; the segment's, and the CTA's, last tile
+constexpr int kWide = 1;  // values in bf16
 struct TileInfo {
   uint32_t valid[4];
   int32_t pivot, flags;
@@ -378,10 +380,14 @@ struct Ring {
   }
 };
 
-// A bounded wait: half a million tries, of about two microseconds each; false once one has run out,
-// after which nothing waits any more (results are void, every loop still ends, and the status word is written at the
-// end). Small on purpose: it is inlined thirty times, and the roles' loops have to fit the instruction cache together
-// (with the library's usual wait, which reads a clock, they did not: 93 % hits, and its refills at 64 % of their peak).
+// A bounded wait: half a million tries, of about two microseconds each; false once one has run out, after which nothing waits any
+// more: results are void, and the status word is written at the end. Then
+//  - every loop still ends: roles count their tiles from the lengths, not from what a wait guards (the softmax's warps meet at barriers
+//    without a limit, so they must all count the same);
+//  - no load is announced over one in flight: who has not waited for a panel, a chunk of V^T or the queries hands on and releases nothing
+//    any more, but leaves, so that the barriers of the rings keep their meaning
+// (both in tests/giveup_sim.cpp). Small on purpose: it is inlined thirty times, and the roles' loops have to fit the instruction cache
+// together (with the library's usual wait, which reads a clock, they did not: 93 % hits, and its refills at 64 % of their peak).
 constexpr uint32_t kWaitTries = 1u << 19;
 __device__ __forceinline__ bool wait_bar(Misc& m, uint32_t bar, uint32_t parity) {
   uint32_t tries = 0;
@@ -655,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     m.dead = 0;
     m.w0 = m.w1 = 0;
+    for (int i = 0; i < 2; ++i) m.left[i] = m.b[i] = m.u[i] = m.len[i] = 0;
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
@@ -698,6 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       m.w0 = w0;
       m.w1 = w0 + per_cta + (static_cast<int32_t>(blockIdx.x) < rest ? 1 : 0);
       m.per_cta = per_cta;
+      m.left[0] = m.left[1] = m.w1 - m.w0;
+      m.b[0] = m.b[1] = b - 1;
+      m.u[0] = m.u[1] = at;
+      m.len[0] = m.len[1] = a.lens[b];
       m.rest = rest;
     }
   }
@@ -791,15 +802,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (seg.next()) {
         const int tiles = seg.tiles();
         // this item's queries, once the last scores of the one before are done
-        wait_bar(m, BAR(q_empty), q_ring.phase ^ 1);
+        if (!wait_bar(m, BAR(q_empty), q_ring.phase ^ 1)) goto scores_over;
         if (first) pdl_wait_primary();
         first = false;
         const uint8_t* const q = a.q_ws + ((static_cast<int64_t>(seg.seg_b) * a.kv + seg.kvh) * a.blocks + seg.blk) * (NP * (GP * 256 + 512));
         mbar_arrive_expect_tx(BAR(q_full), NP * (GP * 256 + 512));
         bulk_load(sbase + Z::kQ, q, NP * GP * 256, BAR(q_full));
         bulk_load(sbase + Z::kQSf, q + NP * GP * 256, NP * 512, BAR(q_full));
-        wait_bar(m, BAR(q_full), q_ring.phase);
+        const bool landed = wait_bar(m, BAR(q_full), q_ring.phase);
         q_ring.next();
+        if (!landed) goto scores_over;
         tc_fence_after();
 #pragma unroll 1
         for (int p = 0; p < NP; ++p) tc_cp_sf_atom(tmem + kColSfQ + 4 * p, sdesc_sf_atom(sbase + Z::kQSf + 512 * p));
@@ -812,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d = tmem + kColS + s.slot * Cols::kSWidth, sfk = tmem + kColSfK + 16 * s.slot;
 #pragma unroll 1
           for (int p = 0; p < NP; ++p) {
-            if (!ready) wait_bar(m, BAR(ring_full[0]) + 8 * rk.slot, rk.phase);
+            if (!ready && !wait_bar(m, BAR(ring_full[0]) + 8 * rk.slot, rk.phase)) goto scores_over;
             tc_fence_after();
             const int slot = rk.slot;
             rk.next();
@@ -836,6 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s.next();
         }
       }
+    scores_over:
       tc_commit(BAR(done));
       if (!first && !mbar_wait_bounded(BAR(q_full), q_ring.phase ^ 1)) m.dead = 1;  // (no copy outlives the CTA)
     }
@@ -860,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < chunks; ++c) {
             const int p = c >> both, h = c & both;
-            if (!ready) wait_bar(m, BAR(v_full[0]) + 8 * vr.slot, vr.phase);
+            if (!ready && !wait_bar(m, BAR(v_full[0]) + 8 * vr.slot, vr.phase)) goto outputs_over;
             tc_fence_after();
             const int slot = vr.slot;
             vr.next();
@@ -876,6 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_commit(BAR(o_full));
       }
+    outputs_over:
       tc_commit(BAR(done));
       if (!mbar_wait_bounded(BAR(done), 0)) m.dead = 1;
     }
@@ -906,8 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_bar(m, BAR(sf_raw[0]) + 8 * sf.slot, sf.phase);
         const bool ok = (info->there >> lane) & 1;
         const uint32_t mine = !ok || n <= 0 ? 0u : n >= 4 ? 15u : (1u << n) - 1;  // these of the lane's tokens take part
-        int32_t flags = i + 1 == tiles ? kLastTile | (seg.left == 0 ? kLastOfAll : 0) : 0;
-        flags |= check_scales<NP, ScaleCopies<GP, NP>::kInOrder>(buf, info, shared_kv, lane, mine, pivot);
+        const int32_t flags = check_scales<NP, ScaleCopies<GP, NP>::kInOrder>(buf, info, shared_kv, lane, mine, pivot);
         if (lane == 0) info->pivot = pivot, info->flags = flags;
         fence_proxy_async_smem();
         __syncwarp();
@@ -931,19 +944,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = 32 * quarter + lane;
     // the row of P of this thread's token: tokens 4 j + i of 16 are rows 2 j + i (i < 2) and 6 + 2 j + i
     const int prow = (t & ~15) + ((t >> 2) & 3) * 2 + (t & 1) + ((t & 2) << 2);
-    Ring sf(Z::kSfBufs), s(SB), pr(Z::kPBufs), fin(2);
-    bool more = m.w1 > m.w0 && warp < 4 + SW;
+    // (where S has as many buffers as P, one position serves both)
+    constexpr bool kOneRing = SB == Z::kPBufs;
+    Ring sf(Z::kSfBufs), pr(Z::kPBufs), s_own(SB), fin(2);
+    Ring& s = kOneRing ? pr : s_own;
+    const int half = (warp - 4) / 4;
 #pragma unroll 1
-    while (more) {  // (the tiles say where a segment ends: its own count would cost registers)
+    while (warp < 4 + SW) {
       float l[SH];
 #pragma unroll
       for (int i = 0; i < SH; ++i) l[i] = 0.f;
-      int32_t pivot = 0;
+      // The segment's tiles, counted by one thread for the warps of the same heads (a walk of each thread's own would cost registers).
+      if ((st & 127) == 0) {
+        cp_async_wait_all();
+        const int32_t left = m.left[half], b = m.b[half] + 1 == a.B ? 0 : m.b[half] + 1;
+        const int32_t n = min(units_of(length_of(a, m.len[half])) - m.u[half], left);
+        m.left[half] = left - n;
+        m.b[half] = b;
+        m.u[half] = 0;
+        m.tiles[half] = (n + 1) >> 1;
+        if (left > n) cp_async<4>(smem_u32(&m.len[half]), a.lens + (b + 1 == a.B ? 0 : b + 1));
+      }
       // (the last segment's references were read before this barrier)
       named_barrier(half_bar, 128);
       if ((st & 127) < SH) m.ref[hl] = -kLowRef;
+      uint32_t state = static_cast<uint32_t>(m.tiles[half]) << 8;  // tiles left, and the pivot in the low byte: one register
       named_barrier(half_bar, 128);
-      bool last, started = false;
+      if (state == 0) break;
+      bool started = false;
       do {
         wait_bar(m, BAR(s_full[0]) + 8 * s.slot, s.phase);
         tc_fence_after();
@@ -953,8 +981,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool valid = (info->valid[quarter] >> lane) & 1;
         const int32_t new_pivot = info->pivot;
         const bool wide = (info->flags & kWide) != 0;
-        last = (info->flags & kLastTile) != 0;
-        more = (info->flags & kLastOfAll) == 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(sf_empty[0]) + 8 * sf.slot);
         sf.next();
@@ -998,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int prev = pr.slot == 0 ? Z::kPBufs - 1 : pr.slot - 1;
               wait_bar(m, BAR(p_empty[0]) + 8 * prev, pr.slot == 0 ? pr.phase ^ 1 : pr.phase);
               tc_fence_after();
-              const int down = pivot - new_pivot;  // <= 0
+              const int down = static_cast<int>(state & 255) - new_pivot;  // <= 0
               const float pf = down < -126 ? 0.f : __uint_as_float((127 + down) << 23);
 #pragma unroll 1
               for (int q = 0; q < NP * (SH / 8); ++q) {
@@ -1013,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tmem_st_wait();
             }
-            pivot = new_pivot;
+            state = (state & ~255u) | (new_pivot & 255);
           }
           constexpr int n = SH < 16 ? 8 : 16;
 #pragma unroll
@@ -1052,13 +1078,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < SH; ++j) e[j] = ex2(e[j]);
           if (move) break;
-          move = named_barrier_or(half_bar, 128, over > kSlack || new_pivot != pivot);
+          move = named_barrier_or(half_bar, 128, over > kSlack || ((state ^ new_pivot) & 255) != 0);
           if (!move) break;
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(s_empty[0]) + 8 * s.slot);
-        s.next();
+        if constexpr (!kOneRing) s.next();
         if (!ready) wait_bar(m, BAR(p_empty[0]) + 8 * pr.slot, pr.phase ^ 1);
         uint8_t* const row = smem + Z::kP + pr.slot * kPanel + prow * 128;
 #pragma unroll
@@ -1081,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(BAR(p_full[0]) + 8 * pr.slot);
         pr.next();
         started = true;
-      } while (!last);
+      } while ((state -= 256) >= 256);
       // sums over the quarter's tokens
       Fin& f = *reinterpret_cast<Fin*>(smem + Z::kFin + fin.slot * sizeof(Fin));
       wait_bar(m, BAR(fin_empty[fin.slot]), fin.phase ^ 1);
@@ -1089,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kShare = 32 / SH;  // lanes that hold the same head
       if (lane % kShare == 0) f.sum[quarter][h0 + lane / kShare] = l[0];
       if (quarter == 0 && lane < SH) f.ref[h0 + lane] = -m.ref[h0 + lane];
-      if (st == 0) f.pivot = pivot;
+      if (st == 0) f.pivot = static_cast<int32_t>(state);
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(fin_full[fin.slot]));
       fin.next();
@@ -1130,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (v_slot >= kVSlots) v_slot -= kVSlots, v_phase ^= 1;
             turn ^= 1;
             if (turn == set) continue;  // (it was the other's)
-            wait_bar(m, BAR(ring_full[0]) + 8 * s, rv.slot == 0 ? rv.phase ^ 1 : rv.phase);
+            if (!__all_sync(0xffffffffu, wait_bar(m, BAR(ring_full[0]) + 8 * s, rv.slot == 0 ? rv.phase ^ 1 : rv.phase))) goto values_over;
 #pragma unroll 1
             for (int h = 0; h < halves; ++h) {
               const uint32_t rows = row_at + s * kPanel + h * 8192, dst = t_lane + kColV + 32 * vs;
@@ -1167,12 +1193,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                   w0[4 * k] = lo[0], w0[4 * k + 1] = lo[1], w0[4 * k + 2] = hi[0], w0[4 * k + 3] = hi[1];
                   w1[4 * k] = lo[2], w1[4 * k + 1] = lo[3], w1[4 * k + 2] = hi[2], w1[4 * k + 3] = hi[3];
                 }
-                if (!__all_sync(0xffffffffu, tested)) wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
+                if (!__all_sync(0xffffffffu, tested) && !__all_sync(0xffffffffu, wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1))) goto values_over;
                 tc_fence_after();
                 tmem_st_16x128b_x8(dst, w0);
                 tmem_st_16x128b_x8(dst + (16u << 16), w1);
               } else {  // the scales span more than fp16 holds: bf16
-                wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1);
+                if (!__all_sync(0xffffffffu, wait_bar(m, BAR(v_empty[0]) + 8 * vs, vphase ^ 1))) goto values_over;
                 tc_fence_after();
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
@@ -1293,6 +1319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       o_ring.next();
       fin.next();
     }
+  values_over:
     if (tid == 12 * 32) a.owner[blockIdx.x] = owner;
   }
   tc_fence_before();
