@@ -14,7 +14,8 @@ using namespace paged;
 namespace {
 
 // Adds the parts of the items that more than one CTA held, always in the CTAs' order of a warp's share:
-//   o = sum_k w_k o_k / sum_k w_k, w_k = l_k 2^(ref_k - max ref), lse = ln 2 (max ref + log2 sum_k w_k).
+//   o = sum_k (w_k / sum_k w_k) o_k, w_k = l_k 2^(ref_k - max ref), lse = ln 2 (max ref + log2 sum_k w_k);
+// divided first, so that no partial sum is larger than the largest part (w_k is up to 2^8 for each token).
 // With few items, which then have many parts, a block takes 128 features of a head and its warps every eighth part; with
 // many a warp takes a head. Also the scale layouts' padding rows. Bound by the chain of loads (owner, statistics, parts) with few
 // parts, 6.6 us alone (serialised, cold), and by L2 with many: 152 parts of 64 x 512, 20 MB, 9.8 us; 216 of them, 28 MB, 11 us.
@@ -42,8 +43,8 @@ __device__ __forceinline__ JoinWork join_work(const Args& a, const int16_t* owne
 __device__ __forceinline__ int join_slot(const JoinWork& w, int k) { return k == 0 ? 2 * w.j0 + 1 : 2 * (w.j0 + k); }
 
 // A warp's features 128 p + 4 lane .. + 3.
-__device__ __forceinline__ void join_store(const Args& a, const JoinWork& w, int p, float4 v, float inv, int lane) {
-  const uint2 y = make_uint2(bf16x2_rn(v.x * inv, v.y * inv), bf16x2_rn(v.z * inv, v.w * inv));
+__device__ __forceinline__ void join_store(const Args& a, const JoinWork& w, int p, float4 v, int lane) {
+  const uint2 y = make_uint2(bf16x2_rn(v.x, v.y), bf16x2_rn(v.z, v.w));
   const int64_t at = (static_cast<int64_t>(w.b) * a.H + w.head) * a.D + 128 * p + 4 * lane;
   if (a.o != nullptr) *reinterpret_cast<uint2*>(a.o + at) = y;
   if (a.oq != nullptr) {
@@ -122,15 +123,21 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
 #pragma unroll 1
       for (int k = lane; k < w.parts; k += 32) top = fmaxf(top, a.stat[join_slot(w, k) * gp + w.h].x);
       top = warp_max(top);
+#pragma unroll 1
+      for (int k = lane; k < w.parts; k += 32) {
+        const float2 s = a.stat[join_slot(w, k) * gp + w.h];
+        sum += s.y * ex2(s.x - top);
+      }
+      sum = warp_sum(sum);
+      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
       float4 v[4] = {};
 #pragma unroll 1
       for (int k0 = 0; k0 < w.parts; k0 += 32) {
         float mine = 0.f;
         if (k0 + lane < w.parts) {
           const float2 s = a.stat[join_slot(w, k0 + lane) * gp + w.h];
-          mine = s.y * ex2(s.x - top);
+          mine = s.y * ex2(s.x - top) * inv;
         }
-        sum += mine;
         const int n = min(32, w.parts - k0);
 #pragma unroll 2
         for (int k = 0; k < n; ++k) {
@@ -141,11 +148,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
             if (p < NP) join_add(v[p], f, x[32 * p]);
         }
       }
-      sum = warp_sum(sum);
-      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
       for (int p = 0; p < 4; ++p)
-        if (p < NP) join_store(a, w, p, v[p], inv, lane);
+        if (p < NP) join_store(a, w, p, v[p], lane);
       if (a.lse != nullptr && lane == 0) a.lse[static_cast<int64_t>(w.b) * a.H + w.head] = lse_of(top, sum);
     }
     return;
@@ -174,6 +179,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < kJoinWarps; ++k) sum += sums[k];
+    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     const float* const x = a.part + w.h * a.D + 128 * p + 4 * lane;
 #pragma unroll 1
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
 #pragma unroll
       for (int u = 0; u < 10; ++u) {
         const int k = k0 + u * kJoinWarps;
-        join_add(v, k < w.parts ? weight[k] : 0.f, f[u]);
+        join_add(v, k < w.parts ? weight[k] * inv : 0.f, f[u]);
       }
     }
     acc[warp][lane] = v;
@@ -195,7 +201,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
     if (warp == 0) {
 #pragma unroll
       for (int k = 1; k < kJoinWarps; ++k) join_add(v, 1.0f, acc[k][lane]);
-      join_store(a, w, p, v, sum > 0.f ? 1.0f / sum : 0.f, lane);
+      join_store(a, w, p, v, lane);
       if (a.lse != nullptr && p == 0 && lane == 0) a.lse[static_cast<int64_t>(w.b) * a.H + w.head] = lse_of(top, sum);
     }
     __syncthreads();  // (the weights and sums of the next)
