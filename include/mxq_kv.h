@@ -80,8 +80,8 @@ MXQ_API mxq_status kv_read_bf16(const mxq_kv_cache* k_cache, const mxq_kv_cache*
  *   (o_q, scales) = mxfp8_quantize(o)                         of that bf16 o as [B, q_heads * dim], bit-identical
  * with G = q_heads / heads query heads for each head of the cache. Without a value cache the values are the
  * keys (a latent cache). Products and sums are in fp32. q enters them as the sum of two MXFP8 numbers (off by at
- * most 2^-21 of its group's largest magnitude), the probabilities in 16 bits (fp16; bf16 where the
- * scales of a tile of values span more than fp16 holds).
+ * most 2^-21 of its group's largest magnitude), the probabilities in 16 bits (fp16, off by at most 2^-11 of itself or 2^-32 of the
+ * largest so far; bf16 where the scales of a tile of values span more than fp16 holds).
  *
  * len_b = min(seq_lens[b], table_width * page_size); tokens on a page outside [0, pages) take no part. A
  * sequence without a token gives zeros and lse -inf. What the cache holds behind a sequence's end is not used,

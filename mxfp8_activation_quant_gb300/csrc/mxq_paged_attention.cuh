@@ -6,9 +6,11 @@
 //   S^T[t, h] = K_t . q_h    tcgen05.mma kind::mxf8f6f4, block-scaled, M = 128 tokens: cache rows go from TMA
 //                            straight into the MMA. bf16 has 8 significant bits and E4M3 4, so q = hi + lo, both
 //                            MXFP8 (lo's scales 2^-4 of hi's): N = 2 GP columns, added where S is read.
-//   P = exp2(S - ref)        ref: a running reference within 2^8 of the running maximum (moved, with O and the
-//                            sums, only when a score passes it by more), so P fits fp16 and a tile
-//                            needs no maximum of its own
+//   P = exp2(S - ref)        ref: a running reference, put 2^7 below the running maximum when it moves (with O and the
+//                            sums; only when a score passes it by more than 2^15), so that a tile needs no maximum of its own and
+//                            P fits fp16, whose largest is 2^16: the largest P is 2^7 or more, so one 2^-21 of it is still a normal
+//                            number, and one of 2^-32 counts (with ref at the maximum, long tails of 2^-25 were lost from O, not
+//                            from the sums)
 //   O^T[d, h] += V^T P^T     kind::f16, M = 128 features a panel: ldmatrix transposes the E4M3 bytes, registers make
 //                            them fp16 with their scales relative to the segment's pivot 2^E, and they
 //                            are stored to TMEM as the A operand. (Dequantized rows in shared memory would
@@ -53,7 +55,7 @@ constexpr int kThreads = 640;     // (five warps a scheduler leave each thread 9
 constexpr int kPanel = 128 * 128;  // bytes of 128 features of a tile
 constexpr int kMaxHeads = 64;     // query heads of an item
 constexpr float kLowRef = -3.4028235e38f;  // ref before the first token: the lowest finite number, so that every score is above
-constexpr float kSlack = 8.0f;
+constexpr float kLead = 7.0f, kSlack = 15.0f;  // of the largest score over ref, in binary orders: where ref is put, and before it moves
 constexpr int32_t kNoScore = static_cast<int32_t>(0x807FFFFFu);  // ordered(-infinity)
 
 // TMEM columns for GP heads: O from 0, S (one buffer of 64 heads, two of fewer, and as many of K's scales, so that a tile's are
@@ -1008,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             named_barrier(half_bar, 128);
             if ((st & 127) < SH) {
-              const float old = -m.ref[hl], now = fmaxf(old, fmaxf(kLowRef, of_ordered(m.red[hl])));
+              const float old = -m.ref[hl], now = fmaxf(old, fmaxf(kLowRef, of_ordered(m.red[hl]) - kLead));
               m.ref[hl] = -now;
               m.fac[hl] = ex2(old - now);
               m.red[hl] = kNoScore;
