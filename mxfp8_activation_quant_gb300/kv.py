@@ -148,8 +148,8 @@ def _workspace(dev: int, raw: int, size: int, stream):
     (freed on return: the pool gives it to work behind this call's only)."""
     if size <= 0:
         return None, 0
-    if stream is not None:  # (memory is owned by the stream that uses it)
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    if stream is not None:  # (memory is owned by the stream that uses it; ExternalStream(0) would be some stream of torch's pool)
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
         with torch.cuda.stream(s):
             return _workspace(dev, raw, size, None)
     if _capturing():
