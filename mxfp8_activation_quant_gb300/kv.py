@@ -138,6 +138,7 @@ def kv_read_bf16(k_cache: MXFP8Cache, block_table: torch.Tensor, cu_rows: torch.
         _check(status, "kv_read_bf16")
 
 
+_PER_THREAD = 2  # cudaStreamPerThread
 _workspaces: dict = {}
 _sharing = threading.Lock()  # held over a call with a kept workspace: two threads may call on one stream
 
@@ -154,6 +155,8 @@ def _workspace(dev: int, raw: int, size: int, stream):
             return _workspace(dev, raw, size, None)
     if _capturing():
         return torch.empty(size, dtype=_U8, device="cuda").data_ptr(), size
+    if raw == _PER_THREAD:
+        raise ValueError("the per-thread default stream is another one in each thread: give a workspace")
     ws = _workspaces.get((dev, raw))
     if ws is None or ws[1] < size:
         t = torch.empty(size, dtype=_U8, device="cuda")
@@ -175,8 +178,8 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
     out [B, q_heads, dim] and/or MXFP8 out_q [B, q_heads * dim] with any subset of the three scale layouts; lse
     fp32 [B, q_heads]. Without v_cache the values are the keys.
 
-    workspace: None = one that this module keeps for the stream (allocated for this call under stream capture), or a
-    uint8 tensor of paged_attention_workspace_bytes(...)."""
+    workspace: None = one that this module keeps for the stream (allocated for this call under stream capture; the per-thread
+    default stream has none), or a uint8 tensor of paged_attention_workspace_bytes(...)."""
     lib = _fns()
     B, H, D = q.shape
     ldq, ldqh, one = q.stride()
