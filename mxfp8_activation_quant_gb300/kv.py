@@ -63,6 +63,14 @@ def _refuse(*tensors: Optional[torch.Tensor]) -> None:
     raise ValueError("a tensor of another device than the current one")
 
 
+def _on(dev: int, t: Optional[torch.Tensor]) -> Optional[int]:
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        _refuse(t)
+    return t.data_ptr()
+
+
 @dataclass
 class MXFP8Cache:
     """A paged cache: E4M3 bytes [pages, page_size, heads, dim] and UE8M0 scales [pages, page_size, heads,
@@ -96,14 +104,14 @@ def kv_write_mxfp8(k: torch.Tensor, slots: torch.Tensor, k_cache: MXFP8Cache, v:
     kt, kh, one = k.stride()
     assert slots.dtype is _I32 and slots.is_contiguous() and (v is None) == (v_cache is None)
     assert k.dtype is _BF16 and one == 1 and k.shape == (T, *k_cache.data.shape[2:])
+    dev = k.get_device()
+    if dev < 0 or slots.get_device() != dev or dev != _device():
+        _refuse(k, slots)
     vp, vt, vh, vc = None, 0, 0, None
     if v is not None:
         vt, vh, one = v.stride()
         assert v.dtype is _BF16 and one == 1 and v.shape == (T, *v_cache.data.shape[2:])
-        vp, vc = _ptr(v), v_cache.c()
-    dev = k.get_device()
-    if dev < 0 or slots.get_device() != dev or dev != _device():
-        _refuse(k, slots)
+        vp, vc = _on(dev, v), v_cache.c()
     status = _fns().kv_write_mxfp8(k.data_ptr(), kt, kh, k_cache.c(), vp, vt, vh, vc, slots.data_ptr(), T,
                                    _raw_stream(dev) if stream is None else _stream(stream))
     if status:
@@ -124,15 +132,15 @@ def kv_read_bf16(k_cache: MXFP8Cache, block_table: torch.Tensor, cu_rows: torch.
     assert starts is None or (starts.dtype is _I32 and starts.shape == (B,) and starts.is_contiguous())
     assert (v_out is None) == (v_cache is None)
     assert k_out.dtype is _BF16 and k_out.is_contiguous() and k_out.shape == (rows, *k_cache.data.shape[2:])
-    vp, vc = None, None
-    if v_out is not None:
-        assert v_out.dtype is _BF16 and v_out.is_contiguous() and v_out.shape == (rows, *v_cache.data.shape[2:])
-        vp, vc = _ptr(v_out), v_cache.c()
     dev = k_out.get_device()
     if dev < 0 or block_table.get_device() != dev or cu_rows.get_device() != dev or dev != _device():
         _refuse(k_out, block_table, cu_rows)
+    vp, vc = None, None
+    if v_out is not None:
+        assert v_out.dtype is _BF16 and v_out.is_contiguous() and v_out.shape == (rows, *v_cache.data.shape[2:])
+        vp, vc = _on(dev, v_out), v_cache.c()
     status = _fns().kv_read_bf16(k_cache.c(), vc, block_table.data_ptr(), ldt, width, cu_rows.data_ptr(),
-                                 None if starts is None else _ptr(starts), B, rows, k_out.data_ptr(), vp,
+                                 _on(dev, starts), B, rows, k_out.data_ptr(), vp,
                                  _raw_stream(dev) if stream is None else _stream(stream))
     if status:
         _check(status, "kv_read_bf16")
@@ -200,16 +208,14 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
     if dev < 0 or block_table.get_device() != dev or seq_lens.get_device() != dev or dev != _device():
         _refuse(q, block_table, seq_lens)
     kc, vc = k_cache.c(), None if v_cache is None else v_cache.c()
-    outs = (None if out is None else _ptr(out), None if out_q is None else _ptr(out_q), None if sf_packed is None else _ptr(sf_packed),
-            None if sf_rowmajor is None else _ptr(sf_rowmajor), None if sf_128x4 is None else _ptr(sf_128x4),
-            None if lse is None else _ptr(lse))
+    outs = _on(dev, out), _on(dev, out_q), _on(dev, sf_packed), _on(dev, sf_rowmajor), _on(dev, sf_128x4), _on(dev, lse)
     args = (q.data_ptr(), ldq, ldqh, kc, vc, block_table.data_ptr(), ldt, width, seq_lens.data_ptr(), B, H, scale, *outs)
-    status_at, raw = None if status is None else _ptr(status), _raw_stream(dev) if stream is None else _stream(stream)
+    status_at, raw = _on(dev, status), _raw_stream(dev) if stream is None else _stream(stream)
     if workspace is None:
         with _sharing:
             at, size = _workspace(dev, raw, lib.mxq_paged_attention_workspace_bytes(B, H, shape[2], D), stream)
             code = lib.paged_attention_mxfp8(*args, at, size, status_at, raw)
     else:
-        code = lib.paged_attention_mxfp8(*args, _ptr(workspace), workspace.nbytes, status_at, raw)
+        code = lib.paged_attention_mxfp8(*args, _on(dev, workspace), workspace.nbytes, status_at, raw)
     if code:
         _check(code, "paged_attention_mxfp8")
