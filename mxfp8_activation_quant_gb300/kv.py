@@ -201,9 +201,11 @@ def paged_attention_mxfp8(q: torch.Tensor, k_cache: MXFP8Cache, block_table: tor
     assert out is None or (out.dtype is _BF16 and out.numel() == n and out.is_contiguous())
     assert out_q is None or (out_q.dtype is _U8 and out_q.numel() == n and out_q.is_contiguous())
     assert lse is None or (lse.dtype is _FP32 and lse.numel() == B * H and lse.is_contiguous())
-    assert sf_rowmajor is None or sf_rowmajor.nbytes * 32 >= n
-    assert sf_packed is None or sf_packed.nbytes * 32 >= -(-B // 4) * 4 * H * D
-    assert sf_128x4 is None or sf_128x4.nbytes * 32 >= -(-B // 128) * 128 * H * D
+    assert sf_rowmajor is None or (sf_rowmajor.nbytes * 32 >= n and sf_rowmajor.is_contiguous())
+    assert sf_packed is None or (sf_packed.nbytes * 32 >= -(-B // 4) * 4 * H * D and sf_packed.is_contiguous())
+    assert sf_128x4 is None or (sf_128x4.nbytes * 32 >= -(-B // 128) * 128 * H * D and sf_128x4.is_contiguous())
+    assert workspace is None or (workspace.dtype is _U8 and workspace.is_contiguous())
+    assert status is None or (status.nbytes >= 4 and status.is_contiguous())
     dev = q.get_device()
     if dev < 0 or block_table.get_device() != dev or seq_lens.get_device() != dev or dev != _device():
         _refuse(q, block_table, seq_lens)

@@ -79,6 +79,23 @@ def test_tensors_of_another_device_are_refused(lib, call):
     assert lib.calls == 1
 
 
+@pytest.mark.parametrize("name", ["sf_packed", "sf_rowmajor", "sf_128x4", "workspace", "status"])
+def test_buffers_that_are_not_dense_are_refused(lib, name):
+    """Their bytes are counted, and a view repeats or skips some: an expanded one has memory for a single element."""
+    full = arguments()["paged_attention_mxfp8"][name].t
+    views = [full[:1].expand(full.shape), full.repeat(2)[::2]]
+    if name == "workspace":
+        views.append(torch.zeros(1024))  # (not bytes)
+    if name == "status":
+        views.append(torch.zeros(0, dtype=torch.int32))
+    for view in views:
+        args = arguments()["paged_attention_mxfp8"]
+        args[name] = Device(view)
+        with pytest.raises(AssertionError):
+            kv.paged_attention_mxfp8(**args)
+    assert lib.calls == 0
+
+
 def test_no_workspace_is_kept_for_the_per_thread_stream(monkeypatch):
     """Its handle, 2, names another stream in each thread, and launches of two threads would share the memory."""
     monkeypatch.setattr(kv, "_workspaces", {})
