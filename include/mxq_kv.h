@@ -81,7 +81,9 @@ MXQ_API mxq_status kv_read_bf16(const mxq_kv_cache* k_cache, const mxq_kv_cache*
  * with G = q_heads / heads query heads for each head of the cache. Without a value cache the values are the
  * keys (a latent cache). Products and sums are in fp32. q enters them as the sum of two MXFP8 numbers (off by at
  * most 2^-21 of its group's largest magnitude), the probabilities in 16 bits (fp16, off by at most 2^-11 of itself or 2^-32 of the
- * largest so far; bf16 where the scales of a tile of values span more than fp16 holds).
+ * largest so far; bf16 where the scales of a tile of values span more than fp16 holds). Values keep their precision beside scales up
+ * to 2^100 times their own; further below the largest of their sequence and cache head they may lose bits or count as zeros, and so may
+ * those of scale byte 0 (at most 448 * 2^-127) beside scales of 2^-112 and more.
  *
  * len_b = min(seq_lens[b], table_width * page_size); tokens on a page outside [0, pages) take no part. A
  * sequence without a token gives zeros and lse -inf. What the cache holds behind a sequence's end is not used,

@@ -16,8 +16,10 @@
 //                            are stored to TMEM as the A operand. (Dequantized rows in shared memory would
 //                            cost 128 KB written and read a tile of 512 features, which alone takes
 //                            2048 of the 2800 cycles in which HBM delivers the tile.)
-// fp16 holds code * 2^(b - E) exactly for b in [E - 15, E + 7]: a tile with a scale above raises E (O is
-// rescaled with ref), one with a nonzero scale below takes P and V as bf16.
+// fp16 holds code * 2^(b - E) exactly for b in [E - 14, E + 7] (the factor is an fp16 of its own, and normal): a tile with a scale above
+// raises E (O is rescaled with ref), one with a nonzero scale byte below takes P and V as bf16. Byte 0 does not ask for that: all-zero
+// groups and tokens that take no part have it. Its factor is 0 once E passes 14, so what values it has, of at most 448 * 2^-127, then
+// count as zeros.
 //
 // Warps: 0 the rows' loads, 1 and 2 MMAs (scores, outputs), 3 scales, 4-11 softmax (two a TMEM lane quarter, half of the
 // heads each), 12-19 V^T (two a quarter; every second panel each) and the outputs (half of the heads each). Of few heads
