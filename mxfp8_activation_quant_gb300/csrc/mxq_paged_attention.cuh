@@ -153,7 +153,7 @@ struct Sizes {
                        kMisc = kFin + 2 * static_cast<int>(sizeof(Fin)), kRing = (kMisc + static_cast<int>(sizeof(Misc)) + 1023) / 1024 * 1024;
   static constexpr int kRoom = (kSmemLimit - kRing) / kPanel, kSlots = kRoom < 16 ? kRoom : 16, kTotal = kRing + kSlots * kPanel;
   static constexpr int kValueSlots = value_ring(kSlots);  // of them, where the values are not the keys
-  static_assert(kSlots >= 6 && kSfBufs <= kMaxSfBufs && ring_ok(kSlots, Columns<GP>::kSlots) && ring_ok(kValueSlots, Columns<GP>::kSlots));
+  static_assert(kSlots >= 6 && kSfBufs <= kMaxSfBufs && scale_ring_ok(kSfBufs) && ring_ok(kSlots, Columns<GP>::kSlots) && ring_ok(kValueSlots, Columns<GP>::kSlots));
 };
 
 // ---- PTX ----------------------------------------------------------------------------------

@@ -14,5 +14,8 @@ constexpr bool ring_ok(int slots, int chunks) { return slots % 2 == 0 || slots >
 // The values' part of `slots`, where keys and values have rings of their own (the scores' thread waits for every panel of the keys):
 // about half, an even number.
 constexpr int value_ring(int slots) { return (slots / 2 + 1) & ~1; }
+// The buffers of scales. With one panel a tile a set waits for its own tiles' alone, every second one; but one warp fills the buffers in
+// order, so a set that has waited for tile n - 2 knows that tile n - bufs is there, odd or even.
+constexpr bool scale_ring_ok(int bufs) { return bufs >= 2; }
 
 }  // namespace mxq
