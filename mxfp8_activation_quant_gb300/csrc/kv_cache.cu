@@ -3,9 +3,10 @@
 //
 // Mapping: as the standalone quantizer's: 8 elements per lane, 4 lanes per 32-element group (amax with two
 // xor-shuffles), 16 lanes per 128-element scale word, and a warp owns a segment of kUnits x 256 columns
-// of a token's heads * dim row. Both bound by HBM: a write moves 2 + 33/32 bytes an element, a read the
-// same the other way. Keys and values go in one launch (grid.y), since a decode step's few tokens take less
-// than a launch does.
+// of a token's heads * dim row. A write moves 2 + 33/32 bytes an element, a read the same the other way: a read of a batch's
+// prefixes is bound by HBM (40960 rows of 8 x 128, keys and values, 41.9 us: 0.90 of a copy's rate), a write of 8192 tokens by its
+// instructions (11.0 us, 0.68 of the copy's rate; issue slots 75 % busy, DRAM 30 %, since its stores stay in L2). Keys and
+// values go in one launch (grid.y), since a decode step's few tokens take less than a launch does.
 #include <cuda_runtime.h>
 
 #include "mxq_device.cuh"
@@ -80,7 +81,7 @@ Tensor tensor(const KvTensor& k) {
 }
 
 // A write's instructions count as much as its bytes: with the compiler's divisions (the 64-bit one by a row's warps above all) 8192
-// tokens of 8 x 128, keys and values, took 12.0 us, now 11.3 (4500 GB/s); 65536 tokens 84.4 and 79.2 (5140 GB/s).
+// tokens of 8 x 128, keys and values, took 12.0 us, now 11.0 (4600 GB/s); 65536 tokens 84.4 and 79.2 (5140 GB/s).
 __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ WriteArgs a) {
   const Tensor& t = a.t[blockIdx.y];
   const int lane = threadIdx.x & 31;

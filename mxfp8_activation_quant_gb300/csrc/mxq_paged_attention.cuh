@@ -29,10 +29,11 @@
 // workspace (at most two a CTA), and join_kernel adds them up in the order of the CTAs.
 //
 // Measured, the whole call (captured, GB300) and the algorithmic bytes' rate:
-//   128 sequences of 1024-4096 tokens, 8 cache heads x 8 query heads of 128: 129 us, 5400 GB/s (a copy: 6770). Bound by HBM;
-//     a tile of 128 tokens takes 0.92 us, of which its bytes need 0.74.
-//   64 sequences of 2048-8192 tokens, latent, 64 heads of 512: 78 us, 2300 GB/s; 1 sequence of 131072: 42 us. Bound by the
-//     instructions: 3000 a scheduler and tile (softmax, conversion of V; issue slots 45 % busy), the waits of the chain TMA ->
+//   128 sequences of 1024-4096 tokens, 8 cache heads x 8 query heads of 128: 132 us, 5300 GB/s (a copy: 6770). Bound by HBM;
+//     a tile of 128 tokens takes 0.94 us, of which its bytes need 0.74. With 16 query heads a cache head 145 us, with 32 175: there the
+//     softmax is as long as the rows.
+//   64 sequences of 2048-8192 tokens, latent, 64 heads of 512: 79 us, 2300 GB/s; 1 sequence of 131072: 43 us. Bound by the
+//     instructions: 3000 a scheduler and tile (softmax, conversion of V; issue slots 46 % busy), the waits of the chain TMA ->
 //     scores -> softmax -> outputs between them, and their fetching: the roles' loops miss the instruction cache in one of
 //     ten requests. Tensor cores 31 % busy. About 18 us are the queries, the first tile and the join.
 // A kernel of fp32 FMAs over the same items, the first that was right, took 10900 and 30000 us.
@@ -616,8 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int GO = GP < 16 ? 16 : GP;   // columns of O a panel: an MMA has 16 at least
   constexpr int HPT = GO / 2;             // heads of an output thread
   // Warps of the softmax, and a thread's heads. With four of them others copy scales and load the values' rows: better where a tile's
-  // softmax is short beside its rows (4 cache heads x 64 sequences of 1024-4096, 16 heads of 128: 52.9 -> 47.7 us, 32 of 512: 137.2 -> 134.5;
-  // but 32 of 384: 107.7 -> 111.6, and 128 sequences x 8 cache heads, 32 of 128: 189 -> 237).
+  // softmax is short beside its rows. Eight warps, four (us): 64 sequences of 1024-4096 on 4 cache heads, 16 heads of 128 57.4, 49.1, of 512
+  // 130.1, 124.9, 32 heads of 128 56.5, 70.7, of 384 106.9, 110.7, of 512 135.1, 135.1; latent of 2048-8192, 16 of 512 60.3, 53.9, 32 of 384
+  // 52.8, 55.0, of 512 63.1, 61.6.
   constexpr int SW = GP <= 16 || GP <= 8 * NP ? 4 : 8;
   constexpr int SH = GP * 4 / SW;
   constexpr bool kCopier = SW == 4;       // then another copies the scales
