@@ -104,6 +104,15 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def torch_stream(stream) -> torch.cuda.Stream:
+    """The torch stream of a stream object or a raw handle (0: the default stream; ExternalStream(0) would be some stream of
+    torch's pool)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = _stream(stream)
+    return torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
+
+
 def _check(status: int, where: str):
     if status != 0:
         detail = load().mxq_last_error_string().decode() if status == 5 else ""
@@ -132,9 +141,10 @@ def workspace_for(stream=None) -> Optional[torch.Tensor]:
     key = (s.device.index if hasattr(s, "device") else torch.cuda.current_device(), _stream(s))
     ws = _workspaces.get(key)
     if ws is None:
-        if torch.cuda.is_current_stream_capturing():
-            return None
-        ws = torch.zeros(workspace_bytes(), dtype=torch.uint8, device=s.device if hasattr(s, "device") else "cuda")
+        with torch.cuda.stream(torch_stream(s)):  # (its memory, and zero before anything that the stream does next)
+            if torch.cuda.is_current_stream_capturing():
+                return None
+            ws = torch.zeros(workspace_bytes(), dtype=torch.uint8, device="cuda")
         _workspaces[key] = ws
     return ws
 

@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import I32, I64, P, _check, _ptr, _stream
+from ._lib import I32, I64, P, _check, _ptr, _stream, torch_stream
 
 _F32 = ctypes.c_float
 _U8, _I32, _BF16, _FP32 = torch.uint8, torch.int32, torch.bfloat16, torch.float32
@@ -157,9 +157,8 @@ def _workspace(dev: int, raw: int, size: int, stream):
     (freed on return: the pool gives it to work behind this call's only)."""
     if size <= 0:
         return None, 0
-    if stream is not None:  # (memory is owned by the stream that uses it; ExternalStream(0) would be some stream of torch's pool)
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
-        with torch.cuda.stream(s):
+    if stream is not None:  # (memory is owned by the stream that uses it)
+        with torch.cuda.stream(torch_stream(stream)):
             return _workspace(dev, raw, size, None)
     if _capturing():
         return torch.empty(size, dtype=_U8, device="cuda").data_ptr(), size
