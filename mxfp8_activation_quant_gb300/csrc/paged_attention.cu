@@ -15,12 +15,13 @@ namespace {
 
 // Adds the parts of the items that more than one CTA held, always in the CTAs' order of a warp's share:
 //   o = sum_k (w_k / sum_k w_k) o_k, w_k = l_k 2^(ref_k - max ref), lse = ln 2 (max ref + log2 sum_k w_k);
-// divided first, so that no partial sum is larger than the largest part (w_k is up to 2^8 for each token).
+// divided first, so that no partial sum is larger than the largest part (w_k is up to 2^15 for each token).
 // With few items, which then have many parts, or where there is a block for each head and panel, a block takes 128 features of a head and
 // its warps every eighth part; else a warp takes a head. The whole call with a block, with a warp (us): 64 heads of 512, 8 items 37.9, 42.6,
 // 16 items 44.9, 35.9, 32 items 64.0, 33.7; 16 heads of 256 (32 blocks an item of 608), 16 items 18.6, 22.3, 24 items 21.9, 21.0; 8 heads of 128
-// (8 blocks), 64 items 16.8, 17.4, 100 items 19.4, 17.5. Also the scale layouts' padding rows. Bound by the chain of loads (owner, statistics, parts) with few
-// parts, 6.6 us alone (serialised, cold), and by L2 with many: 152 parts of 64 x 512, 20 MB, 9.8 us; 216 of them, 28 MB, 11 us.
+// (8 blocks), 64 items 16.8, 17.4, 100 items 19.4, 17.5. Also the scale layouts' padding rows. Bound by the chain of loads (owner,
+// statistics, parts) with few parts, 6.6 us alone (serialised, cold), and by L2 with many: 152 parts of 64 x 512, 20 MB, 9.8 us; 216 of them,
+// 28 MB, 11 us.
 // (Parts asked for before their weights are known: 13.1 us, for the registers.)
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxCtas = 512;
